@@ -92,6 +92,7 @@ typedef enum mqa_variant {
 #define MQA_DEVERR_PAGE_RANGE 0x2u /* a block-table entry in use lies outside [0, num_pages) */
 #define MQA_DEVERR_SEQ_LEN 0x4u    /* seq_len < 1, > capacity, > max_seq_len or past the block table */
 #define MQA_DEVERR_TIMEOUT 0x8u    /* a bounded wait inside a kernel ran out (the result is invalid) */
+#define MQA_DEVERR_TREE 0x20u      /* a tree's depth, parent, token or path entry out of range */
 #define MQA_DEVERR_U8_SCALE 0x10u  /* MQA_U8: a V scale above 1023 was read; those output rows are invalid */
 
 /*
@@ -393,6 +394,126 @@ MQA_API mqa_status mqa_prefill_step(const mqa_kv_layout* layout, int32_t n_new, 
                                     const void* v_new, const int32_t* pos, const int32_t* seq_lens,
                                     int32_t max_seq_len, double rope_base, float scale, float* q_rot, void* out,
                                     int32_t out_dtype, float* lse_out, int32_t* err_word, mqa_stream_t stream);
+
+/*
+ * A tree of drafted tokens: speculative decoding with several candidates for
+ * each position ("Arsitektur Inferensi LLM", section 7, checks a chain of
+ * drafted tokens in one pass of the target; a tree holds many chains that
+ * share their beginnings). One round is
+ *   mqa_tree_step in every layer  ->  the model's probabilities after each node
+ *   ->  mqa_verify_tree  ->  kv_keep_path over all layers  ->  pos += num_kept
+ *
+ * Sequence b has pos[b] cached tokens (0 allowed) and num_nodes[b] nodes,
+ * 0 <= num_nodes[b] <= n_nodes <= 128 (num_nodes NULL: n_nodes each). Node i
+ * occupies cache row pos[b] + i, whatever its place in the tree, and its
+ * position is pos[b] + depth[b, i], 0 <= depth < n_nodes: several nodes may
+ * share a position, and a node's row becomes its position only when the path
+ * is kept. tree_mask [batch, n_nodes, ceil(n_nodes / 32)] uint32: bit t % 32
+ * of word t / 32 of row i says that node i attends to node t. It is taken as
+ * it is (a node attends to itself only if its bit is set; any other relation
+ * than a tree's works as well); bits of nodes past num_nodes[b] are ignored.
+ * Nodes past num_nodes[b] are padding: nothing of theirs is read, appended or
+ * written (q_rot, out and lse_out keep what they held there).
+ * All pointers are device pointers; tensors are dense, inputs bf16.
+ *
+ * kv_append_rope_tree: q_new [batch, n_nodes, h_q, head_dim], k_new / v_new
+ *   [batch, n_nodes, h_kv, head_dim]. As kv_append_rope_multi (the same
+ *   arithmetic and device errors), but node i is rotated by pos[b] + depth[b, i]
+ *   and stored at pos[b] + i, and q_rot [batch, n_nodes, h_q, head_dim] is
+ *   bf16, the operand of the attention. num_nodes[b] out of range sets
+ *   MQA_DEVERR_SEQ_LEN and the sequence is skipped; a depth out of range sets
+ *   MQA_DEVERR_TREE and is taken as the nearest inside.
+ * gqa_tree_attention: for node i and query head h of sequence b,
+ *   O = sum_t softmax_t(scale * q_rot . K_t) V_t over the cached tokens
+ *   t < pos[b] and the nodes of the mask row i; with a window W only those at
+ *   positions above pos[b] + depth[b, i] - W. A row that attends to nothing
+ *   gives O = 0, lse = -inf. scale > 0. out [batch, n_nodes, h_q, head_dim] in
+ *   out_dtype, lse_out optional [batch, n_nodes, h_q] fp32. max_seq_len bounds
+ *   every pos[b] + num_nodes[b]; a sequence past it (or with a negative pos)
+ *   sets MQA_DEVERR_SEQ_LEN and is skipped. depth is read with a window only
+ *   (else it may be NULL). Block-table entries as in the other calls: one in
+ *   use outside the pool sets MQA_DEVERR_PAGE_RANGE and reads as zeros.
+ *   workspace: mqa_tree_workspace_size bytes, 256-byte aligned, need not be
+ *   cleared; calls that may overlap on the GPU need one each.
+ * mqa_tree_step: the two calls on one stream (the second launch streams the
+ *   cached tokens while the first still runs), q_rot the caller's scratch.
+ *
+ * bf16, MQA_U8 and MQA_FP8_E5M2 caches, contiguous or paged, head_dim 64 or
+ * 128 (MQA_F32: MQA_ERR_UNSUPPORTED, as in the multi-token calls). Key rows
+ * past a sequence's nodes, and rows wholly before the window, are never used,
+ * whatever they hold; the values of a node that a row does not attend to are
+ * multiplied by a zero probability, so they have to be finite.
+ */
+MQA_API mqa_status kv_append_rope_tree(const mqa_kv_layout* layout, int32_t n_nodes, const void* q_new,
+                                       const void* k_new, const void* v_new, const int32_t* pos,
+                                       const int32_t* depth, const int32_t* num_nodes, double rope_base, void* q_rot,
+                                       int32_t* err_word, mqa_stream_t stream);
+MQA_API mqa_status gqa_tree_attention(const mqa_kv_layout* layout, int32_t n_nodes, const void* q_rot,
+                                      const int32_t* pos, const int32_t* depth, const int32_t* num_nodes,
+                                      const uint32_t* tree_mask, int32_t max_seq_len, float scale, void* out,
+                                      int32_t out_dtype, float* lse_out, void* workspace, size_t workspace_bytes,
+                                      int32_t* err_word, mqa_stream_t stream);
+MQA_API mqa_status mqa_tree_step(const mqa_kv_layout* layout, int32_t n_nodes, const void* q_new, const void* k_new,
+                                 const void* v_new, const int32_t* pos, const int32_t* depth,
+                                 const int32_t* num_nodes, const uint32_t* tree_mask, int32_t max_seq_len,
+                                 double rope_base, float scale, void* q_rot, void* out, int32_t out_dtype,
+                                 float* lse_out, void* workspace, size_t workspace_bytes, int32_t* err_word,
+                                 mqa_stream_t stream);
+/* Workspace bytes of the two calls above on the current device; 0 for invalid arguments. */
+MQA_API size_t mqa_tree_workspace_size(const mqa_kv_layout* layout, int32_t n_nodes);
+
+/*
+ * mqa_verify_tree -- which drafted tokens stand, and the token after them, so
+ * that what is emitted follows the target's distribution.
+ *
+ * target_probs [batch, n_nodes, row_stride]: row i the target's probabilities
+ * of the token after node i (vocab of them; row_stride >= vocab elements from
+ * row to row); draft_probs the draft's, the same shape and type, or NULL for
+ * drafts that were not drawn at random. probs_dtype MQA_F32 or MQA_BF16. tokens and
+ * parents [batch, n_nodes] int32: node 0 is the last committed token (its
+ * token and parent are not read), parents[i] < i for the others. u_accept
+ * [batch, n_nodes] and u_next [batch] fp32 in [0, 1).
+ *
+ * From node 0, the children of the current node are tried in index order.
+ * With R = p, S = 1 a child with token x is accepted iff u q(x) S < R(x); the
+ * walk goes on from it. A rejection leaves R <- max(R - S q, 0), S <- sum R;
+ * without draft_probs, where q(x) = 1: S <- S - R(x), then R(x) <- 0.
+ * When no child is left the next token is the smallest v with
+ * R(0) + .. + R(v) > u_next * sum R (p's own sum when nothing was rejected;
+ * if R is zero everywhere, the smallest v of the largest p). NaN
+ * probabilities weigh nothing.
+ *
+ * num_kept [batch]: nodes on the path, node 0 among them; path [batch,
+ * n_nodes]: their indices in order, then -1; next_token [batch]. num_nodes[b]
+ * = 0 gives 0, -1 .. and -1. A parent or token out of range sets
+ * MQA_DEVERR_TREE and that node is never tried; num_nodes[b] out of range sets
+ * MQA_DEVERR_SEQ_LEN and counts as 0.
+ * Sums have 64-bit accuracy and the result does not depend on the launch.
+ */
+MQA_API mqa_status mqa_verify_tree(int32_t batch, int32_t n_nodes, int32_t vocab, const void* target_probs,
+                                   const void* draft_probs, int32_t probs_dtype, int64_t row_stride,
+                                   const int32_t* tokens, const int32_t* parents, const int32_t* num_nodes,
+                                   const float* u_accept, const float* u_next, int32_t* num_kept, int32_t* path,
+                                   int32_t* next_token, int32_t* err_word, mqa_stream_t stream);
+
+/*
+ * kv_keep_path -- the accepted path's rows move up behind the cached tokens
+ * in n_layers caches at once: row pos[b] + path[b, i] to row pos[b] + i, for
+ * i < num_kept[b], in place, K and V (and the (scale, zero point) rows of a
+ * MQA_U8 cache) of every kv head; other rows keep what they hold.
+ *
+ * layouts: n_layers host structs that agree in everything but the pointers
+ * (any cache dtype; h_q and window are not used). path [batch, n_nodes]
+ * strictly increasing over its first num_kept[b] entries, which lie in [0,
+ * n_nodes); 0 <= num_kept[b] <= n_nodes. A sequence that breaks this sets
+ * MQA_DEVERR_TREE; a row past the cache sets MQA_DEVERR_POS_RANGE, a page
+ * outside the pool MQA_DEVERR_PAGE_RANGE: that sequence's rows then stay
+ * where they are (in the layer whose table is at fault). Pages that hold
+ * nodes must belong to one sequence.
+ */
+MQA_API mqa_status kv_keep_path(const mqa_kv_layout* layouts, int32_t n_layers, int32_t n_nodes, const int32_t* pos,
+                                const int32_t* path, const int32_t* num_kept, int32_t* err_word,
+                                mqa_stream_t stream);
 
 /* Split count gqa_decode_attention uses for num_splits = 0 on the current device
  * (>= 1), or -1 if the layout is invalid. */

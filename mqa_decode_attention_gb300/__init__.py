@@ -24,6 +24,7 @@ from ._abi import (
     MQA_DEVERR_POS_RANGE,
     MQA_DEVERR_SEQ_LEN,
     MQA_DEVERR_TIMEOUT,
+    MQA_DEVERR_TREE,
     MQA_DEVERR_U8_SCALE,
     MQA_F32,
     MQA_U8,
@@ -51,6 +52,16 @@ __all__ = [
     "gqa_decode_attention_multi",
     "gqa_prefill_attention",
     "prefill_step",
+    "TreeBuffers",
+    "VerifyBuffers",
+    "tree_mask",
+    "tree_workspace_size",
+    "kv_append_rope_tree",
+    "gqa_tree_attention",
+    "tree_step",
+    "verify_tree",
+    "layout_stack",
+    "keep_path",
     "library",
     "MQA_VARIANT_AUTO",
     "MQA_VARIANT_CUDA_CORE",
@@ -59,6 +70,7 @@ __all__ = [
     "MQA_DEVERR_PAGE_RANGE",
     "MQA_DEVERR_SEQ_LEN",
     "MQA_DEVERR_TIMEOUT",
+    "MQA_DEVERR_TREE",
     "MQA_DEVERR_U8_SCALE",
     "MQA_U8",
     "MQA_FP8_E5M2",
@@ -302,3 +314,206 @@ def prefill_step(layout: KVLayout, n_new: int, q_new, k_new, v_new, pos, seq_len
     if st != 0:
         raise MqaError("mqa_prefill_step", st)
     return bufs.out
+
+
+# ------------------------------------------------------ a tree of drafted tokens
+def tree_mask(parents) -> tuple[torch.Tensor, torch.Tensor]:
+    """Mask words and depths of trees given by their nodes' parents, on the
+    parents' device: parents [B, n] int32, parents[b, i] < i, -1 for a root.
+    Returns (mask [B, n, ceil(n / 32)] int32, each node's ancestors and itself
+    as bits; depth [B, n] int32). A loop on the host (one pass over the n
+    nodes): made once per tree, not per step."""
+    parents = torch.as_tensor(parents)
+    if parents.dim() != 2:
+        raise ValueError(f"parents must be [batch, nodes], got {tuple(parents.shape)}")
+    B, n = parents.shape
+    par = parents.cpu().tolist()
+    words = (n + 31) // 32
+    mask, depth = [], []
+    for row in par:
+        bits, deep = [], []
+        for i, a in enumerate(row):
+            if not -1 <= a < i:
+                raise ValueError(f"parent {a} of node {i}: a parent comes before its child")
+            bits.append((bits[a] if a >= 0 else 0) | 1 << i)
+            deep.append(deep[a] + 1 if a >= 0 else 0)
+        for x in bits:
+            for w in range(words):
+                v = x >> (32 * w) & 0xFFFFFFFF
+                mask.append(v - (1 << 32) if v >> 31 else v)
+        depth += deep
+    dev = parents.device
+    return (torch.tensor(mask, dtype=torch.int32, device=dev).view(B, n, words),
+            torch.tensor(depth, dtype=torch.int32, device=dev).view(B, n))
+
+
+def tree_workspace_size(layout: KVLayout, n_nodes: int) -> int:
+    return int(library().mqa_tree_workspace_size(ctypes.byref(layout), int(n_nodes)))
+
+
+@dataclass
+class TreeBuffers:
+    """Caller-owned device buffers of one tree step: q_rot [B, n, H_q, d] bf16
+    and the workspace are scratch, out [B, n, H_q, d], lse [B, n, H_q] or None
+    (not written)."""
+
+    q_rot: torch.Tensor
+    out: torch.Tensor
+    lse: torch.Tensor | None
+    workspace: torch.Tensor
+    err: torch.Tensor
+
+    @staticmethod
+    def allocate(layout: KVLayout, n_nodes: int, max_seq_len: int = 0, out_dtype: torch.dtype = torch.bfloat16,
+                 lse: bool = False, device="cuda") -> "TreeBuffers":
+        """max_seq_len is not needed: the workspace does not grow with it."""
+        ws = tree_workspace_size(layout, n_nodes)
+        if ws == 0:
+            raise MqaError("mqa_tree_workspace_size", _abi.MQA_ERR_INVALID_ARG)
+        rows = (layout.batch, int(n_nodes), layout.h_q)
+        return TreeBuffers(
+            q_rot=torch.empty(*rows, layout.head_dim, dtype=torch.bfloat16, device=device),
+            out=torch.empty(*rows, layout.head_dim, dtype=out_dtype, device=device),
+            lse=torch.empty(*rows, dtype=torch.float32, device=device) if lse else None,
+            workspace=torch.empty(ws, dtype=torch.uint8, device=device),
+            err=torch.zeros(1, dtype=torch.int32, device=device),
+        )
+
+
+def _want(name: str, t, dtype, numel: int) -> int | None:
+    """The address of a dense tensor of `numel` elements of `dtype` (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of {numel} elements is wanted, "
+                         f"got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def kv_append_rope_tree(layout: KVLayout, n_nodes: int, q_new, k_new, v_new, pos, depth, rope_base: float, q_rot,
+                        err, num_nodes=None, stream=None) -> None:
+    """Append a tree's nodes: node i at cache row pos[b] + i, rotated at
+    pos[b] + depth[b, i]; q_new [B, n, H_q, d], k_new / v_new [B, n, H_kv, d],
+    q_rot [B, n, H_q, d], all bf16."""
+    B, n, d = layout.batch, int(n_nodes), layout.head_dim
+    bf, i32 = torch.bfloat16, torch.int32
+    st = library().kv_append_rope_tree(
+        ctypes.byref(layout), n, _want("q_new", q_new, bf, B * n * layout.h_q * d),
+        _want("k_new", k_new, bf, B * n * layout.h_kv * d), _want("v_new", v_new, bf, B * n * layout.h_kv * d),
+        _want("pos", pos, i32, B), _want("depth", depth, i32, B * n), _want("num_nodes", num_nodes, i32, B),
+        float(rope_base), _want("q_rot", q_rot, bf, B * n * layout.h_q * d), _ptr(err), _stream(stream))
+    if st != 0:
+        raise MqaError("kv_append_rope_tree", st)
+
+
+def gqa_tree_attention(layout: KVLayout, n_nodes: int, q_rot, pos, depth, mask, max_seq_len: int, scale: float, out,
+                       num_nodes=None, lse_out=None, workspace=None, err=None, stream=None) -> None:
+    """Attention of a tree's nodes over the pos[b] cached tokens and the nodes
+    their mask rows name: q_rot [B, n, H_q, d] bf16, mask [B, n, ceil(n / 32)]
+    int32 words, out [B, n, H_q, d] bf16 or fp32."""
+    B, n, d = layout.batch, int(n_nodes), layout.head_dim
+    i32, rows = torch.int32, layout.batch * int(n_nodes) * layout.h_q
+    st = library().gqa_tree_attention(
+        ctypes.byref(layout), n, _want("q_rot", q_rot, torch.bfloat16, rows * d), _want("pos", pos, i32, B),
+        _want("depth", depth, i32, B * n), _want("num_nodes", num_nodes, i32, B),
+        _want("mask", mask, i32, B * n * ((n + 31) // 32)), int(max_seq_len), float(scale),
+        _want("out", out, out.dtype, rows * d), _dtype_code(out.dtype), _want("lse_out", lse_out, torch.float32, rows),
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(err),
+        _stream(stream))
+    if st != 0:
+        raise MqaError("gqa_tree_attention", st)
+
+
+def tree_step(layout: KVLayout, n_nodes: int, q_new, k_new, v_new, pos, depth, mask, max_seq_len: int,
+              bufs: TreeBuffers, rope_base: float = 10000.0, scale: float | None = None, num_nodes=None,
+              stream=None) -> torch.Tensor:
+    """A tree of drafted tokens through ``mqa_tree_step``: its nodes appended
+    behind the pos[b] cached tokens (``kv_append_rope_tree``), then their
+    attention (``gqa_tree_attention``). Returns ``bufs.out``; rows of nodes
+    past num_nodes[b] keep what they held."""
+    B, n, d = layout.batch, int(n_nodes), layout.head_dim
+    bf, i32, rows, new = torch.bfloat16, torch.int32, B * n * layout.h_q, B * n * layout.h_kv * d
+    ws, out = bufs.workspace, bufs.out
+    st = library().mqa_tree_step(
+        ctypes.byref(layout), n, _want("q_new", q_new, bf, rows * d), _want("k_new", k_new, bf, new),
+        _want("v_new", v_new, bf, new), _want("pos", pos, i32, B), _want("depth", depth, i32, B * n),
+        _want("num_nodes", num_nodes, i32, B), _want("mask", mask, i32, B * n * ((n + 31) // 32)), int(max_seq_len),
+        float(rope_base), 1.0 / math.sqrt(d) if scale is None else float(scale),
+        _want("q_rot", bufs.q_rot, bf, rows * d), _want("out", out, out.dtype, rows * d), _dtype_code(out.dtype),
+        _want("lse", bufs.lse, torch.float32, rows), _ptr(ws), ws.numel() * ws.element_size(), _ptr(bufs.err),
+        _stream(stream))
+    if st != 0:
+        raise MqaError("mqa_tree_step", st)
+    return out
+
+
+@dataclass
+class VerifyBuffers:
+    """Outputs of ``verify_tree``: num_kept [B], path [B, n] (node indices, then
+    -1), next_token [B], all int32, and the device error word."""
+
+    num_kept: torch.Tensor
+    path: torch.Tensor
+    next_token: torch.Tensor
+    err: torch.Tensor
+
+    @staticmethod
+    def allocate(batch: int, n_nodes: int, device="cuda") -> "VerifyBuffers":
+        return VerifyBuffers(
+            num_kept=torch.empty(batch, dtype=torch.int32, device=device),
+            path=torch.empty(batch, n_nodes, dtype=torch.int32, device=device),
+            next_token=torch.empty(batch, dtype=torch.int32, device=device),
+            err=torch.zeros(1, dtype=torch.int32, device=device),
+        )
+
+
+def verify_tree(target_probs, draft_probs, tokens, parents, u_accept, u_next, bufs: VerifyBuffers, num_nodes=None,
+                stream=None) -> VerifyBuffers:
+    """Which nodes of each drafted tree stand, and the next token, through
+    ``mqa_verify_tree``: target_probs and draft_probs (None: deterministic
+    drafts) [B, n, vocab] fp32 or bf16, row i the distribution after node i.
+    Rows may be padded (a slice [..., :vocab] of a dense tensor)."""
+    if target_probs.dim() != 3:
+        raise ValueError(f"target_probs must be [batch, nodes, vocab], got {tuple(target_probs.shape)}")
+    B, n, vocab = target_probs.shape
+    stride = target_probs.stride(1) if B * n > 1 and n > 1 else target_probs.stride(0) if B > 1 else vocab
+    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
+        if t is not None and (t.shape != target_probs.shape or t.dtype is not target_probs.dtype
+                              or (vocab > 1 and t.stride(2) != 1) or (n > 1 and t.stride(1) != stride)
+                              or (B > 1 and t.stride(0) != n * stride)):
+            raise ValueError(f"{name}: rows of one type, size and spacing are wanted, got {t.dtype} "
+                             f"{tuple(t.shape)} with strides {t.stride()}")
+    i32, f32 = torch.int32, torch.float32
+    st = library().mqa_verify_tree(
+        B, n, vocab, target_probs.data_ptr(), _ptr(draft_probs), _dtype_code(target_probs.dtype), stride,
+        _want("tokens", tokens, i32, B * n), _want("parents", parents, i32, B * n),
+        _want("num_nodes", num_nodes, i32, B), _want("u_accept", u_accept, f32, B * n),
+        _want("u_next", u_next, f32, B), _want("num_kept", bufs.num_kept, i32, B), _want("path", bufs.path, i32, B * n),
+        _want("next_token", bufs.next_token, i32, B), _ptr(bufs.err), _stream(stream))
+    if st != 0:
+        raise MqaError("mqa_verify_tree", st)
+    return bufs
+
+
+def layout_stack(layouts) -> ctypes.Array:
+    """The layouts of a model's layers as the one array ``keep_path`` takes."""
+    layouts = list(layouts)
+    if not layouts:
+        raise ValueError("layout_stack: no layouts")
+    stack = (KVLayout * len(layouts))(*layouts)
+    stack._layouts = layouts  # keeps the caches they point to alive
+    return stack
+
+
+def keep_path(layouts, pos, path, num_kept, err, stream=None) -> None:
+    """Move the rows of an accepted path up behind the cached tokens, in every
+    layer at once, through ``kv_keep_path``: layouts from ``layout_stack`` (or
+    one layout), path [B, n] and num_kept [B] as ``verify_tree`` gives them."""
+    count = 1 if isinstance(layouts, KVLayout) else len(layouts)
+    first = layouts if isinstance(layouts, KVLayout) else layouts[0]
+    B, n, i32 = first.batch, path.shape[-1], torch.int32
+    st = library().kv_keep_path(ctypes.byref(first), count, n, _want("pos", pos, i32, B),
+                                _want("path", path, i32, B * n), _want("num_kept", num_kept, i32, B), _ptr(err),
+                                _stream(stream))
+    if st != 0:
+        raise MqaError("kv_keep_path", st)

@@ -30,6 +30,7 @@ MQA_DEVERR_PAGE_RANGE = 0x2
 MQA_DEVERR_SEQ_LEN = 0x4
 MQA_DEVERR_TIMEOUT = 0x8
 MQA_DEVERR_U8_SCALE = 0x10
+MQA_DEVERR_TREE = 0x20
 
 c_i32 = ctypes.c_int32
 c_vp = ctypes.c_void_p
@@ -91,6 +92,26 @@ _PROTOTYPES = {
         [ctypes.POINTER(KVLayout), c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, ctypes.c_double, ctypes.c_float, c_vp,
          c_vp, c_i32, c_vp, c_vp, c_vp],
     ),
+    "kv_append_rope_tree": (
+        c_i32,
+        [ctypes.POINTER(KVLayout), c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, ctypes.c_double, c_vp, c_vp, c_vp]),
+    "gqa_tree_attention": (
+        c_i32,
+        [ctypes.POINTER(KVLayout), c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, ctypes.c_float, c_vp, c_i32, c_vp, c_vp,
+         ctypes.c_size_t, c_vp, c_vp],
+    ),
+    "mqa_tree_step": (
+        c_i32,
+        [ctypes.POINTER(KVLayout), c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, ctypes.c_double,
+         ctypes.c_float, c_vp, c_vp, c_i32, c_vp, c_vp, ctypes.c_size_t, c_vp, c_vp],
+    ),
+    "mqa_tree_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(KVLayout), c_i32]),
+    "mqa_verify_tree": (
+        c_i32,
+        [c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, ctypes.c_int64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+         c_vp],
+    ),
+    "kv_keep_path": (c_i32, [ctypes.POINTER(KVLayout), c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "mqa_choose_splits_multi": (c_i32, [ctypes.POINTER(KVLayout), c_i32, c_i32, c_i32]),
     "mqa_workspace_size_multi": (ctypes.c_size_t, [ctypes.POINTER(KVLayout), c_i32, c_i32, c_i32, c_i32]),
     "mqa_step_launches": (c_i32, [ctypes.POINTER(KVLayout), c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_i32)]),

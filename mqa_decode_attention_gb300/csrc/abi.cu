@@ -465,9 +465,17 @@ mqa_status check_append_args(const mqa_kv_layout* layout, const void* q_new, con
   return MQA_OK;
 }
 
+// A tree's append: the nodes' depths and counts, and the counters to clear.
+struct TreeAppend {
+  const int32_t* depth;
+  const int32_t* num_nodes;
+  int32_t* zero;
+  int zero_count;
+};
+
 mqa_status append_impl(const mqa_kv_layout* layout, const void* q_new, const void* k_new, const void* v_new,
                        const int32_t* pos, double rope_base, float* q_rot, int32_t* err_word, mqa_stream_t stream,
-                       int n_new = 1) {
+                       int n_new = 1, const TreeAppend* tree = nullptr) {
   const mqa_status st = check_append_args(layout, q_new, k_new, v_new, pos, rope_base, q_rot, err_word);
   if (st != MQA_OK) return st;
   if (n_new < 1 || static_cast<long long>(layout->batch) * n_new > (1ll << 31) - 1) return MQA_ERR_INVALID_ARG;
@@ -495,6 +503,12 @@ mqa_status append_impl(const mqa_kv_layout* layout, const void* q_new, const voi
   p.block_table = layout->block_table;
   p.q_rot = q_rot;
   p.err = err_word;
+  if (tree != nullptr) {
+    p.depth = tree->depth;
+    p.num_nodes = tree->num_nodes;
+    p.zero = tree->zero;
+    p.zero_count = tree->zero_count;
+  }
   fill_theta(p.theta, layout->head_dim, rope_base);
   const cudaError_t e = launch_append_rope(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e);
@@ -1095,6 +1109,263 @@ mqa_status mqa_decode_step_multi(const mqa_kv_layout* layout, int32_t n_new, con
                                  int32_t variant, int32_t* err_word, mqa_stream_t stream) {
   return step_impl(layout, n_new, q_new, k_new, v_new, pos, seq_lens, max_seq_len, rope_base, scale, num_splits,
                    q_rot, out, out_dtype, lse_out, workspace, workspace_bytes, variant, err_word, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- a tree of drafted tokens
+namespace {
+
+mqa_status check_tree_layout(const mqa_kv_layout* L, int n) {
+  const mqa_status st = check_layout(L);
+  if (st != MQA_OK) return st;
+  if (L->cache_dtype == MQA_F32) return MQA_ERR_UNSUPPORTED;  // tensor cores only, as the multi-token calls
+  if (n < 1 || n > kMaxTreeNodes) return MQA_ERR_INVALID_ARG;
+  if (static_cast<long long>(L->batch) * n * L->h_q > (1ll << 31) - 1) return MQA_ERR_INVALID_ARG;
+  return MQA_OK;
+}
+
+struct TreeChoice {
+  TreeShape shape;
+  int ctas;          // blocks launched
+  size_t counters;   // bytes of the counters at the start of the workspace
+  size_t workspace;
+};
+
+TreeChoice tree_choice(const mqa_kv_layout* L, int n) {
+  (void)n;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  TreeChoice c;
+  c.shape = tree_mma_shape(L->head_dim);
+  c.ctas = device_info(dev).sms * c.shape.ctas_per_sm;
+  c.counters = (static_cast<size_t>(c.ctas) * 4 + 255) / 256 * 256;
+  c.workspace = c.counters + static_cast<size_t>(2) * c.ctas * c.shape.rows * (L->head_dim + 2) * 4;
+  return c;
+}
+
+mqa_status check_tree_attention(const mqa_kv_layout* L, int n, const void* q_rot, const int32_t* pos,
+                                const int32_t* depth, const int32_t* num_nodes, const uint32_t* mask, int max_seq_len,
+                                float scale, const void* out, int out_dtype, const float* lse_out,
+                                const void* workspace, size_t workspace_bytes, const int32_t* err_word) {
+  const mqa_status st = check_tree_layout(L, n);
+  if (st != MQA_OK) return st;
+  if (!q_rot || !pos || !mask || !out || !err_word) return MQA_ERR_INVALID_ARG;
+  if (L->window > 0 && !depth) return MQA_ERR_INVALID_ARG;
+  if (!aligned(q_rot, 16) || !aligned(pos, 4) || !aligned(depth, 4) || !aligned(num_nodes, 4) || !aligned(mask, 4) ||
+      !aligned(out, 16) || !aligned(lse_out, 4) || !aligned(err_word, 4))
+    return MQA_ERR_INVALID_ARG;
+  if (max_seq_len < 1 || max_seq_len > token_limit(L)) return MQA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return MQA_ERR_INVALID_ARG;
+  if (out_dtype != MQA_BF16 && out_dtype != MQA_F32) return MQA_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < tree_choice(L, n).workspace) return MQA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return MQA_ERR_INVALID_ARG;
+  return MQA_OK;
+}
+
+// after the checks; early: the append launch, which clears the counters, directly precedes
+mqa_status tree_attention_impl(const mqa_kv_layout* L, int n, const void* q_rot, const int32_t* pos,
+                               const int32_t* depth, const int32_t* num_nodes, const uint32_t* mask, int max_seq_len,
+                               float scale, void* out, int out_dtype, float* lse_out, void* workspace,
+                               int32_t* err_word, cudaStream_t stream, int early) {
+  const TreeChoice c = tree_choice(L, n);
+  TreeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.batch = L->batch;
+  p.h_q = L->h_q;
+  p.h_kv = L->h_kv;
+  p.group = L->h_q / L->h_kv;
+  p.n = n;
+  p.words = (n + 31) / 32;
+  p.cache_dtype = dtype_code(L->cache_dtype);
+  p.head_dim = L->head_dim;
+  p.paged = L->paged;
+  p.k_cache = L->k_cache;
+  p.v_cache = L->v_cache;
+  p.k_sz = static_cast<const float2*>(L->k_scale_zero);
+  p.v_sz = static_cast<const float2*>(L->v_scale_zero);
+  p.capacity = token_limit(L);
+  p.page_size = L->page_size;
+  p.num_pages = L->num_pages;
+  p.max_pages = L->max_pages_per_seq;
+  p.block_table = L->block_table;
+  p.max_seq_len = max_seq_len;
+  p.q_rot = q_rot;
+  p.pos = pos;
+  p.depth = depth;
+  p.num_nodes = num_nodes;
+  p.mask = mask;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.window = L->window;
+  p.out = out;
+  p.out_dtype = out_dtype == MQA_BF16 ? kDtypeBf16 : kDtypeF32;
+  p.lse_out = lse_out;
+  p.arrived = static_cast<int32_t*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.counters);
+  p.err = err_word;
+  p.min_tiles = 2;
+  p.early = early;
+  p.wait_ns = wait_limit(L);
+  if (!early) {
+    const cudaError_t ez = cudaMemsetAsync(workspace, 0, static_cast<size_t>(c.ctas) * 4, stream);
+    if (ez != cudaSuccess) return fail_cuda(ez);
+  }
+  const cudaError_t e = launch_tree_mma(p, c.ctas, stream);
+  if (e != cudaSuccess) return fail_cuda(e);
+  const cudaError_t e2 = cudaGetLastError();
+  return e2 == cudaSuccess ? MQA_OK : fail_cuda(e2);
+}
+
+mqa_status check_tree_append(const mqa_kv_layout* L, int n, const void* q_new, const void* k_new, const void* v_new,
+                             const int32_t* pos, const int32_t* depth, const int32_t* num_nodes, double rope_base,
+                             const void* q_rot, const int32_t* err_word) {
+  const mqa_status st = check_tree_layout(L, n);
+  if (st != MQA_OK) return st;
+  if (!depth || !aligned(depth, 4) || !aligned(num_nodes, 4)) return MQA_ERR_INVALID_ARG;
+  return check_append_args(L, q_new, k_new, v_new, pos, rope_base, static_cast<const float*>(q_rot), err_word);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mqa_tree_workspace_size(const mqa_kv_layout* layout, int32_t n_nodes) {
+  return check_tree_layout(layout, n_nodes) == MQA_OK ? tree_choice(layout, n_nodes).workspace : 0;
+}
+
+mqa_status kv_append_rope_tree(const mqa_kv_layout* layout, int32_t n_nodes, const void* q_new, const void* k_new,
+                               const void* v_new, const int32_t* pos, const int32_t* depth, const int32_t* num_nodes,
+                               double rope_base, void* q_rot, int32_t* err_word, mqa_stream_t stream) {
+  const mqa_status st =
+      check_tree_append(layout, n_nodes, q_new, k_new, v_new, pos, depth, num_nodes, rope_base, q_rot, err_word);
+  if (st != MQA_OK) return st;
+  const TreeAppend tree{depth, num_nodes, nullptr, 0};
+  return append_impl(layout, q_new, k_new, v_new, pos, rope_base, static_cast<float*>(q_rot), err_word, stream,
+                     n_nodes, &tree);
+}
+
+mqa_status gqa_tree_attention(const mqa_kv_layout* layout, int32_t n_nodes, const void* q_rot, const int32_t* pos,
+                              const int32_t* depth, const int32_t* num_nodes, const uint32_t* tree_mask,
+                              int32_t max_seq_len, float scale, void* out, int32_t out_dtype, float* lse_out,
+                              void* workspace, size_t workspace_bytes, int32_t* err_word, mqa_stream_t stream) {
+  const mqa_status st = check_tree_attention(layout, n_nodes, q_rot, pos, depth, num_nodes, tree_mask, max_seq_len,
+                                             scale, out, out_dtype, lse_out, workspace, workspace_bytes, err_word);
+  if (st != MQA_OK) return st;
+  return tree_attention_impl(layout, n_nodes, q_rot, pos, depth, num_nodes, tree_mask, max_seq_len, scale, out,
+                             out_dtype, lse_out, workspace, err_word, reinterpret_cast<cudaStream_t>(stream),
+                             /*early=*/0);
+}
+
+mqa_status mqa_tree_step(const mqa_kv_layout* layout, int32_t n_nodes, const void* q_new, const void* k_new,
+                         const void* v_new, const int32_t* pos, const int32_t* depth, const int32_t* num_nodes,
+                         const uint32_t* tree_mask, int32_t max_seq_len, double rope_base, float scale, void* q_rot,
+                         void* out, int32_t out_dtype, float* lse_out, void* workspace, size_t workspace_bytes,
+                         int32_t* err_word, mqa_stream_t stream) {
+  // both calls' checks before the first launch
+  mqa_status st = check_tree_append(layout, n_nodes, q_new, k_new, v_new, pos, depth, num_nodes, rope_base, q_rot,
+                                    err_word);
+  if (st != MQA_OK) return st;
+  st = check_tree_attention(layout, n_nodes, q_rot, pos, depth, num_nodes, tree_mask, max_seq_len, scale, out,
+                            out_dtype, lse_out, workspace, workspace_bytes, err_word);
+  if (st != MQA_OK) return st;
+  const TreeAppend tree{depth, num_nodes, static_cast<int32_t*>(workspace), tree_choice(layout, n_nodes).ctas};
+  st = append_impl(layout, q_new, k_new, v_new, pos, rope_base, static_cast<float*>(q_rot), err_word, stream, n_nodes,
+                   &tree);
+  if (st != MQA_OK) return st;
+  return tree_attention_impl(layout, n_nodes, q_rot, pos, depth, num_nodes, tree_mask, max_seq_len, scale, out,
+                             out_dtype, lse_out, workspace, err_word, reinterpret_cast<cudaStream_t>(stream),
+                             /*early=*/1);
+}
+
+mqa_status mqa_verify_tree(int32_t batch, int32_t n_nodes, int32_t vocab, const void* target_probs,
+                           const void* draft_probs, int32_t probs_dtype, int64_t row_stride, const int32_t* tokens,
+                           const int32_t* parents, const int32_t* num_nodes, const float* u_accept,
+                           const float* u_next, int32_t* num_kept, int32_t* path, int32_t* next_token,
+                           int32_t* err_word, mqa_stream_t stream) {
+  if (batch < 1 || n_nodes < 1 || n_nodes > kMaxTreeNodes || vocab < 1) return MQA_ERR_INVALID_ARG;
+  if (static_cast<long long>(batch) * n_nodes > (1ll << 31) - 1 || batch > (1 << 27)) return MQA_ERR_INVALID_ARG;
+  if (vocab > (1 << 30) || row_stride < vocab || row_stride > (1ll << 31)) return MQA_ERR_INVALID_ARG;
+  if (!target_probs || !tokens || !parents || !u_accept || !u_next || !num_kept || !path || !next_token || !err_word)
+    return MQA_ERR_INVALID_ARG;
+  if (!aligned(target_probs, 16) || !aligned(draft_probs, 16) || !aligned(tokens, 4) || !aligned(parents, 4) ||
+      !aligned(num_nodes, 4) || !aligned(u_accept, 4) || !aligned(u_next, 4) || !aligned(num_kept, 4) ||
+      !aligned(path, 4) || !aligned(next_token, 4) || !aligned(err_word, 4))
+    return MQA_ERR_INVALID_ARG;
+  if (probs_dtype != MQA_F32 && probs_dtype != MQA_BF16) return MQA_ERR_UNSUPPORTED;
+  VerifyParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.batch = batch;
+  p.n = n_nodes;
+  p.vocab = vocab;
+  p.dtype = probs_dtype == MQA_BF16 ? kDtypeBf16 : kDtypeF32;
+  p.row_stride = row_stride;
+  p.target = target_probs;
+  p.draft = draft_probs;
+  p.tokens = tokens;
+  p.parents = parents;
+  p.num_nodes = num_nodes;
+  p.u_accept = u_accept;
+  p.u_next = u_next;
+  p.num_kept = num_kept;
+  p.path = path;
+  p.next_token = next_token;
+  p.err = err_word;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const cudaError_t e = launch_verify_tree(p, device_info(dev).sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail_cuda(e);
+  const cudaError_t e2 = cudaGetLastError();
+  return e2 == cudaSuccess ? MQA_OK : fail_cuda(e2);
+}
+
+mqa_status kv_keep_path(const mqa_kv_layout* layouts, int32_t n_layers, int32_t n_nodes, const int32_t* pos,
+                        const int32_t* path, const int32_t* num_kept, int32_t* err_word, mqa_stream_t stream) {
+  if (layouts == nullptr || n_layers < 1 || n_nodes < 1 || n_nodes > kMaxTreeNodes) return MQA_ERR_INVALID_ARG;
+  const mqa_kv_layout& f = layouts[0];
+  for (int i = 0; i < n_layers; ++i) {
+    const mqa_kv_layout& L = layouts[i];
+    const mqa_status st = check_layout(&L);
+    if (st != MQA_OK) return st;
+    if (L.cache_dtype != f.cache_dtype || L.batch != f.batch || L.h_kv != f.h_kv || L.head_dim != f.head_dim ||
+        L.paged != f.paged)
+      return MQA_ERR_INVALID_ARG;
+    if (L.paged ? L.page_size != f.page_size || L.num_pages != f.num_pages ||
+                      L.max_pages_per_seq != f.max_pages_per_seq
+                : L.capacity != f.capacity)
+      return MQA_ERR_INVALID_ARG;
+  }
+  if (!pos || !path || !num_kept || !err_word) return MQA_ERR_INVALID_ARG;
+  if (!aligned(pos, 4) || !aligned(path, 4) || !aligned(num_kept, 4) || !aligned(err_word, 4))
+    return MQA_ERR_INVALID_ARG;
+  if (f.h_kv > 65535) return MQA_ERR_UNSUPPORTED;  // grid limit
+  KeepParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.batch = f.batch;
+  p.h_kv = f.h_kv;
+  p.n = n_nodes;
+  p.paged = f.paged;
+  p.row_bytes = f.head_dim * (f.cache_dtype == MQA_F32 ? 4 : (f.cache_dtype == MQA_BF16 ? 2 : 1));
+  p.capacity = token_limit(&f);
+  p.page_size = f.page_size;
+  p.num_pages = f.num_pages;
+  p.max_pages = f.max_pages_per_seq;
+  p.pos = pos;
+  p.path = path;
+  p.num_kept = num_kept;
+  p.err = err_word;
+  for (int i0 = 0; i0 < n_layers; i0 += kMaxKeepLayers) {
+    const int m = std::min(kMaxKeepLayers, n_layers - i0);
+    for (int i = 0; i < m; ++i) {
+      const mqa_kv_layout& L = layouts[i0 + i];
+      const bool u8 = L.cache_dtype == MQA_U8;
+      p.layer[i] = {L.k_cache, L.v_cache, u8 ? static_cast<float2*>(L.k_scale_zero) : nullptr,
+                    u8 ? static_cast<float2*>(L.v_scale_zero) : nullptr, L.block_table};
+    }
+    const cudaError_t e = launch_keep_path(p, m, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail_cuda(e);
+  }
+  const cudaError_t e2 = cudaGetLastError();
+  return e2 == cudaSuccess ? MQA_OK : fail_cuda(e2);
 }
 
 }  // extern "C"

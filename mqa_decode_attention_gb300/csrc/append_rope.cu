@@ -7,6 +7,9 @@
 // rotated. Paged slot: "KV Cache 최적화 심층 분석" (youngju.dev), class
 // PagedKVCache (block pos / block_size, row pos % block_size).
 //
+// A tree of drafted tokens (p.depth): a token's slot and its rotation position
+// differ, and q_rot is the attention's bf16 operand.
+//
 // Blocks cover (sequence, chunk of heads): first the query-head blocks (up to
 // 8 heads each), then the kv-head blocks (2 heads each, so the fp64 key
 // rotation is spread over many SMs). Every thread issues its global loads
@@ -85,6 +88,31 @@ __device__ __noinline__ uint32_t e5m2_pair_fp64(float x, float y, double ang) {
   return e5m2_code(xr) | (e5m2_code(yr) << 8);
 }
 
+// A token of a drafted tree (p.depth set): its rotation position, pos + depth
+// (the slot stays pos + i), and whether it exists. A depth outside [0, n_new)
+// is reported and taken as the nearest inside. `report`: one thread per token.
+__device__ __forceinline__ bool tree_token(const AppendParams& p, int b, int i, bool report, int* at) {
+  const int nodes = p.num_nodes != nullptr ? p.num_nodes[b] : p.n_new;
+  if (nodes < 0 || nodes > p.n_new) {
+    if (report && i == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_SEQ_LEN));
+    return false;
+  }
+  if (i >= nodes) return false;
+  int depth = p.depth[static_cast<long long>(b) * p.n_new + i];
+  if (depth < 0 || depth >= p.n_new) {
+    if (report) atomicOr(p.err, static_cast<int>(MQA_DEVERR_TREE));
+    depth = min(max(depth, 0), p.n_new - 1);
+  }
+  *at = p.pos[b] + depth;
+  return true;
+}
+
+// the first block clears what the attention launch counts in
+__device__ __forceinline__ void tree_zero(const AppendParams& p, bool first) {
+  if (first && p.zero != nullptr)
+    for (int i = threadIdx.x; i < p.zero_count; i += blockDim.x) p.zero[i] = 0;
+}
+
 constexpr int kAppendThreads = 256;
 constexpr int kQHeadsPerBlock = 8;   // 8 heads x 64 pairs = 2 pairs per thread at d = 128
 constexpr int kKvHeadsPerBlock = 2;  // 2 heads x 64 pairs <= one pair per thread
@@ -151,6 +179,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const Appen
   const int n_qblocks = (p.h_q + kQHeadsPerBlock - 1) / kQHeadsPerBlock;
   const bool kv_block = static_cast<int>(blockIdx.y) >= n_qblocks;
   const int pos = p.pos[b] + (bt - b * p.n_new);
+  int at = pos;  // rotation position
+  if (p.depth != nullptr) {
+    tree_zero(p, blockIdx.x == 0 && blockIdx.y == 0);
+    if (!tree_token(p, b, bt - b * p.n_new, threadIdx.x == 0 && blockIdx.y == 0, &at)) return;
+  }
 
   // Issue this thread's loads first (at most 2 pairs per thread).
   int h_begin, h_end;
@@ -171,7 +204,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const Appen
 
   if (threadIdx.x < half) {
     if constexpr (kAngle) {
-      const double ang = reduce_two_pi(static_cast<double>(pos) * p.theta[threadIdx.x]);
+      const double ang = reduce_two_pi(static_cast<double>(at) * p.theta[threadIdx.x]);
       float sf, cf;
       sincosf(static_cast<float>(ang), &sf, &cf);
       s_cos[threadIdx.x] = ang;
@@ -179,7 +212,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const Appen
       s_sf[threadIdx.x] = sf;
     } else {
       double cs, sn;
-      rope_cos_sin(pos, p.theta[threadIdx.x], &cs, &sn);
+      rope_cos_sin(at, p.theta[threadIdx.x], &cs, &sn);
       s_cos[threadIdx.x] = cs;
       s_sin[threadIdx.x] = sn;
     }
@@ -229,7 +262,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const Appen
       const int h = h_begin + idx / half, i = idx % half;
       const float c = kAngle ? s_cf[i] : static_cast<float>(s_cos[i]);
       const float s = kAngle ? s_sf[i] : static_cast<float>(s_sin[i]);
-      *reinterpret_cast<float2*>(qr + h * D + 2 * i) = make_float2(x.x * c - x.y * s, x.x * s + x.y * c);
+      const float2 y = make_float2(x.x * c - x.y * s, x.x * s + x.y * c);
+      if (p.depth != nullptr)  // bf16 q_rot
+        reinterpret_cast<uint32_t*>(p.q_rot)[(static_cast<long long>(bt) * p.h_q + h) * half + i] = pack_bf16x2(y.x, y.y);
+      else
+        *reinterpret_cast<float2*>(qr + h * D + 2 * i) = y;
     }
     return;
   }
@@ -352,6 +389,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_tokens_kernel(cons
   const int b = bt / p.n_new;
   const int D = p.head_dim, half = D >> 1;
   const int pos = p.pos[b] + (bt - b * p.n_new);
+  int at = pos;  // rotation position
+  if (p.depth != nullptr) {
+    tree_zero(p, blockIdx.x == 0);
+    if (!tree_token(p, b, bt - b * p.n_new, threadIdx.x == 0, &at)) return;
+  }
   // bf16 q rows: 16-byte units of four rotation pairs; a thread's first two
   // units are requested before the table is formed, so that their latency
   // and the table's overlap
@@ -363,7 +405,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_tokens_kernel(cons
   if (kVec && static_cast<int>(threadIdx.x) + kAppendThreads < n_units) qpre1 = qsrc[threadIdx.x + kAppendThreads];
   if (threadIdx.x < half) {
     if constexpr (kAngle) {
-      const double ang = reduce_two_pi(static_cast<double>(pos) * p.theta[threadIdx.x]);
+      const double ang = reduce_two_pi(static_cast<double>(at) * p.theta[threadIdx.x]);
       float sf, cf;
       sincosf(static_cast<float>(ang), &sf, &cf);
       s_cos[threadIdx.x] = ang;
@@ -371,7 +413,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_tokens_kernel(cons
       s_sf[threadIdx.x] = sf;
     } else {
       double cs, sn;
-      rope_cos_sin(pos, p.theta[threadIdx.x], &cs, &sn);
+      rope_cos_sin(at, p.theta[threadIdx.x], &cs, &sn);
       s_cos[threadIdx.x] = cs;
       s_sin[threadIdx.x] = sn;
     }
@@ -423,6 +465,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_rope_tokens_kernel(cons
         const float s = kAngle ? s_sf[i0 + k] : static_cast<float>(s_sin[i0 + k]);
         o[2 * k] = x * c - y * s;
         o[2 * k + 1] = x * s + y * c;
+      }
+      if (p.depth != nullptr) {  // bf16 q_rot
+        reinterpret_cast<uint4*>(p.q_rot)[static_cast<long long>(bt) * n_units + w] =
+            make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+        return;
       }
       *reinterpret_cast<float4*>(qr + e0) = make_float4(o[0], o[1], o[2], o[3]);
       *reinterpret_cast<float4*>(qr + e0 + 4) = make_float4(o[4], o[5], o[6], o[7]);

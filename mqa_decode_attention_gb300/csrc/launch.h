@@ -22,6 +22,7 @@ constexpr int kTile = 64;          // tokens per pipeline stage of the decode ke
 constexpr int kMaxNewTokens = 32;      // new tokens per sequence the multi-token attention takes
 constexpr int kMaxFusedNewTokens = 8;  // new tokens per sequence a fused warp-MMA multi-token step takes
 constexpr int kMaxFusedNewTokensTc05 = 16;  // ... a fused tcgen05 multi-token step takes
+constexpr int kMaxTreeNodes = 128;  // drafted tokens per sequence the tree calls take
 constexpr int kMaxHalfDim = 64;    // RoPE frequencies held in the append kernel's parameters
 constexpr int kDtypeBf16 = 0;
 constexpr int kDtypeF32 = 1;
@@ -44,6 +45,14 @@ struct AppendParams {
   int32_t* err;
   float2* k_sz;  // uint8 cache: (scale, zero point) per row
   float2* v_sz;
+  // tree of drafted tokens (depth != nullptr): token i is stored at pos[b] + i
+  // but rotated at pos[b] + depth[b, i]; only tokens i < num_nodes[b] (all
+  // when null) exist. q_rot is then bf16, and `zero` (when not null) is
+  // cleared for the attention launch that follows.
+  const int32_t* depth;      // [B, n_new]
+  const int32_t* num_nodes;  // [B] or null
+  int32_t* zero;
+  int zero_count;
   double theta[kMaxHalfDim];  // RoPE inverse frequencies base^(-2i/d)
 };
 
@@ -220,5 +229,86 @@ bool tc05_merges_splits(const Tc05Params& p);
 // rows of the TMA box (keys per load) the tcgen05 kernel expects for an fp8
 // e5m2 cache
 int tc05_f8_box_rows();
+
+// Attention of a tree of drafted tokens (attn_tree.cu, attn_tree_tc05.cu).
+// Node i of sequence b is the token at cache row pos[b] + i; it attends to
+// the pos[b] cached tokens and to the nodes of its mask row.
+struct TreeParams {
+  int batch, h_q, h_kv, group, n, words;  // n nodes per sequence, words = ceil(n / 32) mask words per node
+  int cache_dtype, head_dim, paged;
+  const void* k_cache;
+  const void* v_cache;
+  const float2* k_sz;  // uint8 cache: (scale, zero point) per row
+  const float2* v_sz;
+  long long capacity;  // tokens a sequence can hold (paged: max_pages * page_size)
+  int page_size, num_pages, max_pages;
+  const int32_t* block_table;
+  int max_seq_len;
+  const void* q_rot;         // [B, n, H_q, d] bf16
+  const int32_t* pos;        // [B] cached tokens
+  const int32_t* depth;      // [B, n], read with a window only
+  const int32_t* num_nodes;  // [B] or null: n each
+  const uint32_t* mask;      // [B, n, words]: bit t of a row, node t is attended
+  float scale_log2;          // score scale times log2(e), > 0
+  int window;
+  void* out;  // [B, n, H_q, d]
+  int out_dtype;
+  float* lse_out;    // [B, n, H_q] or null
+  int32_t* arrived;  // [blocks] zero: blocks that have left a partial of the unit that starts in block c
+  float* part;       // [2 blocks] partial results
+  int32_t* err;
+  int min_tiles;  // a block's run is at least this long
+  int early;      // 1: the preceding launch is the append kernel: the cached tokens may be read before it ends
+  unsigned long long wait_ns;
+};
+struct TreeShape {
+  int rows, keys;   // rows of a block, keys of a tile
+  int ctas_per_sm;  // blocks launched per SM
+};
+// any cache the tensor cores read, head_dim 64 or 128
+TreeShape tree_mma_shape(int head_dim);
+cudaError_t launch_tree_mma(const TreeParams& p, int ctas, cudaStream_t stream);
+
+// Verification of drafted trees (verify_tree.cu).
+struct VerifyParams {
+  int batch, n, vocab, dtype;
+  long long row_stride;  // elements from one row of probabilities to the next
+  const void* target;    // [B, n, row_stride]
+  const void* draft;     // the same, or null: deterministic drafts
+  const int32_t* tokens;     // [B, n]
+  const int32_t* parents;    // [B, n]
+  const int32_t* num_nodes;  // [B] or null
+  const float* u_accept;     // [B, n]
+  const float* u_next;       // [B]
+  int32_t* num_kept;         // [B]
+  int32_t* path;             // [B, n]
+  int32_t* next_token;       // [B]
+  int32_t* err;
+};
+cudaError_t launch_verify_tree(const VerifyParams& p, int sms, cudaStream_t stream);
+
+// Moving an accepted path's cache rows (keep_path.cu): up to kMaxKeepLayers
+// layers a launch (the kernel's parameter space).
+constexpr int kMaxKeepLayers = 64;
+struct KeepLayer {
+  void* k;
+  void* v;
+  float2* k_sz;  // uint8 cache only, else null
+  float2* v_sz;
+  const int32_t* block_table;
+};
+struct KeepParams {
+  int batch, h_kv, n, paged;
+  int row_bytes;  // bytes of one (token, kv head) row
+  long long capacity;
+  int page_size, num_pages, max_pages;
+  int heads_per_block;
+  const int32_t* pos;       // [B]
+  const int32_t* path;      // [B, n]
+  const int32_t* num_kept;  // [B]
+  int32_t* err;
+  KeepLayer layer[kMaxKeepLayers];
+};
+cudaError_t launch_keep_path(KeepParams p, int layers, cudaStream_t stream);
 
 }  // namespace mqa

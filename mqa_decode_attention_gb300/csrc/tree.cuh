@@ -1,0 +1,314 @@
+// What the tree-attention kernels share: the division of the work among the
+// blocks, the mask bits of a run of keys, and the merge of partial results.
+//
+// A unit is (sequence b, kv head j, row block rb): up to `rows` of kv head j's
+// (node i, query head h = j G + hl) pairs, row = i G + hl, over every key
+// tile of the sequence. The units' tiles in order (b, j, rb, tile) form one
+// long line, which is cut into equal runs, one for each block: every block
+// streams the same number of key tiles whatever the lengths, the tree sizes
+// and the batch are. A block's run of one unit is a segment. A segment that
+// holds a whole unit writes its output; otherwise it leaves an unnormalised
+// partial result, and the block that arrives last at the unit's counter merges
+// its partials in block order (the same sums whichever block that is).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "../../include/mqa_decode.h"
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace mqa {
+
+// One sequence as the kernels see it. An invalid one (a negative position,
+// more nodes than the call's, a length past the bound) has no work: nothing of
+// it is read or written.
+struct TreeSeq {
+  int pos, nodes, len;  // cached tokens, nodes, both
+  int lo;               // first key that any node can attend to
+  int first;            // lo rounded down to a multiple of 64: key 0 of tile 0
+  int tiles, blocks;    // key tiles; row blocks
+  bool bad;
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b, int tile, int rows) {
+  TreeSeq s;
+  s.pos = p.pos[b];
+  s.nodes = p.num_nodes != nullptr ? p.num_nodes[b] : p.n;
+  const long long limit = p.capacity < p.max_seq_len ? p.capacity : p.max_seq_len;
+  s.bad = s.pos < 0 || s.nodes < 0 || s.nodes > p.n || static_cast<long long>(s.pos) + s.nodes > limit;
+  if (s.bad) s.pos = s.nodes = 0;
+  s.len = s.pos + s.nodes;
+  // (a node's position is at least pos: the smallest depth is 0)
+  s.lo = p.window > 0 ? max(0, s.pos + 1 - p.window) : 0;
+  s.first = s.lo / 64 * 64;
+  s.tiles = s.nodes > 0 ? (s.len - s.first + tile - 1) / tile : 0;
+  s.blocks = (s.nodes * p.group + rows - 1) / rows;
+  return s;
+}
+
+__device__ __forceinline__ long long tree_work(const TreeParams& p, const TreeSeq& s) {
+  return static_cast<long long>(s.tiles) * s.blocks * p.h_kv;
+}
+
+// Block `cta`'s run of the line. The number of blocks that take part shrinks
+// until each has p.min_tiles tiles: merging more partials would cost more
+// than the shorter runs save.
+struct TreePlan {
+  long long total, begin, end;
+  long long before;  // tiles of the sequences before b
+  int b, ctas;       // the sequence holding `begin`
+};
+
+// By one whole warp; `out` in shared memory. Lane l sums the tiles of its
+// share of the sequences (consecutive ones), a scan over the lanes finds the
+// lane whose share holds `begin`, and that lane walks its share again.
+__device__ __forceinline__ void tree_plan(const TreeParams& p, int tile, int rows, int cta, int grid, TreePlan* out) {
+  const int lane = threadIdx.x & 31;
+  const int per = (p.batch + 31) / 32, b0 = min(lane * per, p.batch), b1 = min(b0 + per, p.batch);
+  long long sum = 0;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const TreeSeq s = tree_seq(p, b, tile, rows);
+    sum += tree_work(p, s);
+    bad |= s.bad;
+  }
+  if (bad && cta == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_SEQ_LEN));
+  long long incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  const long long total = __shfl_sync(0xffffffffu, incl, 31);
+  const long long most = (total + p.min_tiles - 1) / p.min_tiles;
+  const int ctas = static_cast<int>(most < 1 ? 1 : (most < grid ? most : grid));
+  const long long begin = cta < ctas ? total * cta / ctas : total, end = cta < ctas ? total * (cta + 1) / ctas : total;
+  const long long excl = incl - sum;
+  if (lane == 0) {
+    out->total = total;
+    out->begin = begin;
+    out->end = end;
+    out->ctas = ctas;
+  }
+  if (begin < end && begin >= excl && begin < incl) {  // one lane: the shares are disjoint
+    long long before = excl;
+    int b = b0;
+    while (b < b1 - 1) {
+      const long long w = tree_work(p, tree_seq(p, b, tile, rows));
+      if (begin < before + w) break;
+      before += w;
+      ++b;
+    }
+    out->before = before;
+    out->b = b;
+  }
+  __syncwarp();
+}
+
+struct TreeSegment {
+  int b, j, rb;     // the unit
+  int t0, nt;       // first tile, tiles
+  bool head, tail;  // holds the unit's first / last tile
+  long long u0;     // the unit's first tile on the line
+  TreeSeq s;
+};
+
+// A block's segments one after the other; every warp walks them by itself.
+struct TreeWalk {
+  long long at, end, before;
+  int b;
+  TreeSeq s;
+  __device__ __forceinline__ void start(const TreeParams& p, const TreePlan& pl, int tile, int rows) {
+    at = pl.begin;
+    end = pl.end;
+    before = pl.before;
+    b = pl.b;
+    if (at < end) s = tree_seq(p, b, tile, rows);
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p, int tile, int rows, TreeSegment& g) {
+    if (at >= end) return false;
+    while (true) {
+      const long long w = tree_work(p, s);
+      if (at < before + w) break;
+      if (++b >= p.batch) return false;  // (never: at < end <= total)
+      before += w;
+      s = tree_seq(p, b, tile, rows);
+    }
+    const long long off = at - before;
+    const int unit = static_cast<int>(off / s.tiles);
+    g.b = b;
+    g.t0 = static_cast<int>(off - static_cast<long long>(unit) * s.tiles);
+    g.j = unit / s.blocks;
+    g.rb = unit - g.j * s.blocks;
+    g.nt = static_cast<int>(min(static_cast<long long>(s.tiles - g.t0), end - at));
+    g.head = g.t0 == 0;
+    g.tail = g.t0 + g.nt == s.tiles;
+    g.u0 = at - g.t0;
+    g.s = s;
+    at += g.nt;
+    return true;
+  }
+};
+
+// The block whose run holds tile x of the line: the largest c with
+// floor(total c / ctas) <= x.
+__device__ __forceinline__ int tree_cta_of(const TreePlan& pl, long long x) {
+  return static_cast<int>(((x + 1) * pl.ctas - 1) / pl.total);
+}
+
+// A partial result: [rows][d] fp32 sums, then each row's maximum (log2
+// domain) and sum. A block leaves at most two: of the unit it starts in the
+// middle of (slot 2 c) and of the unit it ends in the middle of (slot 2 c + 1;
+// a run inside one unit without its first tile is of the first kind).
+__host__ __device__ __forceinline__ size_t tree_part_floats(int rows, int d) {
+  return static_cast<size_t>(rows) * (d + 2);
+}
+
+// 32 bits, bit c = the row may attend to key k0 + c. m: the row's mask words
+// with the bits of dead nodes cleared (all zero for a dead row), ka its first
+// key, pos the number of cached tokens.
+struct TreeRow {
+  uint32_t m[4];
+  int ka, pos;
+};
+
+__device__ __forceinline__ uint32_t tree_bits(const TreeRow& r, int k0) {
+  // cached tokens: keys [ka, pos)
+  const int a = min(max(r.ka - k0, 0), 32), e = min(max(r.pos - k0, 0), 32);
+  uint32_t v = 0;
+  if (e > a) v = (e == 32 ? 0xffffffffu : (1u << e) - 1u) & (0xffffffffu << a);
+  // nodes: bit t of the mask is key pos + t
+  const int s = k0 - r.pos;  // node of bit 0
+  if (s > -32 && s < 128) {
+    const int w = s >> 5, o = s & 31;  // (arithmetic shift: w = -1 for s < 0)
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i == w) lo = r.m[i];
+      if (i == w + 1) hi = r.m[i];
+    }
+    v |= __funnelshift_r(lo, hi, o);
+  }
+  return v;
+}
+
+// Row r (node i, -1: none) of a unit of sequence b.
+__device__ __forceinline__ TreeRow tree_row(const TreeParams& p, int b, const TreeSeq& s, int i) {
+  TreeRow r;
+  r.pos = s.pos;
+  r.ka = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) r.m[w] = 0;
+  if (i < 0) {
+    r.pos = r.ka = 0;
+    return r;
+  }
+  const uint32_t* m = p.mask + (static_cast<long long>(b) * p.n + i) * p.words;
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    if (w < p.words) {
+      r.m[w] = m[w];
+      const int left = s.nodes - 32 * w;  // nodes past the sequence's own
+      if (left < 32) r.m[w] &= left > 0 ? (1u << left) - 1u : 0u;
+    }
+  if (p.window > 0) {
+    const int32_t* depth = p.depth + static_cast<long long>(b) * p.n;
+    const long long at = static_cast<long long>(s.pos) + max(depth[i], 0);
+    const long long ka = at + 1 - p.window;
+    r.ka = ka > 0 ? static_cast<int>(min(ka, static_cast<long long>(s.pos))) : 0;
+    for (int t = 0; t < s.nodes; ++t) {
+      const bool far = static_cast<long long>(s.pos) + max(depth[t], 0) < ka;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (far && (t >> 5) == w) r.m[w] &= ~(1u << (t & 31));
+    }
+  }
+  return r;
+}
+
+// Four consecutive output values of one row.
+__device__ __forceinline__ void tree_store4(const TreeParams& p, long long o, float a, float b, float c, float d) {
+  if (p.out_dtype == kDtypeBf16) {
+    uint2 w;
+    w.x = pack_bf16x2(a, b);
+    w.y = pack_bf16x2(c, d);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + o) = w;
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = make_float4(a, b, c, d);
+  }
+}
+
+__device__ __forceinline__ long long tree_out_row(const TreeParams& p, const TreeSegment& g, int row) {
+  const int i = row / p.group;
+  return (static_cast<long long>(g.b) * p.n + i) * p.h_q + g.j * p.group + (row - i * p.group);
+}
+
+// After a block has written its partial of segment g (every thread): counts it
+// in and, when it was the unit's last, merges. `threads` threads call it, all
+// of them, `sync` is a barrier over them, `flag` a shared int of theirs, tid
+// their index. A warp takes a row at a time, a lane D / 32 of its values.
+template <int D, class Sync>
+__device__ __forceinline__ void tree_arrive_merge(const TreeParams& p, const TreePlan& pl, const TreeSegment& g,
+                                                  int rows_per_block, int tid, int threads, volatile int* flag,
+                                                  const Sync& sync) {
+  const int ca = tree_cta_of(pl, g.u0), cb = tree_cta_of(pl, g.u0 + g.s.tiles - 1), m = cb - ca + 1;
+  __threadfence();  // this thread's part of the partial, before the count
+  sync();
+  if (tid == 0) *flag = atomicAdd(p.arrived + ca, 1) == m - 1;
+  sync();
+  if (*flag == 0) return;
+  __threadfence();  // the other blocks' partials, after the count
+  const size_t size = tree_part_floats(rows_per_block, D);
+  const int rows = min(rows_per_block, g.s.nodes * p.group - g.rb * rows_per_block);
+  const int warp = tid >> 5, lane = tid & 31;
+  constexpr int kV = D / 32;
+  auto part = [&](int k) { return p.part + size * (k == 0 ? 2 * ca + 1 : 2 * (ca + k)); };
+  for (int r = warp; r < rows; r += threads / 32) {
+    float mx = -INFINITY;
+    for (int k = lane; k < m; k += 32) mx = fmaxf(mx, __ldcg(part(k) + static_cast<size_t>(rows_per_block) * D + r));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    float acc[kV], l = 0.f;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) acc[v] = 0.f;
+    if (mx != -INFINITY) {
+#pragma unroll 2
+      for (int k = 0; k < m; ++k) {
+        const float* q = part(k);
+        const float mk = __ldcg(q + static_cast<size_t>(rows_per_block) * D + r);
+        const float lk = __ldcg(q + static_cast<size_t>(rows_per_block) * (D + 1) + r);
+        float ov[kV];
+        if constexpr (kV == 4) {
+          const float4 t = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(r) * D) + lane);
+          ov[0] = t.x, ov[1] = t.y, ov[2] = t.z, ov[3] = t.w;
+        } else {
+          const float2 t = __ldcg(reinterpret_cast<const float2*>(q + static_cast<size_t>(r) * D) + lane);
+          ov[0] = t.x, ov[1] = t.y;
+        }
+        if (mk != -INFINITY) {  // (else no key of this part: its sums may be anything)
+          const float w = exp2f(mk - mx);
+          l = fmaf(w, lk, l);
+#pragma unroll
+          for (int v = 0; v < kV; ++v) acc[v] = fmaf(w, ov[v], acc[v]);
+        }
+      }
+    }
+    const float inv = mx != -INFINITY ? 1.f / l : 0.f;
+    const long long o = tree_out_row(p, g, g.rb * rows_per_block + r);
+    if constexpr (kV == 4) {
+      tree_store4(p, o * D + 4 * lane, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    } else if (p.out_dtype == kDtypeBf16) {
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + o * D + 2 * lane) =
+          pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    } else {
+      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o * D + 2 * lane) =
+          make_float2(acc[0] * inv, acc[1] * inv);
+    }
+    if (lane == 0 && p.lse_out != nullptr)
+      p.lse_out[o] = mx != -INFINITY ? (mx + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+  }
+}
+
+}  // namespace mqa

@@ -41,6 +41,15 @@ from .decode import (
     run_uncached_sequence,
     window_start,
 )
+from .tree import (
+    keep_path,
+    logical,
+    mask_matrix,
+    tree_append,
+    tree_attention,
+    tree_rotate,
+    verify_tree,
+)
 from .accounting import (
     expected_tokens_per_verify,
     kv_bytes_per_token,

@@ -1127,21 +1127,55 @@ mqa_status check_tree_layout(const mqa_kv_layout* L, int n) {
 
 struct TreeChoice {
   TreeShape shape;
+  int tc05;          // row tiles of a block of the tcgen05 kernel, 0: the warp-MMA kernel
+  int tokens;        // ... nodes of a row tile
   int ctas;          // blocks launched
   size_t counters;   // bytes of the counters at the start of the workspace
   size_t workspace;
 };
 
 TreeChoice tree_choice(const mqa_kv_layout* L, int n) {
-  (void)n;
   int dev = 0;
   cudaGetDevice(&dev);
   TreeChoice c;
+  const int G = L->h_q / L->h_kv;
   c.shape = tree_mma_shape(L->head_dim);
+  c.tc05 = c.tokens = 0;
+  if (L->head_dim == 128 && G <= 128) {
+    c.tc05 = static_cast<long long>(G) * n > 128 ? 2 : 1;
+    c.tokens = std::min(128 / G, n);
+    c.shape = {c.tc05 * c.tokens * G, kTreeTileKeys, 1};
+  }
   c.ctas = device_info(dev).sms * c.shape.ctas_per_sm;
   c.counters = (static_cast<size_t>(c.ctas) * 4 + 255) / 256 * 256;
-  c.workspace = c.counters + static_cast<size_t>(2) * c.ctas * c.shape.rows * (L->head_dim + 2) * 4;
+  c.workspace = c.counters + static_cast<size_t>(2) * c.ctas * tree_part_floats(c.shape.rows, L->head_dim) * 4;
   return c;
+}
+
+// The tcgen05 tree kernel's maps: K and V tiles, and q_rot [batch n tokens]
+// [h_q][128] bf16 in boxes of 64 dims x the group x `tokens`.
+bool make_tree_maps(const mqa_kv_layout* L, const void* q_rot, int n, int tokens, CUtensorMap* tk, CUtensorMap* tv,
+                    CUtensorMap* tq) {
+  if (L->cache_dtype == MQA_BF16) {
+    if (!(L->paged ? make_tc05_paged_map(tk, L->k_cache, L) && make_tc05_paged_map(tv, L->v_cache, L)
+                   : make_tensor_map(tk, L->k_cache, L, true, 1, kTreeTileKeys) &&
+                         make_tensor_map(tv, L->v_cache, L, true, 1, kTreeTileKeys)))
+      return false;
+  } else {
+    CUtensorMap maps[4];
+    if (!make_u8_maps(maps, L, L->paged ? std::min(L->page_size, 64) : kTreeTileKeys, 1)) return false;
+    *tk = maps[0];
+    *tv = maps[1];
+  }
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(L->h_q), static_cast<cuuint64_t>(L->batch) * n};
+  const cuuint64_t strides[2] = {128 * 2, static_cast<cuuint64_t>(L->h_q) * 128 * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(L->h_q / L->h_kv), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q_rot), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 mqa_status check_tree_attention(const mqa_kv_layout* L, int n, const void* q_rot, const int32_t* pos,
@@ -1203,14 +1237,27 @@ mqa_status tree_attention_impl(const mqa_kv_layout* L, int n, const void* q_rot,
   p.arrived = static_cast<int32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.counters);
   p.err = err_word;
-  p.min_tiles = 2;
+  p.min_tiles = c.tc05 ? 1 : 2;
+  p.tokens_per_tile = c.tokens;
   p.early = early;
   p.wait_ns = wait_limit(L);
   if (!early) {
     const cudaError_t ez = cudaMemsetAsync(workspace, 0, static_cast<size_t>(c.ctas) * 4, stream);
     if (ez != cudaSuccess) return fail_cuda(ez);
   }
-  const cudaError_t e = launch_tree_mma(p, c.ctas, stream);
+  cudaError_t e;
+  if (c.tc05) {
+    CUtensorMap tk, tv, tq;
+    if (!make_tree_maps(L, q_rot, n, c.tokens, &tk, &tv, &tq)) {
+      snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled failed or is unavailable");
+      return MQA_ERR_CUDA;
+    }
+    const auto launch = L->cache_dtype == MQA_BF16 ? launch_tree_tc05_bf16
+                                                   : (L->cache_dtype == MQA_U8 ? launch_tree_tc05_u8 : launch_tree_tc05_f8);
+    e = launch(p, c.tc05, c.ctas, tk, tv, tq, stream);
+  } else {
+    e = launch_tree_mma(p, c.ctas, stream);
+  }
   if (e != cudaSuccess) return fail_cuda(e);
   const cudaError_t e2 = cudaGetLastError();
   return e2 == cudaSuccess ? MQA_OK : fail_cuda(e2);

@@ -1,0 +1,847 @@
+// Attention of a tree of drafted tokens over the cache on the 5th-generation
+// tensor cores: head_dim 128, groups of up to 128 heads, every cache the
+// tensor cores read (bf16, uint8, fp8 e5m2; contiguous or paged).
+//
+// One persistent block per SM streams an equal run of the key tiles (tree.cuh)
+// and never lets its ring of K / V tiles run dry between two units: the
+// loader warp goes straight on to the next unit's tiles while the softmax
+// warps finish the last one's rows. For each 128-key tile
+//   S = Q K^T      tcgen05.mma M=128 N=128 K=128, both operands bf16 in shared
+//                  memory, S (f32) into tensor memory
+//   softmax        one row per thread: running maximum and sum
+//                  (FlashAttention, "Arsitektur Inferensi LLM", section 5), O
+//                  rescaled only when a row's maximum grows by more than 2^8;
+//                  P (bf16) written over its S columns
+//   O += P V       tcgen05.mma with A = P from tensor memory
+// Rows are (node i, query head) pairs of one kv head, whole nodes to a block.
+// There are two accumulators (S and O of each in tensor memory, 512 columns)
+// with a softmax warpgroup each:
+//   NT = 2  (more than 128 rows per kv head) two query tiles of up to 128 rows
+//           share every K / V tile; the tensor cores alternate between them.
+//   NT = 1  (up to 128 rows) both accumulators hold the same rows and take the
+//           tiles in turn, so that one's softmax runs beside the other's
+//           products; their results meet in shared memory at a unit's end.
+//           Bound by the HBM stream: a tile of K and V (64 KB) takes 1.45 us
+//           of an SM's share of 6.8 TB/s, its products 0.7 us, and the two
+//           accumulators' chains product-softmax-product about 1 us a tile.
+//
+// Q is loaded by TMA as the append left it (bf16, not scaled): the scale
+// times log2 e goes into the exponent's fused multiply-add. Q and P enter the
+// products as bf16 (2^-9 of each value); a second bf16 term of Q would double
+// the first product, which at 256 rows is already half of what bounds the
+// kernel.
+//
+// One-byte caches: the loader's tiles are codes (16 KB), four converter warps
+// widen each to a bf16 tile -- exactly: an e5m2 value has 3 significant bits,
+// code - zero point is an integer up to 255 -- and, for uint8, put the rows'
+// scales beside it: a K scale multiplies its column of S, a V scale its
+// column of P, in fp32.
+//
+// Keys that no node may read (past the sequence, before the window) have zero
+// V rows whatever the cache holds, so that 0 * NaN never enters a sum.
+//
+// Warps: 0-3 and 4-7 softmax, 8 K / V loader (TMA), 9 MMA issue (one thread)
+// and tensor-memory allocation, 10 Q loader (TMA), 11 idle; 12-15 converters.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/mqa_decode.h"
+#include "launch.h"
+#include "ptx.cuh"
+#include "tc05.cuh"
+#include "tree.cuh"
+
+namespace mqa {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kBM = 128;  // rows of an accumulator
+constexpr int kBN = 128;  // keys per tile
+constexpr int kTileBytes = kBN * kD * 2;  // a bf16 tile: [2 halves of 64 dims][128 rows][128 B], swizzled
+constexpr int kRawBytes = kBN * kD;       // a code tile: [128 rows][128 B], swizzled
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;  // S / P of accumulator q at 128 q, its O at 256 + 128 q
+constexpr float kRescaleLog2 = 8.0f;
+
+// Registers: setmaxnreg moves them from the loader, MMA and converter warps
+// to the softmax warps (a row's 128 scores stay in registers); the shares add
+// up to what the block is launched with.
+template <int NT, int DT>
+struct Cfg {
+  static constexpr bool kByte = DT != kDtypeBf16;
+  static constexpr int kThreads = kByte ? 512 : 384;
+  static constexpr int kRegsLaunch = kByte ? 128 : 168;
+  static constexpr int kRegsSoftmax = kByte ? 200 : 216;
+  static constexpr int kRegsAux = kByte ? 56 : 72;
+  static_assert(kThreads * kRegsLaunch == 256 * kRegsSoftmax + (kThreads - 256) * kRegsAux, "register split");
+  static constexpr int kSlots = kByte ? (NT == 1 ? 4 : 3) : (NT == 1 ? 6 : 5);  // bf16 tiles
+  static constexpr int kRaw = kByte ? (DT == kDtypeU8 ? 3 : 4) : 0;              // code tiles
+  static constexpr int kQOff = 0;
+  static constexpr int kRingOff = NT * kTileBytes;
+  static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
+  // uint8: the scales of each bf16 tile's rows, twice as many places as tiles:
+  // a K tile is given back when its S is there, but its scales are read by
+  // the softmax after that. Load u + 2 kSlots only lands after load u + kSlots
+  // has been given back, which is after the softmax of u's tile.
+  static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;
+  static constexpr int kScales = 2 * kSlots;
+  static constexpr int kBarOff = kScaleOff + (DT == kDtypeU8 ? kScales * kBN * 4 : 0);
+  static constexpr int kSmemBytes = kBarOff + 256 + 1024;  // + alignment slack
+  // mbarriers
+  static constexpr int kQFull = 0;
+  static constexpr int kQFree = 1;
+  static constexpr int kFull = 2;                   // [kSlots]
+  static constexpr int kEmpty = kFull + kSlots;     // [kSlots]
+  static constexpr int kRFull = kEmpty + kSlots;    // [kRaw]
+  static constexpr int kREmpty = kRFull + kRaw;     // [kRaw]
+  static constexpr int kSFull = kREmpty + kRaw;     // [2]
+  static constexpr int kP = kSFull + 2;             // [2]
+  static constexpr int kODone = kP + 2;
+  static constexpr int kOFree = kODone + 1;
+  static constexpr int kDrain = kOFree + 1;
+  static constexpr int kNBars = kDrain + 1;
+  static_assert(kNBars * 8 + 4 <= 256, "barrier area");
+  static_assert(kSmemBytes + 1300 <= 227 * 1024, "shared memory (with the static part)");
+};
+
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+  float2 r;
+  asm("{\n\t.reg .b64 ra, rb, rc, rr;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %4};\n\t"
+      "mov.b64 rc, {%5, %5};\n\t"
+      "fma.rn.f32x2 rr, ra, rb, rc;\n\t"
+      "mov.b64 {%0, %1}, rr;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 ra, rb, rr;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rr, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rr;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 ra, rb, rr;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rr, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rr;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Four e5m2 codes as two bf16 pairs. A code's exponent and mantissa bits put at
+// bf16's places read as the value times 2^-112 (subnormals too), which one
+// exact multiplication undoes; infinities and NaN go through half precision.
+__device__ __forceinline__ uint2 widen_e5m2(uint32_t w) {
+  const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);  // code << 8, twice
+  uint2 r;
+  if (__vcmpgeu4(w & 0x7f7f7f7fu, 0x7c7c7c7cu) == 0u) {
+    const uint32_t a = (lo & 0x80008000u) | ((lo & 0x7f007f00u) >> 3);
+    const uint32_t b = (hi & 0x80008000u) | ((hi & 0x7f007f00u) >> 3);
+    const uint32_t k = 0x77807780u;  // 2^112
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(a), "r"(k));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(b), "r"(k));
+  } else {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    r = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
+  }
+  return r;
+}
+// four uint8 codes minus the zero point (z = 2^23 + zero point)
+__device__ __forceinline__ uint2 widen_u8(uint32_t w, float z) {
+  const float f0 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650)) - z;
+  const float f1 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7651)) - z;
+  const float f2 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7652)) - z;
+  const float f3 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7653)) - z;
+  return make_uint2(pack_bf16x2(f0, f1), pack_bf16x2(f2, f3));
+}
+
+template <int NT, bool PG, int DT>
+__global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
+    attn_tree_tc05_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                          const __grid_constant__ CUtensorMap tmap_q, const TreeParams p) {
+  using C = Cfg<NT, DT>;
+  constexpr bool kByte = C::kByte;
+  constexpr int kSlots = C::kSlots, kRaw = kByte ? C::kRaw : 1;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + C::kNBars * 8);
+  __shared__ TreePlan plan;
+  __shared__ int s_abort, s_skip, s_flag;
+  __shared__ float s_m[kBM], s_l[kBM];
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.group, acc_rows = p.tokens_per_tile * G, rows_per_block = NT * acc_rows;
+
+  if (!p.early) grid_dependency_wait();
+  if (tid == 0) {
+    s_abort = 0;
+    // an earlier block timed out: the result is invalid already
+    s_skip = (*reinterpret_cast<volatile int32_t*>(p.err) & static_cast<int>(MQA_DEVERR_TIMEOUT)) ? 1 : 0;
+    mbar_init(bar(C::kQFull), 1);
+    mbar_init(bar(C::kQFree), NT == 1 ? 8 : 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(bar(C::kFull + s), kByte ? 4 : 1);
+      mbar_init(bar(C::kEmpty + s), 1);
+    }
+    if constexpr (kByte) {
+      for (int s = 0; s < kRaw; ++s) {
+        mbar_init(bar(C::kRFull + s), 1);
+        mbar_init(bar(C::kREmpty + s), 4);
+      }
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(bar(C::kSFull + q), 1);
+      mbar_init(bar(C::kP + q), 4);
+    }
+    mbar_init(bar(C::kODone), 1);
+    mbar_init(bar(C::kOFree), 8);
+    mbar_init(bar(C::kDrain), 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tc05::tmem_alloc(smem_u32(tslot), kTmemCols);
+    tc05::tmem_relinquish();
+  }
+  if (warp == 8) tree_plan(p, kBN, rows_per_block, blockIdx.x, gridDim.x, &plan);
+  tc05::fence_before_sync();
+  __syncthreads();
+  tc05::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tslot);
+  const uint32_t sbase = smem_u32(smem);
+
+  auto fail = [&](bool one) {
+    if (one) {
+      s_abort = 1;
+      atomicOr(p.err, static_cast<int>(MQA_DEVERR_TIMEOUT));
+    }
+  };
+  auto stop = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
+  auto regs_aux = [&]() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsAux)); };
+  TreeWalk walk;
+  walk.start(p, plan, kBN, rows_per_block);
+  if (s_skip) walk.at = walk.end;
+  TreeSegment g;
+
+  if (warp == 8) {
+    regs_aux();
+    // -------------------------------------------------------- K / V loader
+    // load u (2 t + 0 / 1: K / V of the run's tile t) into slot u % slots: the
+    // bf16 tile itself, or the code tile a converter widens
+    constexpr int kN = kByte ? kRaw : kSlots;
+    constexpr int kBytes = kByte ? kRawBytes : kTileBytes;
+    constexpr int kRing = kByte ? C::kRawOff : C::kRingOff;
+    constexpr int kF = kByte ? C::kRFull : C::kFull, kE = kByte ? C::kREmpty : C::kEmpty;
+    const int ps = PG ? p.page_size : 64, rp = ps < 64 ? ps : 64, copies = kBN / rp;
+    bool waited = !p.early, ok = true, bad = false;
+    int u = 0;
+    while (ok && walk.next(p, kBN, rows_per_block, g)) {
+      const int row = g.b * p.h_kv + g.j;
+      const int key_first = g.s.first + g.t0 * kBN;
+      // paged: the page ids of the segment's keys, 32 at a time, one per lane
+      // (wcur: pages wbase .., wnxt: the next 32). Entries of pages that hold
+      // no key to be read are not looked at; a copy there lands zeros (page -1)
+      const int32_t* trow = PG ? p.block_table + static_cast<long long>(g.b) * p.max_pages : nullptr;
+      const int lp_first = g.s.lo / ps, lp_end = (g.s.len + ps - 1) / ps;
+      auto entry = [&](int lp) { return (PG && lp >= lp_first && lp < lp_end) ? __ldg(trow + lp) : -1; };
+      int wbase = key_first / ps;
+      int wcur = entry(wbase + lane), wnxt = entry(wbase + 32 + lane);
+      for (int t = 0; t < g.nt && ok; ++t) {
+        const int key0 = key_first + t * kBN;
+        if (!waited && key0 + kBN > g.s.pos) {  // this tile holds a node's row, which the append writes
+          grid_dependency_wait();
+          waited = true;
+        }
+        for (int kv = 0; kv < 2; ++kv, ++u) {
+          const int slot = u % kN;
+          if (lane == 0) {
+            if (u >= kN) ok = mbar_wait(bar(kE + slot), (u / kN - 1) & 1, p.wait_ns);
+            if (!ok) fail(true);
+            if (stop()) ok = false;
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          const CUtensorMap* map = kv ? &tmap_v : &tmap_k;
+          const uint32_t dst = sbase + kRing + slot * kBytes;
+          if constexpr (PG) {
+            while (key0 / ps - wbase >= 32) {
+              wcur = wnxt;
+              wbase += 32;
+              wnxt = entry(wbase + 32 + lane);
+            }
+            const int k = key0 + lane * rp, lp = k / ps, off = lp - wbase;  // off < 32 + 8
+            const int pc = __shfl_sync(0xffffffffu, wcur, off & 31), pn = __shfl_sync(0xffffffffu, wnxt, off & 31);
+            int page = off < 32 ? pc : pn;
+            const bool needed = lane < copies && lp >= lp_first && lp < lp_end;
+            if (needed && (page < 0 || page >= p.num_pages)) bad = true;
+            if (!needed || page < 0 || page >= p.num_pages) page = -1;
+            if (lane == 0) mbar_arrive_expect_tx(bar(kF + slot), kBytes);
+            __syncwarp();
+            if (lane < copies) {
+              const uint32_t d = dst + lane * rp * 128;
+              if constexpr (kByte) {
+                tma_load_4d(d, map, 0, k & (ps - 1), g.j, page, bar(kF + slot));
+              } else {
+                tma_load_5d(d, map, 0, k & (ps - 1), 0, g.j, page, bar(kF + slot));
+                tma_load_5d(d + 16384, map, 0, k & (ps - 1), 1, g.j, page, bar(kF + slot));
+              }
+            }
+          } else if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kF + slot), kBytes);
+            if constexpr (kByte)
+              tma_load_3d(dst, map, 0, key0, row, bar(kF + slot));
+            else
+              tma_load_4d(dst, map, 0, key0, 0, row, bar(kF + slot));
+          }
+        }
+      }
+    }
+    if (PG && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_PAGE_RANGE));
+    // every copy this warp issued (u of them) lands before the block can exit
+    if (lane == 0)
+      for (int k = u > kN ? u - kN : 0; k < u; ++k) (void)mbar_wait(bar(kF + k % kN), (k / kN) & 1, kWaitLimitNs);
+    __syncwarp();
+  } else if (warp == 10) {
+    regs_aux();
+    // ------------------------------------------------------------ Q loader
+    if (lane == 0) {
+      if (p.early) grid_dependency_wait();
+      bool ok = true;
+      int seg = 0;
+      while (ok && walk.next(p, kBN, rows_per_block, g)) {
+        if (seg > 0) ok = mbar_wait(bar(C::kQFree), (seg - 1) & 1, p.wait_ns);
+        if (!ok) fail(true);
+        if (!ok || stop()) break;
+        // (tokens past the sequence's belong to the next: rows nobody uses)
+        mbar_arrive_expect_tx(bar(C::kQFull), NT * acc_rows * kD * 2);
+        for (int q = 0; q < NT; ++q)
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(sbase + C::kQOff + q * kTileBytes + h * 16384, &tmap_q, 64 * h, g.j * G,
+                        g.b * p.n + (g.rb * NT + q) * p.tokens_per_tile, bar(C::kQFull));
+        ++seg;
+      }
+      if (seg > 0) (void)mbar_wait(bar(C::kQFull), (seg - 1) & 1, kWaitLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    regs_aux();
+    // ----------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t id_s = tc05::idesc_bf16_f32(kBM, kBN, false, false);
+      constexpr uint32_t id_o = tc05::idesc_bf16_f32(kBM, kD, false, true);
+      auto wait = [&](int id, int parity) {  // polls: a suspended wait wakes late
+        const unsigned long long t0 = global_timer_ns();
+        while (!mbar_test(bar(id), parity & 1))
+          if (stop() || global_timer_ns() - t0 > p.wait_ns) return false;
+        return true;
+      };
+      int u0 = 0;            // the segment's first load
+      int ps[2] = {0, 0};    // products P V issued into each accumulator
+      auto full = [&](int u) { return wait(C::kFull + u % kSlots, u / kSlots); };
+      auto issue_s = [&](int q, int t) {  // S_q = Q K(t)^T
+        const uint32_t q_s = sbase + C::kQOff + (NT == 2 ? q * kTileBytes : 0);
+        const uint32_t k_s = sbase + C::kRingOff + ((u0 + 2 * t) % kSlots) * kTileBytes;
+        tc05::fence_after_sync();
+#pragma unroll
+        for (int ks = 0; ks < kD / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+          tc05::mma_bf16(tmem + kColS + q * 128, tc05::smem_desc_sw128(q_s + off, 16, 1024),
+                         tc05::smem_desc_sw128(k_s + off, 16, 1024), id_s, ks > 0);
+        }
+        tc05::commit(bar(C::kSFull + q));
+      };
+      auto issue_pv = [&](int q, int t, bool add) {  // O_q (+)= P_q V(t)
+        const uint32_t v_s = sbase + C::kRingOff + ((u0 + 2 * t + 1) % kSlots) * kTileBytes;
+        tc05::fence_after_sync();
+#pragma unroll
+        for (int ks = 0; ks < kBN / 16; ++ks)
+          tc05::mma_bf16_ta(tmem + kColO + q * 128, tmem + kColS + q * 128 + ks * 8,
+                            tc05::smem_desc_sw128(v_s + ks * 2048, 16384, 1024), id_o, add || ks > 0);
+      };
+      auto free_k = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t) % kSlots)); };
+      auto free_v = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t + 1) % kSlots)); };
+      bool ok = true;
+      int seg = 0;
+      while (ok && walk.next(p, kBN, rows_per_block, g)) {
+        const int T = g.nt;
+        ok = wait(C::kQFull, seg) && full(u0);
+        if (!ok) break;
+        if constexpr (NT == 2) {
+          issue_s(0, 0);
+          issue_s(1, 0);
+          free_k(0);
+          if (T == 1) tc05::commit(bar(C::kQFree));
+          // O of the last segment has been read (S, which P of the last
+          // segment held, was free at its last product)
+          if (seg > 0) ok = wait(C::kOFree, seg - 1);
+          for (int t = 0; ok && t < T; ++t) {
+            ok = wait(C::kP + 0, ps[0]++) && full(u0 + 2 * t + 1);
+            if (!ok) break;
+            issue_pv(0, t, t > 0);
+            if (t + 1 < T) {
+              ok = full(u0 + 2 * t + 2);
+              if (!ok) break;
+              issue_s(0, t + 1);
+            }
+            ok = wait(C::kP + 1, ps[1]++);
+            if (!ok) break;
+            issue_pv(1, t, t > 0);
+            free_v(t);
+            if (t + 1 < T) {
+              issue_s(1, t + 1);
+              free_k(t + 1);
+              if (t + 2 == T) tc05::commit(bar(C::kQFree));
+            }
+          }
+        } else {
+          issue_s(0, 0);
+          free_k(0);
+          if (T > 1) {
+            ok = full(u0 + 2);
+            if (!ok) break;
+            issue_s(1, 1);
+            free_k(1);
+          }
+          if (seg > 0) ok = wait(C::kOFree, seg - 1);
+          for (int t = 0; ok && t < T; ++t) {
+            const int q = t & 1;
+            ok = wait(C::kP + q, ps[q]++) && full(u0 + 2 * t + 1);
+            if (!ok) break;
+            issue_pv(q, t, t > 1);
+            free_v(t);
+            if (t + 2 < T) {
+              ok = full(u0 + 2 * t + 4);
+              if (!ok) break;
+              issue_s(q, t + 2);
+              free_k(t + 2);
+            }
+          }
+        }
+        if (ok) tc05::commit(bar(C::kODone));
+        u0 += 2 * T;
+        ++seg;
+      }
+      if (!ok) fail(true);
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    regs_aux();
+  } else if (kByte && warp >= 12) {
+    regs_aux();
+    // ---------------------------------------------------------- converters
+    // Thread r widens row r (key key0 + r) of every tile.
+    if constexpr (kByte) {
+      const int r = tid - 384;
+      bool ok = true, waited = !p.early;
+      int u = 0;
+      while (ok && walk.next(p, kBN, rows_per_block, g)) {
+        const int key_first = g.s.first + g.t0 * kBN;
+        // uint8: the (scale, zero point) of this thread's row of a tile, zeros
+        // where nothing may be read; requested a tile ahead
+        auto scales = [&](int t, float2* out) {
+          out[0] = out[1] = make_float2(0.f, 0.f);
+          if (DT != kDtypeU8 || t >= g.nt) return;
+          const int key = key_first + t * kBN + r;
+          if (key < g.s.lo || key >= g.s.len) return;
+          long long row;
+          if constexpr (PG) {
+            const int page = __ldg(p.block_table + static_cast<long long>(g.b) * p.max_pages + key / p.page_size);
+            if (page < 0 || page >= p.num_pages) return;
+            row = (static_cast<long long>(page) * p.h_kv + g.j) * p.page_size + (key & (p.page_size - 1));
+          } else {
+            row = (static_cast<long long>(g.b) * p.h_kv + g.j) * p.capacity + key;
+          }
+          // (plain loads: the append of this step may have written them)
+          out[0] = p.k_sz[row];
+          out[1] = p.v_sz[row];
+        };
+        float2 now[2], next[2];
+        if (DT == kDtypeU8 && !waited && key_first + kBN > g.s.pos) {
+          grid_dependency_wait();
+          waited = true;
+        }
+        scales(0, now);
+        for (int t = 0; t < g.nt && ok; ++t) {
+          const int key0 = key_first + t * kBN;
+          const bool live = key0 + r >= g.s.lo && key0 + r < g.s.len;
+          if (DT == kDtypeU8 && !waited && key0 + 2 * kBN > g.s.pos) {
+            grid_dependency_wait();
+            waited = true;
+          }
+          scales(t + 1, next);
+          for (int kv = 0; kv < 2; ++kv, ++u) {
+            const int rs = u % kRaw, slot = u % kSlots;
+            ok = mbar_wait(bar(C::kRFull + rs), (u / kRaw) & 1, p.wait_ns) &&
+                 (u < kSlots || mbar_wait(bar(C::kEmpty + slot), (u / kSlots - 1) & 1, p.wait_ns));
+            if (!ok) fail(true);
+            ok = __all_sync(0xffffffffu, ok && !stop());
+            if (!ok) break;
+            const unsigned char* src = smem + C::kRawOff + rs * kRawBytes + r * 128;
+            unsigned char* dst = smem + C::kRingOff + slot * kTileBytes + r * 128;
+            const float z = 8388608.f + now[kv].y;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {  // 16 codes
+              uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ (r & 7)) << 4));
+              uint2 a, b, e, f;
+              if constexpr (DT == kDtypeU8) {
+                a = widen_u8(w.x, z), b = widen_u8(w.y, z), e = widen_u8(w.z, z), f = widen_u8(w.w, z);
+              } else {
+                a = widen_e5m2(w.x), b = widen_e5m2(w.y), e = widen_e5m2(w.z), f = widen_e5m2(w.w);
+              }
+              if (!live) a = b = e = f = make_uint2(0u, 0u);
+              unsigned char* d = dst + (c >> 2) * 16384;
+              *reinterpret_cast<uint4*>(d + (((2 * c) & 7) ^ (r & 7)) * 16) = make_uint4(a.x, a.y, b.x, b.y);
+              *reinterpret_cast<uint4*>(d + (((2 * c + 1) & 7) ^ (r & 7)) * 16) = make_uint4(e.x, e.y, f.x, f.y);
+            }
+            if constexpr (DT == kDtypeU8)
+              reinterpret_cast<float*>(smem + C::kScaleOff)[(u % C::kScales) * kBN + r] = now[kv].x;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(C::kFull + slot));
+              mbar_arrive(bar(C::kREmpty + rs));
+            }
+          }
+          now[0] = next[0];
+          now[1] = next[1];
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+    // ---------------------------- softmax of accumulator q, row r per thread
+    const int q = warp >> 2, r = tid - q * kBM;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t scol = tmem + lane_base + kColS + q * 128, ocol = tmem + lane_base + kColO + q * 128;
+    const float c = p.scale_log2;
+    const bool warp_rows = (warp & 3) * 32 < acc_rows;  // some lane of this warp holds a row
+    bool waited = !p.early;
+    int u0 = 0, seg = 0, js = 0;  // first load of the segment; segments; tiles of this accumulator
+    bool ok = true;
+    while (walk.next(p, kBN, rows_per_block, g)) {
+      const int gr = g.rb * rows_per_block + (NT == 2 ? q * acc_rows : 0) + r;  // row of the unit's kv head
+      const bool live = r < acc_rows && gr < g.s.nodes * G;
+      const TreeRow row = tree_row(p, g.b, g.s, live ? gr / G : -1);
+      float m_ref = -INFINITY, l = 0.f;
+      for (int t = NT == 2 ? 0 : q; ok && t < g.nt; t += NT == 2 ? 1 : 2, ++js) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kSFull + q), js & 1, p.wait_ns) && !stop());
+        if (!ok) break;
+        tc05::fence_after_sync();
+        const int key0 = g.s.first + (g.t0 + t) * kBN;
+        const int vs = (u0 + 2 * t + 1) % kSlots;  // V's slot
+        if (!kByte && (NT == 1 || q == 0) && (key0 + kBN > g.s.len || key0 < g.s.lo)) {
+          // rows that no node reads may hold anything (NaN included): P = 0
+          // there, and 0 * NaN would still poison O. Their V rows are zeroed
+          // once the tile has landed, before P is published.
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kFull + vs), ((u0 + 2 * t + 1) / kSlots) & 1, p.wait_ns));
+          if (!ok) break;
+          if (key0 + r >= g.s.len || key0 + r < g.s.lo) {
+            unsigned char* vrow = smem + C::kRingOff + vs * kTileBytes + r * 128;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              *reinterpret_cast<uint4*>(vrow + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(vrow + 16384 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+        }
+        if (warp_rows) {
+          float s[kBN];
+#pragma unroll
+          for (int x = 0; x < kBN; x += 32) tc05::ld_32x32b_x32(scol + x, *reinterpret_cast<float(*)[32]>(&s[x]));
+          tc05::wait_ld();
+#pragma unroll
+          for (int x = 0; x < kBN; x += 32) tc05::reg_fence(*reinterpret_cast<float(*)[32]>(&s[x]));
+          if constexpr (DT == kDtypeU8) {
+            const float4* sc = reinterpret_cast<const float4*>(smem + C::kScaleOff) + ((u0 + 2 * t) % C::kScales) * (kBN / 4);
+#pragma unroll
+            for (int x = 0; x < kBN / 4; ++x) {
+              const float4 f = sc[x];
+              const float2 a = mul2(make_float2(s[4 * x], s[4 * x + 1]), make_float2(f.x, f.y));
+              const float2 b = mul2(make_float2(s[4 * x + 2], s[4 * x + 3]), make_float2(f.z, f.w));
+              s[4 * x] = a.x, s[4 * x + 1] = a.y, s[4 * x + 2] = b.x, s[4 * x + 3] = b.y;
+            }
+          }
+          // only tiles that reach a node, the end or the window are masked
+          if (key0 + kBN > g.s.pos || key0 < row.ka) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t bits = tree_bits(row, key0 + 32 * w);
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (!((bits >> x) & 1u)) s[32 * w + x] = -INFINITY;
+            }
+          }
+          float mx8[8];  // eight independent chains, two scores a step
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(s[i], s[8 + i]);
+#pragma unroll
+          for (int x = 16; x < kBN; x += 16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx8[i] = max3(mx8[i], s[x + i], s[x + 8 + i]);
+          }
+          const float mt = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+          // a new reference maximum only when the row's maximum grew by more than 2^8
+          const bool grow = (mt - m_ref) * c > kRescaleLog2 || (m_ref == -INFINITY && mt != -INFINITY);
+          const float m_new = grow ? mt : m_ref;
+          if (__any_sync(0xffffffffu, grow && m_ref != -INFINITY)) {
+            // O is rescaled. The last product into O_q is done: it was issued
+            // before this S_q, whose completion this thread has seen
+            const float alpha = (grow && m_ref != -INFINITY) ? fast_exp2((m_ref - m_new) * c) : 1.f;
+#pragma unroll
+            for (int x = 0; x < kD / 32; ++x) {
+              float v[32];
+              tc05::ld_32x32b_x32(ocol + x * 32, v);
+              tc05::wait_ld();
+              tc05::reg_fence(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] *= alpha;
+              tc05::st_32x32b_x32(ocol + x * 32, v);
+            }
+            l *= alpha;
+          }
+          m_ref = m_new;
+          const float e = m_ref == -INFINITY ? 0.f : -m_ref * c;
+          float2 sm4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          if (DT == kDtypeU8)  // the V tile's scales
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kFull + vs), ((u0 + 2 * t + 1) / kSlots) & 1, p.wait_ns));
+          if (!ok) break;
+          const float4* sv =
+              reinterpret_cast<const float4*>(smem + C::kScaleOff) + ((u0 + 2 * t + 1) % C::kScales) * (kBN / 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const int x = 64 * half + 2 * i;
+              const float2 d0 = fma2(make_float2(s[x], s[x + 1]), c, e), d1 = fma2(make_float2(s[x + 2], s[x + 3]), c, e);
+              float2 p0 = make_float2(fast_exp2(d0.x), fast_exp2(d0.y)), p1 = make_float2(fast_exp2(d1.x), fast_exp2(d1.y));
+              sm4[i & 3] = add2(sm4[i & 3], p0);
+              sm4[(i + 1) & 3] = add2(sm4[(i + 1) & 3], p1);
+              if constexpr (DT == kDtypeU8) {
+                const float4 f = sv[x / 4];
+                p0 = mul2(p0, make_float2(f.x, f.y));
+                p1 = mul2(p1, make_float2(f.z, f.w));
+              }
+              pk[i] = pack_bf16x2(p0.x, p0.y);
+              pk[i + 1] = pack_bf16x2(p1.x, p1.y);
+            }
+            tc05::st_32x32b_x32_u(scol + 32 * half, pk);
+          }
+          l += ((sm4[0].x + sm4[0].y) + (sm4[1].x + sm4[1].y)) + ((sm4[2].x + sm4[2].y) + (sm4[3].x + sm4[3].y));
+          tc05::wait_st();
+          tc05::fence_before_sync();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kP + q));
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kODone), seg & 1, p.wait_ns) && !stop());
+      if (!ok && lane == 0) fail(true);
+      // all eight warps agree whether the segment's result stands
+      if (bar_any(2, 256, !ok)) break;
+      tc05::fence_after_sync();
+      if (!waited) {  // the append clears the counters; out may still be read before it
+        grid_dependency_wait();
+        waited = true;
+      }
+      // ---- the segment's result: this thread's row, O unnormalised in v
+      const bool whole = g.head && g.tail;
+      float* part = p.part + tree_part_floats(rows_per_block, kD) * (2 * static_cast<size_t>(blockIdx.x) + (g.head ? 1 : 0));
+      const int br = gr - g.rb * rows_per_block;  // row of the block
+      long long orow = 0;
+      if (live) orow = tree_out_row(p, g, gr);
+      auto put = [&](int x, const float* v, float inv) {  // 32 values from dim 32 x on
+        if (!live) return;
+        if (!whole) {
+          float* dst = part + static_cast<size_t>(br) * kD + 32 * x;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else if (p.out_dtype == kDtypeBf16) {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + orow * kD + 32 * x;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint4 w;
+            w.x = pack_bf16x2(v[i] * inv, v[i + 1] * inv);
+            w.y = pack_bf16x2(v[i + 2] * inv, v[i + 3] * inv);
+            w.z = pack_bf16x2(v[i + 4] * inv, v[i + 5] * inv);
+            w.w = pack_bf16x2(v[i + 6] * inv, v[i + 7] * inv);
+            *reinterpret_cast<uint4*>(dst + i) = w;
+          }
+        } else {
+          float* dst = static_cast<float*>(p.out) + orow * kD + 32 * x;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(dst + i) =
+                make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+        }
+      };
+      auto put_ml = [&](float m2, float sum) {  // maximum (log2 domain) and sum
+        if (!live) return;
+        if (!whole) {
+          part[static_cast<size_t>(rows_per_block) * kD + br] = m2;
+          part[static_cast<size_t>(rows_per_block) * (kD + 1) + br] = sum;
+        } else if (p.lse_out != nullptr) {
+          p.lse_out[orow] = sum > 0.f ? (m2 + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+        }
+      };
+      float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c;
+      if (NT == 2 || g.nt == 1) {
+        if (NT == 2 || q == 0) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          if (warp_rows) {
+#pragma unroll
+            for (int x = 0; x < kD / 32; ++x) {
+              float v[32];
+              tc05::ld_32x32b_x32(ocol + x * 32, v);
+              tc05::wait_ld();
+              tc05::reg_fence(v);
+              put(x, v, inv);
+            }
+          }
+          put_ml(m2, l);
+        }
+      } else {
+        // the two accumulators of each row meet: the second warpgroup hands its
+        // O over through the Q area (free: every product with Q is done), 32
+        // dims at a time in two buffers of 16 KB
+        unsigned char* xbuf = smem + C::kQOff;
+        auto chunk = [&](int x, int i) {  // float4 i of row r
+          return reinterpret_cast<float4*>(xbuf + (x & 1) * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
+        };
+        if (q == 1) {
+          s_m[r] = m2;
+          s_l[r] = l;
+        }
+        float w0 = 0.f, w1 = 0.f, inv = 1.f;
+#pragma unroll
+        for (int x = 0; x <= kD / 32; ++x) {
+          if (q == 1 && x < kD / 32 && warp_rows) {
+            float v[32];
+            tc05::ld_32x32b_x32(ocol + x * 32, v);
+            tc05::wait_ld();
+            tc05::reg_fence(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *chunk(x, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+          if (q == 0 && x > 0 && warp_rows) {
+            if (x == 1) {
+              const float mo = s_m[r], lo = s_l[r], mx = fmaxf(m2, mo);
+              if (mx != -INFINITY) {
+                w0 = exp2f(m2 - mx);
+                w1 = exp2f(mo - mx);
+              }
+              l = w0 * l + w1 * lo;
+              m2 = mx;
+              if (whole) inv = l > 0.f ? 1.f / l : 0.f;
+            }
+            float v[32];
+            tc05::ld_32x32b_x32(ocol + (x - 1) * 32, v);
+            tc05::wait_ld();
+            tc05::reg_fence(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 o = *chunk(x - 1, i);
+              v[4 * i] = fmaf(w1, o.x, w0 * v[4 * i]);
+              v[4 * i + 1] = fmaf(w1, o.y, w0 * v[4 * i + 1]);
+              v[4 * i + 2] = fmaf(w1, o.z, w0 * v[4 * i + 2]);
+              v[4 * i + 3] = fmaf(w1, o.w, w0 * v[4 * i + 3]);
+            }
+            put(x - 1, v, inv);
+          }
+          if (x < kD / 32) named_bar_sync(1, 256);
+        }
+        if (q == 0) put_ml(m2, l);
+      }
+      // O is read; NT = 1: and the Q area
+      tc05::fence_before_sync();
+      if (NT == 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(C::kOFree));
+        if (NT == 1) mbar_arrive(bar(C::kQFree));
+      }
+      if (!whole)
+        tree_arrive_merge<kD>(p, plan, g, rows_per_block, tid, 256, &s_flag, [] { named_bar_sync(1, 256); });
+      u0 += 2 * g.nt;
+      ++seg;
+    }
+  }
+
+  // ---- teardown: every role is done with tensor memory
+  tc05::fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    if (*reinterpret_cast<volatile int*>(&s_abort)) {
+      // products may still be in flight after a timeout: wait (bounded) for
+      // them before the columns are released
+      if (lane == 0) {
+        tc05::commit(bar(C::kDrain));
+        (void)mbar_wait(bar(C::kDrain), 0, kWaitLimitNs);
+      }
+      __syncwarp();
+    }
+    tc05::fence_after_sync();
+    tc05::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int NT, bool PG, int DT>
+cudaError_t launch_tree_tc05_t(const TreeParams& p, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CUtensorMap& tq, cudaStream_t stream) {
+  using C = Cfg<NT, DT>;
+  auto kern = attn_tree_tc05_kernel<NT, PG, DT>;
+  // a build with another register count at launch would leave setmaxnreg.inc
+  // waiting for registers that never come: it is not launched
+  static const int launch_regs = [&] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : -1;
+  }();
+  if (launch_regs != C::kRegsLaunch) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tk, tv, tq, p);
+}
+
+template <int DT>
+cudaError_t launch_tree_tc05_dt(const TreeParams& p, int tiles, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CUtensorMap& tq, cudaStream_t stream) {
+  if (tiles == 2)
+    return p.paged ? launch_tree_tc05_t<2, true, DT>(p, ctas, tk, tv, tq, stream)
+                   : launch_tree_tc05_t<2, false, DT>(p, ctas, tk, tv, tq, stream);
+  return p.paged ? launch_tree_tc05_t<1, true, DT>(p, ctas, tk, tv, tq, stream)
+                 : launch_tree_tc05_t<1, false, DT>(p, ctas, tk, tv, tq, stream);
+}
+
+}  // namespace
+}  // namespace mqa

@@ -257,10 +257,19 @@ struct TreeParams {
   int32_t* arrived;  // [blocks] zero: blocks that have left a partial of the unit that starts in block c
   float* part;       // [2 blocks] partial results
   int32_t* err;
+  int tokens_per_tile;  // attn_tree_tc05: nodes of an accumulator's row tile
   int min_tiles;  // a block's run is at least this long
   int early;      // 1: the preceding launch is the append kernel: the cached tokens may be read before it ends
   unsigned long long wait_ns;
 };
+// A partial result: [rows][d] fp32 sums, then each row's maximum (log2
+// domain) and sum; a multiple of 16 bytes, whatever the rows. A block leaves
+// at most two: of the unit it starts in the middle of (place 2 c) and of the
+// unit it ends in the middle of (place 2 c + 1; a run inside one unit without
+// its first tile is of the first kind).
+__host__ __device__ inline size_t tree_part_floats(int rows, int d) {
+  return (static_cast<size_t>(rows) * (d + 2) + 3) / 4 * 4;
+}
 struct TreeShape {
   int rows, keys;   // rows of a block, keys of a tile
   int ctas_per_sm;  // blocks launched per SM
@@ -268,6 +277,18 @@ struct TreeShape {
 // any cache the tensor cores read, head_dim 64 or 128
 TreeShape tree_mma_shape(int head_dim);
 cudaError_t launch_tree_mma(const TreeParams& p, int ctas, cudaStream_t stream);
+
+// tcgen05: head_dim 128, group <= 128. `tiles` row tiles of tokens_per_tile *
+// group rows to a block (2 when a kv head has more than 128 rows). Maps: K / V
+// as bf16 tiles of 128 rows (paged: 64-dim halves of min(page_size, 64) rows)
+// or code tiles of as many rows, Q boxes of 64 dims x group x tokens_per_tile.
+constexpr int kTreeTileKeys = 128;
+cudaError_t launch_tree_tc05_bf16(const TreeParams& p, int tiles, int ctas, const CUtensorMap& tk,
+                                  const CUtensorMap& tv, const CUtensorMap& tq, cudaStream_t stream);
+cudaError_t launch_tree_tc05_u8(const TreeParams& p, int tiles, int ctas, const CUtensorMap& tk,
+                                const CUtensorMap& tv, const CUtensorMap& tq, cudaStream_t stream);
+cudaError_t launch_tree_tc05_f8(const TreeParams& p, int tiles, int ctas, const CUtensorMap& tk,
+                                const CUtensorMap& tv, const CUtensorMap& tq, cudaStream_t stream);
 
 // Verification of drafted trees (verify_tree.cu).
 struct VerifyParams {

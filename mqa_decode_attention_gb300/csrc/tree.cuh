@@ -158,14 +158,6 @@ __device__ __forceinline__ int tree_cta_of(const TreePlan& pl, long long x) {
   return static_cast<int>(((x + 1) * pl.ctas - 1) / pl.total);
 }
 
-// A partial result: [rows][d] fp32 sums, then each row's maximum (log2
-// domain) and sum. A block leaves at most two: of the unit it starts in the
-// middle of (slot 2 c) and of the unit it ends in the middle of (slot 2 c + 1;
-// a run inside one unit without its first tile is of the first kind).
-__host__ __device__ __forceinline__ size_t tree_part_floats(int rows, int d) {
-  return static_cast<size_t>(rows) * (d + 2);
-}
-
 // 32 bits, bit c = the row may attend to key k0 + c. m: the row's mask words
 // with the bits of dead nodes cleared (all zero for a dead row), ka its first
 // key, pos the number of cached tokens.

@@ -66,8 +66,7 @@ constexpr uint32_t kColS = 0, kColO = 256;  // S / P of accumulator q at 128 q, 
 constexpr float kRescaleLog2 = 8.0f;
 
 // Registers: setmaxnreg moves them from the loader, MMA and converter warps
-// to the softmax warps (a row's 128 scores stay in registers); the shares add
-// up to what the block is launched with.
+// to the softmax warps; the shares add up to what the block is launched with.
 template <int NT, int DT>
 struct Cfg {
   static constexpr bool kByte = DT != kDtypeBf16;
@@ -186,8 +185,12 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + C::kNBars * 8);
   __shared__ TreePlan plan;
-  __shared__ int s_abort, s_skip, s_flag;
+  __shared__ int s_abort, s_skip, s_flag, s_more[2];
   __shared__ float s_m[kBM], s_l[kBM];
+  // the softmax warps' segment (two places: one may still be read while the
+  // next is written) and the walk that gives it, kept out of their registers
+  __shared__ TreeWalk s_walk;
+  __shared__ TreeSegment s_seg[2];
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -241,7 +244,6 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   TreeWalk walk;
   walk.start(p, plan, kBN, rows_per_block);
   if (s_skip) walk.at = walk.end;
-  TreeSegment g;
 
   if (warp == 8) {
     regs_aux();
@@ -253,6 +255,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     constexpr int kRing = kByte ? C::kRawOff : C::kRingOff;
     constexpr int kF = kByte ? C::kRFull : C::kFull, kE = kByte ? C::kREmpty : C::kEmpty;
     const int ps = PG ? p.page_size : 64, rp = ps < 64 ? ps : 64, copies = kBN / rp;
+    TreeSegment g;
     bool waited = !p.early, ok = true, bad = false;
     int u = 0;
     while (ok && walk.next(p, kBN, rows_per_block, g)) {
@@ -326,6 +329,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     // ------------------------------------------------------------ Q loader
     if (lane == 0) {
       if (p.early) grid_dependency_wait();
+      TreeSegment g;
       bool ok = true;
       int seg = 0;
       while (ok && walk.next(p, kBN, rows_per_block, g)) {
@@ -362,24 +366,27 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         const uint32_t q_s = sbase + C::kQOff + (NT == 2 ? q * kTileBytes : 0);
         const uint32_t k_s = sbase + C::kRingOff + ((u0 + 2 * t) % kSlots) * kTileBytes;
         tc05::fence_after_sync();
+        // (the descriptors' address field counts 16 bytes: the sub-tiles are constant steps)
+        const uint64_t qd = tc05::smem_desc_sw128(q_s, 16, 1024), kd = tc05::smem_desc_sw128(k_s, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < kD / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-          tc05::mma_bf16(tmem + kColS + q * 128, tc05::smem_desc_sw128(q_s + off, 16, 1024),
-                         tc05::smem_desc_sw128(k_s + off, 16, 1024), id_s, ks > 0);
+          const uint64_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+          tc05::mma_bf16(tmem + kColS + q * 128, qd + off, kd + off, id_s, ks > 0);
         }
         tc05::commit(bar(C::kSFull + q));
       };
       auto issue_pv = [&](int q, int t, bool add) {  // O_q (+)= P_q V(t)
         const uint32_t v_s = sbase + C::kRingOff + ((u0 + 2 * t + 1) % kSlots) * kTileBytes;
         tc05::fence_after_sync();
+        const uint64_t vd = tc05::smem_desc_sw128(v_s, 16384, 1024);
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
-          tc05::mma_bf16_ta(tmem + kColO + q * 128, tmem + kColS + q * 128 + ks * 8,
-                            tc05::smem_desc_sw128(v_s + ks * 2048, 16384, 1024), id_o, add || ks > 0);
+          tc05::mma_bf16_ta(tmem + kColO + q * 128, tmem + kColS + q * 128 + ks * 8, vd + ((ks * 2048) >> 4), id_o,
+                            add || ks > 0);
       };
       auto free_k = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t) % kSlots)); };
       auto free_v = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t + 1) % kSlots)); };
+      TreeSegment g;
       bool ok = true;
       int seg = 0;
       while (ok && walk.next(p, kBN, rows_per_block, g)) {
@@ -452,6 +459,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     // Thread r widens row r (key key0 + r) of every tile.
     if constexpr (kByte) {
       const int r = tid - 384;
+      TreeSegment g;
       bool ok = true, waited = !p.early;
       int u = 0;
       while (ok && walk.next(p, kBN, rows_per_block, g)) {
@@ -538,16 +546,34 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     bool waited = !p.early;
     int u0 = 0, seg = 0, js = 0;  // first load of the segment; segments; tiles of this accumulator
     bool ok = true;
-    while (walk.next(p, kBN, rows_per_block, g)) {
+    if (tid == 0) s_walk = walk;
+    while (true) {
+      if (tid == 0) s_more[seg & 1] = s_walk.next(p, kBN, rows_per_block, s_seg[seg & 1]);
+      named_bar_sync(1, 256);
+      if (!s_more[seg & 1]) break;
+      const TreeSegment& g = s_seg[seg & 1];
       const int gr = g.rb * rows_per_block + (NT == 2 ? q * acc_rows : 0) + r;  // row of the unit's kv head
       const bool live = r < acc_rows && gr < g.s.nodes * G;
-      const TreeRow row = tree_row(p, g.b, g.s, live ? gr / G : -1);
+      const int node = live ? gr / G : -1;
+      // this row's first key, the first key that not every row attends to
+      const int ka = tree_first_key(p, g.b, g.s, node), pos = g.s.pos;
+      const int nt = g.nt;
+      int key0 = g.s.first + (g.t0 + (NT == 2 ? 0 : q)) * kBN;
       float m_ref = -INFINITY, l = 0.f;
-      for (int t = NT == 2 ? 0 : q; ok && t < g.nt; t += NT == 2 ? 1 : 2, ++js) {
+      for (int t = NT == 2 ? 0 : q; ok && t < nt; t += NT == 2 ? 1 : 2, ++js, key0 += (NT == 2 ? 1 : 2) * kBN) {
+        // only tiles that reach a node, the end or the window are masked: bit x
+        // of these words, the row attends to key key0 + x
+        // (one answer for the warp: what follows has to stay converged)
+        const bool masked = __any_sync(0xffffffffu, key0 + kBN > pos || key0 < ka);
+        uint32_t bits[4];
+        if (masked && warp_rows) {
+          const TreeRow row = tree_row(p, g.b, g.s, node);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) bits[w] = tree_bits(row, key0 + 32 * w);
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kSFull + q), js & 1, p.wait_ns) && !stop());
         if (!ok) break;
         tc05::fence_after_sync();
-        const int key0 = g.s.first + (g.t0 + t) * kBN;
         const int vs = (u0 + 2 * t + 1) % kSlots;  // V's slot
         if (!kByte && (NT == 1 || q == 0) && (key0 + kBN > g.s.len || key0 < g.s.lo)) {
           // rows that no node reads may hold anything (NaN included): P = 0
@@ -566,41 +592,53 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           }
         }
         if (warp_rows) {
-          float s[kBN];
+          // The row's scores pass through registers 32 at a time, twice: for
+          // the maximum, then for the probabilities (tensor memory is read
+          // again, which costs less than 128 registers and a loop body four
+          // times as long: the instruction fetch of the unrolled form took
+          // microseconds at each unit's first tile). P of 32 keys takes 16
+          // columns, all of them read already.
+          const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff);
+          const float4* sk = reinterpret_cast<const float4*>(sc + ((u0 + 2 * t) % C::kScales) * kBN);
+          const float4* sv = reinterpret_cast<const float4*>(sc + ((u0 + 2 * t + 1) % C::kScales) * kBN);
+          auto scores = [&](int x, float (&s)[32]) {  // keys 32 x .. 32 x + 31, masked ones -inf
+            tc05::wait_ld();
+            tc05::reg_fence(s);
+            if constexpr (DT == kDtypeU8) {
 #pragma unroll
-          for (int x = 0; x < kBN; x += 32) tc05::ld_32x32b_x32(scol + x, *reinterpret_cast<float(*)[32]>(&s[x]));
-          tc05::wait_ld();
-#pragma unroll
-          for (int x = 0; x < kBN; x += 32) tc05::reg_fence(*reinterpret_cast<float(*)[32]>(&s[x]));
-          if constexpr (DT == kDtypeU8) {
-            const float4* sc = reinterpret_cast<const float4*>(smem + C::kScaleOff) + ((u0 + 2 * t) % C::kScales) * (kBN / 4);
-#pragma unroll
-            for (int x = 0; x < kBN / 4; ++x) {
-              const float4 f = sc[x];
-              const float2 a = mul2(make_float2(s[4 * x], s[4 * x + 1]), make_float2(f.x, f.y));
-              const float2 b = mul2(make_float2(s[4 * x + 2], s[4 * x + 3]), make_float2(f.z, f.w));
-              s[4 * x] = a.x, s[4 * x + 1] = a.y, s[4 * x + 2] = b.x, s[4 * x + 3] = b.y;
+              for (int i = 0; i < 8; ++i) {
+                const float4 f = sk[8 * x + i];
+                const float2 a = mul2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(f.x, f.y));
+                const float2 b = mul2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(f.z, f.w));
+                s[4 * i] = a.x, s[4 * i + 1] = a.y, s[4 * i + 2] = b.x, s[4 * i + 3] = b.y;
+              }
             }
-          }
-          // only tiles that reach a node, the end or the window are masked
-          if (key0 + kBN > g.s.pos || key0 < row.ka) {
+            if (masked) {
+              const uint32_t w = x < 2 ? (x == 0 ? bits[0] : bits[1]) : (x == 2 ? bits[2] : bits[3]);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t bits = tree_bits(row, key0 + 32 * w);
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (!((bits >> x) & 1u)) s[32 * w + x] = -INFINITY;
+              for (int i = 0; i < 32; ++i)
+                if (!((w >> i) & 1u)) s[i] = -INFINITY;
             }
+          };
+          float mt = -INFINITY;
+#pragma unroll 1
+          for (int x = 0; x < kBN / 32; x += 2) {
+            float s0[32], s1[32];
+            tc05::ld_32x32b_x32(scol + 32 * x, s0);
+            tc05::ld_32x32b_x32(scol + 32 * x + 32, s1);
+            scores(x, s0);
+            scores(x + 1, s1);
+            float mx[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx[i] = max3(s0[i], s0[8 + i], s0[16 + i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx[i] = max3(mx[i], s0[24 + i], s1[i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx[i] = max3(mx[i], s1[8 + i], s1[16 + i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], s1[24 + i]);
+            mt = max3(mt, max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], max3(mx[5], mx[6], mx[7])));
           }
-          float mx8[8];  // eight independent chains, two scores a step
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(s[i], s[8 + i]);
-#pragma unroll
-          for (int x = 16; x < kBN; x += 16) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mx8[i] = max3(mx8[i], s[x + i], s[x + 8 + i]);
-          }
-          const float mt = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
           // a new reference maximum only when the row's maximum grew by more than 2^8
           const bool grow = (mt - m_ref) * c > kRescaleLog2 || (m_ref == -INFINITY && mt != -INFINITY);
           const float m_new = grow ? mt : m_ref;
@@ -608,7 +646,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             // O is rescaled. The last product into O_q is done: it was issued
             // before this S_q, whose completion this thread has seen
             const float alpha = (grow && m_ref != -INFINITY) ? fast_exp2((m_ref - m_new) * c) : 1.f;
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < kD / 32; ++x) {
               float v[32];
               tc05::ld_32x32b_x32(ocol + x * 32, v);
@@ -623,30 +661,38 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           m_ref = m_new;
           const float e = m_ref == -INFINITY ? 0.f : -m_ref * c;
           float2 sm4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          if (DT == kDtypeU8)  // the V tile's scales
+          if (DT == kDtypeU8) {  // the V tile's scales
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kFull + vs), ((u0 + 2 * t + 1) / kSlots) & 1, p.wait_ns));
-          if (!ok) break;
-          const float4* sv =
-              reinterpret_cast<const float4*>(smem + C::kScaleOff) + ((u0 + 2 * t + 1) % C::kScales) * (kBN / 4);
+            if (!ok) break;
+          }
+          auto probs = [&](int x, const float (&s)[32]) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const int x = 64 * half + 2 * i;
-              const float2 d0 = fma2(make_float2(s[x], s[x + 1]), c, e), d1 = fma2(make_float2(s[x + 2], s[x + 3]), c, e);
+            for (int i = 0; i < 16; i += 2) {
+              const float2 d0 = fma2(make_float2(s[2 * i], s[2 * i + 1]), c, e);
+              const float2 d1 = fma2(make_float2(s[2 * i + 2], s[2 * i + 3]), c, e);
               float2 p0 = make_float2(fast_exp2(d0.x), fast_exp2(d0.y)), p1 = make_float2(fast_exp2(d1.x), fast_exp2(d1.y));
               sm4[i & 3] = add2(sm4[i & 3], p0);
               sm4[(i + 1) & 3] = add2(sm4[(i + 1) & 3], p1);
               if constexpr (DT == kDtypeU8) {
-                const float4 f = sv[x / 4];
+                const float4 f = sv[8 * x + i / 2];
                 p0 = mul2(p0, make_float2(f.x, f.y));
                 p1 = mul2(p1, make_float2(f.z, f.w));
               }
               pk[i] = pack_bf16x2(p0.x, p0.y);
               pk[i + 1] = pack_bf16x2(p1.x, p1.y);
             }
-            tc05::st_32x32b_x32_u(scol + 32 * half, pk);
+            tc05::st_32x32b_x16_u(scol + 16 * x, pk);
+          };
+#pragma unroll 1
+          for (int x = 0; x < kBN / 32; x += 2) {
+            float s0[32], s1[32];
+            tc05::ld_32x32b_x32(scol + 32 * x, s0);
+            tc05::ld_32x32b_x32(scol + 32 * x + 32, s1);
+            scores(x, s0);
+            scores(x + 1, s1);
+            probs(x, s0);
+            probs(x + 1, s1);
           }
           l += ((sm4[0].x + sm4[0].y) + (sm4[1].x + sm4[1].y)) + ((sm4[2].x + sm4[2].y) + (sm4[3].x + sm4[3].y));
           tc05::wait_st();
@@ -710,7 +756,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         if (NT == 2 || q == 0) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
           if (warp_rows) {
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < kD / 32; ++x) {
               float v[32];
               tc05::ld_32x32b_x32(ocol + x * 32, v);
@@ -734,7 +780,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           s_l[r] = l;
         }
         float w0 = 0.f, w1 = 0.f, inv = 1.f;
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x <= kD / 32; ++x) {
           if (q == 1 && x < kD / 32 && warp_rows) {
             float v[32];
@@ -782,7 +828,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         if (NT == 1) mbar_arrive(bar(C::kQFree));
       }
       if (!whole)
-        tree_arrive_merge<kD>(p, plan, g, rows_per_block, tid, 256, &s_flag, [] { named_bar_sync(1, 256); });
+        tree_arrive_merge<kD, 8>(p, plan, g, rows_per_block, tid, 256, &s_flag, [] { named_bar_sync(1, 256); });
       u0 += 2 * g.nt;
       ++seg;
     }

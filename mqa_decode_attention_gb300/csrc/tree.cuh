@@ -186,6 +186,13 @@ __device__ __forceinline__ uint32_t tree_bits(const TreeRow& r, int k0) {
   return v;
 }
 
+// The first key that node i (-1: none) of sequence b may attend to.
+__device__ __forceinline__ int tree_first_key(const TreeParams& p, int b, const TreeSeq& s, int i) {
+  if (p.window <= 0 || i < 0) return 0;
+  const long long ka = static_cast<long long>(s.pos) + max(p.depth[static_cast<long long>(b) * p.n + i], 0) + 1 - p.window;
+  return ka > 0 ? static_cast<int>(min(ka, static_cast<long long>(s.pos))) : 0;
+}
+
 // Row r (node i, -1: none) of a unit of sequence b.
 __device__ __forceinline__ TreeRow tree_row(const TreeParams& p, int b, const TreeSeq& s, int i) {
   TreeRow r;
@@ -207,9 +214,8 @@ __device__ __forceinline__ TreeRow tree_row(const TreeParams& p, int b, const Tr
     }
   if (p.window > 0) {
     const int32_t* depth = p.depth + static_cast<long long>(b) * p.n;
-    const long long at = static_cast<long long>(s.pos) + max(depth[i], 0);
-    const long long ka = at + 1 - p.window;
-    r.ka = ka > 0 ? static_cast<int>(min(ka, static_cast<long long>(s.pos))) : 0;
+    const long long ka = static_cast<long long>(s.pos) + max(depth[i], 0) + 1 - p.window;
+    r.ka = tree_first_key(p, b, s, i);
     for (int t = 0; t < s.nodes; ++t) {
       const bool far = static_cast<long long>(s.pos) + max(depth[t], 0) < ka;
 #pragma unroll
@@ -241,7 +247,7 @@ __device__ __forceinline__ long long tree_out_row(const TreeParams& p, const Tre
 // in and, when it was the unit's last, merges. `threads` threads call it, all
 // of them, `sync` is a barrier over them, `flag` a shared int of theirs, tid
 // their index. A warp takes a row at a time, a lane D / 32 of its values.
-template <int D, class Sync>
+template <int D, int kR, class Sync>
 __device__ __forceinline__ void tree_arrive_merge(const TreeParams& p, const TreePlan& pl, const TreeSegment& g,
                                                   int rows_per_block, int tid, int threads, volatile int* flag,
                                                   const Sync& sync) {
@@ -254,52 +260,72 @@ __device__ __forceinline__ void tree_arrive_merge(const TreeParams& p, const Tre
   __threadfence();  // the other blocks' partials, after the count
   const size_t size = tree_part_floats(rows_per_block, D);
   const int rows = min(rows_per_block, g.s.nodes * p.group - g.rb * rows_per_block);
-  const int warp = tid >> 5, lane = tid & 31;
+  const int warp = tid >> 5, lane = tid & 31, warps = threads / 32;
   constexpr int kV = D / 32;
   auto part = [&](int k) { return p.part + size * (k == 0 ? 2 * ca + 1 : 2 * (ca + k)); };
-  for (int r = warp; r < rows; r += threads / 32) {
-    float mx = -INFINITY;
-    for (int k = lane; k < m; k += 32) mx = fmaxf(mx, __ldcg(part(k) + static_cast<size_t>(rows_per_block) * D + r));
+  // A warp takes kR rows at a time and runs over the partials once, a running
+  // maximum for each row: the loads of all its rows' next partial are in
+  // flight together (row after row with the maximum found first, the merge
+  // of 256 rows took 50 us)
+  for (int r0 = warp; r0 < rows; r0 += kR * warps) {
+    float acc[kR][kV], mx[kR], l[kR];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    float acc[kV], l = 0.f;
+    for (int u = 0; u < kR; ++u) {
+      mx[u] = -INFINITY;
+      l[u] = 0.f;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) acc[v] = 0.f;
-    if (mx != -INFINITY) {
-#pragma unroll 2
-      for (int k = 0; k < m; ++k) {
-        const float* q = part(k);
-        const float mk = __ldcg(q + static_cast<size_t>(rows_per_block) * D + r);
-        const float lk = __ldcg(q + static_cast<size_t>(rows_per_block) * (D + 1) + r);
-        float ov[kV];
-        if constexpr (kV == 4) {
-          const float4 t = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(r) * D) + lane);
-          ov[0] = t.x, ov[1] = t.y, ov[2] = t.z, ov[3] = t.w;
+      for (int v = 0; v < kV; ++v) acc[u][v] = 0.f;
+    }
+#pragma unroll 1
+    for (int k = 0; k < m; ++k) {
+      const float* q = part(k);
+      float mk[kR], lk[kR], ov[kR][kV];
+#pragma unroll
+      for (int u = 0; u < kR; ++u) {
+        const int r = r0 + u * warps;
+        if (r < rows) {
+          mk[u] = __ldcg(q + static_cast<size_t>(rows_per_block) * D + r);
+          lk[u] = __ldcg(q + static_cast<size_t>(rows_per_block) * (D + 1) + r);
+          if constexpr (kV == 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(r) * D) + lane);
+            ov[u][0] = t.x, ov[u][1] = t.y, ov[u][2] = t.z, ov[u][3] = t.w;
+          } else {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(q + static_cast<size_t>(r) * D) + lane);
+            ov[u][0] = t.x, ov[u][1] = t.y;
+          }
         } else {
-          const float2 t = __ldcg(reinterpret_cast<const float2*>(q + static_cast<size_t>(r) * D) + lane);
-          ov[0] = t.x, ov[1] = t.y;
-        }
-        if (mk != -INFINITY) {  // (else no key of this part: its sums may be anything)
-          const float w = exp2f(mk - mx);
-          l = fmaf(w, lk, l);
-#pragma unroll
-          for (int v = 0; v < kV; ++v) acc[v] = fmaf(w, ov[v], acc[v]);
+          mk[u] = -INFINITY;
         }
       }
+#pragma unroll
+      for (int u = 0; u < kR; ++u)
+        if (mk[u] != -INFINITY) {  // (else no key of this part: its sums may be anything)
+          const float top = fmaxf(mx[u], mk[u]);
+          const float a = exp2f(mx[u] - top), w = exp2f(mk[u] - top);
+          mx[u] = top;
+          l[u] = fmaf(w, lk[u], a * l[u]);
+#pragma unroll
+          for (int v = 0; v < kV; ++v) acc[u][v] = fmaf(w, ov[u][v], a * acc[u][v]);
+        }
     }
-    const float inv = mx != -INFINITY ? 1.f / l : 0.f;
-    const long long o = tree_out_row(p, g, g.rb * rows_per_block + r);
-    if constexpr (kV == 4) {
-      tree_store4(p, o * D + 4 * lane, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-    } else if (p.out_dtype == kDtypeBf16) {
-      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + o * D + 2 * lane) =
-          pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    } else {
-      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o * D + 2 * lane) =
-          make_float2(acc[0] * inv, acc[1] * inv);
+#pragma unroll
+    for (int u = 0; u < kR; ++u) {
+      const int r = r0 + u * warps;
+      if (r >= rows) break;
+      const float inv = mx[u] != -INFINITY ? 1.f / l[u] : 0.f;
+      const long long o = tree_out_row(p, g, g.rb * rows_per_block + r);
+      if constexpr (kV == 4) {
+        tree_store4(p, o * D + 4 * lane, acc[u][0] * inv, acc[u][1] * inv, acc[u][2] * inv, acc[u][3] * inv);
+      } else if (p.out_dtype == kDtypeBf16) {
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + o * D + 2 * lane) =
+            pack_bf16x2(acc[u][0] * inv, acc[u][1] * inv);
+      } else {
+        *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o * D + 2 * lane) =
+            make_float2(acc[u][0] * inv, acc[u][1] * inv);
+      }
+      if (lane == 0 && p.lse_out != nullptr)
+        p.lse_out[o] = mx[u] != -INFINITY ? (mx[u] + log2f(l[u])) * 0.69314718055994530942f : -INFINITY;
     }
-    if (lane == 0 && p.lse_out != nullptr)
-      p.lse_out[o] = mx != -INFINITY ? (mx + log2f(l)) * 0.69314718055994530942f : -INFINITY;
   }
 }
 

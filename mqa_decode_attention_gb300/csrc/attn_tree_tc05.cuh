@@ -31,7 +31,7 @@
 // the first product, which at 256 rows is already half of what bounds the
 // kernel.
 //
-// One-byte caches: the loader's tiles are codes (16 KB), four converter warps
+// One-byte caches: the loader's tiles are codes (16 KB), eight converter warps
 // widen each to a bf16 tile -- exactly: an e5m2 value has 3 significant bits,
 // code - zero point is an integer up to 255 -- and, for uint8, put the rows'
 // scales beside it: a K scale multiplies its column of S, a V scale its
@@ -41,7 +41,7 @@
 // V rows whatever the cache holds, so that 0 * NaN never enters a sum.
 //
 // Warps: 0-3 and 4-7 softmax, 8 K / V loader (TMA), 9 MMA issue (one thread)
-// and tensor-memory allocation, 10 Q loader (TMA), 11 idle; 12-15 converters.
+// and tensor-memory allocation, 10 Q loader (TMA), 11 idle; 12-19 converters.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -66,15 +66,16 @@ constexpr uint32_t kColS = 0, kColO = 256;  // S / P of accumulator q at 128 q, 
 constexpr float kRescaleLog2 = 8.0f;
 
 // Registers: setmaxnreg moves them from the loader, MMA and converter warps
-// to the softmax warps; the shares add up to what the block is launched with.
+// to the softmax warps; the shares add up to no more than the block is launched
+// with.
 template <int NT, int DT>
 struct Cfg {
   static constexpr bool kByte = DT != kDtypeBf16;
-  static constexpr int kThreads = kByte ? 512 : 384;
-  static constexpr int kRegsLaunch = kByte ? 128 : 168;
-  static constexpr int kRegsSoftmax = kByte ? 200 : 216;
+  static constexpr int kThreads = kByte ? 640 : 384;
+  static constexpr int kRegsLaunch = kByte ? 96 : 168;
+  static constexpr int kRegsSoftmax = kByte ? 152 : 216;
   static constexpr int kRegsAux = kByte ? 56 : 72;
-  static_assert(kThreads * kRegsLaunch == 256 * kRegsSoftmax + (kThreads - 256) * kRegsAux, "register split");
+  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsAux <= kThreads * kRegsLaunch, "register split");
   static constexpr int kSlots = kByte ? (NT == 1 ? 4 : 3) : (NT == 1 ? 6 : 5);  // bf16 tiles
   static constexpr int kRaw = kByte ? (DT == kDtypeU8 ? 3 : 4) : 0;              // code tiles
   static constexpr int kQOff = 0;
@@ -102,7 +103,7 @@ struct Cfg {
   static constexpr int kDrain = kOFree + 1;
   static constexpr int kNBars = kDrain + 1;
   static_assert(kNBars * 8 + 4 <= 256, "barrier area");
-  static_assert(kSmemBytes + 1300 <= 227 * 1024, "shared memory (with the static part)");
+  static_assert(kSmemBytes + 1500 <= 227 * 1024, "shared memory (with the static part)");
 };
 
 __device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
@@ -145,24 +146,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Four e5m2 codes as two bf16 pairs. A code's exponent and mantissa bits put at
-// bf16's places read as the value times 2^-112 (subnormals too), which one
-// exact multiplication undoes; infinities and NaN go through half precision.
+// Four e5m2 codes as two bf16 pairs: a code is the high byte of an IEEE half.
 __device__ __forceinline__ uint2 widen_e5m2(uint32_t w) {
-  const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);  // code << 8, twice
-  uint2 r;
-  if (__vcmpgeu4(w & 0x7f7f7f7fu, 0x7c7c7c7cu) == 0u) {
-    const uint32_t a = (lo & 0x80008000u) | ((lo & 0x7f007f00u) >> 3);
-    const uint32_t b = (hi & 0x80008000u) | ((hi & 0x7f007f00u) >> 3);
-    const uint32_t k = 0x77807780u;  // 2^112
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(a), "r"(k));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(b), "r"(k));
-  } else {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    r = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
-  }
-  return r;
+  const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
 }
 // four uint8 codes minus the zero point (z = 2^23 + zero point)
 __device__ __forceinline__ uint2 widen_u8(uint32_t w, float z) {
@@ -171,6 +160,33 @@ __device__ __forceinline__ uint2 widen_u8(uint32_t w, float z) {
   const float f2 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7652)) - z;
   const float f3 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7653)) - z;
   return make_uint2(pack_bf16x2(f0, f1), pack_bf16x2(f2, f3));
+}
+
+// N lanes (aligned groups of 8 or 4) hold N pieces of four words each: lane i's
+// piece j goes to lane j's place i.
+template <int N>
+__device__ __forceinline__ void transpose16(uint32_t (&w)[4 * N], int lane) {
+#pragma unroll
+  for (int s = 1; s < N; s <<= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i & s) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t &a = w[4 * i + e], &b = w[4 * (i | s) + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, s);
+        if (up)
+          a = got;
+        else
+          b = got;
+      }
+    }
+  }
+}
+template <class T>
+__device__ __forceinline__ T* shfl_ptr(T* p, int src) {
+  return reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
 }
 
 template <int NT, bool PG, int DT>
@@ -191,6 +207,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   // next is written) and the walk that gives it, kept out of their registers
   __shared__ TreeWalk s_walk;
   __shared__ TreeSegment s_seg[2];
+  __shared__ TreeWalk s_mma_walk;  // the MMA thread's, for the same reason
+  __shared__ TreeSegment s_mma_seg;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -354,6 +372,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       constexpr uint32_t id_s = tc05::idesc_bf16_f32(kBM, kBN, false, false);
       constexpr uint32_t id_o = tc05::idesc_bf16_f32(kBM, kD, false, true);
       auto wait = [&](int id, int parity) {  // polls: a suspended wait wakes late
+        if (mbar_test(bar(id), parity & 1)) return true;
         const unsigned long long t0 = global_timer_ns();
         while (!mbar_test(bar(id), parity & 1))
           if (stop() || global_timer_ns() - t0 > p.wait_ns) return false;
@@ -386,11 +405,11 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       };
       auto free_k = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t) % kSlots)); };
       auto free_v = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t + 1) % kSlots)); };
-      TreeSegment g;
       bool ok = true;
       int seg = 0;
-      while (ok && walk.next(p, kBN, rows_per_block, g)) {
-        const int T = g.nt;
+      s_mma_walk = walk;
+      while (ok && s_mma_walk.next(p, kBN, rows_per_block, s_mma_seg)) {
+        const int T = s_mma_seg.nt;
         ok = wait(C::kQFull, seg) && full(u0);
         if (!ok) break;
         if constexpr (NT == 2) {
@@ -456,82 +475,83 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   } else if (kByte && warp >= 12) {
     regs_aux();
     // ---------------------------------------------------------- converters
-    // Thread r widens row r (key key0 + r) of every tile.
+    // Warps 12-15 widen the K tiles, 16-19 the V tiles: thread r row r (key
+    // key0 + r) of each. One group for both took 3-5 us a tile.
     if constexpr (kByte) {
-      const int r = tid - 384;
+      const int kv = warp >= 16 ? 1 : 0, r = (tid - 384) & 127;
+      const float2* szs = kv ? p.v_sz : p.k_sz;
       TreeSegment g;
       bool ok = true, waited = !p.early;
-      int u = 0;
+      int u = kv;
       while (ok && walk.next(p, kBN, rows_per_block, g)) {
         const int key_first = g.s.first + g.t0 * kBN;
         // uint8: the (scale, zero point) of this thread's row of a tile, zeros
         // where nothing may be read; requested a tile ahead
-        auto scales = [&](int t, float2* out) {
-          out[0] = out[1] = make_float2(0.f, 0.f);
-          if (DT != kDtypeU8 || t >= g.nt) return;
+        auto scale_of = [&](int t) {
+          const float2 none = make_float2(0.f, 0.f);
           const int key = key_first + t * kBN + r;
-          if (key < g.s.lo || key >= g.s.len) return;
+          if (DT != kDtypeU8 || t >= g.nt || key < g.s.lo || key >= g.s.len) return none;
           long long row;
           if constexpr (PG) {
             const int page = __ldg(p.block_table + static_cast<long long>(g.b) * p.max_pages + key / p.page_size);
-            if (page < 0 || page >= p.num_pages) return;
+            if (page < 0 || page >= p.num_pages) return none;
             row = (static_cast<long long>(page) * p.h_kv + g.j) * p.page_size + (key & (p.page_size - 1));
           } else {
             row = (static_cast<long long>(g.b) * p.h_kv + g.j) * p.capacity + key;
           }
-          // (plain loads: the append of this step may have written them)
-          out[0] = p.k_sz[row];
-          out[1] = p.v_sz[row];
+          return szs[row];  // (a plain load: the append of this step may have written it)
         };
-        float2 now[2], next[2];
-        if (DT == kDtypeU8 && !waited && key_first + kBN > g.s.pos) {
-          grid_dependency_wait();
-          waited = true;
-        }
-        scales(0, now);
-        for (int t = 0; t < g.nt && ok; ++t) {
-          const int key0 = key_first + t * kBN;
-          const bool live = key0 + r >= g.s.lo && key0 + r < g.s.len;
-          if (DT == kDtypeU8 && !waited && key0 + 2 * kBN > g.s.pos) {
+        auto appended = [&](int t) {  // before the scales of a tile that holds a node
+          if (DT == kDtypeU8 && !waited && key_first + (t + 1) * kBN > g.s.pos) {
             grid_dependency_wait();
             waited = true;
           }
-          scales(t + 1, next);
-          for (int kv = 0; kv < 2; ++kv, ++u) {
-            const int rs = u % kRaw, slot = u % kSlots;
-            ok = mbar_wait(bar(C::kRFull + rs), (u / kRaw) & 1, p.wait_ns) &&
-                 (u < kSlots || mbar_wait(bar(C::kEmpty + slot), (u / kSlots - 1) & 1, p.wait_ns));
-            if (!ok) fail(true);
-            ok = __all_sync(0xffffffffu, ok && !stop());
-            if (!ok) break;
-            const unsigned char* src = smem + C::kRawOff + rs * kRawBytes + r * 128;
-            unsigned char* dst = smem + C::kRingOff + slot * kTileBytes + r * 128;
-            const float z = 8388608.f + now[kv].y;
+        };
+        appended(0);
+        float2 now = scale_of(0);
+        for (int t = 0; t < g.nt; ++t, u += 2) {
+          const int key = key_first + t * kBN + r;
+          const bool live = key >= g.s.lo && key < g.s.len;
+          appended(t + 1);
+          const float2 next = scale_of(t + 1);
+          const int rs = u % kRaw, slot = u % kSlots;
+          ok = mbar_wait(bar(C::kRFull + rs), (u / kRaw) & 1, p.wait_ns) &&
+               (u < kSlots || mbar_wait(bar(C::kEmpty + slot), (u / kSlots - 1) & 1, p.wait_ns));
+          if (!ok) fail(true);
+          ok = __all_sync(0xffffffffu, ok && !stop());
+          if (!ok) break;
+          const unsigned char* src = smem + C::kRawOff + rs * kRawBytes + r * 128;
+          unsigned char* dst = smem + C::kRingOff + slot * kTileBytes + r * 128;
+          const float z = 8388608.f + now.y;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {  // 16 codes
-              uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ (r & 7)) << 4));
+          for (int c0 = 0; c0 < 8; c0 += 2) {  // 32 codes
+            uint4 w[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) w[x] = *reinterpret_cast<const uint4*>(src + (((c0 + x) ^ (r & 7)) << 4));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int c = c0 + x;
               uint2 a, b, e, f;
               if constexpr (DT == kDtypeU8) {
-                a = widen_u8(w.x, z), b = widen_u8(w.y, z), e = widen_u8(w.z, z), f = widen_u8(w.w, z);
+                a = widen_u8(w[x].x, z), b = widen_u8(w[x].y, z), e = widen_u8(w[x].z, z), f = widen_u8(w[x].w, z);
               } else {
-                a = widen_e5m2(w.x), b = widen_e5m2(w.y), e = widen_e5m2(w.z), f = widen_e5m2(w.w);
+                a = widen_e5m2(w[x].x), b = widen_e5m2(w[x].y), e = widen_e5m2(w[x].z), f = widen_e5m2(w[x].w);
               }
               if (!live) a = b = e = f = make_uint2(0u, 0u);
               unsigned char* d = dst + (c >> 2) * 16384;
               *reinterpret_cast<uint4*>(d + (((2 * c) & 7) ^ (r & 7)) * 16) = make_uint4(a.x, a.y, b.x, b.y);
               *reinterpret_cast<uint4*>(d + (((2 * c + 1) & 7) ^ (r & 7)) * 16) = make_uint4(e.x, e.y, f.x, f.y);
             }
-            if constexpr (DT == kDtypeU8)
-              reinterpret_cast<float*>(smem + C::kScaleOff)[(u % C::kScales) * kBN + r] = now[kv].x;
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(bar(C::kFull + slot));
-              mbar_arrive(bar(C::kREmpty + rs));
-            }
           }
-          now[0] = next[0];
-          now[1] = next[1];
+          if constexpr (DT == kDtypeU8)
+            reinterpret_cast<float*>(smem + C::kScaleOff)[(u % C::kScales) * kBN + r] = now.x;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(C::kFull + slot));
+            mbar_arrive(bar(C::kREmpty + rs));
+          }
+          now = next;
         }
       }
     }
@@ -716,30 +736,39 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       const int br = gr - g.rb * rows_per_block;  // row of the block
       long long orow = 0;
       if (live) orow = tree_out_row(p, g, gr);
-      auto put = [&](int x, const float* v, float inv) {  // 32 values from dim 32 x on
-        if (!live) return;
-        if (!whole) {
-          float* dst = part + static_cast<size_t>(br) * kD + 32 * x;
+      // 32 values of every row of the warp, from dim 32 x on, written so that
+      // neighbouring lanes write neighbouring 16 bytes of one row (a lane
+      // writing its own row touches 32 lines with every store: 256 rows took 6
+      // us): groups of 8 lanes (fp32: a row's 128 bytes; bf16, 4 lanes: 64)
+      // exchange their 16-byte pieces first.
+      auto put = [&](int x, float (&v)[32], float inv) {
+        if (!whole || p.out_dtype == kDtypeF32) {
+          float* base = whole ? static_cast<float*>(p.out) + orow * kD : part + static_cast<size_t>(br) * kD;
+          if (whole) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        } else if (p.out_dtype == kDtypeBf16) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + orow * kD + 32 * x;
+            for (int i = 0; i < 32; ++i) v[i] *= inv;
+          }
+          transpose16<8>(reinterpret_cast<uint32_t(&)[32]>(v), lane);
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint4 w;
-            w.x = pack_bf16x2(v[i] * inv, v[i + 1] * inv);
-            w.y = pack_bf16x2(v[i + 2] * inv, v[i + 3] * inv);
-            w.z = pack_bf16x2(v[i + 4] * inv, v[i + 5] * inv);
-            w.w = pack_bf16x2(v[i + 6] * inv, v[i + 7] * inv);
-            *reinterpret_cast<uint4*>(dst + i) = w;
+          for (int k = 0; k < 8; ++k) {  // the row of lane (group) + k
+            float* dst = shfl_ptr(live ? base : nullptr, (lane & ~7) + k);
+            if (dst != nullptr)
+              *reinterpret_cast<float4*>(dst + 32 * x + 4 * (lane & 7)) =
+                  make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
           }
         } else {
-          float* dst = static_cast<float*>(p.out) + orow * kD + 32 * x;
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(dst + i) =
-                make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+          for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+          transpose16<4>(w, lane);
+          __nv_bfloat16* base = static_cast<__nv_bfloat16*>(p.out) + orow * kD;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            __nv_bfloat16* dst = shfl_ptr(live ? base : nullptr, (lane & ~3) + k);
+            if (dst != nullptr)
+              *reinterpret_cast<uint4*>(dst + 32 * x + 8 * (lane & 3)) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
         }
       };
       auto put_ml = [&](float m2, float sum) {  // maximum (log2 domain) and sum

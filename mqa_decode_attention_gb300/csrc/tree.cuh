@@ -276,7 +276,7 @@ __device__ __forceinline__ void tree_arrive_merge(const TreeParams& p, const Tre
 #pragma unroll
       for (int v = 0; v < kV; ++v) acc[u][v] = 0.f;
     }
-#pragma unroll 1
+#pragma unroll 2
     for (int k = 0; k < m; ++k) {
       const float* q = part(k);
       float mk[kR], lk[kR], ov[kR][kV];

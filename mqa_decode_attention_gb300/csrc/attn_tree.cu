@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) attn_tree_kernel(const TreeParams p)
           part[kRows * (D + 1) + r] = l[h];
         }
       }
-      tree_arrive_merge<D, 4>(p, plan, g, kRows, tid, kThreads, &s_flag, [] { __syncthreads(); });
+      tree_arrive_merge<D, 4>(p, tree_merge(plan, g, blockIdx.x), g, kRows, tid, kThreads, &s_flag, [] { __syncthreads(); });
     }
   }
 }

@@ -64,6 +64,9 @@ constexpr int kRawBytes = kBN * kD;       // a code tile: [128 rows][128 B], swi
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // S / P of accumulator q at 128 q, its O at 256 + 128 q
 constexpr float kRescaleLog2 = 8.0f;
+// parts of a unit up to which its last block merges them row by row on the way
+// out (more: warp by warp over the rows, every partial's loads in flight)
+constexpr int kDirectParts = 4;
 
 // Registers: setmaxnreg moves them from the loader, MMA and converter warps
 // to the softmax warps; the shares add up to no more than the block is launched
@@ -97,8 +100,9 @@ struct Cfg {
   static constexpr int kRFull = kEmpty + kSlots;    // [kRaw]
   static constexpr int kREmpty = kRFull + kRaw;     // [kRaw]
   static constexpr int kSFull = kREmpty + kRaw;     // [2]
-  static constexpr int kP = kSFull + 2;             // [2]
-  static constexpr int kODone = kP + 2;
+  static constexpr int kP = kSFull + 2;             // [2] keys 0-63 of P written
+  static constexpr int kPHi = kP + 2;               // [2] keys 64-127
+  static constexpr int kODone = kPHi + 2;
   static constexpr int kOFree = kODone + 1;
   static constexpr int kDrain = kOFree + 1;
   static constexpr int kNBars = kDrain + 1;
@@ -234,6 +238,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     for (int q = 0; q < 2; ++q) {
       mbar_init(bar(C::kSFull + q), 1);
       mbar_init(bar(C::kP + q), 4);
+      mbar_init(bar(C::kPHi + q), 4);
     }
     mbar_init(bar(C::kODone), 1);
     mbar_init(bar(C::kOFree), 8);
@@ -394,14 +399,23 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         }
         tc05::commit(bar(C::kSFull + q));
       };
-      auto issue_pv = [&](int q, int t, bool add) {  // O_q (+)= P_q V(t)
+      // O_q (+)= P_q V(t) of keys 64 h .. 64 h + 63: each half of P as soon as it is written
+      auto issue_pv = [&](int q, int t, int h, bool add) {
         const uint32_t v_s = sbase + C::kRingOff + ((u0 + 2 * t + 1) % kSlots) * kTileBytes;
         tc05::fence_after_sync();
-        const uint64_t vd = tc05::smem_desc_sw128(v_s, 16384, 1024);
+        const uint64_t vd = tc05::smem_desc_sw128(v_s + h * 8192, 16384, 1024);
+        const uint32_t pa = tmem + kColS + q * 128 + h * 32;
 #pragma unroll
-        for (int ks = 0; ks < kBN / 16; ++ks)
-          tc05::mma_bf16_ta(tmem + kColO + q * 128, tmem + kColS + q * 128 + ks * 8, vd + ((ks * 2048) >> 4), id_o,
-                            add || ks > 0);
+        for (int ks = 0; ks < kBN / 32; ++ks)
+          tc05::mma_bf16_ta(tmem + kColO + q * 128, pa + ks * 8, vd + ((ks * 2048) >> 4), id_o, add || h > 0 || ks > 0);
+      };
+      auto pv = [&](int q, int t, bool add) {
+        const int n = ps[q]++;
+        if (!wait(C::kP + q, n) || !full(u0 + 2 * t + 1)) return false;
+        issue_pv(q, t, 0, add);
+        if (!wait(C::kPHi + q, n)) return false;
+        issue_pv(q, t, 1, add);
+        return true;
       };
       auto free_k = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t) % kSlots)); };
       auto free_v = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t + 1) % kSlots)); };
@@ -421,17 +435,15 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           // segment held, was free at its last product)
           if (seg > 0) ok = wait(C::kOFree, seg - 1);
           for (int t = 0; ok && t < T; ++t) {
-            ok = wait(C::kP + 0, ps[0]++) && full(u0 + 2 * t + 1);
+            ok = pv(0, t, t > 0);
             if (!ok) break;
-            issue_pv(0, t, t > 0);
             if (t + 1 < T) {
               ok = full(u0 + 2 * t + 2);
               if (!ok) break;
               issue_s(0, t + 1);
             }
-            ok = wait(C::kP + 1, ps[1]++);
+            ok = pv(1, t, t > 0);
             if (!ok) break;
-            issue_pv(1, t, t > 0);
             free_v(t);
             if (t + 1 < T) {
               issue_s(1, t + 1);
@@ -451,9 +463,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           if (seg > 0) ok = wait(C::kOFree, seg - 1);
           for (int t = 0; ok && t < T; ++t) {
             const int q = t & 1;
-            ok = wait(C::kP + q, ps[q]++) && full(u0 + 2 * t + 1);
+            ok = pv(q, t, t > 1);
             if (!ok) break;
-            issue_pv(q, t, t > 1);
             free_v(t);
             if (t + 2 < T) {
               ok = full(u0 + 2 * t + 4);
@@ -713,13 +724,20 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             scores(x + 1, s1);
             probs(x, s0);
             probs(x + 1, s1);
+            // these 64 keys' P is in tensor memory: their products may start
+            tc05::wait_st();
+            tc05::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar((x == 0 ? C::kP : C::kPHi) + q));
           }
           l += ((sm4[0].x + sm4[0].y) + (sm4[1].x + sm4[1].y)) + ((sm4[2].x + sm4[2].y) + (sm4[3].x + sm4[3].y));
-          tc05::wait_st();
-          tc05::fence_before_sync();
+        } else {  // no rows here: the arrivals that the products wait for
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(C::kP + q));
+            mbar_arrive(bar(C::kPHi + q));
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::kP + q));
       }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kODone), seg & 1, p.wait_ns) && !stop());
       if (!ok && lane == 0) fail(true);
@@ -730,8 +748,23 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         grid_dependency_wait();
         waited = true;
       }
-      // ---- the segment's result: this thread's row, O unnormalised in v
-      const bool whole = g.head && g.tail;
+      // ---- the segment's result: this thread's row, O unnormalised in v.
+      // A part of a unit whose other parts are all there already is merged
+      // with them on the way out (each thread its own row); else it is left
+      // in the workspace, and the unit's last block merges.
+      bool whole = g.head && g.tail, direct = false;
+      TreeMerge mg = {0, 1, 0};
+      if (!whole) {
+        mg = tree_merge(plan, g, blockIdx.x);
+        if (tid == 0) {
+          int seen;
+          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(p.arrived + mg.ca) : "memory");
+          s_flag = mg.m <= kDirectParts && seen == mg.m - 1;
+        }
+        named_bar_sync(1, 256);
+        direct = whole = s_flag != 0;
+        if (direct) __threadfence();
+      }
       float* part = p.part + tree_part_floats(rows_per_block, kD) * (2 * static_cast<size_t>(blockIdx.x) + (g.head ? 1 : 0));
       const int br = gr - g.rb * rows_per_block;  // row of the block
       long long orow = 0;
@@ -771,6 +804,58 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           }
         }
       };
+      // direct: the row's maximum and sum over all parts, and this part's weight
+      float m_all = -INFINITY, w_own = 1.f;
+      auto meet = [&](float m2, float sum) {
+        m_all = m2;
+        for (int k = 0; k < mg.m; ++k)
+          if (k != mg.own && live)
+            m_all = fmaxf(m_all, __ldcg(tree_part(p, mg, k, rows_per_block, kD) + static_cast<size_t>(rows_per_block) * kD + br));
+        w_own = m2 != -INFINITY ? exp2f(m2 - m_all) : 0.f;
+        float total = 0.f;
+        for (int k = 0; k < mg.m; ++k) {
+          float mk = m2, lk = sum;
+          if (k != mg.own && live) {
+            const float* ml = tree_part(p, mg, k, rows_per_block, kD) + static_cast<size_t>(rows_per_block) * kD + br;
+            mk = __ldcg(ml);
+            lk = __ldcg(ml + rows_per_block);
+          }
+          if (mk != -INFINITY) total = fmaf(exp2f(mk - m_all), lk, total);
+        }
+        return total;
+      };
+      auto join = [&](int x, float (&v)[32]) {  // dims 32 x .. of the whole unit's sums
+        float acc[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < mg.m; ++k) {
+          if (k == mg.own) {
+            if (w_own > 0.f) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[i] = fmaf(w_own, v[i], acc[i]);
+            }
+            continue;
+          }
+          const float* q = tree_part(p, mg, k, rows_per_block, kD);
+          float o[32];
+          const int top = br - (lane & 7);  // the group's first row of the block
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // as put() writes: neighbouring lanes, neighbouring pieces
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(min(top + i, rows_per_block - 1)) * kD + 32 * x) + (lane & 7));
+            o[4 * i] = f.x, o[4 * i + 1] = f.y, o[4 * i + 2] = f.z, o[4 * i + 3] = f.w;
+          }
+          const float mk = live ? __ldcg(q + static_cast<size_t>(rows_per_block) * kD + br) : -INFINITY;
+          transpose16<8>(reinterpret_cast<uint32_t(&)[32]>(o), lane);
+          if (mk != -INFINITY) {
+            const float w = exp2f(mk - m_all);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i] = fmaf(w, o[i], acc[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = acc[i];
+      };
       auto put_ml = [&](float m2, float sum) {  // maximum (log2 domain) and sum
         if (!live) return;
         if (!whole) {
@@ -783,6 +868,10 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c;
       if (NT == 2 || g.nt == 1) {
         if (NT == 2 || q == 0) {
+          if (direct) {
+            l = meet(m2, l);
+            m2 = m_all;
+          }
           const float inv = l > 0.f ? 1.f / l : 0.f;
           if (warp_rows) {
 #pragma unroll 1
@@ -791,6 +880,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
               tc05::ld_32x32b_x32(ocol + x * 32, v);
               tc05::wait_ld();
               tc05::reg_fence(v);
+              if (direct) join(x, v);
               put(x, v, inv);
             }
           }
@@ -828,6 +918,10 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
               }
               l = w0 * l + w1 * lo;
               m2 = mx;
+              if (direct) {
+                l = meet(m2, l);
+                m2 = m_all;
+              }
               if (whole) inv = l > 0.f ? 1.f / l : 0.f;
             }
             float v[32];
@@ -842,6 +936,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
               v[4 * i + 2] = fmaf(w1, o.z, w0 * v[4 * i + 2]);
               v[4 * i + 3] = fmaf(w1, o.w, w0 * v[4 * i + 3]);
             }
+            if (direct) join(x - 1, v);
             put(x - 1, v, inv);
           }
           if (x < kD / 32) named_bar_sync(1, 256);
@@ -857,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         if (NT == 1) mbar_arrive(bar(C::kQFree));
       }
       if (!whole)
-        tree_arrive_merge<kD, 8>(p, plan, g, rows_per_block, tid, 256, &s_flag, [] { named_bar_sync(1, 256); });
+        tree_arrive_merge<kD, 4>(p, mg, g, rows_per_block, tid, 256, &s_flag, [] { named_bar_sync(1, 256); });
       u0 += 2 * g.nt;
       ++seg;
     }

@@ -243,77 +243,86 @@ __device__ __forceinline__ long long tree_out_row(const TreeParams& p, const Tre
   return (static_cast<long long>(g.b) * p.n + i) * p.h_q + g.j * p.group + (row - i * p.group);
 }
 
+// A unit's merge: with M the largest of its partials' maxima,
+//   O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,
+// summed in block order k = 0 .. m - 1 whichever block merges, so that the
+// bits do not depend on who comes last.
+struct TreeMerge {
+  int ca, m, own;  // the unit's first block, its blocks, this block among them
+};
+__device__ __forceinline__ TreeMerge tree_merge(const TreePlan& pl, const TreeSegment& g, int cta) {
+  const int ca = tree_cta_of(pl, g.u0), cb = tree_cta_of(pl, g.u0 + g.s.tiles - 1);
+  return {ca, cb - ca + 1, cta - ca};
+}
+__device__ __forceinline__ const float* tree_part(const TreeParams& p, const TreeMerge& mg, int k, int rows, int d) {
+  return p.part + tree_part_floats(rows, d) * (k == 0 ? 2 * mg.ca + 1 : 2 * (mg.ca + k));
+}
+
 // After a block has written its partial of segment g (every thread): counts it
 // in and, when it was the unit's last, merges. `threads` threads call it, all
 // of them, `sync` is a barrier over them, `flag` a shared int of theirs, tid
-// their index. A warp takes a row at a time, a lane D / 32 of its values.
+// their index. A warp takes kR rows at a time, a lane D / 32 of a row's values;
+// the loads of all its rows' partials are in flight together.
 template <int D, int kR, class Sync>
-__device__ __forceinline__ void tree_arrive_merge(const TreeParams& p, const TreePlan& pl, const TreeSegment& g,
+__device__ __forceinline__ void tree_arrive_merge(const TreeParams& p, const TreeMerge& mg, const TreeSegment& g,
                                                   int rows_per_block, int tid, int threads, volatile int* flag,
                                                   const Sync& sync) {
-  const int ca = tree_cta_of(pl, g.u0), cb = tree_cta_of(pl, g.u0 + g.s.tiles - 1), m = cb - ca + 1;
   __threadfence();  // this thread's part of the partial, before the count
   sync();
-  if (tid == 0) *flag = atomicAdd(p.arrived + ca, 1) == m - 1;
+  if (tid == 0) *flag = atomicAdd(p.arrived + mg.ca, 1) == mg.m - 1;
   sync();
   if (*flag == 0) return;
   __threadfence();  // the other blocks' partials, after the count
-  const size_t size = tree_part_floats(rows_per_block, D);
   const int rows = min(rows_per_block, g.s.nodes * p.group - g.rb * rows_per_block);
   const int warp = tid >> 5, lane = tid & 31, warps = threads / 32;
   constexpr int kV = D / 32;
-  auto part = [&](int k) { return p.part + size * (k == 0 ? 2 * ca + 1 : 2 * (ca + k)); };
-  // A warp takes kR rows at a time and runs over the partials once, a running
-  // maximum for each row: the loads of all its rows' next partial are in
-  // flight together (row after row with the maximum found first, the merge
-  // of 256 rows took 50 us)
   for (int r0 = warp; r0 < rows; r0 += kR * warps) {
+    int row[kR];  // (rows past the end repeat the last one)
     float acc[kR][kV], mx[kR], l[kR];
 #pragma unroll
     for (int u = 0; u < kR; ++u) {
+      row[u] = min(r0 + u * warps, rows - 1);
       mx[u] = -INFINITY;
       l[u] = 0.f;
 #pragma unroll
       for (int v = 0; v < kV; ++v) acc[u][v] = 0.f;
     }
 #pragma unroll 2
-    for (int k = 0; k < m; ++k) {
-      const float* q = part(k);
+    for (int k = 0; k < mg.m; ++k) {
+      const float* q = tree_part(p, mg, k, rows_per_block, D) + static_cast<size_t>(rows_per_block) * D;
+#pragma unroll
+      for (int u = 0; u < kR; ++u) mx[u] = fmaxf(mx[u], __ldcg(q + row[u]));
+    }
+#pragma unroll 2
+    for (int k = 0; k < mg.m; ++k) {
+      const float* q = tree_part(p, mg, k, rows_per_block, D);
       float mk[kR], lk[kR], ov[kR][kV];
 #pragma unroll
       for (int u = 0; u < kR; ++u) {
-        const int r = r0 + u * warps;
-        if (r < rows) {
-          mk[u] = __ldcg(q + static_cast<size_t>(rows_per_block) * D + r);
-          lk[u] = __ldcg(q + static_cast<size_t>(rows_per_block) * (D + 1) + r);
-          if constexpr (kV == 4) {
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(r) * D) + lane);
-            ov[u][0] = t.x, ov[u][1] = t.y, ov[u][2] = t.z, ov[u][3] = t.w;
-          } else {
-            const float2 t = __ldcg(reinterpret_cast<const float2*>(q + static_cast<size_t>(r) * D) + lane);
-            ov[u][0] = t.x, ov[u][1] = t.y;
-          }
+        mk[u] = __ldcg(q + static_cast<size_t>(rows_per_block) * D + row[u]);
+        lk[u] = __ldcg(q + static_cast<size_t>(rows_per_block) * (D + 1) + row[u]);
+        if constexpr (kV == 4) {
+          const float4 t = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(row[u]) * D) + lane);
+          ov[u][0] = t.x, ov[u][1] = t.y, ov[u][2] = t.z, ov[u][3] = t.w;
         } else {
-          mk[u] = -INFINITY;
+          const float2 t = __ldcg(reinterpret_cast<const float2*>(q + static_cast<size_t>(row[u]) * D) + lane);
+          ov[u][0] = t.x, ov[u][1] = t.y;
         }
       }
 #pragma unroll
       for (int u = 0; u < kR; ++u)
         if (mk[u] != -INFINITY) {  // (else no key of this part: its sums may be anything)
-          const float top = fmaxf(mx[u], mk[u]);
-          const float a = exp2f(mx[u] - top), w = exp2f(mk[u] - top);
-          mx[u] = top;
-          l[u] = fmaf(w, lk[u], a * l[u]);
+          const float w = exp2f(mk[u] - mx[u]);
+          l[u] = fmaf(w, lk[u], l[u]);
 #pragma unroll
-          for (int v = 0; v < kV; ++v) acc[u][v] = fmaf(w, ov[u][v], a * acc[u][v]);
+          for (int v = 0; v < kV; ++v) acc[u][v] = fmaf(w, ov[u][v], acc[u][v]);
         }
     }
 #pragma unroll
     for (int u = 0; u < kR; ++u) {
-      const int r = r0 + u * warps;
-      if (r >= rows) break;
+      if (r0 + u * warps >= rows) break;
       const float inv = mx[u] != -INFINITY ? 1.f / l[u] : 0.f;
-      const long long o = tree_out_row(p, g, g.rb * rows_per_block + r);
+      const long long o = tree_out_row(p, g, g.rb * rows_per_block + row[u]);
       if constexpr (kV == 4) {
         tree_store4(p, o * D + 4 * lane, acc[u][0] * inv, acc[u][1] * inv, acc[u][2] * inv, acc[u][3] * inv);
       } else if (p.out_dtype == kDtypeBf16) {

@@ -322,19 +322,22 @@ __global__ void __launch_bounds__(kThreads) attn_tree_kernel(const TreeParams p)
           p.lse_out[orow] = l[h] > 0.f ? (m[h] * c + log2f(l[h])) * 0.69314718055994530942f : -INFINITY;
       }
     } else {
-      float* part = p.part + tree_part_floats(kRows, D) * (2 * blockIdx.x + (g.head ? 1 : 0));
+      float* part = tree_place(p, g, blockIdx.x, kRows, D);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = 16 * warp + (lane >> 2) + 8 * h;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<float2*>(part + r * D + 8 * i + (lane & 3) * 2) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+        for (int i = 0; i < D / 8; ++i)  // columns 8 i + 2 (lane % 4): half of piece 2 i + (lane % 4) / 2
+          *reinterpret_cast<float2*>(part + ((2 * i + ((lane & 3) >> 1)) * kRows + r) * 4 + (lane & 1) * 2) =
+              make_float2(o[i][2 * h], o[i][2 * h + 1]);
         if ((lane & 3) == 0) {
           part[kRows * D + r] = m[h] == -INFINITY ? -INFINITY : m[h] * c;
           part[kRows * (D + 1) + r] = l[h];
         }
       }
-      tree_arrive_merge<D, 4>(p, tree_merge(plan, g, blockIdx.x), g, kRows, tid, kThreads, &s_flag, [] { __syncthreads(); });
+      const TreeMerge mg = tree_merge(plan, g);
+      if (tree_arrive(p, mg, tid, &s_flag, [] { __syncthreads(); }))
+        tree_merge_rows<D>(p, mg, g, kRows, tid, kThreads);
     }
   }
 }

@@ -64,9 +64,6 @@ constexpr int kRawBytes = kBN * kD;       // a code tile: [128 rows][128 B], swi
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // S / P of accumulator q at 128 q, its O at 256 + 128 q
 constexpr float kRescaleLog2 = 8.0f;
-// parts of a unit up to which its last block merges them row by row on the way
-// out (more: warp by warp over the rows, every partial's loads in flight)
-constexpr int kDirectParts = 4;
 
 // Registers: setmaxnreg moves them from the loader, MMA and converter warps
 // to the softmax warps; the shares add up to no more than the block is launched
@@ -94,8 +91,9 @@ struct Cfg {
   static constexpr int kSmemBytes = kBarOff + 256 + 1024;  // + alignment slack
   // mbarriers
   static constexpr int kQFull = 0;
-  static constexpr int kQFree = 1;
-  static constexpr int kFull = 2;                   // [kSlots]
+  static constexpr int kQFree = 1;                  // a segment of two row tiles is done with Q
+  static constexpr int kXFree = 2;                  // one of one row tile: its accumulators have met
+  static constexpr int kFull = 3;                   // [kSlots]
   static constexpr int kEmpty = kFull + kSlots;     // [kSlots]
   static constexpr int kRFull = kEmpty + kSlots;    // [kRaw]
   static constexpr int kREmpty = kRFull + kRaw;     // [kRaw]
@@ -104,7 +102,8 @@ struct Cfg {
   static constexpr int kPHi = kP + 2;               // [2] keys 64-127
   static constexpr int kODone = kPHi + 2;
   static constexpr int kOFree = kODone + 1;
-  static constexpr int kDrain = kOFree + 1;
+  static constexpr int kPart = kOFree + 1;  // a partial result is written
+  static constexpr int kDrain = kPart + 1;
   static constexpr int kNBars = kDrain + 1;
   static_assert(kNBars * 8 + 4 <= 256, "barrier area");
   static_assert(kSmemBytes + 1500 <= 227 * 1024, "shared memory (with the static part)");
@@ -188,11 +187,6 @@ __device__ __forceinline__ void transpose16(uint32_t (&w)[4 * N], int lane) {
     }
   }
 }
-template <class T>
-__device__ __forceinline__ T* shfl_ptr(T* p, int src) {
-  return reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
-}
-
 template <int NT, bool PG, int DT>
 __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     attn_tree_tc05_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -205,12 +199,12 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + C::kNBars * 8);
   __shared__ TreePlan plan;
-  __shared__ int s_abort, s_skip, s_flag, s_more[2];
+  __shared__ int s_abort, s_skip, s_flag, s_pending, s_more[2], s_last[2];
   __shared__ float s_m[kBM], s_l[kBM];
   // the softmax warps' segment (two places: one may still be read while the
   // next is written) and the walk that gives it, kept out of their registers
   __shared__ TreeWalk s_walk;
-  __shared__ TreeSegment s_seg[2];
+  __shared__ TreeSegment s_seg[2], s_first;
   __shared__ TreeWalk s_mma_walk;  // the MMA thread's, for the same reason
   __shared__ TreeSegment s_mma_seg;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -224,7 +218,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     // an earlier block timed out: the result is invalid already
     s_skip = (*reinterpret_cast<volatile int32_t*>(p.err) & static_cast<int>(MQA_DEVERR_TIMEOUT)) ? 1 : 0;
     mbar_init(bar(C::kQFull), 1);
-    mbar_init(bar(C::kQFree), NT == 1 ? 8 : 1);
+    mbar_init(bar(C::kQFree), 1);
+    mbar_init(bar(C::kXFree), 8);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(C::kFull + s), kByte ? 4 : 1);
       mbar_init(bar(C::kEmpty + s), 1);
@@ -242,6 +237,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     }
     mbar_init(bar(C::kODone), 1);
     mbar_init(bar(C::kOFree), 8);
+    mbar_init(bar(C::kPart), 8);
     mbar_init(bar(C::kDrain), 1);
     fence_mbar_init();
   }
@@ -262,6 +258,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       atomicOr(p.err, static_cast<int>(MQA_DEVERR_TIMEOUT));
     }
   };
+  // whether a segment's rows need both accumulators (else both hold them all)
+  auto is_two = [&](const TreeSegment& g) { return NT == 2 && g.s.nodes * G - g.rb * rows_per_block > acc_rows; };
   auto stop = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
   auto regs_aux = [&]() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsAux)); };
   TreeWalk walk;
@@ -353,15 +351,24 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     if (lane == 0) {
       if (p.early) grid_dependency_wait();
       TreeSegment g;
-      bool ok = true;
-      int seg = 0;
+      bool ok = true, last_two = false;
+      int seg = 0, n_two = 0;
       while (ok && walk.next(p, kBN, rows_per_block, g)) {
-        if (seg > 0) ok = mbar_wait(bar(C::kQFree), (seg - 1) & 1, p.wait_ns);
+        // the Q area is free when the last segment's products with Q are done
+        // or, with one row tile, when its accumulators have met there (a
+        // barrier for each kind: every phase of it is waited for, so that a
+        // parity never stands for an older phase)
+        if (seg > 0)
+          ok = last_two ? mbar_wait(bar(C::kQFree), (n_two - 1) & 1, p.wait_ns)
+                        : mbar_wait(bar(C::kXFree), (seg - n_two - 1) & 1, p.wait_ns);
         if (!ok) fail(true);
         if (!ok || stop()) break;
+        last_two = is_two(g);
+        n_two += last_two;
+        const int tiles = last_two ? 2 : 1;
         // (tokens past the sequence's belong to the next: rows nobody uses)
-        mbar_arrive_expect_tx(bar(C::kQFull), NT * acc_rows * kD * 2);
-        for (int q = 0; q < NT; ++q)
+        mbar_arrive_expect_tx(bar(C::kQFull), tiles * acc_rows * kD * 2);
+        for (int q = 0; q < tiles; ++q)
           for (int h = 0; h < 2; ++h)
             tma_load_3d(sbase + C::kQOff + q * kTileBytes + h * 16384, &tmap_q, 64 * h, g.j * G,
                         g.b * p.n + (g.rb * NT + q) * p.tokens_per_tile, bar(C::kQFull));
@@ -386,8 +393,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       int u0 = 0;            // the segment's first load
       int ps[2] = {0, 0};    // products P V issued into each accumulator
       auto full = [&](int u) { return wait(C::kFull + u % kSlots, u / kSlots); };
-      auto issue_s = [&](int q, int t) {  // S_q = Q K(t)^T
-        const uint32_t q_s = sbase + C::kQOff + (NT == 2 ? q * kTileBytes : 0);
+      auto issue_s = [&](int q, int t, int qt) {  // S_q = Q K(t)^T, Q's row tile qt
+        const uint32_t q_s = sbase + C::kQOff + qt * kTileBytes;
         const uint32_t k_s = sbase + C::kRingOff + ((u0 + 2 * t) % kSlots) * kTileBytes;
         tc05::fence_after_sync();
         // (the descriptors' address field counts 16 bytes: the sub-tiles are constant steps)
@@ -426,41 +433,41 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         const int T = s_mma_seg.nt;
         ok = wait(C::kQFull, seg) && full(u0);
         if (!ok) break;
-        if constexpr (NT == 2) {
-          issue_s(0, 0);
-          issue_s(1, 0);
-          free_k(0);
+        const bool two = is_two(s_mma_seg);
+        issue_s(0, 0, 0);
+        if (two) {
+          issue_s(1, 0, 1);
           if (T == 1) tc05::commit(bar(C::kQFree));
-          // O of the last segment has been read (S, which P of the last
-          // segment held, was free at its last product)
-          if (seg > 0) ok = wait(C::kOFree, seg - 1);
+        }
+        free_k(0);
+        if (!two && T > 1) {
+          ok = full(u0 + 2);
+          if (!ok) break;
+          issue_s(1, 1, 0);
+          free_k(1);
+        }
+        // O of the last segment has been read (S, which P of the last segment
+        // held, was free at its last product)
+        if (seg > 0) ok = wait(C::kOFree, seg - 1);
+        if (two) {
           for (int t = 0; ok && t < T; ++t) {
             ok = pv(0, t, t > 0);
             if (!ok) break;
             if (t + 1 < T) {
               ok = full(u0 + 2 * t + 2);
               if (!ok) break;
-              issue_s(0, t + 1);
+              issue_s(0, t + 1, 0);
             }
             ok = pv(1, t, t > 0);
             if (!ok) break;
             free_v(t);
             if (t + 1 < T) {
-              issue_s(1, t + 1);
+              issue_s(1, t + 1, 1);
               free_k(t + 1);
               if (t + 2 == T) tc05::commit(bar(C::kQFree));
             }
           }
         } else {
-          issue_s(0, 0);
-          free_k(0);
-          if (T > 1) {
-            ok = full(u0 + 2);
-            if (!ok) break;
-            issue_s(1, 1);
-            free_k(1);
-          }
-          if (seg > 0) ok = wait(C::kOFree, seg - 1);
           for (int t = 0; ok && t < T; ++t) {
             const int q = t & 1;
             ok = pv(q, t, t > 1);
@@ -469,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             if (t + 2 < T) {
               ok = full(u0 + 2 * t + 4);
               if (!ok) break;
-              issue_s(q, t + 2);
+              issue_s(q, t + 2, 0);
               free_k(t + 2);
             }
           }
@@ -483,6 +490,27 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     __syncwarp();
   } else if (warp == 11) {
     regs_aux();
+    // ---------------------------------------------------- a partial's arrival
+    // Of a block's segments only the first and the last can be parts of a
+    // unit. The first one's partial, when others follow, is counted in here:
+    // the softmax warps go on to the next unit meanwhile (waiting for their
+    // writes and the counter cost them 2 us). Should the unit be complete with
+    // it -- its other blocks as a rule end later -- the softmax warps merge it
+    // after their last segment.
+    TreeSegment g;
+    bool complete = false;
+    if (walk.next(p, kBN, rows_per_block, g) && !(g.head && g.tail) && walk.at < walk.end) {
+      bool ok = mbar_wait(bar(C::kPart), 0, p.wait_ns);
+      if (!ok) fail(lane == 0);
+      if (ok && !stop() && lane == 0) {
+        const TreeMerge mg = tree_merge(plan, g);
+        __threadfence();  // the partial (seen through the barrier), before the count
+        complete = atomicAdd(p.arrived + mg.ca, 1) == mg.m - 1;
+        __threadfence();  // the other blocks' partials, after it
+      }
+    }
+    if (lane == 0) s_pending = complete;
+    named_bar_sync(3, 256 + 32);
   } else if (kByte && warp >= 12) {
     regs_aux();
     // ---------------------------------------------------------- converters
@@ -576,22 +604,27 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     const bool warp_rows = (warp & 3) * 32 < acc_rows;  // some lane of this warp holds a row
     bool waited = !p.early;
     int u0 = 0, seg = 0, js = 0;  // first load of the segment; segments; tiles of this accumulator
-    bool ok = true;
+    bool ok = true, aborted = false;
     if (tid == 0) s_walk = walk;
     while (true) {
-      if (tid == 0) s_more[seg & 1] = s_walk.next(p, kBN, rows_per_block, s_seg[seg & 1]);
+      if (tid == 0) {
+        s_more[seg & 1] = s_walk.next(p, kBN, rows_per_block, s_seg[seg & 1]);
+        s_last[seg & 1] = s_walk.at >= s_walk.end;
+      }
       named_bar_sync(1, 256);
       if (!s_more[seg & 1]) break;
       const TreeSegment& g = s_seg[seg & 1];
-      const int gr = g.rb * rows_per_block + (NT == 2 ? q * acc_rows : 0) + r;  // row of the unit's kv head
+      const bool two = is_two(g);
+      const int step = two ? 1 : 2;
+      const int gr = g.rb * rows_per_block + (two ? q * acc_rows : 0) + r;  // row of the unit's kv head
       const bool live = r < acc_rows && gr < g.s.nodes * G;
       const int node = live ? gr / G : -1;
       // this row's first key, the first key that not every row attends to
       const int ka = tree_first_key(p, g.b, g.s, node), pos = g.s.pos;
       const int nt = g.nt;
-      int key0 = g.s.first + (g.t0 + (NT == 2 ? 0 : q)) * kBN;
+      int key0 = g.s.first + (g.t0 + (two ? 0 : q)) * kBN;
       float m_ref = -INFINITY, l = 0.f;
-      for (int t = NT == 2 ? 0 : q; ok && t < nt; t += NT == 2 ? 1 : 2, ++js, key0 += (NT == 2 ? 1 : 2) * kBN) {
+      for (int t = two ? 0 : q; ok && t < nt; t += step, ++js, key0 += step * kBN) {
         // only tiles that reach a node, the end or the window are masked: bit x
         // of these words, the row attends to key key0 + x
         // (one answer for the warp: what follows has to stay converged)
@@ -606,7 +639,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         if (!ok) break;
         tc05::fence_after_sync();
         const int vs = (u0 + 2 * t + 1) % kSlots;  // V's slot
-        if (!kByte && (NT == 1 || q == 0) && (key0 + kBN > g.s.len || key0 < g.s.lo)) {
+        if (!kByte && (!two || q == 0) && (key0 + kBN > g.s.len || key0 < g.s.lo)) {
           // rows that no node reads may hold anything (NaN included): P = 0
           // there, and 0 * NaN would still poison O. Their V rows are zeroed
           // once the tile has landed, before P is published.
@@ -623,12 +656,6 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           }
         }
         if (warp_rows) {
-          // The row's scores pass through registers 32 at a time, twice: for
-          // the maximum, then for the probabilities (tensor memory is read
-          // again, which costs less than 128 registers and a loop body four
-          // times as long: the instruction fetch of the unrolled form took
-          // microseconds at each unit's first tile). P of 32 keys takes 16
-          // columns, all of them read already.
           const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff);
           const float4* sk = reinterpret_cast<const float4*>(sc + ((u0 + 2 * t) % C::kScales) * kBN);
           const float4* sv = reinterpret_cast<const float4*>(sc + ((u0 + 2 * t + 1) % C::kScales) * kBN);
@@ -651,6 +678,11 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
                 if (!((w >> i) & 1u)) s[i] = -INFINITY;
             }
           };
+          // The row's scores pass through registers 64 at a time, twice: for the
+          // maximum, then for the probabilities. (128 of them kept in registers
+          // between the two need a loop body twice as long, which was slower:
+          // 4096 tokens x 32, 64 nodes 198 vs 192 us, 16 nodes 110 vs 109.) P
+          // of 32 keys takes 16 columns of S, all of them read already.
           float mt = -INFINITY;
 #pragma unroll 1
           for (int x = 0; x < kBN / 32; x += 2) {
@@ -742,219 +774,144 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kODone), seg & 1, p.wait_ns) && !stop());
       if (!ok && lane == 0) fail(true);
       // all eight warps agree whether the segment's result stands
-      if (bar_any(2, 256, !ok)) break;
+      aborted = bar_any(2, 256, !ok);
+      if (aborted) break;
       tc05::fence_after_sync();
       if (!waited) {  // the append clears the counters; out may still be read before it
         grid_dependency_wait();
         waited = true;
       }
-      // ---- the segment's result: this thread's row, O unnormalised in v.
-      // A part of a unit whose other parts are all there already is merged
-      // with them on the way out (each thread its own row); else it is left
-      // in the workspace, and the unit's last block merges.
-      bool whole = g.head && g.tail, direct = false;
-      TreeMerge mg = {0, 1, 0};
-      if (!whole) {
-        mg = tree_merge(plan, g, blockIdx.x);
-        if (tid == 0) {
-          int seen;
-          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(p.arrived + mg.ca) : "memory");
-          s_flag = mg.m <= kDirectParts && seen == mg.m - 1;
-        }
-        named_bar_sync(1, 256);
-        direct = whole = s_flag != 0;
-        if (direct) __threadfence();
-      }
-      float* part = p.part + tree_part_floats(rows_per_block, kD) * (2 * static_cast<size_t>(blockIdx.x) + (g.head ? 1 : 0));
-      const int br = gr - g.rb * rows_per_block;  // row of the block
-      long long orow = 0;
-      if (live) orow = tree_out_row(p, g, gr);
-      // 32 values of every row of the warp, from dim 32 x on, written so that
-      // neighbouring lanes write neighbouring 16 bytes of one row (a lane
-      // writing its own row touches 32 lines with every store: 256 rows took 6
-      // us): groups of 8 lanes (fp32: a row's 128 bytes; bf16, 4 lanes: 64)
-      // exchange their 16-byte pieces first.
-      auto put = [&](int x, float (&v)[32], float inv) {
-        if (!whole || p.out_dtype == kDtypeF32) {
-          float* base = whole ? static_cast<float*>(p.out) + orow * kD : part + static_cast<size_t>(br) * kD;
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= inv;
-          }
-          transpose16<8>(reinterpret_cast<uint32_t(&)[32]>(v), lane);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {  // the row of lane (group) + k
-            float* dst = shfl_ptr(live ? base : nullptr, (lane & ~7) + k);
-            if (dst != nullptr)
-              *reinterpret_cast<float4*>(dst + 32 * x + 4 * (lane & 7)) =
-                  make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          }
-        } else {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
-          transpose16<4>(w, lane);
-          __nv_bfloat16* base = static_cast<__nv_bfloat16*>(p.out) + orow * kD;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            __nv_bfloat16* dst = shfl_ptr(live ? base : nullptr, (lane & ~3) + k);
-            if (dst != nullptr)
-              *reinterpret_cast<uint4*>(dst + 32 * x + 8 * (lane & 3)) =
-                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-          }
-        }
-      };
-      // direct: the row's maximum and sum over all parts, and this part's weight
-      float m_all = -INFINITY, w_own = 1.f;
-      auto meet = [&](float m2, float sum) {
-        m_all = m2;
-        for (int k = 0; k < mg.m; ++k)
-          if (k != mg.own && live)
-            m_all = fmaxf(m_all, __ldcg(tree_part(p, mg, k, rows_per_block, kD) + static_cast<size_t>(rows_per_block) * kD + br));
-        w_own = m2 != -INFINITY ? exp2f(m2 - m_all) : 0.f;
-        float total = 0.f;
-        for (int k = 0; k < mg.m; ++k) {
-          float mk = m2, lk = sum;
-          if (k != mg.own && live) {
-            const float* ml = tree_part(p, mg, k, rows_per_block, kD) + static_cast<size_t>(rows_per_block) * kD + br;
-            mk = __ldcg(ml);
-            lk = __ldcg(ml + rows_per_block);
-          }
-          if (mk != -INFINITY) total = fmaf(exp2f(mk - m_all), lk, total);
-        }
-        return total;
-      };
-      auto join = [&](int x, float (&v)[32]) {  // dims 32 x .. of the whole unit's sums
-        float acc[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-#pragma unroll 1
-        for (int k = 0; k < mg.m; ++k) {
-          if (k == mg.own) {
-            if (w_own > 0.f) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) acc[i] = fmaf(w_own, v[i], acc[i]);
-            }
-            continue;
-          }
-          const float* q = tree_part(p, mg, k, rows_per_block, kD);
-          float o[32];
-          const int top = br - (lane & 7);  // the group's first row of the block
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {  // as put() writes: neighbouring lanes, neighbouring pieces
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(min(top + i, rows_per_block - 1)) * kD + 32 * x) + (lane & 7));
-            o[4 * i] = f.x, o[4 * i + 1] = f.y, o[4 * i + 2] = f.z, o[4 * i + 3] = f.w;
-          }
-          const float mk = live ? __ldcg(q + static_cast<size_t>(rows_per_block) * kD + br) : -INFINITY;
-          transpose16<8>(reinterpret_cast<uint32_t(&)[32]>(o), lane);
-          if (mk != -INFINITY) {
-            const float w = exp2f(mk - m_all);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = fmaf(w, o[i], acc[i]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = acc[i];
-      };
-      auto put_ml = [&](float m2, float sum) {  // maximum (log2 domain) and sum
-        if (!live) return;
-        if (!whole) {
-          part[static_cast<size_t>(rows_per_block) * kD + br] = m2;
-          part[static_cast<size_t>(rows_per_block) * (kD + 1) + br] = sum;
-        } else if (p.lse_out != nullptr) {
-          p.lse_out[orow] = sum > 0.f ? (m2 + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
-        }
-      };
-      float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c;
-      if (NT == 2 || g.nt == 1) {
-        if (NT == 2 || q == 0) {
-          if (direct) {
-            l = meet(m2, l);
-            m2 = m_all;
-          }
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          if (warp_rows) {
-#pragma unroll 1
-            for (int x = 0; x < kD / 32; ++x) {
-              float v[32];
-              tc05::ld_32x32b_x32(ocol + x * 32, v);
-              tc05::wait_ld();
-              tc05::reg_fence(v);
-              if (direct) join(x, v);
-              put(x, v, inv);
-            }
-          }
-          put_ml(m2, l);
-        }
-      } else {
-        // the two accumulators of each row meet: the second warpgroup hands its
-        // O over through the Q area (free: every product with Q is done), 32
-        // dims at a time in two buffers of 16 KB
-        unsigned char* xbuf = smem + C::kQOff;
-        auto chunk = [&](int x, int i) {  // float4 i of row r
-          return reinterpret_cast<float4*>(xbuf + (x & 1) * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
-        };
+      // ---- the segment's result, 32 dims at a time: a whole unit's goes out,
+      // a part's into the workspace. (One copy of this code for every case:
+      // fetching it costs more than running it.)
+      const bool whole = g.head && g.tail, last = s_last[seg & 1] != 0;
+      const bool both = !two && nt > 1;  // the two accumulators of each row meet
+      // ... through the Q area (free: every product with Q is done; NT = 2: the
+      // second row tile's half): the second warpgroup hands its O over in two
+      // buffers of 16 KB
+      unsigned char* xbuf = smem + C::kQOff + (NT - 1) * kTileBytes;
+      float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c, w0 = 1.f, w1 = 0.f;
+      if (both) {
         if (q == 1) {
           s_m[r] = m2;
           s_l[r] = l;
         }
-        float w0 = 0.f, w1 = 0.f, inv = 1.f;
+        named_bar_sync(1, 256);
+        if (q == 0) {
+          const float mo = s_m[r], mx = fmaxf(m2, mo);
+          w0 = mx != -INFINITY ? exp2f(m2 - mx) : 0.f;
+          w1 = mx != -INFINITY ? exp2f(mo - mx) : 0.f;
+          l = w0 * l + w1 * s_l[r];
+          m2 = mx;
+        }
+      }
+      const bool writer = (two || q == 0) && warp_rows;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const long long orow = live ? tree_out_row(p, g, gr) : 0;
+      const int br = gr - g.rb * rows_per_block;  // row of the block
+      float* part = tree_place(p, g, blockIdx.x, rows_per_block, kD);
 #pragma unroll 1
-        for (int x = 0; x <= kD / 32; ++x) {
-          if (q == 1 && x < kD / 32 && warp_rows) {
-            float v[32];
-            tc05::ld_32x32b_x32(ocol + x * 32, v);
-            tc05::wait_ld();
-            tc05::reg_fence(v);
+      for (int x = 0; x < kD / 32; ++x) {
+        auto piece = [&](int i) {  // 16 bytes i of row r
+          return reinterpret_cast<float4*>(xbuf + (x & 1) * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
+        };
+        float v[32];
+        __syncwarp();
+        if (writer || (both && warp_rows)) {
+          tc05::ld_32x32b_x32(ocol + x * 32, v);
+          tc05::wait_ld();
+          tc05::reg_fence(v);
+        }
+        if (both) {
+          if (q == 1 && warp_rows) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) *chunk(x, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) *piece(i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
-          if (q == 0 && x > 0 && warp_rows) {
-            if (x == 1) {
-              const float mo = s_m[r], lo = s_l[r], mx = fmaxf(m2, mo);
-              if (mx != -INFINITY) {
-                w0 = exp2f(m2 - mx);
-                w1 = exp2f(mo - mx);
-              }
-              l = w0 * l + w1 * lo;
-              m2 = mx;
-              if (direct) {
-                l = meet(m2, l);
-                m2 = m_all;
-              }
-              if (whole) inv = l > 0.f ? 1.f / l : 0.f;
-            }
-            float v[32];
-            tc05::ld_32x32b_x32(ocol + (x - 1) * 32, v);
-            tc05::wait_ld();
-            tc05::reg_fence(v);
+          named_bar_sync(1, 256);
+          if (writer) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 o = *chunk(x - 1, i);
+              const float4 o = *piece(i);
               v[4 * i] = fmaf(w1, o.x, w0 * v[4 * i]);
               v[4 * i + 1] = fmaf(w1, o.y, w0 * v[4 * i + 1]);
               v[4 * i + 2] = fmaf(w1, o.z, w0 * v[4 * i + 2]);
               v[4 * i + 3] = fmaf(w1, o.w, w0 * v[4 * i + 3]);
             }
-            if (direct) join(x - 1, v);
-            put(x - 1, v, inv);
           }
-          if (x < kD / 32) named_bar_sync(1, 256);
         }
-        if (q == 0) put_ml(m2, l);
+        if (writer) {
+          if (!whole) {
+            if (live) {
+              float4* dst = reinterpret_cast<float4*>(part) + static_cast<size_t>(8 * x) * rows_per_block + br;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[static_cast<size_t>(i) * rows_per_block] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+          } else if (p.out_dtype == kDtypeF32) {
+            if (live) {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * kD + 32 * x);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+            }
+          } else {
+            // bf16: four lanes exchange their rows' 16-byte pieces, so that
+            // they write 64 bytes of one row together (a lane writing its own
+            // row touches 32 lines with every store: 256 rows took 6 us)
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+            transpose16<4>(w, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const long long to = __shfl_sync(0xffffffffu, live ? orow : -1ll, (lane & ~3) + k);
+              if (to >= 0)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to * kD + 32 * x + 8 * (lane & 3)) =
+                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            }
+          }
+        }
       }
-      // O is read; NT = 1: and the Q area
+      if (writer && live) {
+        if (!whole) {
+          part[static_cast<size_t>(rows_per_block) * kD + br] = m2;
+          part[static_cast<size_t>(rows_per_block) * (kD + 1) + br] = l;
+        } else if (p.lse_out != nullptr) {
+          p.lse_out[orow] = l > 0.f ? (m2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+        }
+      }
+      // O is read, and the Q area
       tc05::fence_before_sync();
-      if (NT == 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(C::kOFree));
-        if (NT == 1) mbar_arrive(bar(C::kQFree));
+        if (!two) mbar_arrive(bar(C::kXFree));
+        if (!whole && !last) mbar_arrive(bar(C::kPart));
       }
-      if (!whole)
-        tree_arrive_merge<kD, 4>(p, mg, g, rows_per_block, tid, 256, &s_flag, [] { named_bar_sync(1, 256); });
-      u0 += 2 * g.nt;
+      if (last) break;
+      u0 += 2 * nt;
       ++seg;
+    }
+    // ---- parts of units: the last segment's is counted in here, the first
+    // one's was by warp 11; a unit that is complete is merged
+    if (tid == 0) {
+      walk.start(p, plan, kBN, rows_per_block);
+      (void)walk.next(p, kBN, rows_per_block, s_first);
+    }
+    named_bar_sync(3, 256 + 32);
+    if (!aborted) {
+      const TreeSegment& g = s_seg[seg & 1];
+      const bool part = s_more[seg & 1] && !(g.head && g.tail);
+      bool complete = false;
+      if (part)
+        complete = tree_arrive(p, tree_merge(plan, g), tid, &s_flag, [] { named_bar_sync(1, 256); });
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i)
+        if (i == 0 ? complete : s_pending != 0) {
+          const TreeSegment& f = i == 0 ? g : s_first;
+          tree_merge_rows<kD>(p, tree_merge(plan, f), f, rows_per_block, tid, 256);
+        }
     }
   }
 

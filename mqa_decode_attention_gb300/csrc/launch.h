@@ -262,8 +262,9 @@ struct TreeParams {
   int early;      // 1: the preceding launch is the append kernel: the cached tokens may be read before it ends
   unsigned long long wait_ns;
 };
-// A partial result: [rows][d] fp32 sums, then each row's maximum (log2
-// domain) and sum; a multiple of 16 bytes, whatever the rows. A block leaves
+// A partial result: fp32 sums as [d / 4][rows] pieces of 16 bytes (neighbouring
+// threads hold neighbouring rows), then each row's maximum (log2 domain) and
+// sum; a multiple of 16 bytes, whatever the rows. A block leaves
 // at most two: of the unit it starts in the middle of (place 2 c) and of the
 // unit it ends in the middle of (place 2 c + 1; a run inside one unit without
 // its first tile is of the first kind).

@@ -243,99 +243,86 @@ __device__ __forceinline__ long long tree_out_row(const TreeParams& p, const Tre
   return (static_cast<long long>(g.b) * p.n + i) * p.h_q + g.j * p.group + (row - i * p.group);
 }
 
-// A unit's merge: with M the largest of its partials' maxima,
-//   O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,
-// summed in block order k = 0 .. m - 1 whichever block merges, so that the
-// bits do not depend on who comes last.
+// A unit's merge: its first block, its blocks, this block among them. Partial
+// k of a unit lies in the places of its k-th block.
 struct TreeMerge {
-  int ca, m, own;  // the unit's first block, its blocks, this block among them
+  int ca, m;
 };
-__device__ __forceinline__ TreeMerge tree_merge(const TreePlan& pl, const TreeSegment& g, int cta) {
+__device__ __forceinline__ TreeMerge tree_merge(const TreePlan& pl, const TreeSegment& g) {
   const int ca = tree_cta_of(pl, g.u0), cb = tree_cta_of(pl, g.u0 + g.s.tiles - 1);
-  return {ca, cb - ca + 1, cta - ca};
+  return {ca, cb - ca + 1};
 }
-__device__ __forceinline__ const float* tree_part(const TreeParams& p, const TreeMerge& mg, int k, int rows, int d) {
-  return p.part + tree_part_floats(rows, d) * (k == 0 ? 2 * mg.ca + 1 : 2 * (mg.ca + k));
+// where block `cta` leaves its partial of segment g
+__device__ __forceinline__ float* tree_place(const TreeParams& p, const TreeSegment& g, int cta, int rows, int d) {
+  return p.part + tree_part_floats(rows, d) * (2 * static_cast<size_t>(cta) + (g.head ? 1 : 0));
 }
 
-// After a block has written its partial of segment g (every thread): counts it
-// in and, when it was the unit's last, merges. `threads` threads call it, all
-// of them, `sync` is a barrier over them, `flag` a shared int of theirs, tid
-// their index. A warp takes kR rows at a time, a lane D / 32 of a row's values;
-// the loads of all its rows' partials are in flight together.
-template <int D, int kR, class Sync>
-__device__ __forceinline__ void tree_arrive_merge(const TreeParams& p, const TreeMerge& mg, const TreeSegment& g,
-                                                  int rows_per_block, int tid, int threads, volatile int* flag,
-                                                  const Sync& sync) {
-  __threadfence();  // this thread's part of the partial, before the count
-  sync();
-  if (tid == 0) *flag = atomicAdd(p.arrived + mg.ca, 1) == mg.m - 1;
-  sync();
-  if (*flag == 0) return;
-  __threadfence();  // the other blocks' partials, after the count
+// Merges a unit all of whose partials are in the workspace, seen by the
+// calling threads (all `threads` of them, tid their index):
+//   M = max_k m_k,  O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k
+// with a running M, in block order whichever block merges. A warp takes 8 rows
+// at a time, lane (row, quarter): a load instruction reads 4 runs of 128
+// bytes, a store writes whole sectors of 8 rows, and a partial's 8 loads (d =
+// 128) are in flight together.
+template <int D>
+__device__ __forceinline__ void tree_merge_rows(const TreeParams& p, const TreeMerge& mg, const TreeSegment& g,
+                                                int rows_per_block, int tid, int threads) {
+  constexpr int kU = D / 16;  // 16-byte pieces of a row per lane
   const int rows = min(rows_per_block, g.s.nodes * p.group - g.rb * rows_per_block);
-  const int warp = tid >> 5, lane = tid & 31, warps = threads / 32;
-  constexpr int kV = D / 32;
-  for (int r0 = warp; r0 < rows; r0 += kR * warps) {
-    int row[kR];  // (rows past the end repeat the last one)
-    float acc[kR][kV], mx[kR], l[kR];
+  const int lane = tid & 31;
+  for (int r0 = (tid >> 5) * 8; r0 < rows; r0 += threads / 32 * 8) {
+    const int r = min(r0 + (lane & 7), rows - 1);
+    float4 acc[kU];
+    float mx = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int u = 0; u < kR; ++u) {
-      row[u] = min(r0 + u * warps, rows - 1);
-      mx[u] = -INFINITY;
-      l[u] = 0.f;
-#pragma unroll
-      for (int v = 0; v < kV; ++v) acc[u][v] = 0.f;
-    }
-#pragma unroll 2
+    for (int u = 0; u < kU; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int k = 0; k < mg.m; ++k) {
-      const float* q = tree_part(p, mg, k, rows_per_block, D) + static_cast<size_t>(rows_per_block) * D;
+      const float* q = p.part + tree_part_floats(rows_per_block, D) * (k == 0 ? 2 * mg.ca + 1 : 2 * (mg.ca + k));
+      const float mk = __ldcg(q + static_cast<size_t>(rows_per_block) * D + r);
+      const float lk = __ldcg(q + static_cast<size_t>(rows_per_block) * (D + 1) + r);
+      float4 o[kU];
 #pragma unroll
-      for (int u = 0; u < kR; ++u) mx[u] = fmaxf(mx[u], __ldcg(q + row[u]));
-    }
-#pragma unroll 2
-    for (int k = 0; k < mg.m; ++k) {
-      const float* q = tree_part(p, mg, k, rows_per_block, D);
-      float mk[kR], lk[kR], ov[kR][kV];
+      for (int u = 0; u < kU; ++u)
+        o[u] = __ldcg(reinterpret_cast<const float4*>(q) + static_cast<size_t>(4 * u + (lane >> 3)) * rows_per_block + r);
+      if (mk != -INFINITY) {  // (else no key of this part: its sums may be anything)
+        const float top = fmaxf(mx, mk), a = exp2f(mx - top), w = exp2f(mk - top);
+        mx = top;
+        l = fmaf(w, lk, a * l);
 #pragma unroll
-      for (int u = 0; u < kR; ++u) {
-        mk[u] = __ldcg(q + static_cast<size_t>(rows_per_block) * D + row[u]);
-        lk[u] = __ldcg(q + static_cast<size_t>(rows_per_block) * (D + 1) + row[u]);
-        if constexpr (kV == 4) {
-          const float4 t = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(row[u]) * D) + lane);
-          ov[u][0] = t.x, ov[u][1] = t.y, ov[u][2] = t.z, ov[u][3] = t.w;
-        } else {
-          const float2 t = __ldcg(reinterpret_cast<const float2*>(q + static_cast<size_t>(row[u]) * D) + lane);
-          ov[u][0] = t.x, ov[u][1] = t.y;
+        for (int u = 0; u < kU; ++u) {
+          acc[u].x = fmaf(w, o[u].x, a * acc[u].x);
+          acc[u].y = fmaf(w, o[u].y, a * acc[u].y);
+          acc[u].z = fmaf(w, o[u].z, a * acc[u].z);
+          acc[u].w = fmaf(w, o[u].w, a * acc[u].w);
         }
       }
-#pragma unroll
-      for (int u = 0; u < kR; ++u)
-        if (mk[u] != -INFINITY) {  // (else no key of this part: its sums may be anything)
-          const float w = exp2f(mk[u] - mx[u]);
-          l[u] = fmaf(w, lk[u], l[u]);
-#pragma unroll
-          for (int v = 0; v < kV; ++v) acc[u][v] = fmaf(w, ov[u][v], acc[u][v]);
-        }
     }
+    if (r0 + (lane & 7) < rows) {
+      const float inv = mx != -INFINITY ? 1.f / l : 0.f;
+      const long long o = tree_out_row(p, g, g.rb * rows_per_block + r);
 #pragma unroll
-    for (int u = 0; u < kR; ++u) {
-      if (r0 + u * warps >= rows) break;
-      const float inv = mx[u] != -INFINITY ? 1.f / l[u] : 0.f;
-      const long long o = tree_out_row(p, g, g.rb * rows_per_block + row[u]);
-      if constexpr (kV == 4) {
-        tree_store4(p, o * D + 4 * lane, acc[u][0] * inv, acc[u][1] * inv, acc[u][2] * inv, acc[u][3] * inv);
-      } else if (p.out_dtype == kDtypeBf16) {
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + o * D + 2 * lane) =
-            pack_bf16x2(acc[u][0] * inv, acc[u][1] * inv);
-      } else {
-        *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o * D + 2 * lane) =
-            make_float2(acc[u][0] * inv, acc[u][1] * inv);
-      }
-      if (lane == 0 && p.lse_out != nullptr)
-        p.lse_out[o] = mx[u] != -INFINITY ? (mx[u] + log2f(l[u])) * 0.69314718055994530942f : -INFINITY;
+      for (int u = 0; u < kU; ++u)
+        tree_store4(p, o * D + 4 * (4 * u + (lane >> 3)), acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv);
+      if (lane < 8 && p.lse_out != nullptr)
+        p.lse_out[o] = mx != -INFINITY ? (mx + log2f(l)) * 0.69314718055994530942f : -INFINITY;
     }
   }
+}
+
+// After a block has written its partial of segment g (all `threads` threads,
+// `sync` a barrier over them): counts it in, true when it was the unit's last.
+template <class Sync>
+__device__ __forceinline__ bool tree_arrive(const TreeParams& p, const TreeMerge& mg, int tid, volatile int* flag,
+                                            const Sync& sync) {
+  sync();
+  if (tid == 0) {
+    __threadfence();  // the block's partial (seen through the barrier), before the count
+    *flag = atomicAdd(p.arrived + mg.ca, 1) == mg.m - 1;
+    __threadfence();  // the other blocks' partials, after it
+  }
+  sync();
+  return *flag != 0;
 }
 
 }  // namespace mqa

@@ -173,6 +173,15 @@ def test_many_sequences_of_many_lengths(m, cache):
     check(m, TreeCase(4, 1, 128, pos, nodes, 9, cache, 16, seed=1))
 
 
+@pytest.mark.parametrize("page", [0, 16])
+def test_units_of_one_and_of_two_row_tiles(m, page):
+    """Trees below and above 128 rows per kv head beside one another, in runs of several units."""
+    rng = np.random.default_rng(6)
+    pos = [int(x) for x in rng.integers(0, 900, 60)]
+    nodes = [int(x) for x in rng.integers(0, 33, 60)]
+    check(m, TreeCase(16, 2, 128, pos, nodes, 32, "bf16", page, seed=2))
+
+
 def test_calls_are_the_step(m):
     """The two calls give the step's bits; so does a second run, on the workspace as the first left it."""
     for d, cache in ((128, "bf16"), (128, "u8"), (64, "e5m2")):

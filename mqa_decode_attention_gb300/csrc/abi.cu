@@ -1152,12 +1152,29 @@ TreeChoice tree_choice(const mqa_kv_layout* L, int n) {
   return c;
 }
 
+// A paged bf16 pool for the tcgen05 tree kernel: (64 dims, 8 rows, the two
+// 64-dim halves, a page's groups of 8 rows, (page, kv head)), a box all of the
+// first three and min(page_size, 64) rows: one copy per page run, landing as
+// [groups][halves][8 rows][128 B].
+bool make_tree_paged_map(CUtensorMap* map, void* base, const mqa_kv_layout* L) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t ps = static_cast<cuuint64_t>(L->page_size);
+  const cuuint64_t dims[5] = {64, 8, 2, ps / 8, static_cast<cuuint64_t>(L->h_kv) * L->num_pages};
+  const cuuint64_t strides[4] = {256, 128, 8 * 256, ps * 256};
+  const cuuint32_t box[5] = {64, 8, 2, static_cast<cuuint32_t>(L->page_size < 64 ? L->page_size : 64) / 8, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The tcgen05 tree kernel's maps: K and V tiles, and q_rot [batch n tokens]
 // [h_q][128] bf16 in boxes of 64 dims x the group x `tokens`.
 bool make_tree_maps(const mqa_kv_layout* L, const void* q_rot, int n, int tokens, CUtensorMap* tk, CUtensorMap* tv,
                     CUtensorMap* tq) {
   if (L->cache_dtype == MQA_BF16) {
-    if (!(L->paged ? make_tc05_paged_map(tk, L->k_cache, L) && make_tc05_paged_map(tv, L->v_cache, L)
+    if (!(L->paged ? make_tree_paged_map(tk, L->k_cache, L) && make_tree_paged_map(tv, L->v_cache, L)
                    : make_tensor_map(tk, L->k_cache, L, true, 1, kTreeTileKeys) &&
                          make_tensor_map(tv, L->v_cache, L, true, 1, kTreeTileKeys)))
       return false;

@@ -59,7 +59,20 @@ namespace {
 constexpr int kD = 128;
 constexpr int kBM = 128;  // rows of an accumulator
 constexpr int kBN = 128;  // keys per tile
-constexpr int kTileBytes = kBN * kD * 2;  // a bf16 tile: [2 halves of 64 dims][128 rows][128 B], swizzled
+constexpr int kTileBytes = kBN * kD * 2;  // a bf16 tile, 128-byte swizzled
+// A bf16 tile is [2 halves of 64 dims][128 rows][128 B]; gathered from pages it
+// is [16 groups of 8 rows][2 halves][8 rows][128 B], so that one copy brings a
+// page's rows with both halves (a copy per page and half kept the TMA unit
+// busy: 16-row pages 4.7 TB/s). Strides of the halves and of the 8-row groups:
+template <bool GROUPED>
+struct Tile {
+  static constexpr int kHalf = GROUPED ? 1024 : 16384;
+  static constexpr int kGroup = GROUPED ? 2048 : 1024;
+};
+template <bool GROUPED>
+__device__ __forceinline__ int tile_row(int r) {  // byte offset of row r's first half
+  return (r >> 3) * Tile<GROUPED>::kGroup + (r & 7) * 128;
+}
 constexpr int kRawBytes = kBN * kD;       // a code tile: [128 rows][128 B], swizzled
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // S / P of accumulator q at 128 q, its O at 256 + 128 q
@@ -73,9 +86,11 @@ struct Cfg {
   static constexpr bool kByte = DT != kDtypeBf16;
   static constexpr int kThreads = kByte ? 640 : 384;
   static constexpr int kRegsLaunch = kByte ? 96 : 168;
-  static constexpr int kRegsSoftmax = kByte ? 152 : 216;
-  static constexpr int kRegsAux = kByte ? 56 : 72;
-  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsAux <= kThreads * kRegsLaunch, "register split");
+  static constexpr int kRegsSoftmax = kByte ? 152 : 200;
+  static constexpr int kRegsAux = kByte ? (DT == kDtypeU8 ? 64 : 80) : 104;  // (72 spilled in the MMA thread, on the way of every product)
+  static constexpr int kRegsConvert = DT == kDtypeU8 ? 56 : 48;
+  static_assert(256 * kRegsSoftmax + 128 * kRegsAux + (kThreads - 384) * kRegsConvert <= kThreads * kRegsLaunch,
+                "register split");
   static constexpr int kSlots = kByte ? (NT == 1 ? 4 : 3) : (NT == 1 ? 6 : 5);  // bf16 tiles
   static constexpr int kRaw = kByte ? (DT == kDtypeU8 ? 3 : 4) : 0;              // code tiles
   static constexpr int kQOff = 0;
@@ -193,6 +208,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
                           const __grid_constant__ CUtensorMap tmap_q, const TreeParams p) {
   using C = Cfg<NT, DT>;
   constexpr bool kByte = C::kByte;
+  constexpr bool kGrouped = PG && !kByte;
+  using L = Tile<kGrouped>;
   constexpr int kSlots = C::kSlots, kRaw = kByte ? C::kRaw : 1;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -322,12 +339,11 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(bar(kF + slot), kBytes);
             __syncwarp();
             if (lane < copies) {
-              const uint32_t d = dst + lane * rp * 128;
+              const uint32_t d = dst + lane * rp * (kByte ? 128 : 256);
               if constexpr (kByte) {
                 tma_load_4d(d, map, 0, k & (ps - 1), g.j, page, bar(kF + slot));
               } else {
-                tma_load_5d(d, map, 0, k & (ps - 1), 0, g.j, page, bar(kF + slot));
-                tma_load_5d(d + 16384, map, 0, k & (ps - 1), 1, g.j, page, bar(kF + slot));
+                tma_load_5d(d, map, 0, 0, 0, (k & (ps - 1)) >> 3, page < 0 ? -1 : page * p.h_kv + g.j, bar(kF + slot));
               }
             }
           } else if (lane == 0) {
@@ -398,23 +414,22 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         const uint32_t k_s = sbase + C::kRingOff + ((u0 + 2 * t) % kSlots) * kTileBytes;
         tc05::fence_after_sync();
         // (the descriptors' address field counts 16 bytes: the sub-tiles are constant steps)
-        const uint64_t qd = tc05::smem_desc_sw128(q_s, 16, 1024), kd = tc05::smem_desc_sw128(k_s, 16, 1024);
+        const uint64_t qd = tc05::smem_desc_sw128(q_s, 16, 1024), kd = tc05::smem_desc_sw128(k_s, 16, L::kGroup);
 #pragma unroll
-        for (int ks = 0; ks < kD / 16; ++ks) {
-          const uint64_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-          tc05::mma_bf16(tmem + kColS + q * 128, qd + off, kd + off, id_s, ks > 0);
-        }
+        for (int ks = 0; ks < kD / 16; ++ks)
+          tc05::mma_bf16(tmem + kColS + q * 128, qd + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                         kd + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4), id_s, ks > 0);
         tc05::commit(bar(C::kSFull + q));
       };
       // O_q (+)= P_q V(t) of keys 64 h .. 64 h + 63: each half of P as soon as it is written
       auto issue_pv = [&](int q, int t, int h, bool add) {
         const uint32_t v_s = sbase + C::kRingOff + ((u0 + 2 * t + 1) % kSlots) * kTileBytes;
         tc05::fence_after_sync();
-        const uint64_t vd = tc05::smem_desc_sw128(v_s + h * 8192, 16384, 1024);
+        const uint64_t vd = tc05::smem_desc_sw128(v_s + h * 8 * L::kGroup, L::kHalf, L::kGroup);
         const uint32_t pa = tmem + kColS + q * 128 + h * 32;
 #pragma unroll
         for (int ks = 0; ks < kBN / 32; ++ks)
-          tc05::mma_bf16_ta(tmem + kColO + q * 128, pa + ks * 8, vd + ((ks * 2048) >> 4), id_o, add || h > 0 || ks > 0);
+          tc05::mma_bf16_ta(tmem + kColO + q * 128, pa + ks * 8, vd + ((ks * 2 * L::kGroup) >> 4), id_o, add || h > 0 || ks > 0);
       };
       auto pv = [&](int q, int t, bool add) {
         const int n = ps[q]++;
@@ -512,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     if (lane == 0) s_pending = complete;
     named_bar_sync(3, 256 + 32);
   } else if (kByte && warp >= 12) {
-    regs_aux();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsConvert));
     // ---------------------------------------------------------- converters
     // Warps 12-15 widen the K tiles, 16-19 the V tiles: thread r row r (key
     // key0 + r) of each. One group for both took 3-5 us a tile.
@@ -646,11 +661,11 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kFull + vs), ((u0 + 2 * t + 1) / kSlots) & 1, p.wait_ns));
           if (!ok) break;
           if (key0 + r >= g.s.len || key0 + r < g.s.lo) {
-            unsigned char* vrow = smem + C::kRingOff + vs * kTileBytes + r * 128;
+            unsigned char* vrow = smem + C::kRingOff + vs * kTileBytes + tile_row<kGrouped>(r);
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
               *reinterpret_cast<uint4*>(vrow + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-              *reinterpret_cast<uint4*>(vrow + 16384 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(vrow + L::kHalf + x * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }

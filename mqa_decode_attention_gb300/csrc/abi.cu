@@ -1142,7 +1142,8 @@ TreeChoice tree_choice(const mqa_kv_layout* L, int n) {
   c.shape = tree_mma_shape(L->head_dim);
   c.tc05 = c.tokens = 0;
   if (L->head_dim == 128 && G <= 128) {
-    c.tc05 = static_cast<long long>(G) * n > 128 ? 2 : 1;
+    // (uint8: one row tile, the kernel has no room for a second beside the scales)
+    c.tc05 = static_cast<long long>(G) * n > 128 && L->cache_dtype != MQA_U8 ? 2 : 1;
     c.tokens = std::min(128 / G, n);
     c.shape = {c.tc05 * c.tokens * G, kTreeTileKeys, 1};
   }

@@ -91,15 +91,24 @@ struct Cfg {
   static constexpr int kRegsConvert = DT == kDtypeU8 ? 56 : 48;
   static_assert(256 * kRegsSoftmax + 128 * kRegsAux + (kThreads - 384) * kRegsConvert <= kThreads * kRegsLaunch,
                 "register split");
-  static constexpr int kSlots = kByte ? (NT == 1 ? 4 : 3) : (NT == 1 ? 6 : 5);  // bf16 tiles
-  static constexpr int kRaw = kByte ? (DT == kDtypeU8 ? 3 : 4) : 0;              // code tiles
+  // bf16 tiles, and code tiles (K's and V's). A tile ring that two converter
+  // groups fill has an even number of places, and the code tiles of K and of V
+  // have rings of their own: each place then belongs to one group, which waits
+  // for every phase of its barriers, so that a parity never stands for an
+  // older phase.
+  static constexpr int kSlots = kByte ? 4 : (NT == 1 ? 6 : 5);
+  static constexpr int kRawK = kByte ? (NT == 1 ? 2 : 1) : 0;
+  static constexpr int kRawV = kByte ? (NT == 1 && DT != kDtypeU8 ? 2 : 1) : 0;
+  static constexpr int kRaw = kRawK + kRawV;
+  static_assert(!kByte || kSlots % 2 == 0, "tile ring");
+  static_assert(NT == 1 || DT != kDtypeU8, "no room for two row tiles beside the scales");
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = NT * kTileBytes;
   static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
   // uint8: the scales of each bf16 tile's rows, twice as many places as tiles:
   // a K tile is given back when its S is there, but its scales are read by
-  // the softmax after that. Load u + 2 kSlots only lands after load u + kSlots
-  // has been given back, which is after the softmax of u's tile.
+  // the softmax after that. Load u + 2 kSlots (four tiles on) only lands after
+  // S of two tiles on, which is issued after the softmax of u's tile.
   static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;
   static constexpr int kScales = 2 * kSlots;
   static constexpr int kBarOff = kScaleOff + (DT == kDtypeU8 ? kScales * kBN * 4 : 0);
@@ -210,7 +219,10 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   constexpr bool kByte = C::kByte;
   constexpr bool kGrouped = PG && !kByte;
   using L = Tile<kGrouped>;
-  constexpr int kSlots = C::kSlots, kRaw = kByte ? C::kRaw : 1;
+  constexpr int kSlots = C::kSlots;
+  // place and phase of load u (2 t + 0 / 1: K / V of the run's tile t) among the code tiles
+  auto raw_slot = [](int u) { return (u & 1) ? C::kRawK + (u >> 1) % max(C::kRawV, 1) : (u >> 1) % max(C::kRawK, 1); };
+  auto raw_lap = [](int u) { return (u >> 1) / max((u & 1) ? C::kRawV : C::kRawK, 1); };
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
@@ -242,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       mbar_init(bar(C::kEmpty + s), 1);
     }
     if constexpr (kByte) {
-      for (int s = 0; s < kRaw; ++s) {
+      for (int s = 0; s < C::kRaw; ++s) {
         mbar_init(bar(C::kRFull + s), 1);
         mbar_init(bar(C::kREmpty + s), 4);
       }
@@ -288,7 +300,6 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     // -------------------------------------------------------- K / V loader
     // load u (2 t + 0 / 1: K / V of the run's tile t) into slot u % slots: the
     // bf16 tile itself, or the code tile a converter widens
-    constexpr int kN = kByte ? kRaw : kSlots;
     constexpr int kBytes = kByte ? kRawBytes : kTileBytes;
     constexpr int kRing = kByte ? C::kRawOff : C::kRingOff;
     constexpr int kF = kByte ? C::kRFull : C::kFull, kE = kByte ? C::kREmpty : C::kEmpty;
@@ -314,9 +325,9 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           waited = true;
         }
         for (int kv = 0; kv < 2; ++kv, ++u) {
-          const int slot = u % kN;
+          const int slot = kByte ? raw_slot(u) : u % kSlots, lap = kByte ? raw_lap(u) : u / kSlots;
           if (lane == 0) {
-            if (u >= kN) ok = mbar_wait(bar(kE + slot), (u / kN - 1) & 1, p.wait_ns);
+            if (lap > 0) ok = mbar_wait(bar(kE + slot), (lap - 1) & 1, p.wait_ns);
             if (!ok) fail(true);
             if (stop()) ok = false;
           }
@@ -357,9 +368,14 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       }
     }
     if (PG && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_PAGE_RANGE));
-    // every copy this warp issued (u of them) lands before the block can exit
+    // every copy this warp issued (u of them) lands before the block can exit:
+    // the last one into each place
     if (lane == 0)
-      for (int k = u > kN ? u - kN : 0; k < u; ++k) (void)mbar_wait(bar(kF + k % kN), (k / kN) & 1, kWaitLimitNs);
+      for (int k = max(u - 2 * kSlots, 0); k < u; ++k) {
+        const int again = kByte ? 2 * ((k & 1) ? C::kRawV : C::kRawK) : kSlots;  // loads on, the same place
+        if (k + again >= u)
+          (void)mbar_wait(bar(kF + (kByte ? raw_slot(k) : k % kSlots)), (kByte ? raw_lap(k) : k / kSlots) & 1, kWaitLimitNs);
+      }
     __syncwarp();
   } else if (warp == 10) {
     regs_aux();
@@ -568,8 +584,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           const bool live = key >= g.s.lo && key < g.s.len;
           appended(t + 1);
           const float2 next = scale_of(t + 1);
-          const int rs = u % kRaw, slot = u % kSlots;
-          ok = mbar_wait(bar(C::kRFull + rs), (u / kRaw) & 1, p.wait_ns) &&
+          const int rs = raw_slot(u), slot = u % kSlots;
+          ok = mbar_wait(bar(C::kRFull + rs), raw_lap(u) & 1, p.wait_ns) &&
                (u < kSlots || mbar_wait(bar(C::kEmpty + slot), (u / kSlots - 1) & 1, p.wait_ns));
           if (!ok) fail(true);
           ok = __all_sync(0xffffffffu, ok && !stop());
@@ -978,9 +994,11 @@ cudaError_t launch_tree_tc05_t(const TreeParams& p, int ctas, const CUtensorMap&
 template <int DT>
 cudaError_t launch_tree_tc05_dt(const TreeParams& p, int tiles, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CUtensorMap& tq, cudaStream_t stream) {
-  if (tiles == 2)
-    return p.paged ? launch_tree_tc05_t<2, true, DT>(p, ctas, tk, tv, tq, stream)
-                   : launch_tree_tc05_t<2, false, DT>(p, ctas, tk, tv, tq, stream);
+  if constexpr (DT != kDtypeU8)
+    if (tiles == 2)
+      return p.paged ? launch_tree_tc05_t<2, true, DT>(p, ctas, tk, tv, tq, stream)
+                     : launch_tree_tc05_t<2, false, DT>(p, ctas, tk, tv, tq, stream);
+  if (tiles != 1) return cudaErrorInvalidValue;
   return p.paged ? launch_tree_tc05_t<1, true, DT>(p, ctas, tk, tv, tq, stream)
                  : launch_tree_tc05_t<1, false, DT>(p, ctas, tk, tv, tq, stream);
 }

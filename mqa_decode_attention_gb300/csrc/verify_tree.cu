@@ -18,16 +18,23 @@
 //
 // Only the rows the walk needs are read: those of nodes where a child is
 // rejected, and of the node it ends at. What is compared decides tokens, so
-// the sums carry 64-bit accuracy: a weight is formed as an unevaluated pair
-// of floats (the product's and the difference's rounding errors kept), a
-// thread's sum as such a pair (relative error below 2^-44), and everything
-// across threads in fp64; the fp64 pipe of this part is too narrow for a
-// vocabulary's worth of additions.
+// the sums carry 64-bit accuracy. The fp64 pipe of this part takes 16 cycles
+// for one warp's addition (with fp64 across the threads a sweep of 128000
+// tokens took 40 us), so weights and sums are unevaluated pairs of floats, the
+// rounding errors of each product, difference and sum kept (relative error
+// below 2^-43), down to one value per block; only the walk's own comparisons
+// and the last element's search are fp64, by one warp.
 //
-// A cluster of up to 8 blocks serves one sequence: every block walks the tree
-// alike, a sum over the vocabulary is split over the blocks (consecutive
-// slices), their warps (consecutive runs) and met through distributed shared
-// memory; the block, then the warp whose run holds the goal looks it up.
+// A cluster of up to 8 blocks serves one sequence: warp 0 of every block walks
+// the tree alike; when it needs a sum over the vocabulary every warp of the
+// cluster adds its share (consecutive slices for blocks, consecutive runs for
+// warps), and the blocks' sums meet through distributed shared memory. The
+// next token is found by the block, then the warp's run, then the eighth of it
+// that holds the goal.
+//
+// Bound: latency at every size -- a row of 128000 fp32 probabilities is 0.08 us
+// of the HBM rate. A sweep is two barriers, a memory round trip or two and a
+// cluster barrier.
 #include <cuda_bf16.h>
 
 #include "../../include/mqa_decode.h"
@@ -37,7 +44,7 @@
 namespace mqa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 
@@ -101,15 +108,19 @@ struct Vec<__nv_bfloat16> {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_tree_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 3) verify_tree_kernel(const VerifyParams p) {
   constexpr int N = Vec<T>::kN;
   __shared__ int s_parent[kMaxTreeNodes], s_token[kMaxTreeNodes], s_path[kMaxTreeNodes];
   __shared__ float s_u[kMaxTreeNodes], s_p[kMaxTreeNodes], s_q[kMaxTreeNodes];
-  __shared__ int s_out[kMaxTreeNodes];   // deterministic drafts: tokens rejected at the current node
-  __shared__ double s_warp[kWarps];      // sums of the warps' runs
-  __shared__ double s_sum[2];            // this block's sum, by the sweep's parity
-  __shared__ float s_top[kWarps];
-  __shared__ int s_at[kWarps];
+  __shared__ int s_out[kMaxTreeNodes];  // deterministic drafts: tokens rejected at the current node
+  __shared__ Pair s_part[kWarps];       // sums of the warps' runs
+  __shared__ double s_sum[2];           // this block's sum, by the sweep's parity
+  __shared__ struct {
+    int what;       // 0 done, 1 a sweep, 2 the eighths of run `run`
+    int node, run;  // the row
+    int rejected;   // entries of s_out
+    float ch, cl;   // the coefficient
+  } s_cmd;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   const int b = blockIdx.x / cs;
@@ -147,262 +158,297 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(const VerifyParam
   }
   __syncthreads();
 
-  // this lane's nodes lane + 32 w: their parents (-1: none, and node 0)
-  int par[4];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) par[w] = lane + 32 * w < nodes ? s_parent[lane + 32 * w] : -1;
-  auto next_child = [&](int cur, int after) {  // the first child of cur past node `after`, -1: none
-    int found = -1;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t hit = __ballot_sync(0xffffffffu, par[w] == cur && lane + 32 * w > after);
-      if (found < 0 && hit != 0) found = 32 * w + __ffs(static_cast<int>(hit)) - 1;
-    }
-    return found;
-  };
-
   // ---- the vocabulary in 16-byte groups of a row (aligned in memory: the
   // first and the last may be cut), shared out to blocks and warps in runs
-  long long row = 0;  // element offset of the current row
-  int mis = 0, run0 = 0, run1 = 0, per_warp = 1, per_cta = 1;
-  auto set_row = [&](int node) {
-    row = (static_cast<long long>(b) * p.n + node) * p.row_stride;
-    mis = static_cast<int>(row & (N - 1));
-    const int groups = (V + mis + N - 1) / N;
-    per_cta = (groups + cs - 1) / cs;
-    per_warp = (per_cta + kWarps - 1) / kWarps;
-    const int end = min(groups, (rank + 1) * per_cta);
-    run0 = min(end, rank * per_cta + warp * per_warp);
-    run1 = min(end, run0 + per_warp);
+  struct Row {
+    long long off;  // element offset
+    int mis, groups, per_cta, per_warp;
   };
-  auto load_group = [&](const T* src, int g, float (&f)[N]) {  // elements N g - mis .. + N, zeros outside the row
-    const int v0 = N * g - mis;
+  auto row_of = [&](int node) {
+    Row r;
+    r.off = (static_cast<long long>(b) * p.n + node) * p.row_stride;
+    r.mis = static_cast<int>(r.off & (N - 1));
+    r.groups = (V + r.mis + N - 1) / N;
+    r.per_cta = (r.groups + cs - 1) / cs;
+    r.per_warp = (r.per_cta + kWarps - 1) / kWarps;
+    return r;
+  };
+  auto run_of = [&](const Row& r, int w, int* g0, int* g1) {  // warp w's run of this block's slice
+    const int end = min(r.groups, (rank + 1) * r.per_cta);
+    *g0 = min(end, rank * r.per_cta + w * r.per_warp);
+    *g1 = min(end, *g0 + r.per_warp);
+  };
+  auto eighth_of = [&](int g0, int g1, int w, int* h0, int* h1) {  // part w of a run
+    const int per = (g1 - g0 + kWarps - 1) / kWarps;
+    *h0 = min(g1, g0 + w * per);
+    *h1 = min(g1, *h0 + per);
+  };
+  auto load_group = [&](const Row& r, const T* src, int g, float (&f)[N]) {  // zeros outside the row
+    const int v0 = N * g - r.mis;
     if (v0 >= 0 && v0 + N <= V) {
-      Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(src + row + v0)), f);
+      Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(src + r.off + v0)), f);
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = v0 + e >= 0 && v0 + e < V ? to_f32(src[row + v0 + e]) : 0.f;
+      for (int e = 0; e < N; ++e) f[e] = v0 + e >= 0 && v0 + e < V ? to_f32(src[r.off + v0 + e]) : 0.f;
     }
   };
-
-  int rejected = 0;  // entries of s_out (deterministic drafts)
-  int parity = 0;
-  double cta_sum[kMaxCluster];
-  // S of the current row for the coefficient c; leaves s_warp and cta_sum
-  auto sweep = [&](double c) {
-    const float ch = static_cast<float>(c), cl = static_cast<float>(c - static_cast<double>(ch));
+  // the weight of groups [g0, g1) for the command's coefficient, on lane 0
+  auto run_sum = [&](const Row& r, int g0, int g1) {
+    const float ch = s_cmd.ch, cl = s_cmd.cl;
+    const bool with_q = Q != nullptr && (ch != 0.f || cl != 0.f);
     Pair acc = {0.f, 0.f};
-    constexpr int kU = 4;
-    for (int g0 = run0 + lane; g0 < run1; g0 += 32 * kU) {
+    constexpr int kU = 16 / N;
+#pragma unroll 1
+    for (int a = g0 + lane; a < g1; a += 32 * kU) {
       float fp[kU][N], fq[kU][N];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int g = g0 + 32 * u;
+        const int g = a + 32 * u;
 #pragma unroll
         for (int e = 0; e < N; ++e) fp[u][e] = fq[u][e] = 0.f;
-        if (g < run1) {
-          load_group(P, g, fp[u]);
-          if (Q != nullptr && c != 0.0) load_group(Q, g, fq[u]);
+        if (g < g1) {
+          load_group(r, P, g, fp[u]);
+          if (with_q) load_group(r, Q, g, fq[u]);
         }
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          const Pair r = residual(fp[u][e], fq[u][e], ch, cl);
-          if (__fadd_rn(r.hi, r.lo) > 0.f) add(acc, r.hi, r.lo);  // (NaN: no weight)
+          const Pair w = residual(fp[u][e], fq[u][e], ch, cl);
+          if (__fadd_rn(w.hi, w.lo) > 0.f) add(acc, w.hi, w.lo);  // (NaN: no weight)
         }
     }
-    double s = static_cast<double>(acc.hi) + static_cast<double>(acc.lo);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    for (int d = 16; d > 0; d >>= 1)
+      add(acc, __shfl_xor_sync(0xffffffffu, acc.hi, d), __shfl_xor_sync(0xffffffffu, acc.lo, d));
     // deterministic drafts: rejected tokens weigh nothing
-    for (int i = 0; i < rejected; ++i) {
-      const int g = (s_out[i] + mis) / N;
-      if (g >= run0 && g < run1) {
-        const float w = to_f32(P[row + s_out[i]]);
-        if (w > 0.f) s -= static_cast<double>(w);
+    for (int i = 0; i < s_cmd.rejected; ++i) {
+      const int g = (s_out[i] + r.mis) / N;
+      if (g >= g0 && g < g1) {
+        const float w = to_f32(P[r.off + s_out[i]]);
+        if (w > 0.f) add(acc, -w, 0.f);
       }
     }
-    if (lane == 0) s_warp[warp] = s > 0.0 ? s : 0.0;
-    __syncthreads();
-    double mine = 0.0;
-    for (int w = 0; w < kWarps; ++w) mine += s_warp[w];
-    if (tid == 0) s_sum[parity] = mine;
-    double total = 0.0;
-    if (cs > 1) {
-      cluster_sync_all();
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) {
-        cta_sum[r] = r < cs ? dsmem_ld_f64(dsmem_map(smem_u32(&s_sum[parity]), r)) : 0.0;
-        total += cta_sum[r];
-      }
+    if (__fadd_rn(acc.hi, acc.lo) <= 0.f) acc = {0.f, 0.f};
+    return acc;
+  };
+  // a command's share of this warp, and what follows for all warps
+  auto serve = [&]() {
+    const Row r = row_of(s_cmd.node);
+    int g0, g1;
+    if (s_cmd.what == 1) {
+      run_of(r, warp, &g0, &g1);
     } else {
-      cta_sum[0] = total = mine;
+      int r0, r1;
+      run_of(r, s_cmd.run, &r0, &r1);
+      eighth_of(r0, r1, warp, &g0, &g1);
     }
-    parity ^= 1;
-    return total;
+    const Pair s = run_sum(r, g0, g1);
+    if (lane == 0) s_part[warp] = s;
+    __syncthreads();
   };
 
-  // ---- the walk
-  int cur = 0, last = 0, kept = nodes > 0 ? 1 : 0;
-  bool swept = false;  // the sums of (cur, c) are there
-  double c = 0.0, S = 1.0;
-  if (kept) {
-    s_path[0] = 0;
-    set_row(0);
+  if (warp != 0) {
     while (true) {
-      const int child = next_child(cur, last);
-      if (child < 0) break;
-      last = child;
-      const double u = s_u[child], x = s_p[child], y = s_q[child];
-      bool accept;
-      if (Q != nullptr) {
-        const double r = x - c * y;
-        accept = u * y * S < (r > 0.0 ? r : 0.0);
+      __syncthreads();  // the command
+      const int what = s_cmd.what;
+      if (what == 0) break;
+      serve();
+      if (what == 1 && cs > 1) cluster_sync_all();
+    }
+  } else {
+    // this lane's nodes lane + 32 w: their parents (-1: none, and node 0)
+    int par[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) par[w] = lane + 32 * w < nodes ? s_parent[lane + 32 * w] : -1;
+    auto next_child = [&](int cur, int after) {  // the first child of cur past node `after`, -1: none
+      int found = -1;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t hit = __ballot_sync(0xffffffffu, par[w] == cur && lane + 32 * w > after);
+        if (found < 0 && hit != 0) found = 32 * w + __ffs(static_cast<int>(hit)) - 1;
+      }
+      return found;
+    };
+    auto command = [&](int what, int node, int run, int rejected, double c) {
+      __syncwarp();
+      if (lane == 0) {
+        const float ch = static_cast<float>(c);
+        s_cmd.what = what;
+        s_cmd.node = node;
+        s_cmd.run = run;
+        s_cmd.rejected = rejected;
+        s_cmd.ch = ch;
+        s_cmd.cl = static_cast<float>(c - static_cast<double>(ch));
+      }
+      __syncthreads();
+      if (what != 0) serve();
+    };
+    // lane i: the sum of part i (a run, or an eighth of one) as a double
+    auto parts = [&]() {
+      return lane < kWarps ? static_cast<double>(s_part[lane].hi) + static_cast<double>(s_part[lane].lo) : 0.0;
+    };
+    // inclusive running sum over the lanes, in lane order
+    auto running = [&](double x) {
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += o;
+      }
+      return x;
+    };
+    // the first lane with any weight whose running sum passes the goal (else
+    // the last with any weight, should rounding leave the goal past it)
+    auto pick = [&](double x, double incl, double goal) {
+      const uint32_t some = __ballot_sync(0xffffffffu, x > 0.0), pass = __ballot_sync(0xffffffffu, x > 0.0 && incl > goal);
+      return pass ? __ffs(static_cast<int>(pass)) - 1 : 31 - __clz(some);
+    };
+    int parity = 0;
+    double block = 0.0;  // lane r: block r's sum
+    auto sweep = [&](int node, int rejected, double c) {
+      command(1, node, 0, rejected, c);
+      const double mine = __shfl_sync(0xffffffffu, running(parts()), 31);
+      if (cs > 1) {
+        if (lane == 0) s_sum[parity] = mine;
+        cluster_sync_all();
+        block = lane < cs ? dsmem_ld_f64(dsmem_map(smem_u32(&s_sum[parity]), lane)) : 0.0;
+        parity ^= 1;
       } else {
-        bool seen = false;
-        for (int i = 0; i < rejected; ++i) seen |= s_out[i] == s_token[child];
-        const double r = seen || !(x > 0.0) ? 0.0 : x;
-        accept = u * S < r;
-        if (!accept) {
-          S -= r;
-          // (an entry for each rejected token once: the sums subtract every entry)
-          if (!seen) {
-            __syncthreads();
-            if (tid == 0) s_out[rejected] = s_token[child];
-            ++rejected;
-            __syncthreads();
-          }
-        }
+        block = lane == 0 ? mine : 0.0;
       }
-      if (accept) {
-        cur = child;
-        if (tid == 0) s_path[kept] = child;
-        ++kept;
-        c = 0.0, S = 1.0;
-        swept = false;
-        rejected = 0;
-        set_row(cur);
-      } else if (Q != nullptr && S > 0.0) {  // (S = 0: nothing is left at all, for any larger c)
-        c += S;
-        S = sweep(c);
-        swept = true;
-      }
-    }
-    if (!swept) S = sweep(c);
-  }
-  __syncthreads();
-  // ---- outputs
-  if (rank == 0) {
-    for (int i = tid; i < p.n; i += kThreads) p.path[static_cast<long long>(b) * p.n + i] = i < kept ? s_path[i] : -1;
-    if (tid == 0) {
-      p.num_kept[b] = kept;
-      if (kept == 0) p.next_token[b] = -1;
-    }
-  }
-  if (kept) {
-    if (S > 0.0) {
-      const double goal = static_cast<double>(p.u_next[b]) * S;
-      // the first block, warp, element whose running sum passes the goal (the
-      // last one with any weight, should rounding leave the goal past it)
-      int at = -1, some = 0;
-      double before = 0.0, run = 0.0;
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r)
-        if (r < cs) {
-          if (cta_sum[r] > 0.0 && at < 0) {
-            some = r;
-            before = run;
-            if (run + cta_sum[r] > goal) at = r;
-          }
-          run += cta_sum[r];
-        }
-      if ((at < 0 ? some : at) == rank) {
-        int wat = -1, wsome = 0;
-        double wbefore = before;
-        run = before;
-        for (int w = 0; w < kWarps; ++w) {
-          if (s_warp[w] > 0.0 && wat < 0) {
-            wsome = w;
-            wbefore = run;
-            if (run + s_warp[w] > goal) wat = w;
-          }
-          run += s_warp[w];
-        }
-        if ((wat < 0 ? wsome : wat) == warp) {
-          run = wbefore;
-          int token = -1, fallback = -1;
-          for (int g0 = run0; g0 < run1 && token < 0; g0 += 32) {
-            const int g = g0 + lane;
-            float fp[N], fq[N];
-#pragma unroll
-            for (int e = 0; e < N; ++e) fp[e] = fq[e] = 0.f;
-            if (g < run1) {
-              load_group(P, g, fp);
-              if (Q != nullptr && c != 0.0) load_group(Q, g, fq);
+      return __shfl_sync(0xffffffffu, running(block), 31);
+    };
+
+    // ---- the walk
+    int cur = 0, last = 0, kept = nodes > 0 ? 1 : 0, rejected = 0;
+    bool swept = false;  // the sums of (cur, c) are there
+    double c = 0.0, S = 1.0;
+    if (kept) {
+      if (lane == 0) s_path[0] = 0;
+      while (true) {
+        const int child = next_child(cur, last);
+        if (child < 0) break;
+        last = child;
+        const double u = s_u[child], x = s_p[child], y = s_q[child];
+        bool accept;
+        if (Q != nullptr) {
+          const double r = x - c * y;
+          accept = u * y * S < (r > 0.0 ? r : 0.0);
+        } else {
+          bool seen = false;
+          for (int i = 0; i < rejected; ++i) seen |= s_out[i] == s_token[child];
+          const double r = seen || !(x > 0.0) ? 0.0 : x;
+          accept = u * S < r;
+          if (!accept) {
+            S -= r;
+            // (an entry for each rejected token once: the sums subtract every entry)
+            if (!seen) {
+              if (lane == 0) s_out[rejected] = s_token[child];
+              ++rejected;
+              __syncwarp();
             }
-            double w[N], sum = 0.0;
-            int mine = -1;  // this lane's last element with any weight
+          }
+        }
+        if (accept) {
+          cur = child;
+          if (lane == 0) s_path[kept] = child;
+          ++kept;
+          c = 0.0, S = 1.0;
+          swept = false;
+          rejected = 0;
+        } else if (Q != nullptr && S > 0.0) {  // (S = 0: nothing is left at all, for any larger c)
+          c += S;
+          S = sweep(cur, 0, c);
+          swept = true;
+        }
+      }
+      if (!swept) S = sweep(cur, rejected, c);
+    }
+    __syncwarp();
+    // ---- outputs
+    if (rank == 0) {
+      for (int i = lane; i < p.n; i += 32) p.path[static_cast<long long>(b) * p.n + i] = i < kept ? s_path[i] : -1;
+      if (lane == 0) {
+        p.num_kept[b] = kept;
+        if (kept == 0) p.next_token[b] = -1;
+      }
+    }
+    if (kept && S > 0.0) {
+      const double goal = static_cast<double>(p.u_next[b]) * S;
+      const double upto = running(block);
+      const int at = pick(block, upto, goal);
+      if (at == rank) {
+        double before = __shfl_sync(0xffffffffu, upto - block, at);
+        const Row r = row_of(cur);
+        double x = parts(), incl = running(x);
+        const int run = pick(x, before + incl, goal);
+        before += __shfl_sync(0xffffffffu, incl - x, run);
+        command(2, cur, run, rejected, c);
+        x = parts();
+        incl = running(x);
+        const int part = pick(x, before + incl, goal);
+        before += __shfl_sync(0xffffffffu, incl - x, part);
+        int r0, r1, h0, h1;
+        run_of(r, run, &r0, &r1);
+        eighth_of(r0, r1, part, &h0, &h1);
+        int token = -1, fallback = 0;
+        for (int a = h0; a < h1 && token < 0; a += 32) {
+          const int g = a + lane;
+          float fp[N], fq[N];
+#pragma unroll
+          for (int e = 0; e < N; ++e) fp[e] = fq[e] = 0.f;
+          if (g < h1) {
+            load_group(r, P, g, fp);
+            if (Q != nullptr && c != 0.0) load_group(r, Q, g, fq);
+          }
+          double w[N], sum = 0.0;
+          int mine = -1;  // this lane's last element with any weight
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const double d = static_cast<double>(fp[e]) - c * static_cast<double>(fq[e]);
+            w[e] = d > 0.0 ? d : 0.0;
+            for (int i = 0; i < rejected; ++i)
+              if (s_out[i] == N * g - r.mis + e) w[e] = 0.0;
+            sum += w[e];
+            if (w[e] > 0.0) mine = N * g - r.mis + e;
+          }
+          const double in = running(sum);
+          const uint32_t pass = __ballot_sync(0xffffffffu, sum > 0.0 && before + in > goal);
+          const uint32_t any = __ballot_sync(0xffffffffu, mine >= 0);
+          if (any) fallback = __shfl_sync(0xffffffffu, mine, 31 - __clz(any));
+          if (pass) {
+            double acc = before + in - sum;
+            int hit = -1;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-              const double r = static_cast<double>(fp[e]) - c * static_cast<double>(fq[e]);
-              w[e] = r > 0.0 ? r : 0.0;
-              for (int i = 0; i < rejected; ++i)
-                if (s_out[i] == N * g - mis + e) w[e] = 0.0;
-              sum += w[e];
-              if (w[e] > 0.0) mine = N * g - mis + e;
+              acc += w[e];
+              if (hit < 0 && w[e] > 0.0 && acc > goal) hit = N * g - r.mis + e;
             }
-            double incl = sum;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-              const double o = __shfl_up_sync(0xffffffffu, incl, d);
-              if (lane >= d) incl += o;
-            }
-            const uint32_t pass = __ballot_sync(0xffffffffu, run + incl > goal && sum > 0.0);
-            const uint32_t any = __ballot_sync(0xffffffffu, mine >= 0);
-            if (any) fallback = __shfl_sync(0xffffffffu, mine, 31 - __clz(any));
-            if (pass) {
-              const int who = __ffs(static_cast<int>(pass)) - 1;
-              double a = run + incl - sum;
-              int hit = -1;
-#pragma unroll
-              for (int e = 0; e < N; ++e) {
-                a += w[e];
-                if (hit < 0 && w[e] > 0.0 && a > goal) hit = N * g - mis + e;
-              }
-              if (hit < 0) hit = mine;
-              token = __shfl_sync(0xffffffffu, hit, who);
-            }
-            run += __shfl_sync(0xffffffffu, incl, 31);
+            token = __shfl_sync(0xffffffffu, hit < 0 ? mine : hit, __ffs(static_cast<int>(pass)) - 1);
           }
-          if (lane == 0) p.next_token[b] = token >= 0 ? token : fallback;
+          before += __shfl_sync(0xffffffffu, in, 31);
         }
+        if (lane == 0) p.next_token[b] = token >= 0 ? token : fallback;
       }
-    } else {
+    } else if (kept && rank == 0) {
       // nothing is left (p <= c q everywhere): the target's most probable token, the lowest of equals
+      const Row r = row_of(cur);
       float top = -INFINITY;
       int at = 0x7fffffff;
-      if (rank == 0) {
-        for (int v = tid; v < V; v += kThreads) {
-          const float f = to_f32(P[row + v]);
-          if (f > top) top = f, at = v;
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-          const float o = __shfl_xor_sync(0xffffffffu, top, d);
-          const int oa = __shfl_xor_sync(0xffffffffu, at, d);
-          if (o > top || (o == top && oa < at)) top = o, at = oa;
-        }
-        if (lane == 0) s_top[warp] = top, s_at[warp] = at;
-        __syncthreads();
-        if (tid == 0) {
-          for (int w = 1; w < kWarps; ++w)
-            if (s_top[w] > top || (s_top[w] == top && s_at[w] < at)) top = s_top[w], at = s_at[w];
-          p.next_token[b] = at < V ? at : 0;
-        }
+      for (int v = lane; v < V; v += 32) {
+        const float f = to_f32(P[r.off + v]);
+        if (f > top) top = f, at = v;
       }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, top, d);
+        const int oa = __shfl_xor_sync(0xffffffffu, at, d);
+        if (o > top || (o == top && oa < at)) top = o, at = oa;
+      }
+      if (lane == 0) p.next_token[b] = at < V ? at : 0;
     }
+    command(0, 0, 0, 0, 0.0);
   }
   if (cs > 1) cluster_sync_all();  // no block leaves while another reads its sum
 }
@@ -410,10 +456,10 @@ __global__ void __launch_bounds__(kThreads) verify_tree_kernel(const VerifyParam
 }  // namespace
 
 cudaError_t launch_verify_tree(const VerifyParams& p, int sms, cudaStream_t stream) {
-  // blocks per sequence: as many as fill the GPU (four 512-thread blocks an
-  // SM), each with 4096 tokens of the vocabulary or more
+  // blocks per sequence: as many as fill the GPU once (three blocks an SM),
+  // each with 2048 tokens of the vocabulary or more
   int cs = kMaxCluster;
-  while (cs > 1 && (static_cast<long long>(p.batch) * cs > 4ll * sms || static_cast<long long>(cs) * 4096 > p.vocab))
+  while (cs > 1 && (static_cast<long long>(p.batch) * cs > 3ll * sms || static_cast<long long>(cs) * 2048 > p.vocab))
     cs >>= 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * cs);

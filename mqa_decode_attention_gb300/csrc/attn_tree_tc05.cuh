@@ -32,10 +32,14 @@
 // kernel.
 //
 // One-byte caches: the loader's tiles are codes (16 KB), eight converter warps
-// widen each to a bf16 tile -- exactly: an e5m2 value has 3 significant bits,
-// code - zero point is an integer up to 255 -- and, for uint8, put the rows'
-// scales beside it: a K scale multiplies its column of S, a V scale its
-// column of P, in fp32.
+// widen each to a 16-bit tile, exactly. An e5m2 code is the high byte of an
+// IEEE half: K and V become f16, and Q and P enter as f16 too. A uint8 code
+// minus its zero point is an integer up to 255: K becomes f16 (two cheap
+// instructions for two codes), V bf16, so that P times its row's scale, of any
+// size, keeps bf16's range. For uint8 the rows' scales are put beside the
+// tile: a K scale multiplies its column of S, a V scale its column of P, in
+// fp32. Q's rows are made f16 in shared memory, each scaled by a power of two
+// of its own.
 //
 // Keys that no node may read (past the sequence, before the window) have zero
 // V rows whatever the cache holds, so that 0 * NaN never enters a sum.
@@ -97,8 +101,11 @@ struct Cfg {
   // for every phase of its barriers, so that a parity never stands for an
   // older phase.
   static constexpr int kSlots = kByte ? 4 : (NT == 1 ? 6 : 5);
-  static constexpr int kRawK = kByte ? (NT == 1 ? 2 : 1) : 0;
-  static constexpr int kRawV = kByte ? (NT == 1 && DT != kDtypeU8 ? 2 : 1) : 0;
+  // (uint8 has room for three code tiles; K's are widened in less time)
+  static constexpr int kRawK = kByte ? (NT == 1 && DT != kDtypeU8 ? 2 : 1) : 0;
+  static constexpr int kRawV = kByte ? (NT == 1 ? 2 : 1) : 0;
+  static constexpr bool kHalfQK = kByte;              // S = Q K^T on f16 operands
+  static constexpr bool kHalfPV = DT == kDtypeF8;     // O += P V on f16 operands (else bf16)
   static constexpr int kRaw = kRawK + kRawV;
   static_assert(!kByte || kSlots % 2 == 0, "tile ring");
   static_assert(NT == 1 || DT != kDtypeU8, "no room for two row tiles beside the scales");
@@ -117,7 +124,8 @@ struct Cfg {
   static constexpr int kQFull = 0;
   static constexpr int kQFree = 1;                  // a segment of two row tiles is done with Q
   static constexpr int kXFree = 2;                  // one of one row tile: its accumulators have met
-  static constexpr int kFull = 3;                   // [kSlots]
+  static constexpr int kQReady = 3;                 // [2] one-byte caches: Q's row tile is f16
+  static constexpr int kFull = 5;                   // [kSlots]
   static constexpr int kEmpty = kFull + kSlots;     // [kSlots]
   static constexpr int kRFull = kEmpty + kSlots;    // [kRaw]
   static constexpr int kREmpty = kRFull + kRaw;     // [kRaw]
@@ -130,7 +138,7 @@ struct Cfg {
   static constexpr int kDrain = kPart + 1;
   static constexpr int kNBars = kDrain + 1;
   static_assert(kNBars * 8 + 4 <= 256, "barrier area");
-  static_assert(kSmemBytes + 1500 <= 227 * 1024, "shared memory (with the static part)");
+  static_assert(kSmemBytes + 1600 <= 227 * 1024, "shared memory (with the static part)");
 };
 
 __device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
@@ -173,20 +181,64 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Four e5m2 codes as two bf16 pairs: a code is the high byte of an IEEE half.
-__device__ __forceinline__ uint2 widen_e5m2(uint32_t w) {
-  const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
+// Four e5m2 codes as two f16 pairs: a code is the high byte of an IEEE half.
+__device__ __forceinline__ uint2 half_e5m2(uint32_t w) {
+  return make_uint2(__byte_perm(w, 0u, 0x1404), __byte_perm(w, 0u, 0x3424));
 }
-// four uint8 codes minus the zero point (z = 2^23 + zero point)
+// Four uint8 codes minus the zero point as two f16 pairs (z = 1024 + zero point
+// twice): 0x6400 | code is the half 1024 + code, and the difference is exact.
+__device__ __forceinline__ uint2 half_u8(uint32_t w, uint32_t z) {
+  uint2 r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r.x) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(z));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r.y) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(z));
+  return r;
+}
+// ... as two bf16 pairs (z = 2^23 + zero point)
 __device__ __forceinline__ uint2 widen_u8(uint32_t w, float z) {
   const float f0 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650)) - z;
   const float f1 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7651)) - z;
   const float f2 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7652)) - z;
   const float f3 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7653)) - z;
   return make_uint2(pack_bf16x2(f0, f1), pack_bf16x2(f2, f3));
+}
+
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack_p(float2 v) {
+  if constexpr (HALF) {
+    const __half2 h = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return pack_bf16x2(v.x, v.y);
+  }
+}
+
+// Row r of a bf16 Q tile in place as f16, times the power of two that brings its
+// largest magnitude to [2^9, 2^10), which is returned (1 for a row of zeros or
+// with an infinity or NaN).
+__device__ __forceinline__ float half_row(unsigned char* tile, int r) {
+  uint32_t top = 0;  // the largest magnitudes' bit patterns, which order as the values do
+  auto chunk = [&](int x) { return reinterpret_cast<uint4*>(tile + (x >> 3) * 16384 + r * 128 + (((x & 7) ^ (r & 7)) << 4)); };
+#pragma unroll 4
+  for (int x = 0; x < 16; ++x) {
+    const uint4 w = *chunk(x);
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+  }
+  const uint32_t m = max(top & 0xffffu, top >> 16);  // bf16 bits
+  const int e = static_cast<int>(m >> 7);            // biased exponent
+  // 2^(9 - (e - 127)); the smallest rows stop at 2^126
+  const float f = m == 0 || e == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(min(127 + 9 + 127 - e, 253)) << 23);
+#pragma unroll 4
+  for (int x = 0; x < 16; ++x) {
+    uint4 w = *chunk(x);
+    uint32_t* v = &w.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(bf16lo_to_f32(v[i]) * f, bf16hi_to_f32(v[i]) * f);
+      v[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *chunk(x) = w;
+  }
+  return f;
 }
 
 // N lanes (aligned groups of 8 or 4) hold N pieces of four words each: lane i's
@@ -229,6 +281,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + C::kNBars * 8);
   __shared__ TreePlan plan;
   __shared__ int s_abort, s_skip, s_flag, s_pending, s_more[2], s_last[2];
+  // what the two accumulators' threads of a row hand over: maxima and sums; at
+  // a segment's start (one-byte caches) the row's score factor
   __shared__ float s_m[kBM], s_l[kBM];
   // the softmax warps' segment (two places: one may still be read while the
   // next is written) and the walk that gives it, kept out of their registers
@@ -249,6 +303,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     mbar_init(bar(C::kQFull), 1);
     mbar_init(bar(C::kQFree), 1);
     mbar_init(bar(C::kXFree), 8);
+    mbar_init(bar(C::kQReady + 0), 4);
+    mbar_init(bar(C::kQReady + 1), 4);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(C::kFull + s), kByte ? 4 : 1);
       mbar_init(bar(C::kEmpty + s), 1);
@@ -413,8 +469,10 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     regs_aux();
     // ----------------------------------------------------------- MMA issue
     if (lane == 0) {
-      constexpr uint32_t id_s = tc05::idesc_bf16_f32(kBM, kBN, false, false);
-      constexpr uint32_t id_o = tc05::idesc_bf16_f32(kBM, kD, false, true);
+      constexpr uint32_t id_s = C::kHalfQK ? tc05::idesc_f16_f32(kBM, kBN, false, false)
+                                           : tc05::idesc_bf16_f32(kBM, kBN, false, false);
+      constexpr uint32_t id_o = C::kHalfPV ? tc05::idesc_f16_f32(kBM, kD, false, true)
+                                           : tc05::idesc_bf16_f32(kBM, kD, false, true);
       auto wait = [&](int id, int parity) {  // polls: a suspended wait wakes late
         if (mbar_test(bar(id), parity & 1)) return true;
         const unsigned long long t0 = global_timer_ns();
@@ -458,13 +516,17 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       auto free_k = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t) % kSlots)); };
       auto free_v = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t + 1) % kSlots)); };
       bool ok = true;
-      int seg = 0;
+      int seg = 0, n_two = 0;
       s_mma_walk = walk;
       while (ok && s_mma_walk.next(p, kBN, rows_per_block, s_mma_seg)) {
         const int T = s_mma_seg.nt;
-        ok = wait(C::kQFull, seg) && full(u0);
-        if (!ok) break;
         const bool two = is_two(s_mma_seg);
+        n_two += two;
+        if constexpr (C::kHalfQK)
+          ok = wait(C::kQReady + 0, seg) && (!two || wait(C::kQReady + 1, n_two - 1)) && full(u0);
+        else
+          ok = wait(C::kQFull, seg) && full(u0);
+        if (!ok) break;
         issue_s(0, 0, 0);
         if (two) {
           issue_s(1, 0, 1);
@@ -592,7 +654,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           if (!ok) break;
           const unsigned char* src = smem + C::kRawOff + rs * kRawBytes + r * 128;
           unsigned char* dst = smem + C::kRingOff + slot * kTileBytes + r * 128;
-          const float z = 8388608.f + now.y;
+          const float zf = 8388608.f + now.y;
+          const uint32_t zh = 0x00010001u * static_cast<uint32_t>(__half_as_ushort(__float2half_rn(1024.f + now.y)));
 #pragma unroll
           for (int c0 = 0; c0 < 8; c0 += 2) {  // 32 codes
             uint4 w[2];
@@ -602,10 +665,12 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             for (int x = 0; x < 2; ++x) {
               const int c = c0 + x;
               uint2 a, b, e, f;
-              if constexpr (DT == kDtypeU8) {
-                a = widen_u8(w[x].x, z), b = widen_u8(w[x].y, z), e = widen_u8(w[x].z, z), f = widen_u8(w[x].w, z);
+              if constexpr (DT == kDtypeF8) {
+                a = half_e5m2(w[x].x), b = half_e5m2(w[x].y), e = half_e5m2(w[x].z), f = half_e5m2(w[x].w);
+              } else if (kv == 0) {
+                a = half_u8(w[x].x, zh), b = half_u8(w[x].y, zh), e = half_u8(w[x].z, zh), f = half_u8(w[x].w, zh);
               } else {
-                a = widen_e5m2(w[x].x), b = widen_e5m2(w[x].y), e = widen_e5m2(w[x].z), f = widen_e5m2(w[x].w);
+                a = widen_u8(w[x].x, zf), b = widen_u8(w[x].y, zf), e = widen_u8(w[x].z, zf), f = widen_u8(w[x].w, zf);
               }
               if (!live) a = b = e = f = make_uint2(0u, 0u);
               unsigned char* d = dst + (c >> 2) * 16384;
@@ -631,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     const int q = warp >> 2, r = tid - q * kBM;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t scol = tmem + lane_base + kColS + q * 128, ocol = tmem + lane_base + kColO + q * 128;
-    const float c = p.scale_log2;
+    float c = p.scale_log2;  // (one-byte caches: over the factor that Q's row was scaled by)
     const bool warp_rows = (warp & 3) * 32 < acc_rows;  // some lane of this warp holds a row
     bool waited = !p.early;
     int u0 = 0, seg = 0, js = 0;  // first load of the segment; segments; tiles of this accumulator
@@ -654,6 +719,23 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       const int ka = tree_first_key(p, g.b, g.s, node), pos = g.s.pos;
       const int nt = g.nt;
       int key0 = g.s.first + (g.t0 + (two ? 0 : q)) * kBN;
+      if constexpr (C::kHalfQK) {
+        // Q's rows as f16, each scaled by a power of two to a largest magnitude
+        // in [2^9, 2^10): exact for all but values 2^24 below the row's largest
+        if (two || q == 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kQFull), seg & 1, p.wait_ns) && !stop());
+          if (ok && r < acc_rows) {
+            c = p.scale_log2 / half_row(smem + C::kQOff + (two ? q : 0) * kTileBytes, r);
+            if (!two) s_m[r] = c;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(bar(C::kQReady + (two ? q : 0)));
+        } else {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kQReady + 0), seg & 1, p.wait_ns) && !stop());
+          c = s_m[r];
+        }
+      }
       float m_ref = -INFINITY, l = 0.f;
       for (int t = two ? 0 : q; ok && t < nt; t += step, ++js, key0 += step * kBN) {
         // only tiles that reach a node, the end or the window are masked: bit x
@@ -773,8 +855,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
                 p0 = mul2(p0, make_float2(f.x, f.y));
                 p1 = mul2(p1, make_float2(f.z, f.w));
               }
-              pk[i] = pack_bf16x2(p0.x, p0.y);
-              pk[i + 1] = pack_bf16x2(p1.x, p1.y);
+              pk[i] = pack_p<C::kHalfPV>(p0);
+              pk[i + 1] = pack_p<C::kHalfPV>(p1);
             }
             tc05::st_32x32b_x16_u(scol + 16 * x, pk);
           };

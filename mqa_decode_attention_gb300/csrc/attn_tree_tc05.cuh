@@ -861,19 +861,17 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             tc05::st_32x32b_x16_u(scol + 16 * x, pk);
           };
 #pragma unroll 1
-          for (int x = 0; x < kBN / 32; x += 2) {
-            float s0[32], s1[32];
+          for (int x = 0; x < kBN / 32; ++x) {
+            float s0[32];
             tc05::ld_32x32b_x32(scol + 32 * x, s0);
-            tc05::ld_32x32b_x32(scol + 32 * x + 32, s1);
             scores(x, s0);
-            scores(x + 1, s1);
             probs(x, s0);
-            probs(x + 1, s1);
+            if (!(x & 1)) continue;
             // these 64 keys' P is in tensor memory: their products may start
             tc05::wait_st();
             tc05::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar((x == 0 ? C::kP : C::kPHi) + q));
+            if (lane == 0) mbar_arrive(bar((x == 1 ? C::kP : C::kPHi) + q));
           }
           l += ((sm4[0].x + sm4[0].y) + (sm4[1].x + sm4[1].y)) + ((sm4[2].x + sm4[2].y) + (sm4[3].x + sm4[3].y));
         } else {  // no rows here: the arrivals that the products wait for

@@ -241,6 +241,63 @@ __device__ __forceinline__ float half_row(unsigned char* tile, int r) {
   return f;
 }
 
+// Groups of products issued by one elected lane of a converged warp (always the
+// same one, as the commits). The warp's control flow is uniform, so that the
+// descriptors can stay in uniform registers: issued by a lane inside a
+// divergent branch, with the operands moved there one by one, a group of eight
+// took as long to issue as to run.
+// D = A B^T over 128 values of K: A and B K-major in shared memory, B's second
+// 64 values BH descriptor units after the first.
+template <int BH>
+__device__ __forceinline__ void mma_128(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred e, z, o;\n\t.reg .b64 x, y;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 z, 0, 0;\n\tsetp.eq.b32 o, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\t"
+      "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, 1024;\n\tadd.s64 y, %2, %4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, 1026;\n\tadd.s64 y, %2, %5;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, 1028;\n\tadd.s64 y, %2, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t"
+      "add.s64 x, %1, 1030;\n\tadd.s64 y, %2, %7;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, o;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "n"(BH), "n"(BH + 2), "n"(BH + 4), "n"(BH + 6)
+      : "memory");
+}
+// D (+)= A B over 64 values of K (keys): A in tensor memory, 8 columns for 16
+// keys, B MN-major in shared memory, 16 keys BK descriptor units apart.
+template <int BK>
+__device__ __forceinline__ void mma_64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred e, z, o;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 z, %4, 0;\n\tsetp.eq.b32 o, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, z;\n\t"
+      "add.s32 x, %1, 8;\n\tadd.s64 y, %2, %5;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
+      "add.s32 x, %1, 16;\n\tadd.s64 y, %2, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
+      "add.s32 x, %1, 24;\n\tadd.s64 y, %2, %7;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "n"(BK), "n"(2 * BK), "n"(3 * BK)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elect(uint32_t mbar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(mbar)
+      : "memory");
+}
+
 // N lanes (aligned groups of 8 or 4) hold N pieces of four words each: lane i's
 // piece j goes to lane j's place i.
 template <int N>
@@ -468,42 +525,38 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   } else if (warp == 9) {
     regs_aux();
     // ----------------------------------------------------------- MMA issue
-    if (lane == 0) {
+    // (the whole warp, converged; one elected lane issues)
+    {
       constexpr uint32_t id_s = C::kHalfQK ? tc05::idesc_f16_f32(kBM, kBN, false, false)
                                            : tc05::idesc_bf16_f32(kBM, kBN, false, false);
       constexpr uint32_t id_o = C::kHalfPV ? tc05::idesc_f16_f32(kBM, kD, false, true)
                                            : tc05::idesc_bf16_f32(kBM, kD, false, true);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sb = __shfl_sync(0xffffffffu, sbase, 0);
       auto wait = [&](int id, int parity) {  // polls: a suspended wait wakes late
-        if (mbar_test(bar(id), parity & 1)) return true;
+        if (__all_sync(0xffffffffu, mbar_test(bar(id), parity & 1))) return true;
         const unsigned long long t0 = global_timer_ns();
-        while (!mbar_test(bar(id), parity & 1))
-          if (stop() || global_timer_ns() - t0 > p.wait_ns) return false;
+        while (!__all_sync(0xffffffffu, mbar_test(bar(id), parity & 1)))
+          if (__any_sync(0xffffffffu, stop() || global_timer_ns() - t0 > p.wait_ns)) return false;
         return true;
       };
       int u0 = 0;            // the segment's first load
       int ps[2] = {0, 0};    // products P V issued into each accumulator
       auto full = [&](int u) { return wait(C::kFull + u % kSlots, u / kSlots); };
       auto issue_s = [&](int q, int t, int qt) {  // S_q = Q K(t)^T, Q's row tile qt
-        const uint32_t q_s = sbase + C::kQOff + qt * kTileBytes;
-        const uint32_t k_s = sbase + C::kRingOff + ((u0 + 2 * t) % kSlots) * kTileBytes;
         tc05::fence_after_sync();
-        // (the descriptors' address field counts 16 bytes: the sub-tiles are constant steps)
-        const uint64_t qd = tc05::smem_desc_sw128(q_s, 16, 1024), kd = tc05::smem_desc_sw128(k_s, 16, L::kGroup);
-#pragma unroll
-        for (int ks = 0; ks < kD / 16; ++ks)
-          tc05::mma_bf16(tmem + kColS + q * 128, qd + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                         kd + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4), id_s, ks > 0);
-        tc05::commit(bar(C::kSFull + q));
+        mma_128<L::kHalf / 16>(tm + kColS + q * 128, tc05::smem_desc_sw128(sb + C::kQOff + qt * kTileBytes, 16, 1024),
+                               tc05::smem_desc_sw128(sb + C::kRingOff + ((u0 + 2 * t) % kSlots) * kTileBytes, 16, L::kGroup),
+                               id_s);
+        commit_elect(bar(C::kSFull + q));
       };
       // O_q (+)= P_q V(t) of keys 64 h .. 64 h + 63: each half of P as soon as it is written
       auto issue_pv = [&](int q, int t, int h, bool add) {
-        const uint32_t v_s = sbase + C::kRingOff + ((u0 + 2 * t + 1) % kSlots) * kTileBytes;
         tc05::fence_after_sync();
-        const uint64_t vd = tc05::smem_desc_sw128(v_s + h * 8 * L::kGroup, L::kHalf, L::kGroup);
-        const uint32_t pa = tmem + kColS + q * 128 + h * 32;
-#pragma unroll
-        for (int ks = 0; ks < kBN / 32; ++ks)
-          tc05::mma_bf16_ta(tmem + kColO + q * 128, pa + ks * 8, vd + ((ks * 2 * L::kGroup) >> 4), id_o, add || h > 0 || ks > 0);
+        mma_64<2 * L::kGroup / 16>(
+            tm + kColO + q * 128, tm + kColS + q * 128 + h * 32,
+            tc05::smem_desc_sw128(sb + C::kRingOff + ((u0 + 2 * t + 1) % kSlots) * kTileBytes + h * 8 * L::kGroup, L::kHalf,
+                                  L::kGroup),
+            id_o, add || h > 0);
       };
       auto pv = [&](int q, int t, bool add) {
         const int n = ps[q]++;
@@ -513,12 +566,16 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         issue_pv(q, t, 1, add);
         return true;
       };
-      auto free_k = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t) % kSlots)); };
-      auto free_v = [&](int t) { tc05::commit(bar(C::kEmpty + (u0 + 2 * t + 1) % kSlots)); };
+      auto free_k = [&](int t) { commit_elect(bar(C::kEmpty + (u0 + 2 * t) % kSlots)); };
+      auto free_v = [&](int t) { commit_elect(bar(C::kEmpty + (u0 + 2 * t + 1) % kSlots)); };
       bool ok = true;
       int seg = 0, n_two = 0;
-      s_mma_walk = walk;
-      while (ok && s_mma_walk.next(p, kBN, rows_per_block, s_mma_seg)) {
+      if (lane == 0) s_mma_walk = walk;
+      while (ok) {
+        __syncwarp();
+        bool more = false;
+        if (lane == 0) more = s_mma_walk.next(p, kBN, rows_per_block, s_mma_seg);
+        if (!__shfl_sync(0xffffffffu, more, 0)) break;
         const int T = s_mma_seg.nt;
         const bool two = is_two(s_mma_seg);
         n_two += two;
@@ -530,7 +587,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         issue_s(0, 0, 0);
         if (two) {
           issue_s(1, 0, 1);
-          if (T == 1) tc05::commit(bar(C::kQFree));
+          if (T == 1) commit_elect(bar(C::kQFree));
         }
         free_k(0);
         if (!two && T > 1) {
@@ -557,7 +614,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             if (t + 1 < T) {
               issue_s(1, t + 1, 1);
               free_k(t + 1);
-              if (t + 2 == T) tc05::commit(bar(C::kQFree));
+              if (t + 2 == T) commit_elect(bar(C::kQFree));
             }
           }
         } else {
@@ -574,11 +631,11 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             }
           }
         }
-        if (ok) tc05::commit(bar(C::kODone));
+        if (ok) commit_elect(bar(C::kODone));
         u0 += 2 * T;
         ++seg;
       }
-      if (!ok) fail(true);
+      if (!ok) fail(lane == 0);
     }
     __syncwarp();
   } else if (warp == 11) {
@@ -656,7 +713,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           unsigned char* dst = smem + C::kRingOff + slot * kTileBytes + r * 128;
           const float zf = 8388608.f + now.y;
           const uint32_t zh = 0x00010001u * static_cast<uint32_t>(__half_as_ushort(__float2half_rn(1024.f + now.y)));
-#pragma unroll
+#pragma unroll 1
           for (int c0 = 0; c0 < 8; c0 += 2) {  // 32 codes
             uint4 w[2];
 #pragma unroll
@@ -1033,10 +1090,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     if (*reinterpret_cast<volatile int*>(&s_abort)) {
       // products may still be in flight after a timeout: wait (bounded) for
       // them before the columns are released
-      if (lane == 0) {
-        tc05::commit(bar(C::kDrain));
-        (void)mbar_wait(bar(C::kDrain), 0, kWaitLimitNs);
-      }
+      commit_elect(bar(C::kDrain));  // (the lane that issued them)
+      if (lane == 0) (void)mbar_wait(bar(C::kDrain), 0, kWaitLimitNs);
       __syncwarp();
     }
     tc05::fence_after_sync();

@@ -37,11 +37,14 @@ constexpr int kRows = 64;    // rows per block
 constexpr int kKeys = 64;    // keys per tile
 constexpr int kThreads = 128;
 
-template <int D>
+template <int D, bool BYTE>
 struct Lay {
-  static constexpr int kTile = kKeys * D * 2;   // one bf16 tile
-  static constexpr int kK = 0, kV = 2 * kTile;  // [2] each
-  static constexpr int kScale = 4 * kTile;      // uint8: K, V scales [2][2][kKeys]
+  static constexpr int kTile = kKeys * D * 2;          // one bf16 tile
+  // bf16: four tiles in flight at d = 64 (two: half the rate); one-byte caches
+  // hold the next tile in registers
+  static constexpr int kStages = BYTE || D == 128 ? 2 : 4;
+  static constexpr int kK = 0, kV = kStages * kTile;   // [kStages] each
+  static constexpr int kScale = 2 * kStages * kTile;   // uint8: K, V scales [2][2][kKeys]
   static constexpr int kBytes = kScale + 4 * kKeys * 4;
 };
 
@@ -75,7 +78,8 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, float z) {
 
 template <int D, int DT>
 __global__ void __launch_bounds__(kThreads) attn_tree_kernel(const TreeParams p) {
-  using Y = Lay<D>;
+  using Y = Lay<D, DT != kDtypeBf16>;
+  constexpr int kStages = Y::kStages;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ TreePlan plan;
   __shared__ int s_flag;
@@ -184,19 +188,27 @@ __global__ void __launch_bounds__(kThreads) attn_tree_kernel(const TreeParams p)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-    request(0, 0);
+    // (a group is committed for each tile, past the last one too: the count of
+    // groups behind tile t is then always kStages - 1)
+    auto ahead = [&](int t) {
+      if (t < g.nt)
+        request(t, t % kStages);
+      else if constexpr (!kByte)
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (kByte) {
+      ahead(0);
+    } else {
+      for (int t = 0; t < kStages - 1; ++t) ahead(t);
+    }
     for (int t = 0; t < g.nt; ++t) {
-      const int st = t & 1;
+      const int st = t % kStages;
       if constexpr (kByte) {
         land(st);
-        if (t + 1 < g.nt) request(t + 1, st ^ 1);
+        ahead(t + 1);
       } else {
-        if (t + 1 < g.nt) {
-          request(t + 1, st ^ 1);
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
+        ahead(t + kStages - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       }
       __syncthreads();
       const uint32_t ks = sb + Y::kK + st * Y::kTile, vs = sb + Y::kV + st * Y::kTile;
@@ -345,12 +357,13 @@ __global__ void __launch_bounds__(kThreads) attn_tree_kernel(const TreeParams p)
 template <int D, int DT>
 cudaError_t launch_t(const TreeParams& p, int ctas, cudaStream_t stream) {
   auto kern = attn_tree_kernel<D, DT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kBytes);
+  constexpr int smem = Lay<D, DT != kDtypeBf16>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Lay<D>::kBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -95,20 +95,12 @@ struct Cfg {
   static constexpr int kRegsConvert = DT == kDtypeU8 ? 56 : 48;
   static_assert(256 * kRegsSoftmax + 128 * kRegsAux + (kThreads - 384) * kRegsConvert <= kThreads * kRegsLaunch,
                 "register split");
-  // bf16 tiles, and code tiles (K's and V's). A tile ring that two converter
-  // groups fill has an even number of places, and the code tiles of K and of V
-  // have rings of their own: each place then belongs to one group, which waits
-  // for every phase of its barriers, so that a parity never stands for an
-  // older phase.
+  // 16-bit tiles, and code tiles
   static constexpr int kSlots = kByte ? 4 : (NT == 1 ? 6 : 5);
-  // (uint8 has room for three code tiles; K's are widened in less time)
-  static constexpr int kRawK = kByte ? (NT == 1 && DT != kDtypeU8 ? 2 : 1) : 0;
-  static constexpr int kRawV = kByte ? (NT == 1 ? 2 : 1) : 0;
+  static constexpr int kRaw = kByte ? (NT == 2 ? 2 : (DT == kDtypeU8 ? 3 : 4)) : 0;
+  static_assert(NT == 1 || DT != kDtypeU8, "no room for two row tiles beside the scales");
   static constexpr bool kHalfQK = kByte;              // S = Q K^T on f16 operands
   static constexpr bool kHalfPV = DT == kDtypeF8;     // O += P V on f16 operands (else bf16)
-  static constexpr int kRaw = kRawK + kRawV;
-  static_assert(!kByte || kSlots % 2 == 0, "tile ring");
-  static_assert(NT == 1 || DT != kDtypeU8, "no room for two row tiles beside the scales");
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = NT * kTileBytes;
   static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
@@ -195,11 +187,12 @@ __device__ __forceinline__ uint2 half_u8(uint32_t w, uint32_t z) {
 }
 // ... as two bf16 pairs (z = 2^23 + zero point)
 __device__ __forceinline__ uint2 widen_u8(uint32_t w, float z) {
-  const float f0 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650)) - z;
-  const float f1 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7651)) - z;
-  const float f2 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7652)) - z;
-  const float f3 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7653)) - z;
-  return make_uint2(pack_bf16x2(f0, f1), pack_bf16x2(f2, f3));
+  const float2 nz = make_float2(-z, -z);
+  const float2 a = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650)),
+                                    __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7651))), nz);
+  const float2 b = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7652)),
+                                    __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7653))), nz);
+  return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
 }
 
 template <bool HALF>
@@ -329,9 +322,6 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   constexpr bool kGrouped = PG && !kByte;
   using L = Tile<kGrouped>;
   constexpr int kSlots = C::kSlots;
-  // place and phase of load u (2 t + 0 / 1: K / V of the run's tile t) among the code tiles
-  auto raw_slot = [](int u) { return (u & 1) ? C::kRawK + (u >> 1) % max(C::kRawV, 1) : (u >> 1) % max(C::kRawK, 1); };
-  auto raw_lap = [](int u) { return (u >> 1) / max((u & 1) ? C::kRawV : C::kRawK, 1); };
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
@@ -363,13 +353,13 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     mbar_init(bar(C::kQReady + 0), 4);
     mbar_init(bar(C::kQReady + 1), 4);
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(bar(C::kFull + s), kByte ? 4 : 1);
+      mbar_init(bar(C::kFull + s), kByte ? 8 : 1);
       mbar_init(bar(C::kEmpty + s), 1);
     }
     if constexpr (kByte) {
       for (int s = 0; s < C::kRaw; ++s) {
         mbar_init(bar(C::kRFull + s), 1);
-        mbar_init(bar(C::kREmpty + s), 4);
+        mbar_init(bar(C::kREmpty + s), 8);
       }
     }
     for (int q = 0; q < 2; ++q) {
@@ -413,6 +403,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     // -------------------------------------------------------- K / V loader
     // load u (2 t + 0 / 1: K / V of the run's tile t) into slot u % slots: the
     // bf16 tile itself, or the code tile a converter widens
+    constexpr int kN = kByte ? C::kRaw : kSlots;
     constexpr int kBytes = kByte ? kRawBytes : kTileBytes;
     constexpr int kRing = kByte ? C::kRawOff : C::kRingOff;
     constexpr int kF = kByte ? C::kRFull : C::kFull, kE = kByte ? C::kREmpty : C::kEmpty;
@@ -438,7 +429,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           waited = true;
         }
         for (int kv = 0; kv < 2; ++kv, ++u) {
-          const int slot = kByte ? raw_slot(u) : u % kSlots, lap = kByte ? raw_lap(u) : u / kSlots;
+          const int slot = u % kN, lap = u / kN;
           if (lane == 0) {
             if (lap > 0) ok = mbar_wait(bar(kE + slot), (lap - 1) & 1, p.wait_ns);
             if (!ok) fail(true);
@@ -481,14 +472,9 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       }
     }
     if (PG && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_PAGE_RANGE));
-    // every copy this warp issued (u of them) lands before the block can exit:
-    // the last one into each place
+    // every copy this warp issued (u of them) lands before the block can exit
     if (lane == 0)
-      for (int k = max(u - 2 * kSlots, 0); k < u; ++k) {
-        const int again = kByte ? 2 * ((k & 1) ? C::kRawV : C::kRawK) : kSlots;  // loads on, the same place
-        if (k + again >= u)
-          (void)mbar_wait(bar(kF + (kByte ? raw_slot(k) : k % kSlots)), (kByte ? raw_lap(k) : k / kSlots) & 1, kWaitLimitNs);
-      }
+      for (int k = u > kN ? u - kN : 0; k < u; ++k) (void)mbar_wait(bar(kF + k % kN), (k / kN) & 1, kWaitLimitNs);
     __syncwarp();
   } else if (warp == 10) {
     regs_aux();
@@ -664,31 +650,33 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   } else if (kByte && warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsConvert));
     // ---------------------------------------------------------- converters
-    // Warps 12-15 widen the K tiles, 16-19 the V tiles: thread r row r (key
-    // key0 + r) of each. One group for both took 3-5 us a tile.
+    // Thread (r, h) widens the 64 dims of half h of row r (key key0 + r) of
+    // every tile. (A group of four warps for K and one for V left the uint8
+    // V tiles, which take 2 us that way, the limit.)
     if constexpr (kByte) {
-      const int kv = warp >= 16 ? 1 : 0, r = (tid - 384) & 127;
-      const float2* szs = kv ? p.v_sz : p.k_sz;
+      constexpr int kRaw = C::kRaw;
+      const int r = (tid - 384) & 127, h = (tid - 384) >> 7;
       TreeSegment g;
       bool ok = true, waited = !p.early;
-      int u = kv;
+      int u = 0;
       while (ok && walk.next(p, kBN, rows_per_block, g)) {
         const int key_first = g.s.first + g.t0 * kBN;
         // uint8: the (scale, zero point) of this thread's row of a tile, zeros
         // where nothing may be read; requested a tile ahead
-        auto scale_of = [&](int t) {
-          const float2 none = make_float2(0.f, 0.f);
+        auto scales = [&](int t, float2& k, float2& v) {
+          k = v = make_float2(0.f, 0.f);
           const int key = key_first + t * kBN + r;
-          if (DT != kDtypeU8 || t >= g.nt || key < g.s.lo || key >= g.s.len) return none;
+          if (DT != kDtypeU8 || t >= g.nt || key < g.s.lo || key >= g.s.len) return;
           long long row;
           if constexpr (PG) {
             const int page = __ldg(p.block_table + static_cast<long long>(g.b) * p.max_pages + key / p.page_size);
-            if (page < 0 || page >= p.num_pages) return none;
+            if (page < 0 || page >= p.num_pages) return;
             row = (static_cast<long long>(page) * p.h_kv + g.j) * p.page_size + (key & (p.page_size - 1));
           } else {
             row = (static_cast<long long>(g.b) * p.h_kv + g.j) * p.capacity + key;
           }
-          return szs[row];  // (a plain load: the append of this step may have written it)
+          k = p.k_sz[row];  // (plain loads: the append of this step may have written them)
+          v = p.v_sz[row];
         };
         auto appended = [&](int t) {  // before the scales of a tile that holds a node
           if (DT == kDtypeU8 && !waited && key_first + (t + 1) * kBN > g.s.pos) {
@@ -696,54 +684,53 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             waited = true;
           }
         };
+        float2 k_now, v_now, k_next, v_next;
         appended(0);
-        float2 now = scale_of(0);
-        for (int t = 0; t < g.nt; ++t, u += 2) {
+        scales(0, k_now, v_now);
+        for (int t = 0; t < g.nt && ok; ++t) {
           const int key = key_first + t * kBN + r;
           const bool live = key >= g.s.lo && key < g.s.len;
           appended(t + 1);
-          const float2 next = scale_of(t + 1);
-          const int rs = raw_slot(u), slot = u % kSlots;
-          ok = mbar_wait(bar(C::kRFull + rs), raw_lap(u) & 1, p.wait_ns) &&
-               (u < kSlots || mbar_wait(bar(C::kEmpty + slot), (u / kSlots - 1) & 1, p.wait_ns));
-          if (!ok) fail(true);
-          ok = __all_sync(0xffffffffu, ok && !stop());
-          if (!ok) break;
-          const unsigned char* src = smem + C::kRawOff + rs * kRawBytes + r * 128;
-          unsigned char* dst = smem + C::kRingOff + slot * kTileBytes + r * 128;
-          const float zf = 8388608.f + now.y;
-          const uint32_t zh = 0x00010001u * static_cast<uint32_t>(__half_as_ushort(__float2half_rn(1024.f + now.y)));
-#pragma unroll 1
-          for (int c0 = 0; c0 < 8; c0 += 2) {  // 32 codes
-            uint4 w[2];
+          scales(t + 1, k_next, v_next);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) w[x] = *reinterpret_cast<const uint4*>(src + (((c0 + x) ^ (r & 7)) << 4));
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int c = c0 + x;
+          for (int kv = 0; kv < 2; ++kv, ++u) {
+            const int rs = u % kRaw, slot = u % kSlots;
+            ok = mbar_wait(bar(C::kRFull + rs), (u / kRaw) & 1, p.wait_ns) &&
+                 (u < kSlots || mbar_wait(bar(C::kEmpty + slot), (u / kSlots - 1) & 1, p.wait_ns));
+            if (!ok) fail(true);
+            ok = __all_sync(0xffffffffu, ok && !stop());
+            if (!ok) break;
+            const unsigned char* src = smem + C::kRawOff + rs * kRawBytes + r * 128;
+            unsigned char* dst = smem + C::kRingOff + slot * kTileBytes + h * 16384 + r * 128;
+            const float2 sz = kv ? v_now : k_now;
+            const float zf = 8388608.f + sz.y;
+            const uint32_t zh = 0x00010001u * static_cast<uint32_t>(__half_as_ushort(__float2half_rn(1024.f + sz.y)));
+#pragma unroll 2
+            for (int c = 0; c < 4; ++c) {  // 16 codes
+              const uint4 w = *reinterpret_cast<const uint4*>(src + (((4 * h + c) ^ (r & 7)) << 4));
               uint2 a, b, e, f;
               if constexpr (DT == kDtypeF8) {
-                a = half_e5m2(w[x].x), b = half_e5m2(w[x].y), e = half_e5m2(w[x].z), f = half_e5m2(w[x].w);
+                a = half_e5m2(w.x), b = half_e5m2(w.y), e = half_e5m2(w.z), f = half_e5m2(w.w);
               } else if (kv == 0) {
-                a = half_u8(w[x].x, zh), b = half_u8(w[x].y, zh), e = half_u8(w[x].z, zh), f = half_u8(w[x].w, zh);
+                a = half_u8(w.x, zh), b = half_u8(w.y, zh), e = half_u8(w.z, zh), f = half_u8(w.w, zh);
               } else {
-                a = widen_u8(w[x].x, zf), b = widen_u8(w[x].y, zf), e = widen_u8(w[x].z, zf), f = widen_u8(w[x].w, zf);
+                a = widen_u8(w.x, zf), b = widen_u8(w.y, zf), e = widen_u8(w.z, zf), f = widen_u8(w.w, zf);
               }
               if (!live) a = b = e = f = make_uint2(0u, 0u);
-              unsigned char* d = dst + (c >> 2) * 16384;
-              *reinterpret_cast<uint4*>(d + (((2 * c) & 7) ^ (r & 7)) * 16) = make_uint4(a.x, a.y, b.x, b.y);
-              *reinterpret_cast<uint4*>(d + (((2 * c + 1) & 7) ^ (r & 7)) * 16) = make_uint4(e.x, e.y, f.x, f.y);
+              *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+              *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(e.x, e.y, f.x, f.y);
+            }
+            if (DT == kDtypeU8 && h == 0)
+              reinterpret_cast<float*>(smem + C::kScaleOff)[(u % C::kScales) * kBN + r] = sz.x;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(C::kFull + slot));
+              mbar_arrive(bar(C::kREmpty + rs));
             }
           }
-          if constexpr (DT == kDtypeU8)
-            reinterpret_cast<float*>(smem + C::kScaleOff)[(u % C::kScales) * kBN + r] = now.x;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(C::kFull + slot));
-            mbar_arrive(bar(C::kREmpty + rs));
-          }
-          now = next;
+          k_now = k_next;
+          v_now = v_next;
         }
       }
     }

@@ -331,6 +331,6 @@ struct KeepParams {
   int32_t* err;
   KeepLayer layer[kMaxKeepLayers];
 };
-cudaError_t launch_keep_path(KeepParams p, int layers, cudaStream_t stream);
+cudaError_t launch_keep_path(KeepParams p, int layers, int sms, cudaStream_t stream);
 
 }  // namespace mqa

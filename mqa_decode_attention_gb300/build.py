@@ -21,7 +21,7 @@ LIB_DIR = os.path.join(PKG_DIR, "lib")
 LIB_NAME = "libmqa_decode.so"
 SOURCES = ["abi.cu", "append_rope.cu", "combine.cu", "decode_fma.cu", "decode_mma.cu", "decode_mma_paged.cu", "decode_mma_u8.cu",
            "noalloc.cu", "attn_tc05.cu", "attn_tc05_keys.cu", "attn_tc05_widen.cu",
-           "attn_tc05_prefill.cu", "attn_tree.cu", "attn_tree_tc05_bf16.cu", "attn_tree_tc05_u8.cu", "attn_tree_tc05_f8.cu",
+           "attn_tc05_prefill.cu", "append_tree.cu", "attn_tree.cu", "attn_tree_tc05_bf16.cu", "attn_tree_tc05_u8.cu", "attn_tree_tc05_f8.cu",
            "verify_tree.cu", "keep_path.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -510,7 +510,13 @@ mqa_status append_impl(const mqa_kv_layout* layout, const void* q_new, const voi
     p.zero_count = tree->zero_count;
   }
   fill_theta(p.theta, layout->head_dim, rope_base);
-  const cudaError_t e = launch_append_rope(p, reinterpret_cast<cudaStream_t>(stream));
+  // few nodes: the blocks of append_rope.cu, which split a node's heads (a step
+  // of one 8-node tree takes 16.7 us with them, 18.0 with append_tree.cu's)
+  const bool wide = tree != nullptr && layout->cache_dtype == MQA_BF16 && p.batch * p.n_new >= kTreeAppendNodes;
+  int dev = 0;
+  if (wide) cudaGetDevice(&dev);
+  const cudaError_t e = wide ? launch_append_tree(p, device_info(dev).sms, reinterpret_cast<cudaStream_t>(stream))
+                            : launch_append_rope(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e);
   const cudaError_t e2 = cudaGetLastError();
   return e2 == cudaSuccess ? MQA_OK : fail_cuda(e2);

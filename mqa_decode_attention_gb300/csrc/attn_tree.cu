@@ -1,7 +1,8 @@
 // Attention of a tree of drafted tokens over the cache on warp-level tensor
 // cores, for every cache the library reads on tensor cores: bf16, uint8 codes
-// and fp8 e5m2, contiguous or paged, head_dim 64 or 128, any group. (A bf16
-// cache with head_dim 128 and enough rows takes attn_tree_tc05.cu.)
+// and fp8 e5m2, contiguous or paged, head_dim 64 or 128, any group.
+// attn_tree_tc05.cuh takes head_dim 128 with up to 128 heads per kv head; this
+// kernel the rest.
 //
 // Rows of kv head j are its (node i, query head h = j G + hl) pairs, row =
 // i G + hl, in blocks of 64: four warps with 16 rows each share every 64-key
@@ -10,18 +11,19 @@
 //   S = Q K^T, masked;  m' = max(m, max S);  P = 2^(c (S - m')), c = scale log2 e
 //   O = 2^(c (m - m')) O + P V;  l = 2^(c (m - m')) l + sum P
 // S, P and O live in registers (m16n8k16 fragments), K and V in shared memory
-// as bf16 (two tiles each: one is used while the other arrives). One-byte
-// caches are widened on the way in, exactly: an e5m2 value has 3 significant
-// bits, code - zero point is an integer of magnitude <= 255 and has 8. The
-// row's scale then multiplies the score (K) or the probability (V) in fp32. P
-// is rounded to bf16, the tensor cores' operand (2^-9 of each probability);
+// as bf16 (two tiles each, four at head_dim 64: one is used while the others
+// arrive). One-byte caches are widened on the way in, exactly: an e5m2 value
+// has 3 significant bits, code - zero point is an integer of magnitude <= 255
+// and has 8. The row's scale then multiplies the score (K) or the probability
+// (V) in fp32. P is rounded to bf16, the tensor cores' operand (2^-8 of each probability);
 // the sum l adds the unrounded ones.
 //
 // Keys that no row may read (past the sequence, before the window) land as
 // zeros whatever the cache holds there.
 //
 // Bound: with few rows the HBM stream of K and V; the tiles' L2-to-SM copies
-// and the 64-row MMA work from about 64 rows per kv head on.
+// and the 64-row MMA work from about 64 rows per kv head on (32 x 16 nodes on
+// 4096 keys, 32 + 8 heads of 64 dims, 273 MB: a step takes 89 us, 3.1 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

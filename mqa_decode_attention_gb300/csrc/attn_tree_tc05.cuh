@@ -18,18 +18,25 @@
 // with a softmax warpgroup each:
 //   NT = 2  (more than 128 rows per kv head) two query tiles of up to 128 rows
 //           share every K / V tile; the tensor cores alternate between them.
+//           One tile of K and V asks for 1.45 us of HBM and 1.38 us of products;
+//           what bounds it is each accumulator's chain product - softmax - product
+//           (32 x 64 nodes on 4096 keys, 32 + 8 heads, 573 MB: 136 us, 4.2 TB/s,
+//           1.0 PFLOP/s). A tree that ends in a block of up to 128 rows has that
+//           block done as below.
 //   NT = 1  (up to 128 rows) both accumulators hold the same rows and take the
 //           tiles in turn, so that one's softmax runs beside the other's
 //           products; their results meet in shared memory at a unit's end.
 //           Bound by the HBM stream: a tile of K and V (64 KB) takes 1.45 us
 //           of an SM's share of 6.8 TB/s, its products 0.7 us, and the two
-//           accumulators' chains product-softmax-product about 1 us a tile.
+//           accumulators' chains product-softmax-product about 1 us a tile
+//           (32 x 16 nodes on 4096 keys, 546 MB: 98 us, 5.6 TB/s; one tree of 32
+//           nodes on 131040 keys: 316 us, 6.8 TB/s).
 //
 // Q is loaded by TMA as the append left it (bf16, not scaled): the scale
 // times log2 e goes into the exponent's fused multiply-add. Q and P enter the
-// products as bf16 (2^-9 of each value); a second bf16 term of Q would double
-// the first product, which at 256 rows is already half of what bounds the
-// kernel.
+// products as bf16 (up to 2^-8 of each value); a second bf16 term of Q would
+// double the first product, at 256 rows a quarter of what an SM does in a
+// tile's time. Sums, maxima and partial results are fp32.
 //
 // One-byte caches: the loader's tiles are codes (16 KB), eight converter warps
 // widen each to a 16-bit tile, exactly. An e5m2 code is the high byte of an
@@ -39,13 +46,18 @@
 // size, keeps bf16's range. For uint8 the rows' scales are put beside the
 // tile: a K scale multiplies its column of S, a V scale its column of P, in
 // fp32. Q's rows are made f16 in shared memory, each scaled by a power of two
-// of its own.
+// of its own. An f16 P is within 2^-11 of its value, or within 2^-25 when it is
+// below 2^-14: the row's largest P is at least 1 (and at most 2^8), so keys that
+// light move the result by less than 2^-25 of the largest |v| each.
+// (64 x 8 nodes of 32 heads on 8192 e5m2 keys of one kv head, 268 MB read: 95 us,
+// 0.7 PFLOP/s; bound by the widening and the chains.)
 //
 // Keys that no node may read (past the sequence, before the window) have zero
 // V rows whatever the cache holds, so that 0 * NaN never enters a sum.
 //
-// Warps: 0-3 and 4-7 softmax, 8 K / V loader (TMA), 9 MMA issue (one thread)
-// and tensor-memory allocation, 10 Q loader (TMA), 11 idle; 12-19 converters.
+// Warps: 0-3 and 4-7 softmax, 8 K / V loader (TMA), 9 MMA issue (converged, one
+// elected lane) and tensor-memory allocation, 10 Q loader (TMA), 11 counts in
+// the first unit's partial result; 12-19 converters.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -291,15 +303,14 @@ __device__ __forceinline__ void commit_elect(uint32_t mbar) {
       : "memory");
 }
 
-// N lanes (aligned groups of 8 or 4) hold N pieces of four words each: lane i's
+// Four lanes (an aligned group) hold four pieces of four words each: lane i's
 // piece j goes to lane j's place i.
-template <int N>
-__device__ __forceinline__ void transpose16(uint32_t (&w)[4 * N], int lane) {
+__device__ __forceinline__ void transpose4(uint32_t (&w)[16], int lane) {
 #pragma unroll
-  for (int s = 1; s < N; s <<= 1) {
+  for (int s = 1; s < 4; s <<= 1) {
     const bool up = (lane & s) != 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < 4; ++i) {
       if (i & s) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -313,6 +324,7 @@ __device__ __forceinline__ void transpose16(uint32_t (&w)[4 * N], int lane) {
     }
   }
 }
+
 template <int NT, bool PG, int DT>
 __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     attn_tree_tc05_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -1016,7 +1028,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
-            transpose16<4>(w, lane);
+            transpose4(w, lane);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const long long to = __shfl_sync(0xffffffffu, live ? orow : -1ll, (lane & ~3) + k);
@@ -1070,6 +1082,9 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     }
   }
 
+  // a block without work ends behind the append all the same: what follows in
+  // the stream may take this launch's end for the append's
+  if (p.early && tid == 0) grid_dependency_wait();
   // ---- teardown: every role is done with tensor memory
   tc05::fence_before_sync();
   __syncthreads();

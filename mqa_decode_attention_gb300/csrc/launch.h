@@ -160,6 +160,9 @@ struct KernelShape {
 
 KernelShape append_rope_shape();
 cudaError_t launch_append_rope(const AppendParams& p, cudaStream_t stream);
+// a tree of drafted tokens (p.depth set) over a bf16 cache, kTreeAppendNodes nodes or more
+constexpr int kTreeAppendNodes = 256;
+cudaError_t launch_append_tree(const AppendParams& p, int sms, cudaStream_t stream);
 
 KernelShape decode_fma_shape(int cache_dtype, int head_dim, int group);
 cudaError_t launch_decode_fma(const DecodeParams& p, cudaStream_t stream);

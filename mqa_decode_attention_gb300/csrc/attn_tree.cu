@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) attn_tree_kernel(const TreeParams p)
   if (warp == 0) tree_plan(p, kKeys, kRows, blockIdx.x, gridDim.x, &plan);
   __syncthreads();
   TreeWalk walk;
-  walk.start(p, plan, kKeys, kRows);
+  walk.start(plan);
   const uint32_t sb = smem_u32(smem);
   const float c = p.scale_log2;
 

@@ -56,8 +56,9 @@
 // V rows whatever the cache holds, so that 0 * NaN never enters a sum.
 //
 // Warps: 0-3 and 4-7 softmax, 8 K / V loader (TMA), 9 MMA issue (converged, one
-// elected lane) and tensor-memory allocation, 10 Q loader (TMA), 11 counts in
-// the first unit's partial result; 12-19 converters.
+// elected lane) and tensor-memory allocation, 10 Q loader (TMA), 11 gives warps
+// 0-7 and 9 their segments and counts in the first unit's partial result; 12-19
+// converters. The loaders and converters walk the segments by themselves.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -123,7 +124,7 @@ struct Cfg {
   static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;
   static constexpr int kScales = 2 * kSlots;
   static constexpr int kBarOff = kScaleOff + (DT == kDtypeU8 ? kScales * kBN * 4 : 0);
-  static constexpr int kSmemBytes = kBarOff + 256 + 1024;  // + alignment slack
+  static constexpr int kSmemBytes = kBarOff + 304 + 1024;  // + alignment slack
   // mbarriers
   static constexpr int kQFull = 0;
   static constexpr int kQFree = 1;                  // a segment of two row tiles is done with Q
@@ -139,9 +140,13 @@ struct Cfg {
   static constexpr int kODone = kPHi + 2;
   static constexpr int kOFree = kODone + 1;
   static constexpr int kPart = kOFree + 1;  // a partial result is written
-  static constexpr int kDrain = kPart + 1;
+  // [2] a segment is in place 0 / 1; the softmax warps are done with it. (A
+  // barrier for each place: none can be two phases ahead of a warp that waits.)
+  static constexpr int kSeg = kPart + 1;
+  static constexpr int kSegFree = kSeg + 2;
+  static constexpr int kDrain = kSegFree + 2;
   static constexpr int kNBars = kDrain + 1;
-  static_assert(kNBars * 8 + 4 <= 256, "barrier area");
+  static_assert(kNBars * 8 + 4 <= 304, "barrier area");
   static_assert(kSmemBytes + 1600 <= 227 * 1024, "shared memory (with the static part)");
 };
 
@@ -343,12 +348,9 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   // what the two accumulators' threads of a row hand over: maxima and sums; at
   // a segment's start (one-byte caches) the row's score factor
   __shared__ float s_m[kBM], s_l[kBM];
-  // the softmax warps' segment (two places: one may still be read while the
-  // next is written) and the walk that gives it, kept out of their registers
-  __shared__ TreeWalk s_walk;
+  // the segments, out of the softmax and MMA warps' registers (two places: one
+  // may still be read while the next is written), and the first one
   __shared__ TreeSegment s_seg[2], s_first;
-  __shared__ TreeWalk s_mma_walk;  // the MMA thread's, for the same reason
-  __shared__ TreeSegment s_mma_seg;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -382,6 +384,10 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     mbar_init(bar(C::kODone), 1);
     mbar_init(bar(C::kOFree), 8);
     mbar_init(bar(C::kPart), 8);
+    mbar_init(bar(C::kSeg + 0), 1);
+    mbar_init(bar(C::kSeg + 1), 1);
+    mbar_init(bar(C::kSegFree + 0), 8);
+    mbar_init(bar(C::kSegFree + 1), 8);
     mbar_init(bar(C::kDrain), 1);
     fence_mbar_init();
   }
@@ -406,9 +412,12 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   auto is_two = [&](const TreeSegment& g) { return NT == 2 && g.s.nodes * G - g.rb * rows_per_block > acc_rows; };
   auto stop = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
   auto regs_aux = [&]() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsAux)); };
-  TreeWalk walk;
-  walk.start(p, plan, kBN, rows_per_block);
-  if (s_skip) walk.at = walk.end;
+  auto begin = [&]() {
+    TreeWalk w;
+    w.start(plan);
+    if (s_skip) w.at = w.end;
+    return w;
+  };
 
   if (warp == 8) {
     regs_aux();
@@ -420,6 +429,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     constexpr int kRing = kByte ? C::kRawOff : C::kRingOff;
     constexpr int kF = kByte ? C::kRFull : C::kFull, kE = kByte ? C::kREmpty : C::kEmpty;
     const int ps = PG ? p.page_size : 64, rp = ps < 64 ? ps : 64, copies = kBN / rp;
+    TreeWalk walk = begin();
     TreeSegment g;
     bool waited = !p.early, ok = true, bad = false;
     int u = 0;
@@ -493,6 +503,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     // ------------------------------------------------------------ Q loader
     if (lane == 0) {
       if (p.early) grid_dependency_wait();
+      TreeWalk walk = begin();
       TreeSegment g;
       bool ok = true, last_two = false;
       int seg = 0, n_two = 0;
@@ -568,14 +579,11 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       auto free_v = [&](int t) { commit_elect(bar(C::kEmpty + (u0 + 2 * t + 1) % kSlots)); };
       bool ok = true;
       int seg = 0, n_two = 0;
-      if (lane == 0) s_mma_walk = walk;
       while (ok) {
-        __syncwarp();
-        bool more = false;
-        if (lane == 0) more = s_mma_walk.next(p, kBN, rows_per_block, s_mma_seg);
-        if (!__shfl_sync(0xffffffffu, more, 0)) break;
-        const int T = s_mma_seg.nt;
-        const bool two = is_two(s_mma_seg);
+        ok = wait(C::kSeg + (seg & 1), seg >> 1);
+        if (!ok || !s_more[seg & 1]) break;
+        const int T = s_seg[seg & 1].nt;
+        const bool two = is_two(s_seg[seg & 1]), last = s_last[seg & 1] != 0;
         n_two += two;
         if constexpr (C::kHalfQK)
           ok = wait(C::kQReady + 0, seg) && (!two || wait(C::kQReady + 1, n_two - 1)) && full(u0);
@@ -630,6 +638,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           }
         }
         if (ok) commit_elect(bar(C::kODone));
+        if (last) break;
         u0 += 2 * T;
         ++seg;
       }
@@ -638,25 +647,44 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     __syncwarp();
   } else if (warp == 11) {
     regs_aux();
-    // ---------------------------------------------------- a partial's arrival
+    // ------------------------------------------------------------- segments
+    // Segment k goes into place k & 1 when segment k - 2 has left it: found while
+    // the softmax warps are at work (the walk's loads and divisions between two
+    // segments cost them 2 us).
     // Of a block's segments only the first and the last can be parts of a
     // unit. The first one's partial, when others follow, is counted in here:
     // the softmax warps go on to the next unit meanwhile (waiting for their
     // writes and the counter cost them 2 us). Should the unit be complete with
     // it -- its other blocks as a rule end later -- the softmax warps merge it
     // after their last segment.
-    TreeSegment g;
     bool complete = false;
-    if (walk.next(p, kBN, rows_per_block, g) && !(g.head && g.tail) && walk.at < walk.end) {
-      bool ok = mbar_wait(bar(C::kPart), 0, p.wait_ns);
-      if (!ok) fail(lane == 0);
-      if (ok && !stop() && lane == 0) {
-        const TreeMerge mg = tree_merge(plan, g);
-        __threadfence();  // the partial (seen through the barrier), before the count
-        complete = atomicAdd(p.arrived + mg.ca, 1) == mg.m - 1;
-        __threadfence();  // the other blocks' partials, after it
+    if (lane == 0) {
+      TreeWalk walk = begin();
+      for (int k = 0;; ++k) {
+        if (k >= 2) {
+          const bool ok = mbar_wait(bar(C::kSegFree + (k & 1)), ((k >> 1) - 1) & 1, p.wait_ns);
+          if (!ok) fail(true);
+          if (!ok || stop()) break;
+        }
+        TreeSegment& g = s_seg[k & 1];
+        const bool more = walk.next(p, kBN, rows_per_block, g), last = walk.at >= walk.end;
+        s_more[k & 1] = more;
+        s_last[k & 1] = last;
+        if (k == 0) s_first = g;
+        mbar_arrive(bar(C::kSeg + (k & 1)));
+        if (k == 1 && !(s_first.head && s_first.tail)) {
+          const bool ok = mbar_wait(bar(C::kPart), 0, p.wait_ns);
+          if (!ok) fail(true);
+          if (!ok || stop()) break;
+          const TreeMerge mg = tree_merge(plan, s_first);
+          __threadfence();  // the partial (seen through the barrier), before the count
+          complete = atomicAdd(p.arrived + mg.ca, 1) == mg.m - 1;
+          __threadfence();  // the other blocks' partials, after it
+        }
+        if (!more || last) break;
       }
     }
+    __syncwarp();
     if (lane == 0) s_pending = complete;
     named_bar_sync(3, 256 + 32);
   } else if (kByte && warp >= 12) {
@@ -668,6 +696,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     if constexpr (kByte) {
       constexpr int kRaw = C::kRaw;
       const int r = (tid - 384) & 127, h = (tid - 384) >> 7;
+      TreeWalk walk = begin();
       TreeSegment g;
       bool ok = true, waited = !p.early;
       int u = 0;
@@ -717,9 +746,14 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             const float2 sz = kv ? v_now : k_now;
             const float zf = 8388608.f + sz.y;
             const uint32_t zh = 0x00010001u * static_cast<uint32_t>(__half_as_ushort(__float2half_rn(1024.f + sz.y)));
-#pragma unroll 2
-            for (int c = 0; c < 4; ++c) {  // 16 codes
-              const uint4 w = *reinterpret_cast<const uint4*>(src + (((4 * h + c) ^ (r & 7)) << 4));
+            // (16 codes a pass, the next ones requested before this pass's stores.
+            // Short code: all four passes unrolled, the uint8 kernel took a quarter
+            // longer, as the instruction cache is shared with the softmax)
+            auto codes = [&](int c) { return *reinterpret_cast<const uint4*>(src + (((4 * h + c) ^ (r & 7)) << 4)); };
+            uint4 w = codes(0), next;
+#pragma unroll(DT == kDtypeU8 ? 1 : 2)
+            for (int c = 0; c < 4; ++c) {
+              next = codes((c + 1) & 3);
               uint2 a, b, e, f;
               if constexpr (DT == kDtypeF8) {
                 a = half_e5m2(w.x), b = half_e5m2(w.y), e = half_e5m2(w.z), f = half_e5m2(w.w);
@@ -731,6 +765,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
               if (!live) a = b = e = f = make_uint2(0u, 0u);
               *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
               *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(e.x, e.y, f.x, f.y);
+              w = next;
             }
             if (DT == kDtypeU8 && h == 0)
               reinterpret_cast<float*>(smem + C::kScaleOff)[(u % C::kScales) * kBN + r] = sz.x;
@@ -757,14 +792,11 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     bool waited = !p.early;
     int u0 = 0, seg = 0, js = 0;  // first load of the segment; segments; tiles of this accumulator
     bool ok = true, aborted = false;
-    if (tid == 0) s_walk = walk;
     while (true) {
-      if (tid == 0) {
-        s_more[seg & 1] = s_walk.next(p, kBN, rows_per_block, s_seg[seg & 1]);
-        s_last[seg & 1] = s_walk.at >= s_walk.end;
-      }
-      named_bar_sync(1, 256);
-      if (!s_more[seg & 1]) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kSeg + (seg & 1)), (seg >> 1) & 1, p.wait_ns) && !stop());
+      if (!ok) fail(lane == 0);
+      aborted = bar_any(2, 256, !ok);  // (and no warp is at the last segment any more)
+      if (aborted || !s_more[seg & 1]) break;
       const TreeSegment& g = s_seg[seg & 1];
       const bool two = is_two(g);
       const int step = two ? 1 : 2;
@@ -952,12 +984,15 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       // a part's into the workspace. (One copy of this code for every case:
       // fetching it costs more than running it.)
       const bool whole = g.head && g.tail, last = s_last[seg & 1] != 0;
-      const bool both = !two && nt > 1;  // the two accumulators of each row meet
-      // ... through the Q area (free: every product with Q is done; NT = 2: the
-      // second row tile's half): the second warpgroup hands its O over in two
-      // buffers of 16 KB
+      // both accumulators hold these rows: each warpgroup hands the other's 64
+      // dims over and puts out its own, through the Q area (free: every product
+      // with Q is done; NT = 2: the second row tile's half), 16 KB a direction
+      const bool both = !two && nt > 1;
       unsigned char* xbuf = smem + C::kQOff + (NT - 1) * kTileBytes;
-      float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c, w0 = 1.f, w1 = 0.f;
+      auto piece = [&](int from, int i) {  // 16 bytes i of row r of warpgroup `from`
+        return reinterpret_cast<float4*>(xbuf + from * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
+      };
+      float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c, w0 = 1.f, w1 = 0.f, mo = 0.f, lo = 0.f;
       if (both) {
         if (q == 1) {
           s_m[r] = m2;
@@ -965,45 +1000,69 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         }
         named_bar_sync(1, 256);
         if (q == 0) {
-          const float mo = s_m[r], mx = fmaxf(m2, mo);
-          w0 = mx != -INFINITY ? exp2f(m2 - mx) : 0.f;
-          w1 = mx != -INFINITY ? exp2f(mo - mx) : 0.f;
-          l = w0 * l + w1 * s_l[r];
-          m2 = mx;
+          mo = s_m[r];
+          lo = s_l[r];
+          s_m[r] = m2;
+          s_l[r] = l;
         }
       }
-      const bool writer = (two || q == 0) && warp_rows;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool writer = (two || both || q == 0) && warp_rows;
       const long long orow = live ? tree_out_row(p, g, gr) : 0;
       const int br = gr - g.rb * rows_per_block;  // row of the block
       float* part = tree_place(p, g, blockIdx.x, rows_per_block, kD);
+      float inv = l > 0.f ? 1.f / l : 0.f;
+      const int x0 = both ? 2 * q : 0, x1 = both ? x0 + 2 : kD / 32;
 #pragma unroll 1
-      for (int x = 0; x < kD / 32; ++x) {
-        auto piece = [&](int i) {  // 16 bytes i of row r
-          return reinterpret_cast<float4*>(xbuf + (x & 1) * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
-        };
+      for (int x = x0; x < x1; ++x) {
         float v[32];
+        if (both) {
+          if (x > x0) named_bar_sync(1, 256);  // what was handed over has been read
+          __syncwarp();
+          if (warp_rows) {
+            tc05::ld_32x32b_x32(ocol + (x ^ 2) * 32, v);
+            tc05::wait_ld();
+            tc05::reg_fence(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *piece(q, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+          named_bar_sync(1, 256);
+        }
         __syncwarp();
-        if (writer || (both && warp_rows)) {
+        if (writer) {
           tc05::ld_32x32b_x32(ocol + x * 32, v);
           tc05::wait_ld();
           tc05::reg_fence(v);
         }
         if (both) {
-          if (q == 1 && warp_rows) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) *piece(i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-          named_bar_sync(1, 256);
-          if (writer) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 o = *piece(i);
-              v[4 * i] = fmaf(w1, o.x, w0 * v[4 * i]);
-              v[4 * i + 1] = fmaf(w1, o.y, w0 * v[4 * i + 1]);
-              v[4 * i + 2] = fmaf(w1, o.z, w0 * v[4 * i + 2]);
-              v[4 * i + 3] = fmaf(w1, o.w, w0 * v[4 * i + 3]);
+          if (x == x0) {
+            if (q == 1) {
+              mo = s_m[r];
+              lo = s_l[r];
             }
+            const float mx = fmaxf(m2, mo);
+            w0 = mx != -INFINITY ? exp2f(m2 - mx) : 0.f;
+            w1 = mx != -INFINITY ? exp2f(mo - mx) : 0.f;
+            l = w0 * l + w1 * lo;
+            m2 = mx;
+            inv = l > 0.f ? 1.f / l : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 o = *piece(1 - q, i);
+            v[4 * i] = fmaf(w1, o.x, w0 * v[4 * i]);
+            v[4 * i + 1] = fmaf(w1, o.y, w0 * v[4 * i + 1]);
+            v[4 * i + 2] = fmaf(w1, o.z, w0 * v[4 * i + 2]);
+            v[4 * i + 3] = fmaf(w1, o.w, w0 * v[4 * i + 3]);
+          }
+        }
+        if (x + 1 == x1) {  // O is read, the Q area, and the segment's place
+          tc05::fence_before_sync();
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(C::kOFree));
+            mbar_arrive(bar(C::kSegFree + (seg & 1)));
+            if (!two) mbar_arrive(bar(C::kXFree));
           }
         }
         if (writer) {
@@ -1039,7 +1098,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           }
         }
       }
-      if (writer && live) {
+      if (writer && live && (two || q == 0)) {
         if (!whole) {
           part[static_cast<size_t>(rows_per_block) * kD + br] = m2;
           part[static_cast<size_t>(rows_per_block) * (kD + 1) + br] = l;
@@ -1047,25 +1106,14 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           p.lse_out[orow] = l > 0.f ? (m2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
         }
       }
-      // O is read, and the Q area
-      tc05::fence_before_sync();
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(C::kOFree));
-        if (!two) mbar_arrive(bar(C::kXFree));
-        if (!whole && !last) mbar_arrive(bar(C::kPart));
-      }
+      if (lane == 0 && !whole && !last) mbar_arrive(bar(C::kPart));
       if (last) break;
       u0 += 2 * nt;
       ++seg;
     }
     // ---- parts of units: the last segment's is counted in here, the first
     // one's was by warp 11; a unit that is complete is merged
-    if (tid == 0) {
-      walk.start(p, plan, kBN, rows_per_block);
-      (void)walk.next(p, kBN, rows_per_block, s_first);
-    }
     named_bar_sync(3, 256 + 32);
     if (!aborted) {
       const TreeSegment& g = s_seg[seg & 1];

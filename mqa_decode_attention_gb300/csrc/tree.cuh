@@ -59,6 +59,7 @@ struct TreePlan {
   long long total, begin, end;
   long long before;  // tiles of the sequences before b
   int b, ctas;       // the sequence holding `begin`
+  TreeSeq s;         // that sequence
 };
 
 // By one whole warp; `out` in shared memory. Lane l sums the tiles of its
@@ -103,6 +104,7 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, int tile, int row
     }
     out->before = before;
     out->b = b;
+    out->s = tree_seq(p, b, tile, rows);
   }
   __syncwarp();
 }
@@ -115,17 +117,17 @@ struct TreeSegment {
   TreeSeq s;
 };
 
-// A block's segments one after the other; every warp walks them by itself.
+// A block's segments one after the other.
 struct TreeWalk {
   long long at, end, before;
   int b;
   TreeSeq s;
-  __device__ __forceinline__ void start(const TreeParams& p, const TreePlan& pl, int tile, int rows) {
+  __device__ __forceinline__ void start(const TreePlan& pl) {
     at = pl.begin;
     end = pl.end;
     before = pl.before;
     b = pl.b;
-    if (at < end) s = tree_seq(p, b, tile, rows);
+    s = pl.s;
   }
   __device__ __forceinline__ bool next(const TreeParams& p, int tile, int rows, TreeSegment& g) {
     if (at >= end) return false;

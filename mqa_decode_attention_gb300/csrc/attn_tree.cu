@@ -60,16 +60,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
-// four codes (one word) as two bf16 pairs; z the row's zero point
+// four codes (one word) as two bf16 pairs; z: u8_zero of the row's zero point
 template <int DT>
-__device__ __forceinline__ uint2 widen4(uint32_t w, float z) {
+__device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t z) {
   if constexpr (DT == kDtypeU8) {
-    const float b = 8388608.f + z;  // 2^23 + zero point: exact
-    const float f0 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650)) - b;
-    const float f1 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7651)) - b;
-    const float f2 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7652)) - b;
-    const float f3 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7653)) - b;
-    return make_uint2(pack_bf16x2(f0, f1), pack_bf16x2(f2, f3));
+    return widen_u8(w, z);
   } else {  // an e5m2 code is the high byte of an IEEE half
     const uint32_t h01 = __byte_perm(w, 0u, 0x1404), h23 = __byte_perm(w, 0u, 0x3424);
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h01));
@@ -172,13 +167,14 @@ __global__ void __launch_bounds__(kThreads) attn_tree_kernel(const TreeParams p)
           for (int kv = 0; kv < 2; ++kv) {
             const uint4 w = kv ? vr[u] : kr[u];
             const float2 sz = kv ? vsz[u] : ksz[u];
-            const uint2 a = widen4<DT>(w.x, sz.y), e = widen4<DT>(w.y, sz.y);
-            const uint2 f = widen4<DT>(w.z, sz.y), h = widen4<DT>(w.w, sz.y);
+            const uint32_t z = DT == kDtypeU8 ? u8_zero(sz.y) : 0u;
+            const uint2 a = widen4<DT>(w.x, z), e = widen4<DT>(w.y, z);
+            const uint2 f = widen4<DT>(w.z, z), h = widen4<DT>(w.w, z);
             unsigned char* dst = smem + (kv ? Y::kV : Y::kK) + st * Y::kTile;
             *reinterpret_cast<uint4*>(dst + chunk_at<D>(r, 2 * cc)) = make_uint4(a.x, a.y, e.x, e.y);
             *reinterpret_cast<uint4*>(dst + chunk_at<D>(r, 2 * cc + 1)) = make_uint4(f.x, f.y, h.x, h.y);
             if (DT == kDtypeU8 && cc == 0)
-              reinterpret_cast<float*>(smem + Y::kScale)[(kv * 2 + st) * kKeys + r] = sz.x;
+              reinterpret_cast<float*>(smem + Y::kScale)[(kv * 2 + st) * kKeys + r] = sz.x * kU8Unit;
           }
         }
       }

@@ -40,15 +40,14 @@
 //
 // One-byte caches: the loader's tiles are codes (16 KB), eight converter warps
 // widen each to a 16-bit tile, exactly. An e5m2 code is the high byte of an
-// IEEE half: K and V become f16, and Q and P enter as f16 too. A uint8 code
-// minus its zero point is an integer up to 255: K becomes f16 (two cheap
-// instructions for two codes), V bf16, so that P times its row's scale, of any
-// size, keeps bf16's range. For uint8 the rows' scales are put beside the
-// tile: a K scale multiplies its column of S, a V scale its column of P, in
-// fp32. Q's rows are made f16 in shared memory, each scaled by a power of two
-// of its own. An f16 P is within 2^-11 of its value, or within 2^-25 when it is
-// below 2^-14: the row's largest P is at least 1 (and at most 2^8), so keys that
-// light move the result by less than 2^-25 of the largest |v| each.
+// IEEE half: K and V become f16, and Q and P enter as f16 too: Q's rows are made
+// f16 in shared memory, each scaled by a power of two of its own. A uint8 code
+// minus its zero point is an integer up to 255 and becomes a bf16 (widen_u8);
+// the rows' scales are put beside the tile: a K scale multiplies its column of
+// S, a V scale its column of P, in fp32, before P is rounded.
+// An f16 P is within 2^-11 of its value, or within 2^-25 when it is below 2^-14:
+// the row's largest P is at least 1 (and at most 2^8), so keys that light move
+// the result by less than 2^-25 of the largest |v| each.
 // (64 x 8 nodes of 32 heads on 8192 e5m2 keys of one kv head, 268 MB read: 95 us,
 // 0.7 PFLOP/s; bound by the widening and the chains.)
 //
@@ -112,8 +111,7 @@ struct Cfg {
   static constexpr int kSlots = kByte ? 4 : (NT == 1 ? 6 : 5);
   static constexpr int kRaw = kByte ? (NT == 2 ? 2 : (DT == kDtypeU8 ? 3 : 4)) : 0;
   static_assert(NT == 1 || DT != kDtypeU8, "no room for two row tiles beside the scales");
-  static constexpr bool kHalfQK = kByte;              // S = Q K^T on f16 operands
-  static constexpr bool kHalfPV = DT == kDtypeF8;     // O += P V on f16 operands (else bf16)
+  static constexpr bool kHalf = DT == kDtypeF8;  // f16 operands (else bf16)
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = NT * kTileBytes;
   static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
@@ -129,7 +127,7 @@ struct Cfg {
   static constexpr int kQFull = 0;
   static constexpr int kQFree = 1;                  // a segment of two row tiles is done with Q
   static constexpr int kXFree = 2;                  // one of one row tile: its accumulators have met
-  static constexpr int kQReady = 3;                 // [2] one-byte caches: Q's row tile is f16
+  static constexpr int kQReady = 3;                 // [2] e5m2: Q's row tile is f16
   static constexpr int kFull = 5;                   // [kSlots]
   static constexpr int kEmpty = kFull + kSlots;     // [kSlots]
   static constexpr int kRFull = kEmpty + kSlots;    // [kRaw]
@@ -194,24 +192,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ uint2 half_e5m2(uint32_t w) {
   return make_uint2(__byte_perm(w, 0u, 0x1404), __byte_perm(w, 0u, 0x3424));
 }
-// Four uint8 codes minus the zero point as two f16 pairs (z = 1024 + zero point
-// twice): 0x6400 | code is the half 1024 + code, and the difference is exact.
-__device__ __forceinline__ uint2 half_u8(uint32_t w, uint32_t z) {
-  uint2 r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r.x) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(z));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r.y) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(z));
-  return r;
-}
-// ... as two bf16 pairs (z = 2^23 + zero point)
-__device__ __forceinline__ uint2 widen_u8(uint32_t w, float z) {
-  const float2 nz = make_float2(-z, -z);
-  const float2 a = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650)),
-                                    __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7651))), nz);
-  const float2 b = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7652)),
-                                    __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7653))), nz);
-  return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
-}
-
 template <bool HALF>
 __device__ __forceinline__ uint32_t pack_p(float2 v) {
   if constexpr (HALF) {
@@ -346,7 +326,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   __shared__ TreePlan plan;
   __shared__ int s_abort, s_skip, s_flag, s_pending, s_more[2], s_last[2];
   // what the two accumulators' threads of a row hand over: maxima and sums; at
-  // a segment's start (one-byte caches) the row's score factor
+  // a segment's start (e5m2) the row's score factor
   __shared__ float s_m[kBM], s_l[kBM];
   // the segments, out of the softmax and MMA warps' registers (two places: one
   // may still be read while the next is written), and the first one
@@ -512,9 +492,13 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         // or, with one row tile, when its accumulators have met there (a
         // barrier for each kind: every phase of it is waited for, so that a
         // parity never stands for an older phase)
-        if (seg > 0)
-          ok = last_two ? mbar_wait(bar(C::kQFree), (n_two - 1) & 1, p.wait_ns)
-                        : mbar_wait(bar(C::kXFree), (seg - n_two - 1) & 1, p.wait_ns);
+        auto poll = [&](int id, int parity) {  // (a suspended wait wakes late, and the next S waits for it)
+          const unsigned long long t0 = global_timer_ns();
+          while (!mbar_test(bar(id), parity & 1))
+            if (stop() || global_timer_ns() - t0 > p.wait_ns) return false;
+          return true;
+        };
+        if (seg > 0) ok = last_two ? poll(C::kQFree, n_two - 1) : poll(C::kXFree, seg - n_two - 1);
         if (!ok) fail(true);
         if (!ok || stop()) break;
         last_two = is_two(g);
@@ -536,9 +520,9 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     // ----------------------------------------------------------- MMA issue
     // (the whole warp, converged; one elected lane issues)
     {
-      constexpr uint32_t id_s = C::kHalfQK ? tc05::idesc_f16_f32(kBM, kBN, false, false)
+      constexpr uint32_t id_s = C::kHalf ? tc05::idesc_f16_f32(kBM, kBN, false, false)
                                            : tc05::idesc_bf16_f32(kBM, kBN, false, false);
-      constexpr uint32_t id_o = C::kHalfPV ? tc05::idesc_f16_f32(kBM, kD, false, true)
+      constexpr uint32_t id_o = C::kHalf ? tc05::idesc_f16_f32(kBM, kD, false, true)
                                            : tc05::idesc_bf16_f32(kBM, kD, false, true);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sb = __shfl_sync(0xffffffffu, sbase, 0);
       auto wait = [&](int id, int parity) {  // polls: a suspended wait wakes late
@@ -585,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         const int T = s_seg[seg & 1].nt;
         const bool two = is_two(s_seg[seg & 1]), last = s_last[seg & 1] != 0;
         n_two += two;
-        if constexpr (C::kHalfQK)
+        if constexpr (C::kHalf)
           ok = wait(C::kQReady + 0, seg) && (!two || wait(C::kQReady + 1, n_two - 1)) && full(u0);
         else
           ok = wait(C::kQFull, seg) && full(u0);
@@ -691,8 +675,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsConvert));
     // ---------------------------------------------------------- converters
     // Thread (r, h) widens the 64 dims of half h of row r (key key0 + r) of
-    // every tile. (A group of four warps for K and one for V left the uint8
-    // V tiles, which take 2 us that way, the limit.)
+    // every tile.
     if constexpr (kByte) {
       constexpr int kRaw = C::kRaw;
       const int r = (tid - 384) & 127, h = (tid - 384) >> 7;
@@ -744,8 +727,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             const unsigned char* src = smem + C::kRawOff + rs * kRawBytes + r * 128;
             unsigned char* dst = smem + C::kRingOff + slot * kTileBytes + h * 16384 + r * 128;
             const float2 sz = kv ? v_now : k_now;
-            const float zf = 8388608.f + sz.y;
-            const uint32_t zh = 0x00010001u * static_cast<uint32_t>(__half_as_ushort(__float2half_rn(1024.f + sz.y)));
+            const uint32_t z = u8_zero(sz.y);
             // (16 codes a pass, the next ones requested before this pass's stores.
             // Short code: all four passes unrolled, the uint8 kernel took a quarter
             // longer, as the instruction cache is shared with the softmax)
@@ -757,10 +739,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
               uint2 a, b, e, f;
               if constexpr (DT == kDtypeF8) {
                 a = half_e5m2(w.x), b = half_e5m2(w.y), e = half_e5m2(w.z), f = half_e5m2(w.w);
-              } else if (kv == 0) {
-                a = half_u8(w.x, zh), b = half_u8(w.y, zh), e = half_u8(w.z, zh), f = half_u8(w.w, zh);
               } else {
-                a = widen_u8(w.x, zf), b = widen_u8(w.y, zf), e = widen_u8(w.z, zf), f = widen_u8(w.w, zf);
+                a = widen_u8(w.x, z), b = widen_u8(w.y, z), e = widen_u8(w.z, z), f = widen_u8(w.w, z);
               }
               if (!live) a = b = e = f = make_uint2(0u, 0u);
               *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
@@ -768,7 +748,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
               w = next;
             }
             if (DT == kDtypeU8 && h == 0)
-              reinterpret_cast<float*>(smem + C::kScaleOff)[(u % C::kScales) * kBN + r] = sz.x;
+              reinterpret_cast<float*>(smem + C::kScaleOff)[(u % C::kScales) * kBN + r] = sz.x * kU8Unit;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
@@ -787,7 +767,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     const int q = warp >> 2, r = tid - q * kBM;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t scol = tmem + lane_base + kColS + q * 128, ocol = tmem + lane_base + kColO + q * 128;
-    float c = p.scale_log2;  // (one-byte caches: over the factor that Q's row was scaled by)
+    float c = p.scale_log2;  // (e5m2: over the factor that Q's row was scaled by)
     const bool warp_rows = (warp & 3) * 32 < acc_rows;  // some lane of this warp holds a row
     bool waited = !p.early;
     int u0 = 0, seg = 0, js = 0;  // first load of the segment; segments; tiles of this accumulator
@@ -807,8 +787,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       const int ka = tree_first_key(p, g.b, g.s, node), pos = g.s.pos;
       const int nt = g.nt;
       int key0 = g.s.first + (g.t0 + (two ? 0 : q)) * kBN;
-      if constexpr (C::kHalfQK) {
-        // Q's rows as f16, each scaled by a power of two to a largest magnitude
+      if constexpr (C::kHalf) {
+        // e5m2: Q's rows as f16, each scaled by a power of two to a largest magnitude
         // in [2^9, 2^10): exact for all but values 2^24 below the row's largest
         if (two || q == 0) {
           ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kQFull), seg & 1, p.wait_ns) && !stop());
@@ -943,8 +923,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
                 p0 = mul2(p0, make_float2(f.x, f.y));
                 p1 = mul2(p1, make_float2(f.z, f.w));
               }
-              pk[i] = pack_p<C::kHalfPV>(p0);
-              pk[i + 1] = pack_p<C::kHalfPV>(p1);
+              pk[i] = pack_p<C::kHalf>(p0);
+              pk[i + 1] = pack_p<C::kHalf>(p1);
             }
             tc05::st_32x32b_x16_u(scol + 16 * x, pk);
           };

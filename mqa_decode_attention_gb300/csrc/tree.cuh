@@ -160,6 +160,23 @@ __device__ __forceinline__ int tree_cta_of(const TreePlan& pl, long long x) {
   return static_cast<int>(((x + 1) * pl.ctas - 1) / pl.total);
 }
 
+// Four uint8 codes minus the zero point as two bf16 pairs, times 2^-6, exactly.
+// A code in the low byte is the bf16 code * 2^-133 (subnormal below 128, normal
+// from there on: the patterns go on evenly), so one fused multiply-add makes
+// code * 2^-6 - zero point * 2^-6: an integer of 8 bits at most, times 2^-6. The
+// 2^6 goes into the row's scale. z = u8_zero(zero point); two instructions for
+// two codes (through fp32 and a conversion: four).
+constexpr float kU8Unit = 64.f;
+__device__ __forceinline__ uint32_t u8_zero(float zero_point) {
+  return pack_bf16x2(zero_point * -(1.f / kU8Unit), zero_point * -(1.f / kU8Unit));
+}
+__device__ __forceinline__ uint2 widen_u8(uint32_t w, uint32_t z) {
+  uint2 r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r.x) : "r"(__byte_perm(w, 0u, 0x4140)), "r"(0x7f007f00u), "r"(z));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r.y) : "r"(__byte_perm(w, 0u, 0x4342)), "r"(0x7f007f00u), "r"(z));
+  return r;
+}
+
 // 32 bits, bit c = the row may attend to key k0 + c. m: the row's mask words
 // with the bits of dead nodes cleared (all zero for a dead row), ka its first
 // key, pos the number of cached tokens.

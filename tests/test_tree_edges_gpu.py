@@ -260,3 +260,35 @@ def test_a_scale_of_any_size(m):  # noqa: F811
     assert clear.any()
     assert np.all(np.abs(got - pick)[clear] <= 2 * 2.0 ** -8 * np.abs(pick)[clear] + 2.0 ** -22)  # P and the output in bf16
     assert math.isfinite(float(b.out.float().abs().max()))
+
+
+@pytest.mark.parametrize("d", [128, 64])
+def test_u8_every_code_and_zero_point(m, d):  # noqa: F811
+    """Every code with zero points from end to end, scales over 2^-20 .. 2^20: an
+    exact widening (one row attended: the value itself comes out)."""
+    T = 256
+    B = 3
+    g = torch.Generator().manual_seed(1)
+    k = torch.randint(0, 256, (B, 2, T + 2, d), generator=g, dtype=torch.int32).to(torch.uint8)
+    v = ((torch.arange(T + 2)[:, None] * 3 + torch.arange(d)) % 256).to(torch.uint8).expand(B, 2, -1, -1).contiguous()
+    ksz = torch.ones(B, 2, T + 2, 2)
+    ksz[..., 1] = 128
+    vsz = torch.ones(B, 2, T + 2, 2)
+    vsz[..., 1] = (torch.arange(T + 2) * 7 % 256).float()
+    vsz[..., 0] = 2.0 ** (torch.arange(T + 2) % 41 - 20).float()
+    k, v, ksz, vsz = (x.cuda().contiguous() for x in (k, v, ksz, vsz))
+    lay = m.layout_contiguous(k, v, 4, 0, ksz, vsz)
+    q = torch.zeros(B, 1, 4, d, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(B, 1, 4, d, device="cuda")
+    bufs = m.TreeBuffers.allocate(lay, 1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for t in range(0, T, 5):  # a window of one: the node attends to itself alone, cache row t
+        lay = m.layout_contiguous(k, v, 4, 1, ksz, vsz)
+        pos = i32([t, (t + 1) % T, (t + 2) % T])
+        m.gqa_tree_attention(lay, 1, q, pos, i32([[0]] * 3), i32([[[1]]] * 3), T + 2, 1.0, out, None, None, bufs.workspace,
+                             bufs.err)
+        torch.cuda.synchronize()
+        assert int(bufs.err.item()) == 0
+        for b, at in enumerate(pos.tolist()):
+            want = (v[b, 0, at].float() - vsz[b, 0, at, 1]) * vsz[b, 0, at, 0]
+            assert torch.equal(out[b, 0], want.expand(4, d))

@@ -94,6 +94,18 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // S / P of accumulator q at 128 q, its O at 256 + 128 q
 constexpr float kRescaleLog2 = 8.0f;
 
+// What the warps of a block share beside the tiles and barriers.
+struct TreeMisc {
+  TreePlan plan;
+  // the segments, out of the softmax and MMA warps' registers (two places: one
+  // may still be read while the next is written), and the first one
+  TreeSegment seg[2], first;
+  int abort, skip, flag, pending, more[2], last[2];
+  // what the two accumulators' threads of a row hand over: maxima [0] and sums
+  // [1]; at a segment's start (e5m2) [0] the row's score factor
+  float row[2][128];
+};
+
 // Registers: setmaxnreg moves them from the loader, MMA and converter warps
 // to the softmax warps; the shares add up to no more than the block is launched
 // with.
@@ -103,7 +115,7 @@ struct Cfg {
   static constexpr int kThreads = kByte ? 640 : 384;
   static constexpr int kRegsLaunch = kByte ? 96 : 168;
   static constexpr int kRegsSoftmax = kByte ? 152 : 200;
-  static constexpr int kRegsAux = kByte ? (DT == kDtypeU8 ? 64 : 80) : 104;  // (72 spilled in the MMA thread, on the way of every product)
+  static constexpr int kRegsAux = kByte ? (DT == kDtypeU8 ? 64 : 80) : 104;
   static constexpr int kRegsConvert = DT == kDtypeU8 ? 56 : 48;
   static_assert(256 * kRegsSoftmax + 128 * kRegsAux + (kThreads - 384) * kRegsConvert <= kThreads * kRegsLaunch,
                 "register split");
@@ -122,7 +134,8 @@ struct Cfg {
   static constexpr int kScaleOff = kRawOff + kRaw * kRawBytes;
   static constexpr int kScales = 2 * kSlots;
   static constexpr int kBarOff = kScaleOff + (DT == kDtypeU8 ? kScales * kBN * 4 : 0);
-  static constexpr int kSmemBytes = kBarOff + 304 + 1024;  // + alignment slack
+  static constexpr int kMiscOff = kBarOff + 304;           // TreeMisc
+  static constexpr int kSmemBytes = kMiscOff + static_cast<int>(sizeof(TreeMisc));
   // mbarriers
   static constexpr int kQFull = 0;
   static constexpr int kQFree = 1;                  // a segment of two row tiles is done with Q
@@ -145,7 +158,7 @@ struct Cfg {
   static constexpr int kDrain = kSegFree + 2;
   static constexpr int kNBars = kDrain + 1;
   static_assert(kNBars * 8 + 4 <= 304, "barrier area");
-  static_assert(kSmemBytes + 1600 <= 227 * 1024, "shared memory (with the static part)");
+  static_assert(kMiscOff % 16 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
@@ -319,28 +332,25 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   constexpr bool kGrouped = PG && !kByte;
   using L = Tile<kGrouped>;
   constexpr int kSlots = C::kSlots;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char smem[];  // (no static part: every byte is needed)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + C::kNBars * 8);
-  __shared__ TreePlan plan;
-  __shared__ int s_abort, s_skip, s_flag, s_pending, s_more[2], s_last[2];
-  // what the two accumulators' threads of a row hand over: maxima and sums; at
-  // a segment's start (e5m2) the row's score factor
-  __shared__ float s_m[kBM], s_l[kBM];
-  // the segments, out of the softmax and MMA warps' registers (two places: one
-  // may still be read while the next is written), and the first one
-  __shared__ TreeSegment s_seg[2], s_first;
+  TreeMisc& sh = *reinterpret_cast<TreeMisc*>(smem + C::kMiscOff);
+  TreePlan& plan = sh.plan;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.group, acc_rows = p.tokens_per_tile * G, rows_per_block = NT * acc_rows;
 
   if (!p.early) grid_dependency_wait();
+  if (smem_u32(smem) & 1023u) {  // tiles and descriptors need the alignment that the declaration asks for
+    if (tid == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_TIMEOUT));
+    return;
+  }
   if (tid == 0) {
-    s_abort = 0;
+    sh.abort = 0;
     // an earlier block timed out: the result is invalid already
-    s_skip = (*reinterpret_cast<volatile int32_t*>(p.err) & static_cast<int>(MQA_DEVERR_TIMEOUT)) ? 1 : 0;
+    sh.skip = (*reinterpret_cast<volatile int32_t*>(p.err) & static_cast<int>(MQA_DEVERR_TIMEOUT)) ? 1 : 0;
     mbar_init(bar(C::kQFull), 1);
     mbar_init(bar(C::kQFree), 1);
     mbar_init(bar(C::kXFree), 8);
@@ -384,18 +394,18 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
 
   auto fail = [&](bool one) {
     if (one) {
-      s_abort = 1;
+      sh.abort = 1;
       atomicOr(p.err, static_cast<int>(MQA_DEVERR_TIMEOUT));
     }
   };
   // whether a segment's rows need both accumulators (else both hold them all)
   auto is_two = [&](const TreeSegment& g) { return NT == 2 && g.s.nodes * G - g.rb * rows_per_block > acc_rows; };
-  auto stop = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
+  auto stop = [&]() { return *reinterpret_cast<volatile int*>(&sh.abort) != 0; };
   auto regs_aux = [&]() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsAux)); };
   auto begin = [&]() {
     TreeWalk w;
     w.start(plan);
-    if (s_skip) w.at = w.end;
+    if (sh.skip) w.at = w.end;
     return w;
   };
 
@@ -565,9 +575,9 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       int seg = 0, n_two = 0;
       while (ok) {
         ok = wait(C::kSeg + (seg & 1), seg >> 1);
-        if (!ok || !s_more[seg & 1]) break;
-        const int T = s_seg[seg & 1].nt;
-        const bool two = is_two(s_seg[seg & 1]), last = s_last[seg & 1] != 0;
+        if (!ok || !sh.more[seg & 1]) break;
+        const int T = sh.seg[seg & 1].nt;
+        const bool two = is_two(sh.seg[seg & 1]), last = sh.last[seg & 1] != 0;
         n_two += two;
         if constexpr (C::kHalf)
           ok = wait(C::kQReady + 0, seg) && (!two || wait(C::kQReady + 1, n_two - 1)) && full(u0);
@@ -650,17 +660,17 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           if (!ok) fail(true);
           if (!ok || stop()) break;
         }
-        TreeSegment& g = s_seg[k & 1];
+        TreeSegment& g = sh.seg[k & 1];
         const bool more = walk.next(p, kBN, rows_per_block, g), last = walk.at >= walk.end;
-        s_more[k & 1] = more;
-        s_last[k & 1] = last;
-        if (k == 0) s_first = g;
+        sh.more[k & 1] = more;
+        sh.last[k & 1] = last;
+        if (k == 0) sh.first = g;
         mbar_arrive(bar(C::kSeg + (k & 1)));
-        if (k == 1 && !(s_first.head && s_first.tail)) {
+        if (k == 1 && !(sh.first.head && sh.first.tail)) {
           const bool ok = mbar_wait(bar(C::kPart), 0, p.wait_ns);
           if (!ok) fail(true);
           if (!ok || stop()) break;
-          const TreeMerge mg = tree_merge(plan, s_first);
+          const TreeMerge mg = tree_merge(plan, sh.first);
           __threadfence();  // the partial (seen through the barrier), before the count
           complete = atomicAdd(p.arrived + mg.ca, 1) == mg.m - 1;
           __threadfence();  // the other blocks' partials, after it
@@ -669,7 +679,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       }
     }
     __syncwarp();
-    if (lane == 0) s_pending = complete;
+    if (lane == 0) sh.pending = complete;
     named_bar_sync(3, 256 + 32);
   } else if (kByte && warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsConvert));
@@ -764,7 +774,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
     // ---------------------------- softmax of accumulator q, row r per thread
-    const int q = warp >> 2, r = tid - q * kBM;
+    const int q = warp >> 2, r = tid & (kBM - 1);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t scol = tmem + lane_base + kColS + q * 128, ocol = tmem + lane_base + kColO + q * 128;
     float c = p.scale_log2;  // (e5m2: over the factor that Q's row was scaled by)
@@ -776,8 +786,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kSeg + (seg & 1)), (seg >> 1) & 1, p.wait_ns) && !stop());
       if (!ok) fail(lane == 0);
       aborted = bar_any(2, 256, !ok);  // (and no warp is at the last segment any more)
-      if (aborted || !s_more[seg & 1]) break;
-      const TreeSegment& g = s_seg[seg & 1];
+      if (aborted || !sh.more[seg & 1]) break;
+      const TreeSegment& g = sh.seg[seg & 1];
       const bool two = is_two(g);
       const int step = two ? 1 : 2;
       const int gr = g.rb * rows_per_block + (two ? q * acc_rows : 0) + r;  // row of the unit's kv head
@@ -794,27 +804,31 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kQFull), seg & 1, p.wait_ns) && !stop());
           if (ok && r < acc_rows) {
             c = p.scale_log2 / half_row(smem + C::kQOff + (two ? q : 0) * kTileBytes, r);
-            if (!two) s_m[r] = c;
+            if (!two) sh.row[0][r] = c;
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(bar(C::kQReady + (two ? q : 0)));
         } else {
           ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kQReady + 0), seg & 1, p.wait_ns) && !stop());
-          c = s_m[r];
+          c = sh.row[0][r];
         }
       }
       float m_ref = -INFINITY, l = 0.f;
       for (int t = two ? 0 : q; ok && t < nt; t += step, ++js, key0 += step * kBN) {
-        // only tiles that reach a node, the end or the window are masked: bit x
-        // of these words, the row attends to key key0 + x
+        // only tiles that reach a node, the end or the window are masked
         // (one answer for the warp: what follows has to stay converged)
         const bool masked = __any_sync(0xffffffffu, key0 + kBN > pos || key0 < ka);
-        uint32_t bits[4];
+        // (uint8: the bits where they are used, which suits that loop's registers:
+        // 32 x 16 nodes over 4096 keys 123 -> 117 us; bf16 32 x 64 nodes 145 -> 147.5)
+        TreeRow row;
+        uint32_t bits[4];  // bit x: the row attends to key key0 + x
         if (masked && warp_rows) {
-          const TreeRow row = tree_row(p, g.b, g.s, node);
+          row = tree_row(p, g.b, g.s, node);
+          if constexpr (DT != kDtypeU8) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) bits[w] = tree_bits(row, key0 + 32 * w);
+            for (int w = 0; w < 4; ++w) bits[w] = tree_bits(row, key0 + 32 * w);
+          }
         }
         ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kSFull + q), js & 1, p.wait_ns) && !stop());
         if (!ok) break;
@@ -840,6 +854,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff);
           const float4* sk = reinterpret_cast<const float4*>(sc + ((u0 + 2 * t) % C::kScales) * kBN);
           const float4* sv = reinterpret_cast<const float4*>(sc + ((u0 + 2 * t + 1) % C::kScales) * kBN);
+          constexpr bool kMaskS = DT == kDtypeF8;
           auto scores = [&](int x, float (&s)[32]) {  // keys 32 x .. 32 x + 31, masked ones -inf
             tc05::wait_ld();
             tc05::reg_fence(s);
@@ -852,18 +867,38 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
                 s[4 * i] = a.x, s[4 * i + 1] = a.y, s[4 * i + 2] = b.x, s[4 * i + 3] = b.y;
               }
             }
-            if (masked) {
-              const uint32_t w = x < 2 ? (x == 0 ? bits[0] : bits[1]) : (x == 2 ? bits[2] : bits[3]);
+            if (!kMaskS && masked) {  // (uint8: past the scales, which may be anything in a masked row)
+              uint32_t w;
+              if constexpr (DT == kDtypeU8)
+                w = tree_bits(row, key0 + 32 * x);
+              else
+                w = x < 2 ? (x == 0 ? bits[0] : bits[1]) : (x == 2 ? bits[2] : bits[3]);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!((w >> i) & 1u)) s[i] = -INFINITY;
             }
           };
-          // The row's scores pass through registers 64 at a time, twice: for the
-          // maximum, then for the probabilities. (128 of them kept in registers
-          // between the two need a loop body twice as long, which was slower:
-          // 4096 tokens x 32, 64 nodes 198 vs 192 us, 16 nodes 110 vs 109.) P
-          // of 32 keys takes 16 columns of S, all of them read already.
+          // e5m2: -inf into S itself, out of the way of the other tiles' code (32 x 64
+          // nodes over 4096 keys 155 -> 150 us; bf16 145 -> 147.5)
+          if (kMaskS && masked) {
+#pragma unroll 1
+            for (int x = 0; x < kBN / 16; ++x) {
+              const uint32_t w = (x < 4 ? (x < 2 ? bits[0] : bits[1]) : (x < 6 ? bits[2] : bits[3])) >> (16 * (x & 1));
+              float v[16];
+              tc05::ld_32x32b_x16(scol + 16 * x, v);
+              tc05::wait_ld();
+              tc05::reg_fence(v);
+              uint32_t m[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) m[i] = (w >> i) & 1u ? __float_as_uint(v[i]) : 0xff800000u;
+              tc05::st_32x32b_x16_u(scol + 16 * x, m);
+            }
+            tc05::wait_st();
+          }
+          // A thread's scores pass through registers twice, for the maximum and
+          // for the probabilities. (128 of them kept in registers between the two
+          // need a loop body twice as long, which was slower; 64 do not fit.) P of
+          // 32 keys takes 16 columns of S that this thread has read already.
           float mt = -INFINITY;
 #pragma unroll 1
           for (int x = 0; x < kBN / 32; x += 2) {
@@ -891,14 +926,15 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             // before this S_q, whose completion this thread has seen
             const float alpha = (grow && m_ref != -INFINITY) ? fast_exp2((m_ref - m_new) * c) : 1.f;
 #pragma unroll 1
-            for (int x = 0; x < kD / 32; ++x) {
-              float v[32];
-              tc05::ld_32x32b_x32(ocol + x * 32, v);
+            for (int x = 0; x < kD / 16; ++x) {  // (16 dims a pass: twice as many took 4 % of the kernel's time, as longer code)
+              float v[16];
+              tc05::ld_32x32b_x16(ocol + x * 16, v);
               tc05::wait_ld();
               tc05::reg_fence(v);
+              uint32_t w[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] *= alpha;
-              tc05::st_32x32b_x32(ocol + x * 32, v);
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * alpha);
+              tc05::st_32x32b_x16_u(ocol + x * 16, w);
             }
             l *= alpha;
           }
@@ -963,27 +999,24 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       // ---- the segment's result, 32 dims at a time: a whole unit's goes out,
       // a part's into the workspace. (One copy of this code for every case:
       // fetching it costs more than running it.)
-      const bool whole = g.head && g.tail, last = s_last[seg & 1] != 0;
+      const bool whole = g.head && g.tail, last = sh.last[seg & 1] != 0;
       // both accumulators hold these rows: each warpgroup hands the other's 64
       // dims over and puts out its own, through the Q area (free: every product
       // with Q is done; NT = 2: the second row tile's half), 16 KB a direction
       const bool both = !two && nt > 1;
       unsigned char* xbuf = smem + C::kQOff + (NT - 1) * kTileBytes;
-      auto piece = [&](int from, int i) {  // 16 bytes i of row r of warpgroup `from`
-        return reinterpret_cast<float4*>(xbuf + from * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
-      };
       float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c, w0 = 1.f, w1 = 0.f, mo = 0.f, lo = 0.f;
       if (both) {
         if (q == 1) {
-          s_m[r] = m2;
-          s_l[r] = l;
+          sh.row[0][r] = m2;
+          sh.row[1][r] = l;
         }
         named_bar_sync(1, 256);
         if (q == 0) {
-          mo = s_m[r];
-          lo = s_l[r];
-          s_m[r] = m2;
-          s_l[r] = l;
+          mo = sh.row[0][r];
+          lo = sh.row[1][r];
+          sh.row[0][r] = m2;
+          sh.row[1][r] = l;
         }
       }
       const bool writer = (two || both || q == 0) && warp_rows;
@@ -991,10 +1024,22 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       const int br = gr - g.rb * rows_per_block;  // row of the block
       float* part = tree_place(p, g, blockIdx.x, rows_per_block, kD);
       float inv = l > 0.f ? 1.f / l : 0.f;
+      auto weights = [&]() {  // of the two accumulators in what both hold
+        const float mx = fmaxf(m2, mo);
+        w0 = mx != -INFINITY ? exp2f(m2 - mx) : 0.f;
+        w1 = mx != -INFINITY ? exp2f(mo - mx) : 0.f;
+        l = w0 * l + w1 * lo;
+        m2 = mx;
+        inv = l > 0.f ? 1.f / l : 0.f;
+      };
+      // this thread's pieces of 32 dims
       const int x0 = both ? 2 * q : 0, x1 = both ? x0 + 2 : kD / 32;
 #pragma unroll 1
       for (int x = x0; x < x1; ++x) {
         float v[32];
+        auto piece = [&](int from, int i) {  // 16 bytes i of row r of accumulator `from`
+          return reinterpret_cast<float4*>(xbuf + from * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
+        };
         if (both) {
           if (x > x0) named_bar_sync(1, 256);  // what was handed over has been read
           __syncwarp();
@@ -1016,15 +1061,10 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         if (both) {
           if (x == x0) {
             if (q == 1) {
-              mo = s_m[r];
-              lo = s_l[r];
+              mo = sh.row[0][r];
+              lo = sh.row[1][r];
             }
-            const float mx = fmaxf(m2, mo);
-            w0 = mx != -INFINITY ? exp2f(m2 - mx) : 0.f;
-            w1 = mx != -INFINITY ? exp2f(mo - mx) : 0.f;
-            l = w0 * l + w1 * lo;
-            m2 = mx;
-            inv = l > 0.f ? 1.f / l : 0.f;
+            weights();
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -1096,15 +1136,15 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     // one's was by warp 11; a unit that is complete is merged
     named_bar_sync(3, 256 + 32);
     if (!aborted) {
-      const TreeSegment& g = s_seg[seg & 1];
-      const bool part = s_more[seg & 1] && !(g.head && g.tail);
+      const TreeSegment& g = sh.seg[seg & 1];
+      const bool part = sh.more[seg & 1] && !(g.head && g.tail);
       bool complete = false;
       if (part)
-        complete = tree_arrive(p, tree_merge(plan, g), tid, &s_flag, [] { named_bar_sync(1, 256); });
+        complete = tree_arrive(p, tree_merge(plan, g), tid, &sh.flag, [] { named_bar_sync(1, 256); });
 #pragma unroll 1
       for (int i = 0; i < 2; ++i)
-        if (i == 0 ? complete : s_pending != 0) {
-          const TreeSegment& f = i == 0 ? g : s_first;
+        if (i == 0 ? complete : sh.pending != 0) {
+          const TreeSegment& f = i == 0 ? g : sh.first;
           tree_merge_rows<kD>(p, tree_merge(plan, f), f, rows_per_block, tid, 256);
         }
     }
@@ -1117,7 +1157,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   tc05::fence_before_sync();
   __syncthreads();
   if (warp == 9) {
-    if (*reinterpret_cast<volatile int*>(&s_abort)) {
+    if (*reinterpret_cast<volatile int*>(&sh.abort)) {
       // products may still be in flight after a timeout: wait (bounded) for
       // them before the columns are released
       commit_elect(bar(C::kDrain));  // (the lane that issued them)

@@ -15,15 +15,16 @@
 // arrive). One-byte caches are widened on the way in, exactly: an e5m2 value
 // has 3 significant bits, code - zero point is an integer of magnitude <= 255
 // and has 8. The row's scale then multiplies the score (K) or the probability
-// (V) in fp32. P is rounded to bf16, the tensor cores' operand (2^-8 of each probability);
-// the sum l adds the unrounded ones.
+// (V) in fp32. P enters its product as two bf16 terms (split_p, within 2^-15;
+// one term, 2^-8, was more than half of the output's error).
 //
 // Keys that no row may read (past the sequence, before the window) land as
 // zeros whatever the cache holds there.
 //
 // Bound: with few rows the HBM stream of K and V; the tiles' L2-to-SM copies
 // and the 64-row MMA work from about 64 rows per kv head on (32 x 16 nodes on
-// 4096 keys, 32 + 8 heads of 64 dims, 273 MB: a step takes 89 us, 3.1 TB/s).
+// 4096 keys, 32 + 8 heads of 64 dims, 273 MB: a step takes 105 us, 2.6 TB/s;
+// with P in one term 89 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -74,7 +75,7 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t z) {
 }
 
 template <int D, int DT>
-__global__ void __launch_bounds__(kThreads) attn_tree_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) attn_tree_kernel(const TreeParams p) {
   using Y = Lay<D, DT != kDtypeBf16>;
   constexpr int kStages = Y::kStages;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -291,9 +292,10 @@ __global__ void __launch_bounds__(kThreads) attn_tree_kernel(const TreeParams p)
       // ---- O += P V
 #pragma unroll
       for (int k = 0; k < kKeys / 16; ++k) {
-        const uint32_t a[4] = {pack_bf16x2(s[2 * k][0], s[2 * k][1]), pack_bf16x2(s[2 * k][2], s[2 * k][3]),
-                               pack_bf16x2(s[2 * k + 1][0], s[2 * k + 1][1]),
-                               pack_bf16x2(s[2 * k + 1][2], s[2 * k + 1][3])};
+        uint32_t a[4], al[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          split_p(make_float2(s[2 * k + (i >> 1)][2 * (i & 1)], s[2 * k + (i >> 1)][2 * (i & 1) + 1]), a[i], al[i]);
 #pragma unroll
         for (int dp = 0; dp < D / 16; ++dp) {
           const int r = k * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, cc = 2 * dp + (lane >> 4);
@@ -301,6 +303,8 @@ __global__ void __launch_bounds__(kThreads) attn_tree_kernel(const TreeParams p)
           ldsm_x4_trans(vs + chunk_at<D>(r, cc), b0, b1, b2, b3);
           mma_bf16_16816(o[2 * dp], a, b0, b1);
           mma_bf16_16816(o[2 * dp + 1], a, b2, b3);
+          mma_bf16_16816(o[2 * dp], al, b0, b1);
+          mma_bf16_16816(o[2 * dp + 1], al, b2, b3);
         }
       }
       __syncthreads();  // the tile is read: the next request may overwrite it
@@ -373,7 +377,8 @@ cudaError_t launch_t(const TreeParams& p, int ctas, cudaStream_t stream) {
 
 }  // namespace
 
-// (blocks per SM: what their registers allow, 255 and 168 a thread)
+// (blocks per SM: what their registers allow, 255 and 168 a thread, the latter
+// by the launch bounds: left alone, uint8 took more and 133 us instead of 109)
 TreeShape tree_mma_shape(int head_dim) { return {kRows, kKeys, head_dim == 128 ? 2 : 3}; }
 
 cudaError_t launch_tree_mma(const TreeParams& p, int ctas, cudaStream_t stream) {

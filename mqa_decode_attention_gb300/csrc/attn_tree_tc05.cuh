@@ -11,32 +11,37 @@
 //   softmax        one row per thread: running maximum and sum
 //                  (FlashAttention, "Arsitektur Inferensi LLM", section 5), O
 //                  rescaled only when a row's maximum grows by more than 2^8;
-//                  P (bf16) written over its S columns
+//                  P (two bf16 terms) written over its S columns
 //   O += P V       tcgen05.mma with A = P from tensor memory
 // Rows are (node i, query head) pairs of one kv head, whole nodes to a block.
 // There are two accumulators (S and O of each in tensor memory, 512 columns)
 // with a softmax warpgroup each:
 //   NT = 2  (more than 128 rows per kv head) two query tiles of up to 128 rows
 //           share every K / V tile; the tensor cores alternate between them.
-//           One tile of K and V asks for 1.45 us of HBM and 1.38 us of products;
-//           what bounds it is each accumulator's chain product - softmax - product
-//           (32 x 64 nodes on 4096 keys, 32 + 8 heads, 573 MB: 136 us, 4.2 TB/s,
-//           1.0 PFLOP/s). A tree that ends in a block of up to 128 rows has that
-//           block done as below.
+//           One tile of K and V asks for 1.45 us of HBM and 1.04 us of products
+//           (0.69 with P in one term); what bounds it is each accumulator's chain
+//           product - softmax - product (32 x 64 nodes on 4096 keys, 32 + 8
+//           heads, 573 MB: a step 169 us, 0.8 PFLOP/s without the second terms). A
+//           tree that ends in a block of up to 128 rows has that block done as
+//           below.
 //   NT = 1  (up to 128 rows) both accumulators hold the same rows and take the
 //           tiles in turn, so that one's softmax runs beside the other's
 //           products; their results meet in shared memory at a unit's end.
 //           Bound by the HBM stream: a tile of K and V (64 KB) takes 1.45 us
-//           of an SM's share of 6.8 TB/s, its products 0.7 us, and the two
-//           accumulators' chains product-softmax-product about 1 us a tile
-//           (32 x 16 nodes on 4096 keys, 546 MB: 98 us, 5.6 TB/s; one tree of 32
-//           nodes on 131040 keys: 316 us, 6.8 TB/s).
+//           of an SM's share of 6.8 TB/s, its products 0.5 us, and the two
+//           accumulators' chains product-softmax-product about 1.1 us a tile
+//           (a step of 32 x 16 nodes on 4096 keys, 549 MB: 103 us, 5.3 TB/s; of 4 x
+//           32 nodes on 131040 keys, 2.15 GB: 326 us, 6.6 TB/s).
 //
 // Q is loaded by TMA as the append left it (bf16, not scaled): the scale
-// times log2 e goes into the exponent's fused multiply-add. Q and P enter the
-// products as bf16 (up to 2^-8 of each value); a second bf16 term of Q would
-// double the first product, at 256 rows a quarter of what an SM does in a
-// tile's time. Sums, maxima and partial results are fp32.
+// times log2 e goes into the exponent's fused multiply-add. A second bf16 term of
+// Q has no room in shared memory beside two row tiles. P over a bf16 cache enters
+// as two bf16 terms (split_p, within 2^-15; the two take the columns that S had):
+// with one term (2^-8) the output's error against 64 bits is 1.7 times that of
+// its own rounding to bf16, with two 1.4 times, which Q's rounding leaves. The
+// price: 32 x 64 nodes 146 -> 169 us, 32 x 16 nodes 101 -> 103 us. Over e5m2 P
+// has an f16's 2^-11, over uint8 one bf16 term (1.35 times). Sums, maxima and
+// partial results are fp32.
 //
 // One-byte caches: the loader's tiles are codes (16 KB), eight converter warps
 // widen each to a 16-bit tile, exactly. An e5m2 code is the high byte of an
@@ -48,8 +53,8 @@
 // An f16 P is within 2^-11 of its value, or within 2^-25 when it is below 2^-14:
 // the row's largest P is at least 1 (and at most 2^8), so keys that light move
 // the result by less than 2^-25 of the largest |v| each.
-// (64 x 8 nodes of 32 heads on 8192 e5m2 keys of one kv head, 268 MB read: 95 us,
-// 0.7 PFLOP/s; bound by the widening and the chains.)
+// (A step of 64 x 8 nodes of 32 heads on 8192 e5m2 keys of one kv head: 92 us, 0.75
+// PFLOP/s; bound by the widening and the chains.)
 //
 // Keys that no node may read (past the sequence, before the window) have zero
 // V rows whatever the cache holds, so that 0 * NaN never enters a sum.
@@ -124,6 +129,7 @@ struct Cfg {
   static constexpr int kRaw = kByte ? (NT == 2 ? 2 : (DT == kDtypeU8 ? 3 : 4)) : 0;
   static_assert(NT == 1 || DT != kDtypeU8, "no room for two row tiles beside the scales");
   static constexpr bool kHalf = DT == kDtypeF8;  // f16 operands (else bf16)
+  static constexpr bool kSplitP = DT == kDtypeBf16;  // P as two bf16 terms: [16 columns][16 columns] of each 32 keys
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = NT * kTileBytes;
   static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
@@ -276,8 +282,9 @@ __device__ __forceinline__ void mma_128(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 // D (+)= A B over 64 values of K (keys): A in tensor memory, 8 columns for 16
-// keys, B MN-major in shared memory, 16 keys BK descriptor units apart.
-template <int BK>
+// keys (the second 32 keys AK columns after the first), B MN-major in shared
+// memory, 16 keys BK descriptor units apart.
+template <int BK, int AK>
 __device__ __forceinline__ void mma_64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
       "{\n\t.reg .pred e, z, o;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\t"
@@ -286,11 +293,12 @@ __device__ __forceinline__ void mma_64(uint32_t d, uint32_t a, uint64_t b, uint3
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, z;\n\t"
       "add.s32 x, %1, 8;\n\tadd.s64 y, %2, %5;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
-      "add.s32 x, %1, 16;\n\tadd.s64 y, %2, %6;\n\t"
+      "add.s32 x, %1, %8;\n\tadd.s64 y, %2, %6;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t"
-      "add.s32 x, %1, 24;\n\tadd.s64 y, %2, %7;\n\t"
+      "add.s32 x, %1, %9;\n\tadd.s64 y, %2, %7;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, o;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "n"(BK), "n"(2 * BK), "n"(3 * BK)
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "n"(BK), "n"(2 * BK), "n"(3 * BK), "n"(AK),
+      "n"(AK + 8)
       : "memory");
 }
 __device__ __forceinline__ void commit_elect(uint32_t mbar) {
@@ -555,11 +563,11 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       // O_q (+)= P_q V(t) of keys 64 h .. 64 h + 63: each half of P as soon as it is written
       auto issue_pv = [&](int q, int t, int h, bool add) {
         tc05::fence_after_sync();
-        mma_64<2 * L::kGroup / 16>(
-            tm + kColO + q * 128, tm + kColS + q * 128 + h * 32,
-            tc05::smem_desc_sw128(sb + C::kRingOff + ((u0 + 2 * t + 1) % kSlots) * kTileBytes + h * 8 * L::kGroup, L::kHalf,
-                                  L::kGroup),
-            id_o, add || h > 0);
+        const uint64_t v = tc05::smem_desc_sw128(
+            sb + C::kRingOff + ((u0 + 2 * t + 1) % kSlots) * kTileBytes + h * 8 * L::kGroup, L::kHalf, L::kGroup);
+        const uint32_t a = tm + kColS + q * 128 + h * (C::kSplitP ? 64 : 32);
+        mma_64<2 * L::kGroup / 16, C::kSplitP ? 32 : 16>(tm + kColO + q * 128, a, v, id_o, add || h > 0);
+        if constexpr (C::kSplitP) mma_64<2 * L::kGroup / 16, 32>(tm + kColO + q * 128, a + 16, v, id_o, true);
       };
       auto pv = [&](int q, int t, bool add) {
         const int n = ps[q]++;
@@ -897,8 +905,8 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           }
           // A thread's scores pass through registers twice, for the maximum and
           // for the probabilities. (128 of them kept in registers between the two
-          // need a loop body twice as long, which was slower; 64 do not fit.) P of
-          // 32 keys takes 16 columns of S that this thread has read already.
+          // need a loop body twice as long, which was slower.) P of 32 keys takes
+          // columns of S that this thread has read already.
           float mt = -INFINITY;
 #pragma unroll 1
           for (int x = 0; x < kBN / 32; x += 2) {
@@ -946,7 +954,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             if (!ok) break;
           }
           auto probs = [&](int x, const float (&s)[32]) {
-            uint32_t pk[16];
+            uint32_t pk[C::kSplitP ? 32 : 16];
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const float2 d0 = fma2(make_float2(s[2 * i], s[2 * i + 1]), c, e);
@@ -959,10 +967,18 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
                 p0 = mul2(p0, make_float2(f.x, f.y));
                 p1 = mul2(p1, make_float2(f.z, f.w));
               }
-              pk[i] = pack_p<C::kHalf>(p0);
-              pk[i + 1] = pack_p<C::kHalf>(p1);
+              if constexpr (C::kSplitP) {
+                split_p(p0, pk[i], pk[16 + i]);
+                split_p(p1, pk[i + 1], pk[17 + i]);
+              } else {
+                pk[i] = pack_p<C::kHalf>(p0);
+                pk[i + 1] = pack_p<C::kHalf>(p1);
+              }
             }
-            tc05::st_32x32b_x16_u(scol + 16 * x, pk);
+            if constexpr (C::kSplitP)
+              tc05::st_32x32b_x32_u(scol + 32 * x, pk);
+            else
+              tc05::st_32x32b_x16_u(scol + 16 * x, pk);
           };
 #pragma unroll 1
           for (int x = 0; x < kBN / 32; ++x) {

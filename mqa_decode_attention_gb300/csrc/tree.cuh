@@ -177,6 +177,14 @@ __device__ __forceinline__ uint2 widen_u8(uint32_t w, uint32_t z) {
   return r;
 }
 
+// Two probabilities as two bf16 terms: the upper half of each value's bits, and
+// what that leaves (below 2^-7 of the value), rounded: together within 2^-15.
+__device__ __forceinline__ void split_p(float2 v, uint32_t& hi, uint32_t& lo) {
+  const uint32_t x = __float_as_uint(v.x), y = __float_as_uint(v.y);
+  hi = __byte_perm(x, y, 0x7632);
+  lo = pack_bf16x2(v.x - __uint_as_float(x & 0xffff0000u), v.y - __uint_as_float(y & 0xffff0000u));
+}
+
 // 32 bits, bit c = the row may attend to key k0 + c. m: the row's mask words
 // with the bits of dead nodes cleared (all zero for a dead row), ka its first
 // key, pos the number of cached tokens.

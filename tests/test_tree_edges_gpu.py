@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import oracle
-from test_tree_gpu import check, check_append, live, m, run_step  # noqa: F401 (m: fixture)
+from test_tree_gpu import check, check_append, check_attention, live, m, run_step  # noqa: F401 (m: fixture)
 from tree_cases import TreeCase, raw
 
 pytestmark = pytest.mark.gpu
@@ -292,3 +292,20 @@ def test_u8_every_code_and_zero_point(m, d):  # noqa: F811
         for b, at in enumerate(pos.tolist()):
             want = (v[b, 0, at].float() - vsz[b, 0, at, 1]) * vsz[b, 0, at, 0]
             assert torch.equal(out[b, 0], want.expand(4, d))
+
+
+@pytest.mark.parametrize("cache,d,hq,hkv,nodes", [("bf16", 128, 32, 8, 9), ("bf16", 128, 32, 8, 60), ("bf16", 64, 12, 3, 31),
+                                                  ("e5m2", 64, 12, 3, 31), ("u8", 64, 12, 3, 31), ("bf16", 128, 160, 1, 2),
+                                                  ("e5m2", 128, 32, 8, 60)])
+@pytest.mark.parametrize("page", [0, 16])
+def test_probabilities_keep_more_than_a_bf16(m, cache, d, hq, hkv, nodes, page):  # noqa: F811
+    """fp32 outputs against the oracle's on the same operands: P as two bf16 terms
+    is within 2^-7 (what the first leaves) times 2^-8 (the second's rounding) =
+    2^-15 of its value; as an f16 (e5m2, head_dim 128) within 2^-11, or 2^-25 where
+    it is below 2^-14 and the row's largest at least 1: 700 keys, 2^-15 at most of
+    the largest |v|, which is below 2^3 and over the mean |v| by less than 2^4."""
+    c = TreeCase(hq, hkv, d, [600, 37], [nodes, nodes - 1], nodes, cache, page, seed=nodes)
+    t, bufs = run_step(m, c, torch.float32)
+    assert int(bufs.err.item()) == 0
+    p_err = 2.0 ** -15 if cache != "e5m2" or d == 64 else 2.0 ** -11 + 2.0 ** -11
+    check_attention(c, t, bufs.q_rot, bufs.out, bufs.lse, p_err=p_err)

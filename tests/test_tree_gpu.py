@@ -80,7 +80,7 @@ def check_append(c, t, q_rot):
         assert np.array_equal(raw(t.ksz), ksz, equal_nan=True) and np.array_equal(raw(t.vsz), vsz, equal_nan=True)
 
 
-def check_attention(c, t, q_rot, out, lse, max_key=None):
+def check_attention(c, t, q_rot, out, lse, p_err=E):
     scale = 1 / math.sqrt(c.d)
     tokens = c.max_len
     keys = oracle.logical(c.cache, raw(t.k), None if t.ksz is None else raw(t.ksz), c.table, c.page, tokens)
@@ -92,7 +92,7 @@ def check_attention(c, t, q_rot, out, lse, max_key=None):
     assert glse is None or np.all(glse[~rows] == 7.0)
     want, size, reach = ref["out"][rows], ref["size"][rows], ref["reach"][rows][..., None]
     score = (c.d + 6) * 2.0 ** -24 * reach
-    bound = E * size + (2 * (score + 2.0 ** -20) + 2.0 ** -15) * size
+    bound = p_err * size + (2 * (score + 2.0 ** -20) + 2.0 ** -15) * size
     bound = bound + (E if out.dtype == torch.bfloat16 else 2.0 ** -24) * (np.abs(want) + bound) + 1e-30
     err = np.abs(got[rows] - want)
     assert np.isfinite(got[rows]).all()

@@ -1261,9 +1261,10 @@ mqa_status tree_attention_impl(const mqa_kv_layout* L, int n, const void* q_rot,
   p.arrived = static_cast<int32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.counters);
   p.err = err_word;
-  // (1, 3, 6, 12 tiles measured: 8 kv heads x 700 tokens 16.3, 16.9, 16.9, 27.0 us,
-  // x 3000 tokens 26.1, 20.4, 20.2, 24.0; 2 x 8 heads x 4096 tokens, 64 nodes 60.6, 60.9, 54.2, 57.1)
-  p.min_tiles = 6;
+  // (2, 3, 4, 6 tiles measured: 8 kv heads, 8 nodes, 700 tokens 14.9, 16.7, 18.8, 17.2 us;
+  // 3000 tokens 20.7, 19.7, 21.3, 24.0, over e5m2 31.0, 21.3, 26.8, 27.0; 8000 tokens 25.9,
+  // 21.7, 21.0, 21.8)
+  p.min_tiles = 3;
   p.tokens_per_tile = c.tokens;
   p.early = early;
   p.wait_ns = wait_limit(L);

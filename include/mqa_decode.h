@@ -421,7 +421,8 @@ MQA_API mqa_status mqa_prefill_step(const mqa_kv_layout* layout, int32_t n_new, 
  *   arithmetic and device errors), but node i is rotated by pos[b] + depth[b, i]
  *   and stored at pos[b] + i, and q_rot [batch, n_nodes, h_q, head_dim] is
  *   bf16, the operand of the attention. num_nodes[b] out of range sets
- *   MQA_DEVERR_SEQ_LEN and the sequence is skipped; a depth out of range sets
+ *   MQA_DEVERR_SEQ_LEN, a negative pos[b] (with nodes) MQA_DEVERR_POS_RANGE:
+ *   nothing of that sequence is written. A depth out of range sets
  *   MQA_DEVERR_TREE and is taken as the nearest inside.
  * gqa_tree_attention: for node i and query head h of sequence b,
  *   O = sum_t softmax_t(scale * q_rot . K_t) V_t over the cached tokens

@@ -89,8 +89,10 @@ __device__ __noinline__ uint32_t e5m2_pair_fp64(float x, float y, double ang) {
 }
 
 // A token of a drafted tree (p.depth set): its rotation position, pos + depth
-// (the slot stays pos + i), and whether it exists. A depth outside [0, n_new)
-// is reported and taken as the nearest inside. `report`: one thread per token.
+// (the slot stays pos + i), and whether it exists: a sequence at a negative
+// position has no tokens at all (those that would land in rows 0, 1, .. would
+// overwrite its first cached ones). A depth outside [0, n_new) is reported and
+// taken as the nearest inside. `report`: one thread per token.
 __device__ __forceinline__ bool tree_token(const AppendParams& p, int b, int i, bool report, int* at) {
   const int nodes = p.num_nodes != nullptr ? p.num_nodes[b] : p.n_new;
   if (nodes < 0 || nodes > p.n_new) {
@@ -98,12 +100,17 @@ __device__ __forceinline__ bool tree_token(const AppendParams& p, int b, int i, 
     return false;
   }
   if (i >= nodes) return false;
+  const int pos = p.pos[b];
+  if (pos < 0) {
+    if (report && i == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_POS_RANGE));
+    return false;
+  }
   int depth = p.depth[static_cast<long long>(b) * p.n_new + i];
   if (depth < 0 || depth >= p.n_new) {
     if (report) atomicOr(p.err, static_cast<int>(MQA_DEVERR_TREE));
     depth = min(max(depth, 0), p.n_new - 1);
   }
-  *at = p.pos[b] + depth;
+  *at = pos + depth;
   return true;
 }
 

@@ -59,15 +59,17 @@ __global__ void __launch_bounds__(kThreads) append_tree_kernel(const AppendParam
     const int k = e / kHalf, pi = e - k * kHalf, bt = first + k, b = bt / p.n_new, i = bt - b * p.n_new;
     const int pos = p.pos[b], nodes = p.num_nodes != nullptr ? p.num_nodes[b] : p.n_new;
     int depth = p.depth[bt];
-    const bool live = nodes >= 0 && nodes <= p.n_new && i < nodes;
+    // (at a negative position none: nodes in rows 0, 1, .. would overwrite cached tokens)
+    const bool live = nodes >= 0 && nodes <= p.n_new && i < nodes && pos >= 0;
     if (pi == 0) {
       int err = 0;
       if ((nodes < 0 || nodes > p.n_new) && i == 0) err |= static_cast<int>(MQA_DEVERR_SEQ_LEN);
+      if (pos < 0 && nodes > 0 && nodes <= p.n_new && i == 0) err |= static_cast<int>(MQA_DEVERR_POS_RANGE);
       long long row = -1;
       if (live) {
         if (depth < 0 || depth >= p.n_new) err |= static_cast<int>(MQA_DEVERR_TREE);
         const long long slot = static_cast<long long>(pos) + i;
-        if (slot < 0 || slot >= limit) {
+        if (slot >= limit) {
           err |= static_cast<int>(MQA_DEVERR_POS_RANGE);
         } else if (!p.paged) {
           row = (static_cast<long long>(b) * p.h_kv * p.capacity + slot) * D;

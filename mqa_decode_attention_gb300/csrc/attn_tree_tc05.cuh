@@ -50,9 +50,13 @@
 // minus its zero point is an integer up to 255 and becomes a bf16 (widen_u8);
 // the rows' scales are put beside the tile: a K scale multiplies its column of
 // S, a V scale its column of P, in fp32, before P is rounded.
-// An f16 P is within 2^-11 of its value, or within 2^-25 when it is below 2^-14:
-// the row's largest P is at least 1 (and at most 2^8), so keys that light move
-// the result by less than 2^-25 of the largest |v| each.
+// An f16 P is within 2^-11 of its value, or within 2^-25 when it is below 2^-14.
+// It is taken times 2^kHalfShift, as are the sums l (and the maxima handed on
+// less that): the row's largest P is then in [2^7, 2^15], below f16's 65504, and
+// a key moves the result by 2^-32 of the largest |v| at most beside its 2^-11,
+// 2^17 of them by 2^-15. (Without the factor keys below 2^-25 of the largest were
+// lost to O but not to l: one key before 10^5 that weigh 2.5e-8 each took up to 0.26%
+// of the result, a third of a bf16 step.)
 // (A step of 64 x 8 nodes of 32 heads on 8192 e5m2 keys of one kv head: 92 us, 0.75
 // PFLOP/s; bound by the widening and the chains.)
 //
@@ -98,6 +102,7 @@ constexpr int kRawBytes = kBN * kD;       // a code tile: [128 rows][128 B], swi
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // S / P of accumulator q at 128 q, its O at 256 + 128 q
 constexpr float kRescaleLog2 = 8.0f;
+constexpr float kHalfShift = 7.0f;  // P as f16: kRescaleLog2 + this < 16
 
 // What the warps of a block share beside the tiles and barriers.
 struct TreeMisc {
@@ -947,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             l *= alpha;
           }
           m_ref = m_new;
-          const float e = m_ref == -INFINITY ? 0.f : -m_ref * c;
+          const float e = m_ref == -INFINITY ? 0.f : (C::kHalf ? kHalfShift - m_ref * c : -m_ref * c);
           float2 sm4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           if (DT == kDtypeU8) {  // the V tile's scales
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kFull + vs), ((u0 + 2 * t + 1) / kSlots) & 1, p.wait_ns));
@@ -1021,7 +1026,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       // with Q is done; NT = 2: the second row tile's half), 16 KB a direction
       const bool both = !two && nt > 1;
       unsigned char* xbuf = smem + C::kQOff + (NT - 1) * kTileBytes;
-      float m2 = m_ref == -INFINITY ? -INFINITY : m_ref * c, w0 = 1.f, w1 = 0.f, mo = 0.f, lo = 0.f;
+      float m2 = m_ref == -INFINITY ? -INFINITY : (C::kHalf ? m_ref * c - kHalfShift : m_ref * c), w0 = 1.f, w1 = 0.f, mo = 0.f, lo = 0.f;
       if (both) {
         if (q == 1) {
           sh.row[0][r] = m2;

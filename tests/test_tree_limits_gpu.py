@@ -2,6 +2,8 @@
 refused, waits that ran out before, scores that span many powers of two, values
 that are no numbers."""
 
+import math
+
 import pytest
 import torch
 
@@ -45,3 +47,55 @@ def test_a_negative_position_appends_nothing(m, cache, B, d, page, whole_step): 
     assert (got[0][4][bad] == 3.0).all()
     for other in got[1:]:
         assert all(same_bits(a, b) for a, b in zip(got[0], other))
+
+
+# --------------------------------------------------------------- e5m2, wide range
+
+@pytest.mark.parametrize("hq,n", [(8, 1), (32, 5)])  # one row tile, two of them
+@pytest.mark.parametrize("first,score", [(True, 17.5), (False, 17.5), (False, 5.5)])
+def test_e5m2_light_keys_count(m, hq, n, first, score):  # noqa: F811
+    """102400 cached e5m2 keys, 16 of them with a score, the others at 0; values 1
+    there, 0 (dims 0 .. 63) or -2 (dims 64 ..) at the 16. The light keys weigh
+    e^-17.5 = 2^-25.2 of the heavy ones each, 0.016% in all, which is all of the
+    output's first half. (score 5.5, behind the others: below 2^8 of the running
+    maximum that was, which stays: the largest P there is.)
+
+    Bound, for weights w relative to the largest: P as an f16 times 2^7 is off by
+    2^-11 w, or by 2^-25 2^-7 = 2^-32 where it is subnormal; fp32 sums over T keys by
+    (T / 64 + 128) 2^-24 of sum w |v|, in l as in O; the scores (one product, a
+    rounding of 2^-24 each in the product, its scaling and the exponent, of up to
+    score log2 e < 32 = 2^5, and ex2 2^-22) by 3 * 2^-19 + 2^-22 above and below the
+    line. Weights below that are lost to O would be off by all of the first half.
+
+    The caches are one page of each kind, which all sequences share."""
+    T, B, ps, d = 102400, 300, 16, 128
+    kinds = dict(light=0, heavy=1, nodes=2)
+    k = torch.zeros(3, 1, ps, d)
+    v = torch.ones(3, 1, ps, d)
+    k[kinds["heavy"], :, :, 0] = 1.0
+    v[kinds["heavy"], :, :, :64], v[kinds["heavy"], :, :, 64:] = 0.0, -2.0
+    k, v = (x.to(torch.float8_e5m2).cuda() for x in (k, v))
+    table = torch.zeros(B, T // ps + 1, dtype=torch.int32)
+    table[:, 0 if first else T // ps - 1] = kinds["heavy"]
+    table[:, T // ps] = kinds["nodes"]
+    lay = m.layout_paged(k, v, table.cuda(), hq)
+    bufs = m.TreeBuffers.allocate(lay, n, out_dtype=torch.float32, lse=True)
+    q = torch.zeros(B, n, hq, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = score
+    pos = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    none = torch.zeros(B, n, 1, dtype=torch.int32, device="cuda")  # the nodes see the cached tokens only
+    m.gqa_tree_attention(lay, n, q, pos, None, none, T + n, 1.0, bufs.out, None, bufs.lse, bufs.workspace, bufs.err)
+    torch.cuda.synchronize()
+    assert int(bufs.err.item()) == 0
+    w, N = math.exp(-score), T - ps
+    total = ps + w * N
+    sums, scores = (T / 64 + 128) * 2.0 ** -24, 2 * (3 * 2.0 ** -19 + 2.0 ** -22)
+    for half, value in ((slice(0, 64), 0.0), (slice(64, d), -2.0)):
+        want, size = (w * N + ps * value) / total, (w * N + ps * abs(value)) / total
+        p_err = (ps * abs(value) * 2.0 ** -11 + N * max(2.0 ** -11 * w, 2.0 ** -32)) / total
+        bound = p_err + (2 * sums + scores) * size
+        err = (bufs.out[..., half].double() - want).abs().max().item()
+        assert err <= bound, (half, err, bound)
+        assert value or bound < 0.1 * want  # (the light keys' part is seen)
+    want = score + math.log(total)
+    assert (bufs.lse.double() - want).abs().max().item() <= sums + scores + 2.0 ** -20 * want

@@ -145,7 +145,10 @@ typedef enum mqa_variant {
  * then ORs MQA_DEVERR_TIMEOUT into err_word, lets its own copies and tensor
  * core products still in flight complete (those waits keep the one-second
  * limit), releases what it holds and returns; its outputs are then invalid,
- * and the next call on the stream runs normally. A healthy wait lasts
+ * and the next call on the stream runs normally. (The tcgen05 kernels of the
+ * decode, multi-token and prefill calls do no work while err_word already
+ * holds MQA_DEVERR_TIMEOUT: clear it before the next such call. The tree calls
+ * and the warp-MMA and CUDA-core kernels run whatever it holds.) A healthy wait lasts
  * microseconds: a short limit only serves to exercise this path (below one
  * second the waits poll instead of letting the hardware suspend the warp,
  * which could outlast the limit). (The

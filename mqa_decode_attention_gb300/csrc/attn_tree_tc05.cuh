@@ -110,7 +110,7 @@ struct TreeMisc {
   // the segments, out of the softmax and MMA warps' registers (two places: one
   // may still be read while the next is written), and the first one
   TreeSegment seg[2], first;
-  int abort, skip, flag, pending, more[2], last[2];
+  int abort, flag, pending, more[2], last[2];
   // what the two accumulators' threads of a row hand over: maxima [0] and sums
   // [1]; at a segment's start (e5m2) [0] the row's score factor
   float row[2][128];
@@ -361,9 +361,9 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
     return;
   }
   if (tid == 0) {
+    // (whatever the error word holds: an earlier call's bits are no reason to leave
+    // this call's work undone, and this call's blocks are all resident at once)
     sh.abort = 0;
-    // an earlier block timed out: the result is invalid already
-    sh.skip = (*reinterpret_cast<volatile int32_t*>(p.err) & static_cast<int>(MQA_DEVERR_TIMEOUT)) ? 1 : 0;
     mbar_init(bar(C::kQFull), 1);
     mbar_init(bar(C::kQFree), 1);
     mbar_init(bar(C::kXFree), 8);
@@ -418,7 +418,6 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
   auto begin = [&]() {
     TreeWalk w;
     w.start(plan);
-    if (sh.skip) w.at = w.end;
     return w;
   };
 

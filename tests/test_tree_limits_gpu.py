@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from test_tree_gpu import m  # noqa: F401 (fixture)
+from test_tree_gpu import m, run_step  # noqa: F401 (m: fixture)
 from tree_cases import TreeCase
 
 pytestmark = pytest.mark.gpu
@@ -99,3 +99,24 @@ def test_e5m2_light_keys_count(m, hq, n, first, score):  # noqa: F811
         assert value or bound < 0.1 * want  # (the light keys' part is seen)
     want = score + math.log(total)
     assert (bufs.lse.double() - want).abs().max().item() <= sums + scores + 2.0 ** -20 * want
+
+
+# ---------------------------------------------------------- bounded waits
+
+@pytest.mark.parametrize("cache", ["bf16", "e5m2", "u8"])
+@pytest.mark.parametrize("nodes", [8, 64])  # one row tile, two of them
+def test_a_call_after_a_timeout_runs_normally(m, cache, nodes):  # noqa: F811
+    """The error word keeps the bit of a wait that ran out until the host clears
+    it; a call that finds it there computes what it always does."""
+    c = TreeCase(32, 8, 128, [1500, 300, 900], [nodes, 5, nodes - 3], nodes, cache)
+    _, ref = run_step(m, c)
+    lay, t = c.gpu(m)
+    bufs = m.TreeBuffers.allocate(lay, c.n, lse=True)
+    for limit in (1, 0):
+        lay.wait_limit_ns = limit
+        bufs.out.fill_(7.0)
+        bufs.lse.fill_(7.0)
+        m.tree_step(lay, c.n, t.q_new, t.k_new, t.v_new, t.pos, t.depth, t.mask, c.max_len, bufs, num_nodes=t.num)
+        torch.cuda.synchronize()
+        assert int(bufs.err.item()) == m.MQA_DEVERR_TIMEOUT
+    assert torch.equal(bufs.out, ref.out) and torch.equal(bufs.lse, ref.lse)

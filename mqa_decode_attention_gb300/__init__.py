@@ -507,12 +507,15 @@ def layout_stack(layouts) -> ctypes.Array:
 
 def keep_path(layouts, pos, path, num_kept, err, stream=None) -> None:
     """Move the rows of an accepted path up behind the cached tokens, in every
-    layer at once, through ``kv_keep_path``: layouts from ``layout_stack`` (or
-    one layout), path [B, n] and num_kept [B] as ``verify_tree`` gives them."""
-    count = 1 if isinstance(layouts, KVLayout) else len(layouts)
-    first = layouts if isinstance(layouts, KVLayout) else layouts[0]
-    B, n, i32 = first.batch, path.shape[-1], torch.int32
-    st = library().kv_keep_path(ctypes.byref(first), count, n, _want("pos", pos, i32, B),
+    layer at once, through ``kv_keep_path``: layouts from ``layout_stack``, made
+    once per model (any other sequence of layouts is put together on each call),
+    or one layout; path [B, n] and num_kept [B] as ``verify_tree`` gives them."""
+    if isinstance(layouts, KVLayout):
+        layouts = (KVLayout * 1)(layouts)
+    elif not (isinstance(layouts, ctypes.Array) and layouts._type_ is KVLayout):
+        layouts = layout_stack(layouts)  # the library reads one array
+    B, n, i32 = layouts[0].batch, path.shape[-1], torch.int32
+    st = library().kv_keep_path(layouts, len(layouts), n, _want("pos", pos, i32, B),
                                 _want("path", path, i32, B * n), _want("num_kept", num_kept, i32, B), _ptr(err),
                                 _stream(stream))
     if st != 0:

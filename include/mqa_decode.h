@@ -492,7 +492,11 @@ MQA_API size_t mqa_tree_workspace_size(const mqa_kv_layout* layout, int32_t n_no
  * = 0 gives 0, -1 .. and -1. A parent or token out of range sets
  * MQA_DEVERR_TREE and that node is never tried; num_nodes[b] out of range sets
  * MQA_DEVERR_SEQ_LEN and counts as 0.
- * Sums have 64-bit accuracy and the result does not depend on the launch.
+ * Sums are formed in pairs of floats: a weight is within 2^-46 of S q, a sum
+ * within about 2^-44 of itself (tokens rejected without draft_probs are not in
+ * it). Their order depends on batch, vocab and the rows' addresses, so a
+ * comparison that is closer than that may fall either way; the same call gives
+ * the same result each time.
  */
 MQA_API mqa_status mqa_verify_tree(int32_t batch, int32_t n_nodes, int32_t vocab, const void* target_probs,
                                    const void* draft_probs, int32_t probs_dtype, int64_t row_stride,

@@ -21,9 +21,13 @@
 // the sums carry 64-bit accuracy. The fp64 pipe of this part takes 16 cycles
 // for one warp's addition (with fp64 across the threads a sweep of 128000
 // tokens took 40 us), so weights and sums are unevaluated pairs of floats, the
-// rounding errors of each product, difference and sum kept (relative error
-// below 2^-43), down to one value per block; only the walk's own comparisons
-// and the last element's search are fp64, by one warp.
+// rounding errors of each product, difference and sum kept, down to one value
+// per block; only the walk's own comparisons and the last element's search are
+// fp64, by one warp. A weight p - c q is within 2^-46 of c q; a sum of n weights on
+// one lane is off by n^2 2^-49 of itself at most and by about n 2^-51 as a rule (n
+// = 63 for 128000 tokens on eight blocks). Rejected tokens of deterministic
+// drafts are left out of the sums, not taken off them: what remains may weigh
+// less than the rounding of what was rejected, or nothing at all.
 //
 // A cluster of up to 8 blocks serves one sequence: warp 0 of every block walks
 // the tree alike; when it needs a sum over the vocabulary every warp of the
@@ -198,39 +202,50 @@ __global__ void __launch_bounds__(kThreads, 3) verify_tree_kernel(const VerifyPa
     const bool with_q = Q != nullptr && (ch != 0.f || cl != 0.f);
     Pair acc = {0.f, 0.f};
     constexpr int kU = 16 / N;
-#pragma unroll 1
-    for (int a = g0 + lane; a < g1; a += 32 * kU) {
-      float fp[kU][N], fq[kU][N];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int g = a + 32 * u;
-#pragma unroll
-        for (int e = 0; e < N; ++e) fp[u][e] = fq[u][e] = 0.f;
-        if (g < g1) {
-          load_group(r, P, g, fp[u]);
-          if (with_q) load_group(r, Q, g, fq[u]);
-        }
+    // deterministic drafts: rejected tokens weigh nothing. The run goes in pieces
+    // from one group that holds any to the next; of such a group lane e takes
+    // element e, if it was not rejected.
+    const int rejected = s_cmd.rejected;
+    while (true) {
+      int cut = 0x7fffffff;  // the next such group
+      for (int i = lane; i < rejected; i += 32) {
+        const int g = (s_out[i] + r.mis) / N;
+        if (g >= g0) cut = min(cut, g);
       }
+      cut = __reduce_min_sync(0xffffffffu, cut);
+      const int end = min(cut, g1);
+#pragma unroll 1
+      for (int a = g0 + lane; a < end; a += 32 * kU) {
+        float fp[kU][N], fq[kU][N];
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
+        for (int u = 0; u < kU; ++u) {
+          const int g = a + 32 * u;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const Pair w = residual(fp[u][e], fq[u][e], ch, cl);
-          if (__fadd_rn(w.hi, w.lo) > 0.f) add(acc, w.hi, w.lo);  // (NaN: no weight)
+          for (int e = 0; e < N; ++e) fp[u][e] = fq[u][e] = 0.f;
+          if (g < end) {
+            load_group(r, P, g, fp[u]);
+            if (with_q) load_group(r, Q, g, fq[u]);
+          }
         }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const Pair w = residual(fp[u][e], fq[u][e], ch, cl);
+            if (__fadd_rn(w.hi, w.lo) > 0.f) add(acc, w.hi, w.lo);  // (NaN: no weight)
+          }
+      }
+      if (cut >= g1) break;
+      const int v = N * cut - r.mis + lane;
+      bool live = lane < N && v >= 0 && v < V;
+      for (int i = 0; i < rejected; ++i) live &= s_out[i] != v;
+      const float w = live ? to_f32(P[r.off + v]) : 0.f;
+      if (w > 0.f) add(acc, w, 0.f);
+      g0 = cut + 1;
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
       add(acc, __shfl_xor_sync(0xffffffffu, acc.hi, d), __shfl_xor_sync(0xffffffffu, acc.lo, d));
-    // deterministic drafts: rejected tokens weigh nothing
-    for (int i = 0; i < s_cmd.rejected; ++i) {
-      const int g = (s_out[i] + r.mis) / N;
-      if (g >= g0 && g < g1) {
-        const float w = to_f32(P[r.off + s_out[i]]);
-        if (w > 0.f) add(acc, -w, 0.f);
-      }
-    }
-    if (__fadd_rn(acc.hi, acc.lo) <= 0.f) acc = {0.f, 0.f};
     return acc;
   };
   // a command's share of this warp, and what follows for all warps
@@ -342,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 3) verify_tree_kernel(const VerifyPa
           accept = u * S < r;
           if (!accept) {
             S -= r;
-            // (an entry for each rejected token once: the sums subtract every entry)
+            // (an entry for each rejected token once)
             if (!seen) {
               if (lane == 0) s_out[rejected] = s_token[child];
               ++rejected;
@@ -406,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, 3) verify_tree_kernel(const VerifyPa
           int mine = -1;  // this lane's last element with any weight
 #pragma unroll
           for (int e = 0; e < N; ++e) {
-            const double d = static_cast<double>(fp[e]) - c * static_cast<double>(fq[e]);
-            w[e] = d > 0.0 ? d : 0.0;
+            const Pair d = residual(fp[e], fq[e], s_cmd.ch, s_cmd.cl);  // (as in the sums that led here)
+            w[e] = __fadd_rn(d.hi, d.lo) > 0.f ? static_cast<double>(d.hi) + static_cast<double>(d.lo) : 0.0;
             for (int i = 0; i < rejected; ++i)
               if (s_out[i] == N * g - r.mis + e) w[e] = 0.0;
             sum += w[e];

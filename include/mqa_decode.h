@@ -431,10 +431,11 @@ MQA_API mqa_status mqa_prefill_step(const mqa_kv_layout* layout, int32_t n_new, 
  *   O = sum_t softmax_t(scale * q_rot . K_t) V_t over the cached tokens
  *   t < pos[b] and the nodes of the mask row i; with a window W only those at
  *   positions above pos[b] + depth[b, i] - W. A row that attends to nothing
- *   gives O = 0, lse = -inf. scale > 0. out [batch, n_nodes, h_q, head_dim] in
- *   out_dtype, lse_out optional [batch, n_nodes, h_q] fp32. max_seq_len bounds
- *   every pos[b] + num_nodes[b]; a sequence past it (or with a negative pos)
- *   sets MQA_DEVERR_SEQ_LEN and is skipped. depth is read with a window only
+ *   gives O = 0, lse = -inf; one with a NaN score gives NaN in both. scale > 0.
+ *   out [batch, n_nodes, h_q, head_dim] in out_dtype, lse_out optional [batch,
+ *   n_nodes, h_q] fp32. max_seq_len bounds every pos[b] + num_nodes[b]; a
+ *   sequence past it (or with a negative pos) sets MQA_DEVERR_SEQ_LEN and is
+ *   skipped. depth is read with a window only
  *   (else it may be NULL). Block-table entries as in the other calls: one in
  *   use outside the pool sets MQA_DEVERR_PAGE_RANGE and reads as zeros.
  *   workspace: mqa_tree_workspace_size bytes, 256-byte aligned, need not be

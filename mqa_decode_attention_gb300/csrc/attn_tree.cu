@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) attn_tree_kernel(c
       for (int h = 0; h < 2; ++h) {
         const int r = h == 0 ? ra : rb;
         if (r >= rows_unit) continue;
-        const float inv = l[h] > 0.f ? 1.f / l[h] : 0.f;
+        const float inv = l[h] != 0.f ? 1.f / l[h] : 0.f;  // (a NaN score: NaN)
         const long long orow = tree_out_row(p, g, r);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) attn_tree_kernel(c
             *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(x, y);
         }
         if ((lane & 3) == 0 && p.lse_out != nullptr)
-          p.lse_out[orow] = l[h] > 0.f ? (m[h] * c + log2f(l[h])) * 0.69314718055994530942f : -INFINITY;
+          p.lse_out[orow] = l[h] != 0.f ? (m[h] * c + log2f(l[h])) * 0.69314718055994530942f : -INFINITY;
       }
     } else {
       float* part = tree_place(p, g, blockIdx.x, kRows, D);

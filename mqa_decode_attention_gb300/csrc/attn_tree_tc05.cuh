@@ -1043,14 +1043,14 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
       const long long orow = live ? tree_out_row(p, g, gr) : 0;
       const int br = gr - g.rb * rows_per_block;  // row of the block
       float* part = tree_place(p, g, blockIdx.x, rows_per_block, kD);
-      float inv = l > 0.f ? 1.f / l : 0.f;
+      float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN score: NaN)
       auto weights = [&]() {  // of the two accumulators in what both hold
         const float mx = fmaxf(m2, mo);
         w0 = mx != -INFINITY ? exp2f(m2 - mx) : 0.f;
         w1 = mx != -INFINITY ? exp2f(mo - mx) : 0.f;
         l = w0 * l + w1 * lo;
         m2 = mx;
-        inv = l > 0.f ? 1.f / l : 0.f;
+        inv = l != 0.f ? 1.f / l : 0.f;
       };
       // this thread's pieces of 32 dims
       const int x0 = both ? 2 * q : 0, x1 = both ? x0 + 2 : kD / 32;
@@ -1143,7 +1143,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           part[static_cast<size_t>(rows_per_block) * kD + br] = m2;
           part[static_cast<size_t>(rows_per_block) * (kD + 1) + br] = l;
         } else if (p.lse_out != nullptr) {
-          p.lse_out[orow] = l > 0.f ? (m2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+          p.lse_out[orow] = l != 0.f ? (m2 + log2f(l)) * 0.69314718055994530942f : -INFINITY;
         }
       }
       __syncwarp();

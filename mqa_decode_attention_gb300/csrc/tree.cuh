@@ -310,7 +310,7 @@ __device__ __forceinline__ void tree_merge_rows(const TreeParams& p, const TreeM
 #pragma unroll
       for (int u = 0; u < kU; ++u)
         o[u] = __ldcg(reinterpret_cast<const float4*>(q) + static_cast<size_t>(4 * u + (lane >> 3)) * rows_per_block + r);
-      if (mk != -INFINITY) {  // (else no key of this part: its sums may be anything)
+      if (lk != 0.f) {  // (else no key of this part. A NaN score: the sum is NaN, whatever the maximum)
         const float top = fmaxf(mx, mk), a = exp2f(mx - top), w = exp2f(mk - top);
         mx = top;
         l = fmaf(w, lk, a * l);
@@ -324,13 +324,13 @@ __device__ __forceinline__ void tree_merge_rows(const TreeParams& p, const TreeM
       }
     }
     if (r0 + (lane & 7) < rows) {
-      const float inv = mx != -INFINITY ? 1.f / l : 0.f;
+      const float inv = l != 0.f ? 1.f / l : 0.f;
       const long long o = tree_out_row(p, g, g.rb * rows_per_block + r);
 #pragma unroll
       for (int u = 0; u < kU; ++u)
         tree_store4(p, o * D + 4 * (4 * u + (lane >> 3)), acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv);
       if (lane < 8 && p.lse_out != nullptr)
-        p.lse_out[o] = mx != -INFINITY ? (mx + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+        p.lse_out[o] = l != 0.f ? (mx + log2f(l)) * 0.69314718055994530942f : -INFINITY;
     }
   }
 }

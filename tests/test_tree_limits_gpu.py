@@ -120,3 +120,37 @@ def test_a_call_after_a_timeout_runs_normally(m, cache, nodes):  # noqa: F811
         torch.cuda.synchronize()
         assert int(bufs.err.item()) == m.MQA_DEVERR_TIMEOUT
     assert torch.equal(bufs.out, ref.out) and torch.equal(bufs.lse, ref.lse)
+
+
+# ------------------------------------------------------------- NaN attended to
+
+@pytest.mark.parametrize("cache", ["bf16", "e5m2", "u8"])
+@pytest.mark.parametrize("hq,hkv,d,n", [(32, 8, 128, 6), (32, 8, 128, 40), (12, 3, 64, 31)])
+@pytest.mark.parametrize("where", ["query", "key"])
+def test_nan_scores_give_nan(m, cache, hq, hkv, d, n, where):  # noqa: F811
+    """A NaN in a row's query, or in a cached key that it attends to, makes that
+    row NaN, output and lse, whole or merged of parts; the other rows keep their
+    bits."""
+    c = TreeCase(hq, hkv, d, [3000, 300, 20, 0], [n, n, n, n], n, cache, seed=n)
+    _, ref = run_step(m, c)
+    lay, t = c.gpu(m)
+    bad = torch.zeros(4, n, hq, dtype=torch.bool, device="cuda")
+    if where == "query":
+        for b in range(4):
+            t.q_new[b, n // 2, b + 1, 10] = float("nan")
+            bad[b, n // 2, b + 1] = True
+    else:
+        for b, at in ((0, 2990), (1, 150), (2, 0)):
+            if cache == "u8":
+                t.ksz[b, 1, at, 0] = float("nan")
+            elif cache == "e5m2":
+                t.k.view(torch.uint8)[b, 1, at, 7] = 0x7F
+            else:
+                t.k[b, 1, at, 7] = float("nan")
+            bad[b, :, hq // hkv: 2 * (hq // hkv)] = True
+    bufs = m.TreeBuffers.allocate(lay, n, lse=True)
+    m.tree_step(lay, n, t.q_new, t.k_new, t.v_new, t.pos, t.depth, t.mask, c.max_len, bufs, num_nodes=t.num)
+    torch.cuda.synchronize()
+    assert int(bufs.err.item()) == 0
+    assert bufs.out[bad].isnan().all() and bufs.lse[bad].isnan().all()
+    assert torch.equal(bufs.out[~bad], ref.out[~bad]) and torch.equal(bufs.lse[~bad], ref.lse[~bad])

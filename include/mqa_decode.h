@@ -518,7 +518,9 @@ MQA_API mqa_status mqa_verify_tree(int32_t batch, int32_t n_nodes, int32_t vocab
  * MQA_DEVERR_TREE; a row past the cache sets MQA_DEVERR_POS_RANGE, a page
  * outside the pool MQA_DEVERR_PAGE_RANGE: that sequence's rows then stay
  * where they are (in the layer whose table is at fault). Pages that hold
- * nodes must belong to one sequence.
+ * nodes must belong to one sequence, and rows to one layer, to its K or its V
+ * (the same cache twice, or the same pool twice with one block table:
+ * MQA_ERR_INVALID_ARG).
  */
 MQA_API mqa_status kv_keep_path(const mqa_kv_layout* layouts, int32_t n_layers, int32_t n_nodes, const int32_t* pos,
                                 const int32_t* path, const int32_t* num_kept, int32_t* err_word,

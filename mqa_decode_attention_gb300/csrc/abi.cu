@@ -1299,6 +1299,15 @@ mqa_status check_tree_append(const mqa_kv_layout* L, int n, const void* q_new, c
   return check_append_args(L, q_new, k_new, v_new, pos, rope_base, static_cast<const float*>(q_rot), err_word);
 }
 
+// Whether a K or V of one of kv_keep_path's layers holds rows of another's (or, a
+// = b, its K those of its V): they would be moved more than once. Layers may share a
+// pool, each with a table of its own.
+bool same_rows(const mqa_kv_layout& a, const mqa_kv_layout& b) {
+  if (a.paged && a.block_table != b.block_table) return false;
+  if (&a == &b) return a.k_cache == a.v_cache;
+  return a.k_cache == b.k_cache || a.k_cache == b.v_cache || a.v_cache == b.k_cache || a.v_cache == b.v_cache;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1407,6 +1416,8 @@ mqa_status kv_keep_path(const mqa_kv_layout* layouts, int32_t n_layers, int32_t 
                       L.max_pages_per_seq != f.max_pages_per_seq
                 : L.capacity != f.capacity)
       return MQA_ERR_INVALID_ARG;
+    for (int j = 0; j <= i; ++j)
+      if (same_rows(layouts[j], L)) return MQA_ERR_INVALID_ARG;
   }
   if (!pos || !path || !num_kept || !err_word) return MQA_ERR_INVALID_ARG;
   if (!aligned(pos, 4) || !aligned(path, 4) || !aligned(num_kept, 4) || !aligned(err_word, 4))

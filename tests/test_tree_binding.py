@@ -60,3 +60,21 @@ def test_a_list_with_an_invalid_layout_is_refused(built_lib):
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     with pytest.raises(m.MqaError, match="kv_keep_path"):
         m.keep_path(lays, i32(2), i32(2, 4), i32(2), i32(1), stream=0)
+
+
+def test_layers_that_hold_the_same_rows_are_refused(built_lib):
+    """One cache twice in a call would be moved by two blocks at once, a K that is
+    its V twice by one. (One pool with a table for each layer is fine: not tried
+    here, it would be launched.)"""
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    a, b = layouts(2)
+    crossed = layouts(1)[0]
+    crossed.v_cache = a.k_cache
+    same = layouts(1)[0]
+    same.v_cache = same.k_cache
+    pool = [torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16) for _ in "kv"]
+    table = i32(2, 2)
+    paged = [m.layout_paged(*pool, table, 8) for _ in "ab"]
+    for lays in ([a, b, a], [a, crossed], [same], paged):
+        with pytest.raises(m.MqaError, match="invalid argument"):
+            m.keep_path(lays, i32(2), i32(2, 4), i32(2), i32(1), stream=0)

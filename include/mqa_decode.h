@@ -469,15 +469,20 @@ MQA_API size_t mqa_tree_workspace_size(const mqa_kv_layout* layout, int32_t n_no
 
 /*
  * mqa_verify_tree -- which drafted tokens stand, and the token after them, so
- * that what is emitted follows the target's distribution.
+ * that what is emitted follows the target's distribution. With draft_probs that
+ * holds if the children of a node were drawn from the node's row of it, each
+ * independently of the others (a token may occur twice). Children drawn without
+ * replacement (the k most probable tokens, Gumbel top-k) are no such draws: what
+ * is emitted then leans away from the drafted tokens. For them, as for any
+ * choice of children at all, the call without draft_probs is exact.
  *
  * target_probs [batch, n_nodes, row_stride]: row i the target's probabilities
  * of the token after node i (vocab of them; row_stride >= vocab elements from
  * row to row); draft_probs the draft's, the same shape and type, or NULL for
- * drafts that were not drawn at random. probs_dtype MQA_F32 or MQA_BF16. tokens and
- * parents [batch, n_nodes] int32: node 0 is the last committed token (its
- * token and parent are not read), parents[i] < i for the others. u_accept
- * [batch, n_nodes] and u_next [batch] fp32 in [0, 1).
+ * drafts that are not independent draws from it. probs_dtype MQA_F32 or
+ * MQA_BF16. tokens and parents [batch, n_nodes] int32: node 0 is the last
+ * committed token (its token and parent are not used), parents[i] < i for the
+ * others. u_accept [batch, n_nodes] and u_next [batch] fp32 in [0, 1).
  *
  * From node 0, the children of the current node are tried in index order.
  * With R = p, S = 1 a child with token x is accepted iff u q(x) S < R(x); the

@@ -470,8 +470,10 @@ class VerifyBuffers:
 def verify_tree(target_probs, draft_probs, tokens, parents, u_accept, u_next, bufs: VerifyBuffers, num_nodes=None,
                 stream=None) -> VerifyBuffers:
     """Which nodes of each drafted tree stand, and the next token, through
-    ``mqa_verify_tree``: target_probs and draft_probs (None: deterministic
-    drafts) [B, n, vocab] fp32 or bf16, row i the distribution after node i.
+    ``mqa_verify_tree``: target_probs and draft_probs [B, n, vocab] fp32 or bf16,
+    row i the distribution after node i. draft_probs is for children that were
+    drawn from it independently of each other; None for any others (chosen, or
+    drawn without replacement): only then does what is emitted follow the target.
     Rows may be padded (a slice [..., :vocab] of a dense tensor)."""
     if target_probs.dim() != 3:
         raise ValueError(f"target_probs must be [batch, nodes, vocab], got {tuple(target_probs.shape)}")

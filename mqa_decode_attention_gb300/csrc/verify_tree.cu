@@ -1,7 +1,8 @@
 // Verification of a tree of drafted tokens against the target's probabilities
 // from given random numbers (speculative sampling over several candidates),
 // "Arsitektur Inferensi LLM", section 7: the result follows the target's
-// distribution whatever the draft proposes.
+// distribution if a node's children are independent draws from the draft's, or
+// (no draft probabilities given) whatever they are.
 //
 // Node 0 is the last committed token. From it the walk goes down: p and q are
 // the target's and the draft's next-token probabilities after the current

@@ -131,8 +131,9 @@ def verify_tree(target, draft, tokens, parents, nodes, u_accept, u_next):
     is defined: the target's distribution is tried against each child, and
     after a rejection replaced by the normalised positive part of itself minus
     the draft's; without a draft's distribution a rejected token's probability
-    is struck out and the rest measured against what is left of 1. Returns (num_kept [B], path [B, n], next_token [B], margin):
-    margin is the smallest distance of a comparison from a tie, as a
+    is struck out and the rest measured against what is left of 1. (The first
+    is for children drawn from draft independently of each other, the second for
+    any.) Returns (num_kept [B], path [B, n], next_token [B], margin): margin is the smallest distance of a comparison from a tie, as a
     probability (a sum formed in another order may decide those closer than
     its own rounding otherwise)."""
     target = _f64(target)

@@ -35,13 +35,14 @@
 //
 // Q is loaded by TMA as the append left it (bf16, not scaled): the scale
 // times log2 e goes into the exponent's fused multiply-add. A second bf16 term of
-// Q has no room in shared memory beside two row tiles. P over a bf16 cache enters
-// as two bf16 terms (split_p, within 2^-15; the two take the columns that S had):
-// with one term (2^-8) the output's error against 64 bits is 1.7 times that of
-// its own rounding to bf16, with two 1.4 times, which Q's rounding leaves. The
-// price: 32 x 64 nodes 146 -> 169 us, 32 x 16 nodes 101 -> 103 us. Over e5m2 P
-// has an f16's 2^-11, over uint8 one bf16 term (1.35 times). Sums, maxima and
-// partial results are fp32.
+// Q has no room in shared memory beside two row tiles. P over bf16 and uint8
+// caches enters as two bf16 terms (split_p, within 2^-15; the two take the columns
+// that S had): with one term (2^-8) the output's error against 64 bits is 1.7 times
+// that of its own rounding to bf16 for a step, with two 1.4 times, which Q's
+// rounding leaves; on given bf16 queries over uint8 1.4 and 1.0 times. The price:
+// bf16, 32 x 64 nodes 146 -> 169 us, 32 x 16 nodes 101 -> 103 us; uint8 227 -> 252
+// and 117 -> 128 us. Over e5m2 P has an f16's 2^-11. Sums, maxima and partial
+// results are fp32.
 //
 // One-byte caches: the loader's tiles are codes (16 KB), eight converter warps
 // widen each to a 16-bit tile, exactly. An e5m2 code is the high byte of an
@@ -134,7 +135,7 @@ struct Cfg {
   static constexpr int kRaw = kByte ? (NT == 2 ? 2 : (DT == kDtypeU8 ? 3 : 4)) : 0;
   static_assert(NT == 1 || DT != kDtypeU8, "no room for two row tiles beside the scales");
   static constexpr bool kHalf = DT == kDtypeF8;  // f16 operands (else bf16)
-  static constexpr bool kSplitP = DT == kDtypeBf16;  // P as two bf16 terms: [16 columns][16 columns] of each 32 keys
+  static constexpr bool kSplitP = !kHalf;  // P as two bf16 terms: [16 columns][16 columns] of each 32 keys
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = NT * kTileBytes;
   static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;

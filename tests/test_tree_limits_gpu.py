@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from test_tree_gpu import m, run_step  # noqa: F401 (m: fixture)
+from test_tree_gpu import check_attention, m, run_step  # noqa: F401 (m: fixture)
 from tree_cases import TreeCase
 
 pytestmark = pytest.mark.gpu
@@ -154,3 +154,17 @@ def test_nan_scores_give_nan(m, cache, hq, hkv, d, n, where):  # noqa: F811
     assert int(bufs.err.item()) == 0
     assert bufs.out[bad].isnan().all() and bufs.lse[bad].isnan().all()
     assert torch.equal(bufs.out[~bad], ref.out[~bad]) and torch.equal(bufs.lse[~bad], ref.lse[~bad])
+
+
+# ------------------------------------------------------- uint8: probabilities
+
+@pytest.mark.parametrize("hq,hkv,nodes", [(32, 8, 9), (28, 4, 13), (32, 1, 8), (32, 8, 60)])
+@pytest.mark.parametrize("page", [0, 16])
+def test_u8_probabilities_keep_more_than_a_bf16(m, hq, hkv, nodes, page):  # noqa: F811
+    """fp32 outputs over a uint8 cache at head_dim 128: a probability times its V
+    scale enters as two bf16 terms, within 2^-15 of its value (2^-7 that the first
+    leaves times 2^-8 of the second's rounding)."""
+    c = TreeCase(hq, hkv, 128, [600, 37], [nodes, nodes - 1], nodes, "u8", page, seed=nodes)
+    t, bufs = run_step(m, c, torch.float32)
+    assert int(bufs.err.item()) == 0
+    check_attention(c, t, bufs.q_rot, bufs.out, bufs.lse, p_err=2.0 ** -15)

@@ -121,7 +121,8 @@ typedef enum mqa_variant {
  * zero_point) clamped to [0, 255], in float32, rounding half to even; the
  * key is quantised after its fp64 rotation, rounded to float32. q_new,
  * k_new and v_new are bf16. Attention over a MQA_U8 cache runs on tensor
- * cores only.
+ * cores only, and takes zero points for whole numbers in [0, 255], as the append
+ * writes them (some kernels round others to a whole number or to bf16).
  *
  * MQA_FP8_E5M2 cache (the fp8_e5m2 KV-cache dtype of the pages' vLLM
  * serving examples): one byte per element, 1 sign, 5 exponent (bias 15) and
@@ -415,7 +416,7 @@ MQA_API mqa_status mqa_prefill_step(const mqa_kv_layout* layout, int32_t n_new, 
  * of word t / 32 of row i says that node i attends to node t. It is taken as
  * it is (a node attends to itself only if its bit is set; any other relation
  * than a tree's works as well); bits of nodes past num_nodes[b] are ignored.
- * Nodes past num_nodes[b] are padding: nothing of theirs is read, appended or
+ * Nodes past num_nodes[b] are padding: nothing of theirs is used, appended or
  * written (q_rot, out and lse_out keep what they held there).
  * All pointers are device pointers; tensors are dense, inputs bf16.
  *
@@ -444,10 +445,15 @@ MQA_API mqa_status mqa_prefill_step(const mqa_kv_layout* layout, int32_t n_new, 
  *   cached tokens while the first still runs), q_rot the caller's scratch.
  *
  * bf16, MQA_U8 and MQA_FP8_E5M2 caches, contiguous or paged, head_dim 64 or
- * 128 (MQA_F32: MQA_ERR_UNSUPPORTED, as in the multi-token calls). Key rows
- * past a sequence's nodes, and rows wholly before the window, are never used,
- * whatever they hold; the values of a node that a row does not attend to are
- * multiplied by a zero probability, so they have to be finite.
+ * 128 (MQA_F32: MQA_ERR_UNSUPPORTED, as in the multi-token calls). Rows past a
+ * sequence's nodes, and rows before pos[b] + 1 - W (the window of a node of
+ * depth 0, whether there is one or not), are never used, whatever they hold; the
+ * values of other rows that a node does not attend to are multiplied by a zero
+ * probability, so they have to be finite.
+ * Beside q_rot and out only the probabilities are rounded below fp32: to two
+ * bf16 terms, 2^-15 together (e5m2 at head_dim 128: to f16, or to 2^-32 of the
+ * row's largest). The single-token and multi-token calls take a query over a
+ * one-byte cache with more bits (fp16, or two e4m3 parts) than q_rot's bf16 has.
  */
 MQA_API mqa_status kv_append_rope_tree(const mqa_kv_layout* layout, int32_t n_nodes, const void* q_new,
                                        const void* k_new, const void* v_new, const int32_t* pos,

@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
         // (one answer for the warp: what follows has to stay converged)
         const bool masked = __any_sync(0xffffffffu, key0 + kBN > pos || key0 < ka);
         // (uint8: the bits where they are used, which suits that loop's registers:
-        // 32 x 16 nodes over 4096 keys 123 -> 117 us; bf16 32 x 64 nodes 145 -> 147.5)
+        // 32 x 16 nodes over 4096 keys 136 -> 129 us)
         TreeRow row;
         uint32_t bits[4];  // bit x: the row attends to key key0 + x
         if (masked && warp_rows) {
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
           const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff);
           const float4* sk = reinterpret_cast<const float4*>(sc + ((u0 + 2 * t) % C::kScales) * kBN);
           const float4* sv = reinterpret_cast<const float4*>(sc + ((u0 + 2 * t + 1) % C::kScales) * kBN);
-          constexpr bool kMaskS = DT == kDtypeF8;
+          constexpr bool kMaskS = DT != kDtypeU8;
           auto scores = [&](int x, float (&s)[32]) {  // keys 32 x .. 32 x + 31, masked ones -inf
             tc05::wait_ld();
             tc05::reg_fence(s);
@@ -880,19 +880,15 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
                 s[4 * i] = a.x, s[4 * i + 1] = a.y, s[4 * i + 2] = b.x, s[4 * i + 3] = b.y;
               }
             }
-            if (!kMaskS && masked) {  // (uint8: past the scales, which may be anything in a masked row)
-              uint32_t w;
-              if constexpr (DT == kDtypeU8)
-                w = tree_bits(row, key0 + 32 * x);
-              else
-                w = x < 2 ? (x == 0 ? bits[0] : bits[1]) : (x == 2 ? bits[2] : bits[3]);
+            if (!kMaskS && masked) {  // (past the scales, which may be anything in a masked row)
+              const uint32_t w = tree_bits(row, key0 + 32 * x);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!((w >> i) & 1u)) s[i] = -INFINITY;
             }
           };
-          // e5m2: -inf into S itself, out of the way of the other tiles' code (32 x 64
-          // nodes over 4096 keys 155 -> 150 us; bf16 145 -> 147.5)
+          // bf16, e5m2: -inf into S itself, out of the way of the other tiles' code (32 x
+          // 64 nodes over 4096 keys, bf16 169.3 -> 167.2 us, e5m2 157.3 -> 152)
           if (kMaskS && masked) {
 #pragma unroll 1
             for (int x = 0; x < kBN / 16; ++x) {
@@ -939,7 +935,7 @@ __global__ void __launch_bounds__(Cfg<NT, DT>::kThreads, 1)
             // before this S_q, whose completion this thread has seen
             const float alpha = (grow && m_ref != -INFINITY) ? fast_exp2((m_ref - m_new) * c) : 1.f;
 #pragma unroll 1
-            for (int x = 0; x < kD / 16; ++x) {  // (16 dims a pass: twice as many took 4 % of the kernel's time, as longer code)
+            for (int x = 0; x < kD / 16; ++x) {  // (16 dims a pass: as fast as 32, in half the code)
               float v[16];
               tc05::ld_32x32b_x16(ocol + x * 16, v);
               tc05::wait_ld();

@@ -451,8 +451,8 @@ MQA_API mqa_status mqa_prefill_step(const mqa_kv_layout* layout, int32_t n_new, 
  * values of other rows that a node does not attend to are multiplied by a zero
  * probability, so they have to be finite.
  * Beside q_rot and out only the probabilities are rounded below fp32: to two
- * bf16 terms, 2^-15 together (e5m2 at head_dim 128: to f16, or to 2^-32 of the
- * row's largest). The single-token and multi-token calls take a query over a
+ * bf16 terms, 2^-15 together (e5m2 at head_dim 128, up to 128 heads per kv head:
+ * to f16, or to 2^-32 of the row's largest). The single-token and multi-token calls take a query over a
  * one-byte cache with more bits (fp16, or two e4m3 parts) than q_rot's bf16 has.
  */
 MQA_API mqa_status kv_append_rope_tree(const mqa_kv_layout* layout, int32_t n_nodes, const void* q_new,

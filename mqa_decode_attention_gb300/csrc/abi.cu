@@ -510,8 +510,9 @@ mqa_status append_impl(const mqa_kv_layout* layout, const void* q_new, const voi
     p.zero_count = tree->zero_count;
   }
   fill_theta(p.theta, layout->head_dim, rope_base);
-  // few nodes: the blocks of append_rope.cu, which split a node's heads (a step
-  // of one 8-node tree takes 16.7 us with them, 18.0 with append_tree.cu's)
+  // few nodes: the blocks of append_rope.cu, which split a node's heads (a step of 8
+  // nodes takes 17.0 us with them, 17.9 with append_tree.cu's; of 64 20.0 and 19.4, of
+  // 256 40.2 and 39.8; the append alone of 2048 21.7 and 11.6)
   const bool wide = tree != nullptr && layout->cache_dtype == MQA_BF16 && p.batch * p.n_new >= kTreeAppendNodes;
   int dev = 0;
   if (wide) cudaGetDevice(&dev);
@@ -1261,9 +1262,9 @@ mqa_status tree_attention_impl(const mqa_kv_layout* L, int n, const void* q_rot,
   p.arrived = static_cast<int32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.counters);
   p.err = err_word;
-  // (2, 3, 4, 6 tiles measured: 8 kv heads, 8 nodes, 700 tokens 14.9, 16.7, 18.8, 17.2 us;
-  // 3000 tokens 20.7, 19.7, 21.3, 24.0, over e5m2 31.0, 21.3, 26.8, 27.0; 8000 tokens 25.9,
-  // 21.7, 21.0, 21.8)
+  // (2, 3, 4, 6 tiles measured: 8 kv heads, 8 nodes, 700 tokens 16.0, 17.0, 19.3, 17.6 us;
+  // 3000 tokens 20.8, 20.6, 20.0, 21.0, over e5m2 22.9, 22.2, 22.8, 23.0, over uint8 24.9,
+  // 23.6, 25.0, 27.1; 8000 tokens 33.0, 32.5, 33.1, 27.1)
   p.min_tiles = 3;
   p.tokens_per_tile = c.tokens;
   p.early = early;

@@ -20,8 +20,9 @@
 //
 // One block of 1024 threads an SM: what matters to a step is when the last block
 // of each SM leaves, since the attention's blocks need the SM's whole shared
-// memory. The step of 32 x 64 nodes at 4096 keys takes 149 us with it, 149 with
-// four blocks of 256, 150 with two of 512; of 32 x 16 nodes 101.3, 103.4, 104.9.
+// memory. Steps called one after the other, of 32 x 64 nodes at 4096 keys 174.5 us
+// with it, 174.5 with four blocks of 256, 173.8 with two of 512; of 32 x 16 nodes
+// 106.3, 108.5, 108.6.
 #include <cuda_bf16.h>
 
 #include "../../include/mqa_decode.h"

@@ -18,20 +18,21 @@
 // with a softmax warpgroup each:
 //   NT = 2  (more than 128 rows per kv head) two query tiles of up to 128 rows
 //           share every K / V tile; the tensor cores alternate between them.
-//           One tile of K and V asks for 1.45 us of HBM and 1.04 us of products
-//           (0.69 with P in one term); what bounds it is each accumulator's chain
-//           product - softmax - product (32 x 64 nodes on 4096 keys, 32 + 8
-//           heads, 573 MB: a step 169 us, 0.8 PFLOP/s without the second terms). A
-//           tree that ends in a block of up to 128 rows has that block done as
-//           below.
+//           One tile of K and V asks for 1.45 us of HBM and 2.0 us of products
+//           (1.35 with P in one term) at an SM's share of 6.8 TB/s and of 1.89
+//           PFLOP/s, and takes 2.8: what bounds it is each accumulator's chain
+//           product - softmax - product (32 x 64 nodes on 4096 keys, 32 + 8 heads,
+//           573 MB: a step 167 us, 178 on inputs that change, 0.8 PFLOP/s without
+//           the second terms). A tree that ends in a block of up to 128 rows has
+//           that block done as below.
 //   NT = 1  (up to 128 rows) both accumulators hold the same rows and take the
 //           tiles in turn, so that one's softmax runs beside the other's
 //           products; their results meet in shared memory at a unit's end.
 //           Bound by the HBM stream: a tile of K and V (64 KB) takes 1.45 us
-//           of an SM's share of 6.8 TB/s, its products 0.5 us, and the two
-//           accumulators' chains product-softmax-product about 1.1 us a tile
-//           (a step of 32 x 16 nodes on 4096 keys, 549 MB: 103 us, 5.3 TB/s; of 4 x
-//           32 nodes on 131040 keys, 2.15 GB: 326 us, 6.6 TB/s).
+//           of an SM's share of 6.8 TB/s, its products 1.0 us (128 rows, P in two
+//           terms) (a step of 32 x 16 nodes on 4096 keys, 549 MB: 102 us, 5.4 TB/s;
+//           of 4 x 32 nodes on 131040 keys, 2.15 GB: 328 us, 6.6 TB/s, 356 on inputs
+//           that change).
 //
 // Q is loaded by TMA as the append left it (bf16, not scaled): the scale
 // times log2 e goes into the exponent's fused multiply-add. A second bf16 term of

@@ -284,7 +284,7 @@ cudaError_t launch_tree_mma(const TreeParams& p, int ctas, cudaStream_t stream);
 
 // tcgen05: head_dim 128, group <= 128. `tiles` row tiles of tokens_per_tile *
 // group rows to a block (2 when a kv head has more than 128 rows). Maps: K / V
-// as bf16 tiles of 128 rows (paged: 64-dim halves of min(page_size, 64) rows)
+// as bf16 tiles of 128 rows (paged: min(page_size, 64) rows, both 64-dim halves)
 // or code tiles of as many rows, Q boxes of 64 dims x group x tokens_per_tile.
 constexpr int kTreeTileKeys = 128;
 cudaError_t launch_tree_tc05_bf16(const TreeParams& p, int tiles, int ctas, const CUtensorMap& tk,

@@ -1152,7 +1152,7 @@ TreeChoice tree_choice(const mqa_kv_layout* L, int n) {
     // (uint8: one row tile, the kernel has no room for a second beside the scales)
     c.tc05 = static_cast<long long>(G) * n > 128 && L->cache_dtype != MQA_U8 ? 2 : 1;
     c.tokens = std::min(128 / G, n);
-    c.shape = {c.tc05 * c.tokens * G, kTreeTileKeys, 1};
+    c.shape = {c.tc05 * c.tokens * G, 1};
   }
   c.ctas = device_info(dev).sms * c.shape.ctas_per_sm;
   c.counters = (static_cast<size_t>(c.ctas) * 4 + 255) / 256 * 256;

@@ -379,7 +379,7 @@ cudaError_t launch_t(const TreeParams& p, int ctas, cudaStream_t stream) {
 
 // (blocks per SM: what their registers allow, 255 and 168 a thread, the latter
 // by the launch bounds: left alone, uint8 took more and 133 us instead of 109)
-TreeShape tree_mma_shape(int head_dim) { return {kRows, kKeys, head_dim == 128 ? 2 : 3}; }
+TreeShape tree_mma_shape(int head_dim) { return {kRows, head_dim == 128 ? 2 : 3}; }
 
 cudaError_t launch_tree_mma(const TreeParams& p, int ctas, cudaStream_t stream) {
   if (p.head_dim == 128) {

@@ -233,7 +233,7 @@ bool tc05_merges_splits(const Tc05Params& p);
 // e5m2 cache
 int tc05_f8_box_rows();
 
-// Attention of a tree of drafted tokens (attn_tree.cu, attn_tree_tc05.cu).
+// Attention of a tree of drafted tokens (attn_tree.cu, attn_tree_tc05.cuh).
 // Node i of sequence b is the token at cache row pos[b] + i; it attends to
 // the pos[b] cached tokens and to the nodes of its mask row.
 struct TreeParams {
@@ -275,7 +275,7 @@ __host__ __device__ inline size_t tree_part_floats(int rows, int d) {
   return (static_cast<size_t>(rows) * (d + 2) + 3) / 4 * 4;
 }
 struct TreeShape {
-  int rows, keys;   // rows of a block, keys of a tile
+  int rows;         // rows of a block
   int ctas_per_sm;  // blocks launched per SM
 };
 // any cache the tensor cores read, head_dim 64 or 128

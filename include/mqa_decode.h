@@ -77,14 +77,15 @@ typedef enum mqa_dtype {
   MQA_BF16 = 0,
   MQA_F32 = 1,
   MQA_U8 = 2, /* cache only: uint8 codes + (scale, zero point) per cached (token, kv head); q/k/v new in bf16 */
-  MQA_FP8_E5M2 = 3 /* cache only: fp8 e5m2 values, one byte per element; q/k/v new in bf16 */
+  MQA_FP8_E5M2 = 3, /* cache only: fp8 e5m2 values, one byte per element; q/k/v new in bf16 */
+  MQA_U4 = 5 /* cache only: 4-bit codes, two to a byte + a bf16 (scale, minimum) pair per row; q/k/v new in bf16 */
 } mqa_dtype;
 
 /* Which decode-attention kernel to run (gqa_decode_attention `variant`). */
 typedef enum mqa_variant {
-  MQA_VARIANT_AUTO = 0,        /* tensor cores for a bf16 cache, else CUDA cores */
+  MQA_VARIANT_AUTO = 0,        /* CUDA cores for an f32 cache, else tensor cores */
   MQA_VARIANT_CUDA_CORE = 1,   /* fp32 FMA on CUDA cores; bf16 and f32 caches */
-  MQA_VARIANT_TENSOR_CORE = 2  /* bf16 tensor-core MMA; bf16 cache only */
+  MQA_VARIANT_TENSOR_CORE = 2  /* tensor-core MMA; every cache but f32 */
 } mqa_variant;
 
 /* Bits a kernel ORs into the caller's device error word. */
@@ -140,6 +141,30 @@ typedef enum mqa_variant {
  * significant bits of precision beyond a single e4m3 rounding; fewer rows, or
  * a paged pool, take the warp-MMA kernels.
  *
+ * MQA_U4 cache: four bits per element. A cached (token, kv head) row is
+ * head_dim / 2 bytes of codes 0..15 (element 2i in the low half of byte i,
+ * 2i + 1 in the high half) and a (scale s, minimum m) pair of bf16 values in
+ * k_scale_zero / v_scale_zero (bf16 [batch, h_kv, capacity, 2], or [num_pages,
+ * h_kv, page_size, 2]); the value is m + s * code. k_cache / v_cache have
+ * head_dim / 2 bytes in the place of head_dim elements; a contiguous capacity
+ * is a multiple of 4. The append rounds the turned key once to bf16, as for a
+ * bf16 cache, and stores the bf16 rows of k and v so: m = the row's minimum, s
+ * = the smallest bf16 with 15 s >= maximum - m, code = (x - m) / s rounded to
+ * nearest, ties to even, every decision exact. Magnitudes above 2^126 are taken
+ * as 2^126; a row with a value that is not finite gets s = NaN and reads as
+ * NaN. q_new, k_new and v_new are bf16. Appends, the one-token and multi-token
+ * attention and steps (tensor cores) and kv_read_rows take it; prefill, the
+ * tree calls and kv_keep_path return MQA_ERR_UNSUPPORTED (a prompt runs over
+ * a bf16 layout and is appended to the 4-bit one as well; kv_read_rows gives the
+ * bf16 rows of a prefix for it). num_splits: 1 = one block per (sequence, kv
+ * head), no workspace; anything else = equal runs of the cached tokens over
+ * all SMs, whatever the lengths (mqa_choose_splits says 2); calls that may
+ * overlap on the GPU need a workspace each. The query is rounded to fp16 (11
+ * bits), the probabilities times s to 11 bits; the values of a window's or a
+ * sequence's tokens that a query does not see are multiplied by a zero
+ * probability, so they have to be finite; rows outside [0, L), and before the
+ * window of a sequence's first new token, may hold anything.
+ *
  * Bounded waits: inside the attention kernels every wait for another warp's
  * progress (a tile landing, a tile freed, a product done) gives up after
  * wait_limit_ns nanoseconds (0 selects the default, one second). The kernel
@@ -177,8 +202,8 @@ typedef struct mqa_kv_layout {
   int32_t max_pages_per_seq;
   int32_t window; /* 0: full context; W > 0: sliding window of the last W tokens */
   const int32_t* block_table;
-  void* k_scale_zero; /* MQA_U8 only: float32 (scale, zero_point) per cached row of K */
-  void* v_scale_zero; /* MQA_U8 only: same for V */
+  void* k_scale_zero; /* per cached row of K, MQA_U8: float32 (scale, zero_point), MQA_U4: bf16 (scale, minimum) */
+  void* v_scale_zero; /* same for V */
   uint64_t wait_limit_ns; /* 0: 1 s; see "Bounded waits" above */
 } mqa_kv_layout;
 
@@ -205,6 +230,53 @@ typedef struct mqa_kv_layout {
 MQA_API mqa_status kv_append_rope(const mqa_kv_layout* layout, const void* q_new, const void* k_new, const void* v_new,
                           const int32_t* pos, double rope_base, float* q_rot, int32_t* err_word,
                           mqa_stream_t stream);
+
+/*
+ * kv_append_norm_rope -- kv_append_rope_multi for models that normalise the
+ * queries and keys of each head before the rotation, and for positions with
+ * several axes (the time, height and width of an image or a video), in the
+ * same pass. n_new >= 1 tokens per sequence; the pointers, token i's cache row
+ * pos[b] + i and the device errors are those of kv_append_rope_multi; any cache.
+ *   y = x / sqrt(mean(x^2) + eps) * w  for each head's q and k (w = q_weight,
+ *       k_weight: [head_dim], in the type of q_new; a NULL one: y = x)
+ *   the pairs of y are turned as kv_append_rope turns them, pair i by position
+ *       axis_pos[a, b, token] of the axis a whose section holds i: the first
+ *       section[0] pairs by axis 0, the next section[1] by axis 1, and so on
+ *       (n_axes = 0: all by pos[b] + token). theta_i depends on i alone.
+ * The key is formed as a pair of floats (2^-36 of the pair's length) and
+ * rounded once to the type of k_new; a bf16 or f32 cache holds that, the others
+ * hold it encoded (MQA_U8 and MQA_FP8_E5M2 as kv_append_rope encodes a value,
+ * so there a key is rounded to bf16 first). q_rot is formed in fp32. A pair of
+ * k with a value that is not finite becomes NaN. options NULL: no norm, one axis.
+ */
+typedef struct mqa_norm_rope {
+  const void* q_weight;    /* device, 16-byte aligned, or NULL */
+  const void* k_weight;
+  float eps;               /* > 0 with a weight */
+  int32_t n_axes;          /* 0..4 */
+  int32_t section[4];      /* rotation pairs of each axis; their sum is head_dim / 2 */
+  const int32_t* axis_pos; /* device [n_axes, batch, n_new], any int32 */
+} mqa_norm_rope;
+MQA_API mqa_status kv_append_norm_rope(const mqa_kv_layout* layout, int32_t n_new, const void* q_new,
+                                       const void* k_new, const void* v_new, const int32_t* pos,
+                                       const mqa_norm_rope* options, double rope_base, float* q_rot,
+                                       int32_t* err_word, mqa_stream_t stream);
+
+/*
+ * kv_read_rows -- cached rows as values: row start[b] + i of K and V, i in [0,
+ * num_rows[b]), to k_out / v_out [batch, h_kv, n_rows, head_dim] (out_dtype
+ * MQA_BF16 or MQA_F32: the layout of a contiguous cache, for a prefill that
+ * continues a quantised prefix, or to move a cache). Any cache type; start NULL:
+ * 0, num_rows NULL: n_rows each. Rows i >= num_rows[b] are left as they are.
+ * MQA_U8 (code - zero_point) * scale and MQA_U4 m + s * code in fp32, then one
+ * rounding. num_rows[b] outside [0, n_rows] sets MQA_DEVERR_SEQ_LEN, rows past
+ * the cache (or the block table) MQA_DEVERR_POS_RANGE: nothing of that sequence
+ * is written; a page outside the pool sets MQA_DEVERR_PAGE_RANGE: its rows are
+ * not written.
+ */
+MQA_API mqa_status kv_read_rows(const mqa_kv_layout* layout, int32_t n_rows, const int32_t* start,
+                                const int32_t* num_rows, void* k_out, void* v_out, int32_t out_dtype,
+                                int32_t* err_word, mqa_stream_t stream);
 
 /*
  * gqa_decode_attention -- step 3: for every sequence b and query head h,
@@ -333,7 +405,7 @@ MQA_API mqa_status gqa_decode_attention_noalloc(const mqa_kv_layout* layout, con
  *   <= 128 -- with the cache rows bit for bit those of the two calls.
  * 1 <= n_new <= 32 for the attention (kv_append_rope_multi takes any n_new;
  * longer runs of new tokens go to gqa_prefill_attention). n_new > 1 runs on
- * tensor cores only (MQA_ERR_UNSUPPORTED on CUDA cores): over a bf16 cache,
+ * tensor cores only (MQA_ERR_UNSUPPORTED on CUDA cores): over a MQA_U4 cache, over a bf16 cache,
  * contiguous or paged (32 or more query rows per kv head on the tcgen05
  * kernel, which gathers a paged key tile page by page); over a MQA_FP8_E5M2
  * cache (contiguous with head_dim 128 and (h_q / h_kv) * n_new >= 32: the

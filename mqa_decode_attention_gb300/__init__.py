@@ -29,6 +29,7 @@ from ._abi import (
     MQA_F32,
     MQA_U8,
     MQA_FP8_E5M2,
+    MQA_U4,
     MQA_VARIANT_AUTO,
     MQA_VARIANT_CUDA_CORE,
     MQA_VARIANT_TENSOR_CORE,
@@ -49,6 +50,8 @@ __all__ = [
     "decode_step",
     "decode_step_multi",
     "kv_append_rope_multi",
+    "kv_append_norm_rope",
+    "kv_read_rows",
     "gqa_decode_attention_multi",
     "gqa_prefill_attention",
     "prefill_step",
@@ -74,6 +77,7 @@ __all__ = [
     "MQA_DEVERR_U8_SCALE",
     "MQA_U8",
     "MQA_FP8_E5M2",
+    "MQA_U4",
 ]
 
 
@@ -113,16 +117,40 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _four_bit(what: str, codes: torch.Tensor, pairs) -> None:
+    for name, x, dtype, last in (("codes", codes, torch.uint8, None), ("(scale, minimum) pairs", pairs, torch.bfloat16, 2)):
+        if x is None or x.dtype is not dtype or not x.is_contiguous() or x.shape[:-1] != codes.shape[:-1] or \
+                last not in (None, x.shape[-1]):
+            raise ValueError(f"{what} {name} of a 4-bit cache: contiguous {dtype} [..., {last or 'head_dim / 2'}] is wanted, "
+                             f"got {None if x is None else (x.dtype, tuple(x.shape))}")
+
+
+def _cache_kind(k: torch.Tensor, v: torch.Tensor, k_sz, v_sz, cache_dtype: int | None) -> tuple[int, int]:
+    """(cache dtype code, head_dim) of a cache pair; cache_dtype only says that uint8 tensors hold 4-bit codes."""
+    if cache_dtype == MQA_U4:
+        _four_bit("K", k, k_sz)
+        _four_bit("V", v, v_sz)
+        return MQA_U4, 2 * k.shape[3]
+    kind = _dtype_code(k.dtype)
+    if cache_dtype not in (None, kind):
+        raise ValueError(f"cache_dtype {cache_dtype} with tensors of {k.dtype}")
+    return kind, k.shape[3]
+
+
 def layout_contiguous(k_cache: torch.Tensor, v_cache: torch.Tensor, h_q: int, window: int = 0,
-                      k_scale_zero: torch.Tensor | None = None, v_scale_zero: torch.Tensor | None = None) -> KVLayout:
+                      k_scale_zero: torch.Tensor | None = None, v_scale_zero: torch.Tensor | None = None,
+                      cache_dtype: int | None = None) -> KVLayout:
     """Layout of a contiguous cache pair, each [batch, h_kv, capacity, head_dim]
     (bf16, fp32, fp8 e5m2, or uint8 codes with float32 [batch, h_kv, capacity,
-    2] scale / zero-point pairs); window > 0 restricts the attention to the
-    last `window` tokens."""
+    2] scale / zero-point pairs; with cache_dtype=MQA_U4 uint8 [batch, h_kv,
+    capacity, head_dim / 2] of two 4-bit codes to a byte, with bf16 [batch, h_kv,
+    capacity, 2] scale / minimum pairs); window > 0 restricts the attention to
+    the last `window` tokens."""
     assert k_cache.shape == v_cache.shape and k_cache.dim() == 4
     assert k_cache.is_contiguous() and v_cache.is_contiguous()
-    B, h_kv, cap, d = k_cache.shape
-    lay = KVLayout(_dtype_code(k_cache.dtype), B, h_q, h_kv, d, 0, k_cache.data_ptr(), v_cache.data_ptr(), cap,
+    B, h_kv, cap, _ = k_cache.shape
+    kind, d = _cache_kind(k_cache, v_cache, k_scale_zero, v_scale_zero, cache_dtype)
+    lay = KVLayout(kind, B, h_q, h_kv, d, 0, k_cache.data_ptr(), v_cache.data_ptr(), cap,
                    0, 0, 0, window, None, _ptr(k_scale_zero), _ptr(v_scale_zero))
     lay._tensors = (k_cache, v_cache, k_scale_zero, v_scale_zero)  # the struct holds raw pointers: keep them alive
     return lay
@@ -130,16 +158,18 @@ def layout_contiguous(k_cache: torch.Tensor, v_cache: torch.Tensor, h_q: int, wi
 
 def layout_paged(k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor, h_q: int,
                  window: int = 0, k_scale_zero: torch.Tensor | None = None,
-                 v_scale_zero: torch.Tensor | None = None) -> KVLayout:
+                 v_scale_zero: torch.Tensor | None = None, cache_dtype: int | None = None) -> KVLayout:
     """Layout of a paged pool pair, each [num_pages, h_kv, page_size, head_dim]
-    (uint8 pools take [num_pages, h_kv, page_size, 2] scale / zero-point pairs),
-    with an int32 block table [batch, max_pages_per_seq]; window > 0 restricts
-    the attention to the last `window` tokens."""
+    (uint8 pools take [num_pages, h_kv, page_size, 2] scale / zero-point pairs;
+    cache_dtype=MQA_U4: codes and pairs as in ``layout_contiguous``), with an
+    int32 block table [batch, max_pages_per_seq]; window > 0 restricts the
+    attention to the last `window` tokens."""
     assert k_pool.shape == v_pool.shape and k_pool.dim() == 4
     assert block_table.dtype == torch.int32 and block_table.is_contiguous()
-    n, h_kv, ps, d = k_pool.shape
+    n, h_kv, ps, _ = k_pool.shape
+    kind, d = _cache_kind(k_pool, v_pool, k_scale_zero, v_scale_zero, cache_dtype)
     B, mp = block_table.shape
-    lay = KVLayout(_dtype_code(k_pool.dtype), B, h_q, h_kv, d, 1, k_pool.data_ptr(), v_pool.data_ptr(), 0, ps, n,
+    lay = KVLayout(kind, B, h_q, h_kv, d, 1, k_pool.data_ptr(), v_pool.data_ptr(), 0, ps, n,
                    mp, window, block_table.data_ptr(), _ptr(k_scale_zero), _ptr(v_scale_zero))
     lay._tensors = (k_pool, v_pool, block_table, k_scale_zero, v_scale_zero)  # keep the pointed-to tensors alive
     return lay
@@ -181,6 +211,52 @@ def kv_append_rope_multi(layout: KVLayout, n_new: int, q_new, k_new, v_new, pos,
                                         _ptr(pos), float(rope_base), _ptr(q_rot), _ptr(err), _stream(stream))
     if st != 0:
         raise MqaError("kv_append_rope_multi", st)
+
+
+def kv_append_norm_rope(layout: KVLayout, n_new: int, q_new, k_new, v_new, pos, rope_base: float, q_rot, err,
+                        q_weight=None, k_weight=None, eps: float = 1e-6, axis_pos=None, sections=None,
+                        stream=None) -> None:
+    """``kv_append_rope_multi`` with the queries and keys of each head normalised
+    first (root mean square, weights [head_dim] of q_new's type; None: not), and
+    with positions of up to four axes: axis_pos [axes, B, n] int32, sections[a]
+    rotation pairs for axis a (their sum is head_dim / 2). q_new [B, n, H_q, d],
+    k_new / v_new [B, n, H_kv, d], bf16 (fp32 for an fp32 cache); q_rot [B, n,
+    H_q, d] fp32; token i goes to row pos[b] + i of any cache."""
+    B, n, d, i32 = layout.batch, int(n_new), layout.head_dim, torch.int32
+    dt = torch.float32 if layout.cache_dtype == MQA_F32 else torch.bfloat16
+    if (axis_pos is None) != (sections is None):
+        raise ValueError("axis_pos and sections come together")
+    sections = [int(x) for x in sections or ()]
+    if len(sections) > 4:
+        raise ValueError(f"at most 4 axes, got {len(sections)}")
+    opts = _abi.NormRope(_want("q_weight", q_weight, dt, d), _want("k_weight", k_weight, dt, d), float(eps), len(sections),
+                         (ctypes.c_int32 * 4)(*sections), _want("axis_pos", axis_pos, i32, len(sections) * B * n))
+    st = library().kv_append_norm_rope(
+        ctypes.byref(layout), n, _want("q_new", q_new, dt, B * n * layout.h_q * d),
+        _want("k_new", k_new, dt, B * n * layout.h_kv * d), _want("v_new", v_new, dt, B * n * layout.h_kv * d),
+        _want("pos", pos, i32, B), ctypes.byref(opts), float(rope_base),
+        _want("q_rot", q_rot, torch.float32, B * n * layout.h_q * d), _want("err", err, i32, 1), _stream(stream))
+    if st != 0:
+        raise MqaError("kv_append_norm_rope", st)
+
+
+def kv_read_rows(layout: KVLayout, start, num_rows, k_out, v_out, err, stream=None) -> None:
+    """Rows start[b] .. start[b] + num_rows[b] of a cache of any type as values:
+    k_out / v_out [B, H_kv, n, d], bf16 or fp32, n >= every num_rows[b] (None: n
+    each; start None: 0). The outputs have the shape of a contiguous cache:
+    ``layout_contiguous`` over them serves a prefill that continues the rows."""
+    if k_out.dim() != 4:
+        raise ValueError(f"k_out must be [batch, h_kv, rows, head_dim], got {tuple(k_out.shape)}")
+    B, h, n, d = k_out.shape
+    if (B, h, d) != (layout.batch, layout.h_kv, layout.head_dim):
+        raise ValueError(f"k_out {tuple(k_out.shape)} for a layout of batch {layout.batch}, h_kv {layout.h_kv}, head_dim {layout.head_dim}")
+    i32 = torch.int32
+    st = library().kv_read_rows(ctypes.byref(layout), n, _want("start", start, i32, B), _want("num_rows", num_rows, i32, B),
+                                _want("k_out", k_out, k_out.dtype, k_out.numel()),
+                                _want("v_out", v_out, k_out.dtype, k_out.numel()), _dtype_code(k_out.dtype),
+                                _want("err", err, i32, 1), _stream(stream))
+    if st != 0:
+        raise MqaError("kv_read_rows", st)
 
 
 def gqa_decode_attention_multi(layout: KVLayout, n_new: int, q_rot, seq_lens, max_seq_len: int, scale: float,

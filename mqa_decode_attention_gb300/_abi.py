@@ -20,6 +20,7 @@ MQA_BF16 = 0
 MQA_F32 = 1
 MQA_U8 = 2
 MQA_FP8_E5M2 = 3
+MQA_U4 = 5
 
 MQA_VARIANT_AUTO = 0
 MQA_VARIANT_CUDA_CORE = 1
@@ -60,7 +61,25 @@ class KVLayout(ctypes.Structure):
     ]
 
 
+class NormRope(ctypes.Structure):
+    """mqa_norm_rope"""
+
+    _fields_ = [
+        ("q_weight", c_vp),
+        ("k_weight", c_vp),
+        ("eps", ctypes.c_float),
+        ("n_axes", c_i32),
+        ("section", c_i32 * 4),
+        ("axis_pos", c_vp),
+    ]
+
+
 _PROTOTYPES = {
+    "kv_append_norm_rope": (
+        c_i32,
+        [ctypes.POINTER(KVLayout), c_i32, c_vp, c_vp, c_vp, c_vp, ctypes.POINTER(NormRope), ctypes.c_double, c_vp, c_vp,
+         c_vp]),
+    "kv_read_rows": (c_i32, [ctypes.POINTER(KVLayout), c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp]),
     "kv_append_rope": (c_i32, [ctypes.POINTER(KVLayout), c_vp, c_vp, c_vp, c_vp, ctypes.c_double, c_vp, c_vp, c_vp]),
     "gqa_decode_attention": (
         c_i32,

@@ -42,13 +42,13 @@ bool is_pow2(long long x) { return x > 0 && (x & (x - 1)) == 0; }
 mqa_status check_layout(const mqa_kv_layout* L) {
   if (L == nullptr) return MQA_ERR_INVALID_ARG;
   if (L->cache_dtype != MQA_BF16 && L->cache_dtype != MQA_F32 && L->cache_dtype != MQA_U8 &&
-      L->cache_dtype != MQA_FP8_E5M2)
+      L->cache_dtype != MQA_FP8_E5M2 && L->cache_dtype != MQA_U4)
     return MQA_ERR_UNSUPPORTED;
-  if (L->cache_dtype == MQA_U8) {
+  if (L->cache_dtype == MQA_U8 || L->cache_dtype == MQA_U4) {
     if (L->k_scale_zero == nullptr || L->v_scale_zero == nullptr) return MQA_ERR_INVALID_ARG;
     if (!aligned(L->k_scale_zero, 16) || !aligned(L->v_scale_zero, 16)) return MQA_ERR_INVALID_ARG;
-    // the (scale, zero) rows of a kv head are copied by TMA: 16-byte strides
-    if (!L->paged && L->capacity % 2 != 0) return MQA_ERR_UNSUPPORTED;
+    // the (scale, zero) or (scale, minimum) rows of a kv head are copied in units of 16 bytes
+    if (!L->paged && L->capacity % (L->cache_dtype == MQA_U8 ? 2 : 4) != 0) return MQA_ERR_UNSUPPORTED;
   }
   if (L->batch < 1 || L->h_q < 1 || L->h_kv < 1 || L->h_q % L->h_kv != 0) return MQA_ERR_INVALID_ARG;
   if (L->head_dim != 64 && L->head_dim != 128) return MQA_ERR_UNSUPPORTED;
@@ -76,11 +76,11 @@ int resolve_variant(const mqa_kv_layout* L, int variant) {
   return variant;
 }
 
-// Which cache dtypes a kernel family reads: tensor cores bf16, uint8 and fp8
-// e5m2, CUDA cores bf16 and fp32.
+// Which cache dtypes a kernel family reads: tensor cores bf16, uint8, fp8
+// e5m2 and 4 bit, CUDA cores bf16 and fp32.
 bool variant_supports(int variant, int cache_dtype) {
   if (variant == MQA_VARIANT_TENSOR_CORE)
-    return cache_dtype == MQA_BF16 || cache_dtype == MQA_U8 || cache_dtype == MQA_FP8_E5M2;
+    return cache_dtype == MQA_BF16 || cache_dtype == MQA_U8 || cache_dtype == MQA_FP8_E5M2 || cache_dtype == MQA_U4;
   return cache_dtype == MQA_BF16 || cache_dtype == MQA_F32;
 }
 
@@ -89,6 +89,7 @@ int dtype_code(int cache_dtype) {
     case MQA_BF16: return kDtypeBf16;
     case MQA_F32: return kDtypeF32;
     case MQA_U8: return kDtypeU8;
+    case MQA_U4: return kDtypeU4;
     default: return kDtypeF8;
   }
 }
@@ -157,7 +158,32 @@ int head_blocks(const mqa_kv_layout* L, const KernelShape& ks, int n_new = 1) {
 // kernel's fp8 form for 32 or more rows per kv head over a contiguous e5m2
 // cache).
 bool multi_supported(const mqa_kv_layout* L, int variant, int n_new) {
-  return n_new == 1 || (variant == MQA_VARIANT_TENSOR_CORE && (L->cache_dtype == MQA_BF16 || byte_cache(L->cache_dtype)));
+  return n_new == 1 || (variant == MQA_VARIANT_TENSOR_CORE && (L->cache_dtype == MQA_BF16 || L->cache_dtype == MQA_U4 ||
+                                                               byte_cache(L->cache_dtype)));
+}
+
+// A 4-bit cache: blocks take equal runs of all tiles (attn_u4.cu), whatever the
+// lengths, unless one split is asked for. The workspace holds a counter and two
+// partial results for each block.
+struct U4Plan {
+  U4Shape shape;
+  int row_blocks;
+  int ctas;
+  size_t counters;   // bytes at the start of the workspace
+  size_t workspace;
+};
+
+U4Plan u4_plan(const mqa_kv_layout* L, int n_new) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  U4Plan c;
+  const int rows = (L->h_q / L->h_kv) * n_new;
+  c.shape = u4_shape(L->head_dim, rows);
+  c.row_blocks = (rows + c.shape.rows - 1) / c.shape.rows;
+  c.ctas = device_info(dev).sms * c.shape.ctas_per_sm;
+  c.counters = (static_cast<size_t>(c.ctas) * 4 + 255) / 256 * 256;
+  c.workspace = c.counters + static_cast<size_t>(2) * c.ctas * u4_part_floats(c.shape.rows, L->head_dim) * 4;
+  return c;
 }
 
 // Tokens one (sequence, kv head) may need read: the bound, or with a sliding
@@ -175,6 +201,7 @@ int read_span(const mqa_kv_layout* L, int max_len, int n_new = 1) {
 // partial-output traffic and a second wave), and 4096-token chunks balance a
 // paged batch of lengths spread over [128, 16384].
 int choose_splits(const mqa_kv_layout* L, int max_len_in, int variant, int n_new = 1) {
+  if (L->cache_dtype == MQA_U4) return 2;  // equal runs
   const int max_len = read_span(L, max_len_in);
   int dev = 0;
   cudaGetDevice(&dev);
@@ -197,8 +224,14 @@ int choose_splits(const mqa_kv_layout* L, int max_len_in, int variant, int n_new
   return std::max(1, std::min(s, tiles));
 }
 
-// Effective split count and chunk for a requested count.
-void split_plan(int requested, int max_len, int* splits, int* chunk) {
+// Effective split count and chunk for a requested count (a 4-bit cache: one, or
+// more than one, which stands for equal runs).
+void split_plan(const mqa_kv_layout* L, int requested, int max_len, int* splits, int* chunk) {
+  if (L->cache_dtype == MQA_U4) {
+    *splits = requested > 1 ? 2 : 1;
+    *chunk = 0;
+    return;
+  }
   const int per = (max_len + requested - 1) / requested;
   const int c = ((per + kTile - 1) / kTile) * kTile;
   *chunk = c;
@@ -207,6 +240,7 @@ void split_plan(int requested, int max_len, int* splits, int* chunk) {
 
 size_t partial_bytes(const mqa_kv_layout* L, int splits, int n_new = 1) {
   if (splits <= 1) return 0;
+  if (L->cache_dtype == MQA_U4) return u4_plan(L, n_new).workspace;
   const size_t rows = static_cast<size_t>(L->batch) * n_new * L->h_q;
   const size_t o_bytes = ((rows * splits * L->head_dim * 4) + 255) / 256 * 256;
   return o_bytes + rows * splits * 4;
@@ -473,12 +507,66 @@ struct TreeAppend {
   int zero_count;
 };
 
+// after the checks; options NULL: no norm, one position. zero: counters to
+// clear for the attention launch that follows.
+mqa_status norm_append(const mqa_kv_layout* layout, int n_new, const void* q_new, const void* k_new, const void* v_new,
+                       const int32_t* pos, const mqa_norm_rope* options, double rope_base, float* q_rot, int32_t* zero,
+                       int zero_count, int32_t* err_word, cudaStream_t stream) {
+  NormAppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.batch = layout->batch;
+  p.h_q = layout->h_q;
+  p.h_kv = layout->h_kv;
+  p.head_dim = layout->head_dim;
+  p.cache_dtype = dtype_code(layout->cache_dtype);
+  p.paged = layout->paged;
+  p.n_new = n_new;
+  p.q_new = q_new;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.pos = pos;
+  p.eps = 1.f;
+  if (options != nullptr) {
+    p.q_weight = options->q_weight;
+    p.k_weight = options->k_weight;
+    if (p.q_weight || p.k_weight) p.eps = options->eps;
+    if (options->n_axes > 0) {
+      p.axis_pos = options->axis_pos;
+      int end = 0;
+      for (int a = 0; a < kMaxAxes; ++a) p.section_end[a] = end += a < options->n_axes ? options->section[a] : 0;
+    }
+  }
+  p.k_cache = layout->k_cache;
+  p.v_cache = layout->v_cache;
+  p.capacity = layout->capacity;
+  p.page_size = layout->page_size;
+  p.num_pages = layout->num_pages;
+  p.max_pages = layout->max_pages_per_seq;
+  p.block_table = layout->block_table;
+  p.k_sz = layout->k_scale_zero;
+  p.v_sz = layout->v_scale_zero;
+  p.q_rot = q_rot;
+  p.err = err_word;
+  p.zero = zero;
+  p.zero_count = zero_count;
+  fill_theta(p.theta, layout->head_dim, rope_base);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const cudaError_t e = launch_append_norm(p, device_info(dev).sms, stream);
+  if (e != cudaSuccess) return fail_cuda(e);
+  const cudaError_t e2 = cudaGetLastError();
+  return e2 == cudaSuccess ? MQA_OK : fail_cuda(e2);
+}
+
 mqa_status append_impl(const mqa_kv_layout* layout, const void* q_new, const void* k_new, const void* v_new,
                        const int32_t* pos, double rope_base, float* q_rot, int32_t* err_word, mqa_stream_t stream,
-                       int n_new = 1, const TreeAppend* tree = nullptr) {
+                       int n_new = 1, const TreeAppend* tree = nullptr, int32_t* zero = nullptr, int zero_count = 0) {
   const mqa_status st = check_append_args(layout, q_new, k_new, v_new, pos, rope_base, q_rot, err_word);
   if (st != MQA_OK) return st;
   if (n_new < 1 || static_cast<long long>(layout->batch) * n_new > (1ll << 31) - 1) return MQA_ERR_INVALID_ARG;
+  if (layout->cache_dtype == MQA_U4)
+    return norm_append(layout, n_new, q_new, k_new, v_new, pos, nullptr, rope_base, q_rot, zero, zero_count, err_word,
+                       reinterpret_cast<cudaStream_t>(stream));
   AppendParams p;
   std::memset(&p, 0, sizeof(p));
   p.n_new = n_new;
@@ -569,6 +657,74 @@ bool fusable_multi(const mqa_kv_layout* L, int variant, int n_new) {
   return head_blocks(L, decode_shape(L, variant, n_new), n_new) == 1;
 }
 
+// V codes of a 4-bit cache: boxes of whole rows x min(kU4Tile, page_size) tokens,
+// swizzled over a row's bytes, so that the 8 rows of an ldmatrix lie in different banks.
+bool make_u4_map(CUtensorMap* map, const mqa_kv_layout* L) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t row = L->head_dim / 2, rows = L->paged ? static_cast<cuuint64_t>(L->page_size) : static_cast<cuuint64_t>(L->capacity);
+  const cuuint64_t heads = L->paged ? static_cast<cuuint64_t>(L->h_kv) : static_cast<cuuint64_t>(L->batch) * L->h_kv;
+  const cuuint64_t dims[4] = {row, rows, heads, static_cast<cuuint64_t>(L->num_pages)};
+  const cuuint64_t strides[3] = {row, rows * row, rows * row * heads};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(row), static_cast<cuuint32_t>(L->paged ? std::min(L->page_size, kU4Tile) : kU4Tile), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, L->paged ? 4 : 3, L->v_cache, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// after attention_impl's checks
+mqa_status u4_attention(const mqa_kv_layout* L, int n_new, const float* q_rot, const int32_t* seq_lens, int max_seq_len,
+                        float scale, bool whole, void* out, int out_dtype, float* lse_out, void* workspace,
+                        int32_t* err_word, cudaStream_t stream, int early) {
+  const U4Plan c = u4_plan(L, n_new);
+  if (whole && static_cast<long long>(L->batch) * L->h_kv * c.row_blocks > (1ll << 31) - 1) return MQA_ERR_INVALID_ARG;
+  U4Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.batch = L->batch;
+  p.h_q = L->h_q;
+  p.h_kv = L->h_kv;
+  p.group = L->h_q / L->h_kv;
+  p.n_new = n_new;
+  p.rows = p.group * n_new;
+  p.head_dim = L->head_dim;
+  p.row_blocks = c.row_blocks;
+  p.paged = L->paged;
+  p.page_size = L->page_size;
+  p.num_pages = L->num_pages;
+  p.max_pages = L->max_pages_per_seq;
+  p.k_cache = static_cast<const uint8_t*>(L->k_cache);
+  p.v_cache = static_cast<const uint8_t*>(L->v_cache);
+  p.k_sm = static_cast<const uint32_t*>(L->k_scale_zero);
+  p.v_sm = static_cast<const uint32_t*>(L->v_scale_zero);
+  p.capacity = L->capacity;
+  p.block_table = L->block_table;
+  p.max_seq_len = max_seq_len;
+  p.q_rot = q_rot;
+  p.seq_lens = seq_lens;
+  p.scale = scale;
+  p.window = L->window;
+  p.out = out;
+  p.out_dtype = out_dtype == MQA_BF16 ? kDtypeBf16 : kDtypeF32;
+  p.lse_out = lse_out;
+  p.whole = whole;
+  p.min_tiles = 4;
+  p.arrived = static_cast<int32_t*>(workspace);
+  p.part = whole ? nullptr : reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.counters);
+  p.err = err_word;
+  p.early = early;
+  p.wait_ns = wait_limit(L);
+  CUtensorMap tv;
+  if (!make_u4_map(&tv, L)) {
+    snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled failed or is unavailable");
+    return MQA_ERR_CUDA;
+  }
+  const cudaError_t e = launch_attn_u4(p, tv, c.ctas, /*clear=*/!whole && !early, stream);
+  if (e != cudaSuccess) return fail_cuda(e);
+  const cudaError_t e2 = cudaGetLastError();
+  return e2 == cudaSuccess ? MQA_OK : fail_cuda(e2);
+}
+
 mqa_status attention_impl(const mqa_kv_layout* layout, const float* q_rot, const int32_t* seq_lens, int32_t max_seq_len,
                           float scale, int32_t num_splits, void* out, int32_t out_dtype, float* lse_out,
                           void* workspace, size_t workspace_bytes, int32_t variant, int32_t* err_word,
@@ -591,12 +747,16 @@ mqa_status attention_impl(const mqa_kv_layout* layout, const float* q_rot, const
 
   const int req = num_splits == 0 ? choose_splits(layout, max_seq_len, v, n_new) : num_splits;
   int splits, chunk;
-  split_plan(req, read_span(layout, max_seq_len, n_new), &splits, &chunk);
+  split_plan(layout, req, read_span(layout, max_seq_len, n_new), &splits, &chunk);
   const size_t need = partial_bytes(layout, splits, n_new);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need) return MQA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return MQA_ERR_INVALID_ARG;
   }
+
+  if (layout->cache_dtype == MQA_U4)
+    return u4_attention(layout, n_new, q_rot, seq_lens, max_seq_len, scale, splits == 1, out, out_dtype, lse_out,
+                        workspace, err_word, reinterpret_cast<cudaStream_t>(stream), early);
 
   const KernelShape ks = decode_shape(layout, v, n_new);
   bool merged = false;  // the attention launch merged its splits itself: no combine
@@ -970,7 +1130,7 @@ size_t mqa_workspace_size_multi(const mqa_kv_layout* layout, int32_t n_new, int3
   const int v = resolve_variant(layout, variant);
   const int req = num_splits == 0 ? choose_splits(layout, max_seq_len, v, n_new) : num_splits;
   int splits, chunk;
-  split_plan(req, read_span(layout, max_seq_len, n_new), &splits, &chunk);
+  split_plan(layout, req, read_span(layout, max_seq_len, n_new), &splits, &chunk);
   return partial_bytes(layout, splits, n_new);
 }
 
@@ -988,7 +1148,7 @@ int32_t mqa_step_launches(const mqa_kv_layout* layout, int32_t n_new, int32_t ma
   if (!variant_supports(v, layout->cache_dtype) || !multi_supported(layout, v, n_new)) return -1;
   const int req = num_splits == 0 ? choose_splits(layout, max_seq_len, v, n_new) : num_splits;
   int splits, chunk;
-  split_plan(req, read_span(layout, max_seq_len, n_new), &splits, &chunk);
+  split_plan(layout, req, read_span(layout, max_seq_len, n_new), &splits, &chunk);
   // the decisions step_impl and attention_impl take
   const bool fused = (n_new == 1 && fusable(layout, v)) || fusable_multi(layout, v, n_new);
   bool merged = false;
@@ -1005,6 +1165,7 @@ int32_t mqa_step_launches(const mqa_kv_layout* layout, int32_t n_new, int32_t ma
              tc05_keys_applies(t.group, n_new, layout->head_dim, layout->paged))
       merged = tc05_widen_merges_splits(t);
   }
+  if (layout->cache_dtype == MQA_U4) merged = true;
   if (fused_append) *fused_append = fused ? 1 : 0;
   return (fused ? 1 : 2) + (splits > 1 && !merged ? 1 : 0);
 }
@@ -1071,15 +1232,19 @@ mqa_status step_impl(const mqa_kv_layout* layout, int n_new, const void* q_new, 
   if (!seq_lens || !out || max_seq_len < n_new || max_seq_len > token_limit(layout)) return MQA_ERR_INVALID_ARG;
   if (variant < MQA_VARIANT_AUTO || variant > MQA_VARIANT_TENSOR_CORE || num_splits < 0)
     return MQA_ERR_INVALID_ARG;
+  if (!aligned(seq_lens, 4) || !aligned(out, 16) || !aligned(lse_out, 4) || !std::isfinite(scale) ||
+      static_cast<long long>(layout->batch) * n_new * layout->h_q > (1ll << 31) - 1)
+    return MQA_ERR_INVALID_ARG;
   if (out_dtype != MQA_BF16 && out_dtype != MQA_F32) return MQA_ERR_UNSUPPORTED;
   const int v = resolve_variant(layout, variant);
   if (!variant_supports(v, layout->cache_dtype) || !multi_supported(layout, v, n_new)) return MQA_ERR_UNSUPPORTED;
   {
     const int req = num_splits == 0 ? choose_splits(layout, max_seq_len, v, n_new) : num_splits;
     int splits, chunk;
-    split_plan(req, read_span(layout, max_seq_len, n_new), &splits, &chunk);
+    split_plan(layout, req, read_span(layout, max_seq_len, n_new), &splits, &chunk);
     const size_t need = partial_bytes(layout, splits, n_new);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MQA_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 256)) return MQA_ERR_INVALID_ARG;
   }
   const mqa_status ca = check_append_args(layout, q_new, k_new, v_new, pos, rope_base, q_rot, err_word);
   if (ca != MQA_OK) return ca;
@@ -1089,7 +1254,11 @@ mqa_status step_impl(const mqa_kv_layout* layout, int n_new, const void* q_new, 
     return attention_impl(layout, q_rot, seq_lens, max_seq_len, scale, num_splits, out, out_dtype, lse_out,
                           workspace, workspace_bytes, variant, err_word, stream, /*early=*/0, &rope, n_new);
   }
-  const mqa_status a = append_impl(layout, q_new, k_new, v_new, pos, rope_base, q_rot, err_word, stream, n_new);
+  // (a 4-bit cache: the append clears the attention's counters)
+  const bool runs = layout->cache_dtype == MQA_U4 && num_splits != 1;
+  const mqa_status a = append_impl(layout, q_new, k_new, v_new, pos, rope_base, q_rot, err_word, stream, n_new, nullptr,
+                                   runs ? static_cast<int32_t*>(workspace) : nullptr,
+                                   runs ? u4_plan(layout, n_new).ctas : 0);
   if (a != MQA_OK) return a;
   const RopeArgs rope{q_new, pos, rope_base, 0, nullptr, nullptr, nullptr};
   return attention_impl(layout, q_rot, seq_lens, max_seq_len, scale, num_splits, out, out_dtype, lse_out, workspace,
@@ -1126,7 +1295,8 @@ namespace {
 mqa_status check_tree_layout(const mqa_kv_layout* L, int n) {
   const mqa_status st = check_layout(L);
   if (st != MQA_OK) return st;
-  if (L->cache_dtype == MQA_F32) return MQA_ERR_UNSUPPORTED;  // tensor cores only, as the multi-token calls
+  // tensor cores only, as the multi-token calls; no 4-bit form
+  if (L->cache_dtype == MQA_F32 || L->cache_dtype == MQA_U4) return MQA_ERR_UNSUPPORTED;
   if (n < 1 || n > kMaxTreeNodes) return MQA_ERR_INVALID_ARG;
   if (static_cast<long long>(L->batch) * n * L->h_q > (1ll << 31) - 1) return MQA_ERR_INVALID_ARG;
   return MQA_OK;
@@ -1410,6 +1580,7 @@ mqa_status kv_keep_path(const mqa_kv_layout* layouts, int32_t n_layers, int32_t 
     const mqa_kv_layout& L = layouts[i];
     const mqa_status st = check_layout(&L);
     if (st != MQA_OK) return st;
+    if (L.cache_dtype == MQA_U4) return MQA_ERR_UNSUPPORTED;
     if (L.cache_dtype != f.cache_dtype || L.batch != f.batch || L.h_kv != f.h_kv || L.head_dim != f.head_dim ||
         L.paged != f.paged)
       return MQA_ERR_INVALID_ARG;
@@ -1452,6 +1623,72 @@ mqa_status kv_keep_path(const mqa_kv_layout* layouts, int32_t n_layers, int32_t 
     const cudaError_t e = launch_keep_path(p, m, device_info(dev).sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail_cuda(e);
   }
+  const cudaError_t e2 = cudaGetLastError();
+  return e2 == cudaSuccess ? MQA_OK : fail_cuda(e2);
+}
+
+mqa_status kv_append_norm_rope(const mqa_kv_layout* layout, int32_t n_new, const void* q_new, const void* k_new,
+                               const void* v_new, const int32_t* pos, const mqa_norm_rope* options, double rope_base,
+                               float* q_rot, int32_t* err_word, mqa_stream_t stream) {
+  const mqa_status st = check_append_args(layout, q_new, k_new, v_new, pos, rope_base, q_rot, err_word);
+  if (st != MQA_OK) return st;
+  if (n_new < 1 || static_cast<long long>(layout->batch) * n_new > (1ll << 31) - 1) return MQA_ERR_INVALID_ARG;
+  if (options != nullptr) {
+    if (!aligned(options->q_weight, 16) || !aligned(options->k_weight, 16)) return MQA_ERR_INVALID_ARG;
+    if ((options->q_weight || options->k_weight) && (!(options->eps > 0.f) || !std::isfinite(options->eps)))
+      return MQA_ERR_INVALID_ARG;
+    if (options->n_axes < 0 || options->n_axes > kMaxAxes) return MQA_ERR_INVALID_ARG;
+    if (options->n_axes > 0) {
+      if (options->axis_pos == nullptr || !aligned(options->axis_pos, 4)) return MQA_ERR_INVALID_ARG;
+      long long pairs = 0;
+      for (int a = 0; a < options->n_axes; ++a) {
+        if (options->section[a] < 0) return MQA_ERR_INVALID_ARG;
+        pairs += options->section[a];
+      }
+      if (pairs != layout->head_dim / 2) return MQA_ERR_INVALID_ARG;
+    }
+  }
+  return norm_append(layout, n_new, q_new, k_new, v_new, pos, options, rope_base, q_rot, nullptr, 0, err_word,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+mqa_status kv_read_rows(const mqa_kv_layout* layout, int32_t n_rows, const int32_t* start, const int32_t* num_rows,
+                        void* k_out, void* v_out, int32_t out_dtype, int32_t* err_word, mqa_stream_t stream) {
+  const mqa_status st = check_layout(layout);
+  if (st != MQA_OK) return st;
+  if (!k_out || !v_out || !err_word) return MQA_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(start, 4) || !aligned(num_rows, 4) || !aligned(err_word, 4))
+    return MQA_ERR_INVALID_ARG;
+  if (n_rows < 1 || n_rows > token_limit(layout)) return MQA_ERR_INVALID_ARG;
+  if (out_dtype != MQA_BF16 && out_dtype != MQA_F32) return MQA_ERR_UNSUPPORTED;
+  // (at least 64 rows to a block)
+  if ((static_cast<long long>(n_rows) + 63) / 64 * layout->batch * layout->h_kv > (1ll << 31) - 1) return MQA_ERR_INVALID_ARG;
+  ReadParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.batch = layout->batch;
+  p.h_kv = layout->h_kv;
+  p.head_dim = layout->head_dim;
+  p.cache_dtype = dtype_code(layout->cache_dtype);
+  p.paged = layout->paged;
+  p.k_cache = layout->k_cache;
+  p.v_cache = layout->v_cache;
+  p.k_sz = layout->k_scale_zero;
+  p.v_sz = layout->v_scale_zero;
+  p.capacity = layout->capacity;
+  p.limit = token_limit(layout);
+  p.page_size = layout->page_size;
+  p.num_pages = layout->num_pages;
+  p.max_pages = layout->max_pages_per_seq;
+  p.block_table = layout->block_table;
+  p.start = start;
+  p.num_rows = num_rows;
+  p.n_rows = n_rows;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.out_dtype = out_dtype == MQA_BF16 ? kDtypeBf16 : kDtypeF32;
+  p.err = err_word;
+  const cudaError_t e = launch_read_rows(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail_cuda(e);
   const cudaError_t e2 = cudaGetLastError();
   return e2 == cudaSuccess ? MQA_OK : fail_cuda(e2);
 }

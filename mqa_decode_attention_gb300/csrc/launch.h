@@ -28,6 +28,7 @@ constexpr int kDtypeBf16 = 0;
 constexpr int kDtypeF32 = 1;
 constexpr int kDtypeU8 = 2;  // cache only: uint8 codes + float2 (scale, zero point) per row
 constexpr int kDtypeF8 = 3;  // cache only: fp8 e5m2 values
+constexpr int kDtypeU4 = 4;  // cache only: 4-bit codes + a bf16 (scale, minimum) pair per row, held as one uint32
 
 struct AppendParams {
   int batch, h_q, h_kv, head_dim, cache_dtype, paged;
@@ -54,6 +55,85 @@ struct AppendParams {
   int32_t* zero;
   int zero_count;
   double theta[kMaxHalfDim];  // RoPE inverse frequencies base^(-2i/d)
+};
+
+// kv_append_norm_rope, and kv_append_rope over a 4-bit cache (append_norm.cu):
+// one warp for a (token, head) row, normalised when the weight is given.
+constexpr int kMaxAxes = 4;
+struct NormAppendParams {
+  int batch, h_q, h_kv, head_dim, cache_dtype, paged;
+  int n_new;
+  const void* q_new;
+  const void* k_new;
+  const void* v_new;
+  const void* q_weight;  // [head_dim] in the type of q_new, or null: no norm
+  const void* k_weight;
+  float eps;
+  const int32_t* pos;       // [B]: token i goes into row pos[b] + i
+  const int32_t* axis_pos;  // [n_axes, B, n_new] rotation positions, or null: pos[b] + i
+  int section_end[kMaxAxes];  // rotation pairs [section_end[a - 1], section_end[a]) turn by axis a
+  void* k_cache;
+  void* v_cache;
+  long long capacity;
+  int page_size, num_pages, max_pages;
+  const int32_t* block_table;
+  void* k_sz;  // uint8 cache: float2, 4-bit cache: uint32 per row
+  void* v_sz;
+  float* q_rot;
+  int32_t* err;
+  int32_t* zero;  // cleared for the attention launch that follows (or null)
+  int zero_count;
+  double theta[kMaxHalfDim];
+};
+
+// kv_read_rows (read_rows.cu)
+struct ReadParams {
+  int batch, h_kv, head_dim, cache_dtype, paged;
+  const void* k_cache;
+  const void* v_cache;
+  const void* k_sz;
+  const void* v_sz;
+  long long capacity;  // contiguous: rows of a (sequence, kv head)
+  long long limit;     // tokens a sequence can hold
+  int page_size, num_pages, max_pages;
+  const int32_t* block_table;
+  const int32_t* start;     // [B] first row, or null: 0
+  const int32_t* num_rows;  // [B] or null: n_rows each
+  int n_rows;
+  void* k_out;  // [B, h_kv, n_rows, head_dim]
+  void* v_out;
+  int out_dtype;
+  int32_t* err;
+};
+
+// Attention over a 4-bit cache (attn_u4.cu): blocks take equal runs of the
+// tiles of all (sequence, kv head, block of query rows) units.
+constexpr int kU4Tile = 64;  // tokens per tile
+struct U4Params {
+  int batch, h_q, h_kv, head_dim, group, n_new, rows;  // rows = group * n_new query rows of a kv head
+  int row_blocks;  // blocks of query rows a kv head is cut into
+  int paged, page_size, num_pages, max_pages;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const uint32_t* k_sm;  // (scale, minimum) of each row, bf16 pair
+  const uint32_t* v_sm;
+  long long capacity;  // contiguous: rows of a (sequence, kv head)
+  const int32_t* block_table;
+  int max_seq_len;
+  const float* q_rot;  // [B, n_new, H_q, d]
+  const int32_t* seq_lens;
+  float scale;
+  int window;
+  void* out;
+  int out_dtype;
+  float* lse_out;
+  int whole;         // 1: one block for each unit, no workspace; 0: equal runs
+  int min_tiles;     // a run is at least this long
+  int32_t* arrived;  // [blocks] zero: blocks that have left a partial of the unit that starts in block c
+  float* part;       // [2 blocks] partial results
+  int32_t* err;
+  int early;  // 1: the preceding launch appends the last n_new rows: wait for it before reading them or q_rot
+  unsigned long long wait_ns;
 };
 
 struct DecodeParams {
@@ -189,6 +269,23 @@ cudaError_t launch_decode_u8(const DecodeParams& p, const CUtensorMap* maps, cud
 // uint8 kernel (4 or 2), or 0 when it does not apply. Its maps box `hg` heads.
 int decode_u8_heads_group(const DecodeParams& p);
 cudaError_t launch_decode_u8_heads(const DecodeParams& p, int hg, const CUtensorMap* maps, cudaStream_t stream);
+
+cudaError_t launch_append_norm(const NormAppendParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_read_rows(const ReadParams& p, cudaStream_t stream);
+
+// Attention over a 4-bit cache. rows: query rows a block serves; ctas_per_sm:
+// resident blocks per SM.
+struct U4Shape {
+  int rows;
+  int ctas_per_sm;
+};
+U4Shape u4_shape(int head_dim, int rows);
+// floats of one partial result: each row's sums, maximum (log2 domain) and sum
+inline size_t u4_part_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
+// ctas: blocks of a launch with p.whole == 0. clear: the counters are cleared by
+// a launch of its own first (else the append launch has done it). tmap_v: V codes
+// in boxes of min(kU4Tile, page_size) rows, swizzled over the row's bytes.
+cudaError_t launch_attn_u4(const U4Params& p, const CUtensorMap& tmap_v, int ctas, bool clear, cudaStream_t stream);
 
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
 

@@ -50,6 +50,16 @@ from .tree import (
     tree_rotate,
     verify_tree,
 )
+from .fourbit import (
+    attention_values,
+    bf16_bits,
+    bf16_from_bits,
+    dequantize_u4,
+    norm_rope,
+    pack_u4,
+    quantize_u4,
+    unpack_u4,
+)
 from .accounting import (
     expected_tokens_per_verify,
     kv_bytes_per_token,

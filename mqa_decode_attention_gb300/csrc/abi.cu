@@ -201,7 +201,13 @@ int read_span(const mqa_kv_layout* L, int max_len, int n_new = 1) {
 // partial-output traffic and a second wave), and 4096-token chunks balance a
 // paged batch of lengths spread over [128, 16384].
 int choose_splits(const mqa_kv_layout* L, int max_len_in, int variant, int n_new = 1) {
-  if (L->cache_dtype == MQA_U4) return 2;  // equal runs
+  if (L->cache_dtype == MQA_U4) {
+    // equal runs, but for contiguous caches with units for more than half of the blocks: a block for each then loses less
+    // by its unequal load than the runs by their merging (256 units of 4096 tokens 34 us, in runs 41; the lengths of a paged
+    // batch are taken as unequal)
+    const U4Plan c = u4_plan(L, n_new);
+    return !L->paged && 2ll * L->batch * L->h_kv * c.row_blocks > c.ctas ? 1 : 2;
+  }
   const int max_len = read_span(L, max_len_in);
   int dev = 0;
   cudaGetDevice(&dev);

@@ -49,7 +49,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 
 template <int D, int NT, int STAGES>
 struct Cfg {
-  static constexpr int kMt = NT == 1 ? 4 : 2;      // tiles of 16 tokens whose scores are held at a time
+  static constexpr int kMt = NT == 1 ? 4 : NT == 2 ? 2 : 1;      // tiles of 16 tokens whose scores are held at a time
   static constexpr int kCode = D / 2;              // bytes of a row's codes
   static constexpr int kTileCodes = kU4Tile * kCode;
   static constexpr int kStage = 2 * kTileCodes;    // V codes (swizzled), K codes
@@ -57,33 +57,51 @@ struct Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kM = D / 16;   // 16-row tiles of O^T; also the k16 steps of q . c
   static constexpr int kPairRing = kWarps * STAGES * kStage;
-  static constexpr bool kQreg = NT <= 2;  // q as operands: in registers, else [k16 step][pair of n tiles][lane][2] in shared memory
+  // q as operands: NT <= 2 in registers, formed by each warp from the rows in shared memory (a lane's quarter row a slot
+  // of 16 bytes more, so that 8 lanes read different banks); else [k16 step][pair of n tiles][lane][2], by all warps
+  static constexpr bool kQreg = NT <= 2;
+  static constexpr int kSlot = D + 16;
   static constexpr int kQ = kPairRing + kWarps * STAGES * kPairs;
-  static constexpr int kQsum = kQ + (kQreg ? 0 : kM * NT * 32 * 8);     // [rows] (sum of q, factor)
-  // parts of a unit that warps leave: O in a stage of their own ring (NT <= 2), else in one place; maxima and sums
+  static constexpr int kQsum = kQ + (kQreg ? NT * 32 * kSlot : kM * NT * 32 * 8);     // [rows] (sum of q, factor)
+  // parts of a unit that warps leave: O in a stage of their own ring (NT <= 2), else in one place; maxima and sums behind
+  // it (NT = 1) or in places of their own
   static constexpr int kPart = kM * NT * 32 * 16, kPartMl = 2 * NT * 32 * 8;
   static constexpr int kMerge = kQsum + (kQreg ? 0 : kRows * 8);
   static constexpr int kMl = kMerge + (kQreg ? 0 : kPart);
-  static constexpr int kBar = kMl + (kQreg ? kWarps : 1) * kPartMl;     // [warps][stages], then left [warps] and taken [warps]
-  static constexpr int kFlag = kBar + kWarps * (STAGES + 2) * 8;
+  // .. of the run's last unit: in the pairs' ring
+  static constexpr int kEnd = NT == 4 ? kMl + kPartMl : kPairRing, kEndStep = NT == 4 ? kPartMl : STAGES * kPairs;
+  static constexpr int kBar = NT == 1 ? kMl : NT == 2 ? kMl + kWarps * STAGES * kPartMl : kMl + (1 + kWarps) * kPartMl;
+  static_assert(NT == 4 || kPartMl <= kEndStep, "maxima and sums fit the pairs' ring");
+  // barriers: a stage is full, a stage is empty [warps][stages]; q has come, q has been read; the chain [warps] and its place
+  static constexpr int kFlag = kBar + (2 * kWarps * STAGES + 2 + kWarps + 1) * 8;
+  static_assert(NT != 1 || kPart + kPartMl <= kStage, "a part fits a stage");
   static_assert(!kQreg || kPart <= kStage, "a part fits a stage");
-  static constexpr int kSmem = kFlag + 56 + (2 + kWarps) * 4 * kWarps;
+  static constexpr int kWords = 10 + kWarps * (2 + 1 + kWarps + 1);  // (see flag)
+  static constexpr int kSmem = kFlag + 4 * kWords;
 };
 
 // d += A B, d the pairs of columns of rows r and r + 8
 __device__ __forceinline__ void mma_f16(float2 (&d)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0].x), "+f"(d[0].y), "+f"(d[1].x), "+f"(d[1].y)
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// d = A B
+__device__ __forceinline__ void mma_f16_first(float2 (&d)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0].x), "=f"(d[0].y), "=f"(d[1].x), "=f"(d[1].y)
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // an 8 x 8 matrix of 16-bit values across the warp, transposed
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -231,27 +249,33 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   const int units = p.h_kv * p.row_blocks;
-  const uint32_t ring = smem_u32(smem) + warp * STAGES * C::kStage;
-  const uint32_t pair_ring = smem_u32(smem) + C::kPairRing + warp * STAGES * C::kPairs;
-  const uint32_t bars = smem_u32(smem) + C::kBar + warp * STAGES * 8;
-  const uint32_t left = smem_u32(smem) + C::kBar + kWarps * STAGES * 8;  // [w]: warp w has left its part of a unit
-  const uint32_t taken = left + 8 * kWarps;                              // [w]: it has been taken
-  volatile int* where = reinterpret_cast<volatile int*>(smem + C::kFlag) + 10;  // [w]: the stage that holds it
-  // NT <= 2: counts of the parts left and taken instead of barriers: a warp may be any number of units ahead of another's
-  // part, which the parity of a barrier's phase could not tell apart.
-  const uint32_t left_count = smem_u32(smem) + C::kFlag + 56, taken_count = left_count + 4 * kWarps;
-  volatile int* flag = reinterpret_cast<volatile int*>(smem + C::kFlag);  // units to merge at the end, [2]: flag, sequence, unit, base, end
+  // a warp's stages and their barriers
+  auto stage_at = [&](int w, int st) { return (w * STAGES + st) * C::kStage; };
+  auto pairs_at = [&](int w, int st) { return C::kPairRing + (w * STAGES + st) * C::kPairs; };
+  const uint32_t base = smem_u32(smem);
+  auto full = [&](int w, int st) { return base + C::kBar + (w * STAGES + st) * 8; };
+  auto empty = [&](int w, int st) { return base + C::kBar + (kWarps * STAGES + w * STAGES + st) * 8; };
+  const uint32_t q_come = base + C::kBar + 2 * kWarps * STAGES * 8, q_read = q_come + 8;
+  const uint32_t chain = q_read + 8, chain_free = chain + 8 * kWarps;  // NT = 4
+  // words: units to merge at the end [2]: flag, sequence, unit, first and last block; [w][2] the stage of a part that warp w
+  // has left (of its n-th in n % 2); [w] how many it has left; [w][w] .. as far as another warp has come; [w] the stage of its
+  // part of the run's last unit
+  volatile int* flag = reinterpret_cast<volatile int*>(smem + C::kFlag);
+  volatile int* where = flag + 10;
+  // (counts, not a barrier: a warp may be any number of units ahead of another's part, which the parity of a phase could
+  // not tell apart)
+  const uint32_t left_count = base + C::kFlag + 4 * (10 + 2 * kWarps);
+  volatile uint32_t* parts = reinterpret_cast<volatile uint32_t*>(flag + 10 + 3 * kWarps) + kWarps * warp;
 
-  if (lane == 0) {
-    if (warp == 0) prefetch_tensormap(&tmap_v);
-    for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 1);
-    mbar_init(left + 8 * warp, 1);
-    mbar_init(taken + 8 * warp, 1);
-    publish(left_count + 4 * warp, 0);
-    publish(taken_count + 4 * warp, 0);
-    for (int w = 0; w < kWarps; ++w) publish(taken_count + 4 * kWarps * (1 + warp) + 4 * w, 0);
+  const int first_len = !p.whole && lane < p.batch ? p.seq_lens[lane] : 0;
+  for (int i = threadIdx.x; i < C::kWords; i += kThreads) flag[i] = 0;
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmap_v);
+    for (int i = 0; i < 2 * kWarps * STAGES; ++i) mbar_init(base + C::kBar + 8 * i, 1);
+    mbar_init(q_come, 1);
+    mbar_init(q_read, kWarps);
+    for (int w = 0; w <= kWarps; ++w) mbar_init(chain + 8 * w, 1);
     fence_mbar_init();
-    if (warp < 2) flag[5 * warp] = 0;
   }
   __syncthreads();
 
@@ -269,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
   } else {
     // (every warp finds it for itself; 32 sequences at a time, the first 32 kept)
     auto tiles_of = [&](int b) { return b < p.batch ? span_of(p, p.seq_lens[b]).tiles : 0; };
-    const int mine = tiles_of(lane);
+    const int mine = lane < p.batch ? span_of(p, first_len).tiles : 0;
     bool bad = lane < p.batch && mine == 0;
     unsigned long long total = __reduce_add_sync(kFull, static_cast<unsigned>(mine));
     for (int b0 = 32; b0 < p.batch; b0 += 32) {
@@ -299,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
       if (past) {
         const int l = __ffs(past) - 1;
         at.b = b0 + l;
-        at.s = span_of(p, p.seq_lens[at.b]);
+        at.s = span_of(p, b0 == 0 ? __shfl_sync(kFull, first_len, l) : p.seq_lens[at.b]);
         const long long off = start - (seen + __shfl_sync(kFull, upto, l) - at.s.tiles) * units;
         at.u = off < 1ll << 31 ? static_cast<unsigned>(off) / at.s.tiles : static_cast<int>(off / at.s.tiles);
         at.base = -static_cast<int>(off - static_cast<long long>(at.u) * at.s.tiles);
@@ -310,311 +334,373 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
   }
   if (run <= 0) return;  // the whole block
 
-  // --------------------------------------------------- filling the ring
-  // Lanes 0-3 copy the V codes (a tensor map, so that they land swizzled), the K
-  // codes, the K pairs and the V pairs of a tile; with pages shorter than a tile
-  // lanes 4-7, .. those of its further pages.
+  // -------------------------------------------------- filling the rings
+  // Tile k of the run goes to warp k % 4, into stage k / 4 % STAGES of its ring. Four lanes, each a copy: V codes (through a tensor map, so that they land swizzled), K codes, K
+  // pairs, V pairs; of a paged pool four lanes for each page.
   Place fill = at;
-  int fill_k = warp, fill_stage = 0, issued = 0;
+  int fill_k = warp, issued = 0;
+  int fill_t = 0, head = 0, page = 0;  // the next tile's first token, its kv head, this lane's page of it
   const int kind = lane & 3;
   const int size = kind < 2 ? C::kCode : 4;  // bytes of a row
-  const int piece = PAGED ? min(p.page_size, kU4Tile) : kU4Tile;  // tokens of a copy
-  const int at_row = (lane >> 2) * piece;                         // the copy's first token in the tile
-  const bool copies = at_row < kU4Tile;
   const unsigned char* from = kind == 1   ? p.k_cache
                               : kind == 2 ? reinterpret_cast<const unsigned char*>(p.k_sm)
                                           : reinterpret_cast<const unsigned char*>(p.v_sm);
-  const uint32_t to = kind < 2 ? ring + (kind == 1 ? C::kTileCodes : 0) + at_row * C::kCode
-                               : pair_ring + (kind - 2) * 4 * kU4Tile + at_row * 4;
-  const int ring_step = kind < 2 ? C::kStage : C::kPairs;
-  int head = 0, fill_t = 0, page = 0;  // first token of the next tile; page of this lane's copy
-  const unsigned char* unit_rows = from;  // contiguous: token 0's row of the unit
-  uint32_t fill_bar = bars, fill_to = to;
-  auto unit_changed = [&]() {
-    head = fill.u / p.row_blocks;
-    if (!PAGED) {
-      head += fill.b * p.h_kv;
-      unit_rows = from + static_cast<long long>(head) * p.capacity * size;
-    }
+  const int piece = PAGED ? min(p.page_size, kU4Tile) : kU4Tile;  // tokens of a copy
+  const int at_row = (lane >> 2) * piece;                         // a lane's first token in the tile
+  auto wanted = [&]() {  // this lane's page has a token that is seen
+    const int t = fill_t + at_row;
+    return at_row < kU4Tile && t < fill.s.len && t + piece > fill.s.lo;
   };
-  auto look = [&]() {  // tile fill_k's place, and its page (looked up one fill ahead)
+  auto look = [&]() {  // tile fill_k's place, and its pages (looked up one fill ahead)
     if (fill_k >= run) return;
-    if (fill_k >= fill.end()) {
-      do fill.next(p, units);
-      while (fill_k >= fill.end());
-      unit_changed();
-    }
+    while (fill_k >= fill.end()) fill.next(p, units);
+    head = fill.u / p.row_blocks;
+    if (!PAGED) head += fill.b * p.h_kv;
     fill_t = (fill.s.first + fill_k - fill.base) * kU4Tile;
+    if (PAGED) page = wanted() ? p.block_table[static_cast<long long>(fill.b) * p.max_pages + (fill_t + at_row) / p.page_size] : -1;
+  };
+  auto fill_next = [&](int w, int st) {  // tile fill_k < run; the stage is empty
+    const uint32_t bar = full(w, st);
+    const uint32_t dst = base + at_row * size +
+                         (kind < 2 ? stage_at(w, st) + (kind == 1 ? C::kTileCodes : 0) : pairs_at(w, st) + (kind == 3 ? 4 * kU4Tile : 0));
+    // (a part of a unit may have been written and read there by threads, the tile comes by the async proxy)
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (PAGED) {
-      const int t = fill_t + at_row;
-      page = -1;
-      if (copies && t < fill.s.len && t + piece > fill.s.lo)
-        page = p.block_table[static_cast<long long>(fill.b) * p.max_pages + t / p.page_size];
-    }
-  };
-  unit_changed();
-  look();
-  // row r of n tile n of a unit's query rows, quarter c of its dims
-  auto load_q = [&](const Place& u, int n, float (&q)[D / 4]) {
-    const int j = u.u / p.row_blocks, ridx = (u.u - j * p.row_blocks) * C::kRows + 8 * n + r, tok = ridx / p.group;
-    if (ridx < p.rows) {
-      const float4* src = reinterpret_cast<const float4*>(
-          p.q_rot + ((static_cast<long long>(u.b) * p.n_new + tok) * p.h_q + j * p.group + ridx - tok * p.group) * D + c * (D / 4));
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const float4 v = src[i];
-        q[4 * i] = v.x, q[4 * i + 1] = v.y, q[4 * i + 2] = v.z, q[4 * i + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) q[i] = 0.f;
-    }
-  };
-  // The rows of the unit after, into the L2 cache: a load from memory would wait behind the tiles under way.
-  auto prefetch_q = [&](Place u) {
-    if (warp != kWarps - 1 || u.end() >= run) return;
-    u.next(p, units);
-    const int j = u.u / p.row_blocks;
-#pragma unroll
-    for (int i = lane; i < C::kRows * (D / 32); i += 32) {
-      const int ridx = (u.u - j * p.row_blocks) * C::kRows + i / (D / 32), tok = ridx / p.group;
-      if (ridx < p.rows)
-        prefetch_l2(p.q_rot + ((static_cast<long long>(u.b) * p.n_new + tok) * p.h_q + j * p.group + ridx - tok * p.group) * D + i % (D / 32) * 32);
-    }
-  };
-  // The first unit's q is asked for before the first tiles: behind them it would wait until they have all come (31 MB
-  // from all blocks, 5 us). When the append launch still forms it, one tile goes ahead.
-  float q[C::kQreg ? NT : 1][D / 4];
-  if (!p.early) {
-#pragma unroll
-    for (int n = 0; n < (C::kQreg ? NT : 1); ++n) load_q(at, C::kQreg ? n : warp, q[n]);
-    prefetch_q(at);
-  }
-  auto fill_next = [&]() {  // fill_k < run
-    if (PAGED) {
-      const int t = fill_t + at_row;
-      const bool want = copies && t < fill.s.len && t + piece > fill.s.lo;
-      const bool copy = want && page >= 0 && page < p.num_pages;
-      if (want && !copy && kind == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_PAGE_RANGE));
-      const int parts = __popc(__ballot_sync(kFull, copy)) / 4;
-      if (lane == 0) mbar_arrive_expect_tx(fill_bar, parts * piece * (2 * C::kCode + 8));
+      const bool copy = page >= 0 && page < p.num_pages;
+      if (!copy && kind == 0 && wanted()) atomicOr(p.err, static_cast<int>(MQA_DEVERR_PAGE_RANGE));
+      const int copies = __popc(__ballot_sync(kFull, copy)) / 4;
+      if (lane == 0) mbar_arrive_expect_tx(bar, copies * piece * (2 * C::kCode + 8));
       __syncwarp();
       if (copy) {
-        const int in_page = t & (p.page_size - 1);
+        const int in_page = (fill_t + at_row) & (p.page_size - 1);
         if (kind == 0)
-          tma_load_4d(fill_to, &tmap_v, 0, in_page, head, page, fill_bar);
+          tma_load_4d(dst, &tmap_v, 0, in_page, head, page, bar);
         else
-          bulk_g2s(fill_to, from + ((static_cast<long long>(page) * p.h_kv + head) * p.page_size + in_page) * size, piece * size, fill_bar);
+          bulk_g2s(dst, from + ((static_cast<long long>(page) * p.h_kv + head) * p.page_size + in_page) * size, piece * size, bar);
       }
     } else {
       // (the capacity is a multiple of 4 rows: copies of 16 bytes; the tensor map's are whole tiles)
       const int n = min(kU4Tile, (fill.s.len - fill_t + 3) & ~3);
       if (lane == 0) {
-        mbar_arrive_expect_tx(fill_bar, kU4Tile * C::kCode + n * (C::kCode + 8));
-        tma_load_3d(fill_to, &tmap_v, 0, fill_t, head, fill_bar);
+        mbar_arrive_expect_tx(bar, kU4Tile * C::kCode + n * (C::kCode + 8));
+        tma_load_3d(dst, &tmap_v, 0, fill_t, head, bar);
       }
       __syncwarp();
-      if (lane - 1u < 3u) bulk_g2s(fill_to, unit_rows + static_cast<long long>(fill_t) * size, n * size, fill_bar);
+      if (lane - 1u < 3u) bulk_g2s(dst, from + (head * p.capacity + fill_t) * size, n * size, bar);
     }
     ++issued;
-    fill_to += ring_step;
-    fill_bar += 8;
-    if (++fill_stage == STAGES) fill_stage = 0, fill_bar = bars, fill_to = to;
     fill_k += kWarps;
-    look();
+    if (!PAGED && fill_k < min(run, fill.end()))
+      fill_t += kWarps * kU4Tile;
+    else
+      look();
   };
-  // before the append has ended only a tile without new rows
-  if (fill_k < run && (!p.early || fill_t + kU4Tile <= fill.s.len - p.n_new)) fill_next();
-  grid_dependency_wait();
-  if (p.early) {
+  // A unit's query rows: lane (r, c) has row r of an n tile, quarter c of its dims.
+  auto q_row = [&](const Place& u, int n) -> const float* {  // null past the last row
+    const int j = u.u / p.row_blocks, ridx = (u.u - j * p.row_blocks) * C::kRows + 8 * n + r, tok = ridx / p.group;
+    return ridx < p.rows ? p.q_rot + ((static_cast<long long>(u.b) * p.n_new + tok) * p.h_q + j * p.group + ridx - tok * p.group) * D + c * (D / 4)
+                         : nullptr;
+  };
+  // NT <= 2: copied by one warp, a unit ahead: a load would wait behind the tiles under way
+  auto send_q = [&](const Place& u) {
+    const float* src[NT];
+    uint32_t bytes = 0;
 #pragma unroll
-    for (int n = 0; n < (C::kQreg ? NT : 1); ++n) load_q(at, C::kQreg ? n : warp, q[n]);
-    prefetch_q(at);
+    for (int n = 0; n < NT; ++n) {
+      src[n] = q_row(u, n);
+      bytes += src[n] != nullptr ? D : 0;
+    }
+    bytes = __reduce_add_sync(kFull, bytes);
+    if (lane == 0) mbar_arrive_expect_tx(q_come, bytes);
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (src[n] != nullptr) bulk_g2s(base + C::kQ + (n * 32 + lane) * C::kSlot, src[n], D, q_come);
+  };
+  bool dead = false;  // a wait ran out
+  // before the append has ended only a tile without new rows
+  look();
+  if (p.early && fill_k < run && fill_t + kU4Tile <= fill.s.len - p.n_new) fill_next(warp, 0);
+  grid_dependency_wait();
+  // The first unit's q by loads ahead of the other tiles: behind them it would wait until they have all come (31 MB from
+  // all blocks, 5 us). NT <= 2: warp 0 puts it where the others look for it; else a warp has the rows of its n tile.
+  float4 q0[C::kQreg ? NT : 1][D / 16];
+  if (warp == 0 || !C::kQreg) {
+#pragma unroll
+    for (int n = 0; n < (C::kQreg ? NT : 1); ++n) {
+      const float4* src = reinterpret_cast<const float4*>(q_row(at, C::kQreg ? n : warp));
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) q0[n][i] = src != nullptr ? src[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   }
-  while (issued < STAGES && fill_k < run) fill_next();
+  while (issued < STAGES && fill_k < run) fill_next(warp, issued);
+
+  // q as operands: lane (r, c) forms those of row r, quarter c of the dims, of an n tile. Even dims meet single codes, odd
+  // dims code pairs (even + 16 odd): x = q_odd / 16 and q_even - x, each rounded.
+  auto operands = [&](const float4 (&q4)[D / 16], uint32_t (&h)[C::kM][2], float& total, float& factor) {
+    float q[D / 4];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) q[4 * i] = q4[i].x, q[4 * i + 1] = q4[i].y, q[4 * i + 2] = q4[i].z, q[4 * i + 3] = q4[i].w;
+    uint32_t most = 0;  // bits of the largest finite magnitude
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) {
+      const uint32_t m = __float_as_uint(q[i]) & 0x7fffffffu;
+      most = max(most, m < 0x7f800000u ? m : 0u);
+    }
+    most = __reduce_max_sync(kFull, most);  // (one factor for the 8 rows)
+    const int e = min(max(static_cast<int>(most >> 23) - 127, -80), 127);  // 2^e <= largest < 2^(e + 1)
+    // (two factors: their product may leave the range)
+    const float up0 = pow2((13 - e) / 2), up1 = pow2((13 - e) - (13 - e) / 2);
+    const float sign = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
+    total = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < C::kM; ++ks) {
+      const int d = ks / 2 * 8 + (ks & 1) * 2;  // dims d, d + 1 and d + 4, d + 5
+      __half2 x, y;
+      x.x = __float2half_rn(q[d + 1] * sign * up0 * up1 * 0.0625f);
+      x.y = __float2half_rn(q[d + 5] * sign * up0 * up1 * 0.0625f);
+      const float2 xf = __half22float2(x);
+      y.x = __float2half_rn(q[d] * sign * up0 * up1 - xf.x);
+      y.y = __float2half_rn(q[d + 4] * sign * up0 * up1 - xf.y);
+      const float2 yf = __half22float2(y);
+      total += yf.x + yf.y + 17.f * (xf.x + xf.y);
+      h[ks][0] = *reinterpret_cast<const uint32_t*>(&y);
+      h[ks][1] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    total += __shfl_xor_sync(kFull, total, 1);
+    total += __shfl_xor_sync(kFull, total, 2);
+    factor = fabsf(p.scale) * 1.4426950408889634f * 0x1p24f / up0 / up1;
+    total *= 0x1p-24f * factor;
+  };
+  // NT = 4: each warp forms the operands of an n tile for all
+  auto share_q = [&](const float4 (&q4)[D / 16]) {
+    uint32_t h[C::kM][2];
+    float total, factor;
+    operands(q4, h, total, factor);
+    __syncthreads();  // the unit before has been read
+    float2* rows = reinterpret_cast<float2*>(smem + C::kQsum);
+#pragma unroll
+    for (int ks = 0; ks < C::kM; ++ks)
+      *reinterpret_cast<uint2*>(smem + C::kQ + ((ks * (NT / 2) + warp / 2) * 32 + lane) * 16 + (warp & 1) * 8) = make_uint2(h[ks][0], h[ks][1]);
+    if (c == 0) rows[8 * warp + r] = make_float2(total, factor);
+    __syncthreads();
+  };
+  if constexpr (C::kQreg) {
+    if (warp == 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) reinterpret_cast<float4*>(smem + C::kQ + (n * 32 + lane) * C::kSlot)[i] = q0[n][i];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_come);
+    }
+  } else {
+    static_assert(C::kQreg || NT == kWarps, "each warp forms the operands of one n tile");
+    share_q(q0[0]);
+  }
 
   // ------------------------------------------------------------ the run
   // Columns 2 c, 2 c + 1 of each n tile as pairs. o: rows r (the even dims) and
   // r + 8 (even + 16 odd, until the unit ends). base_sum: sum p (m + 8 s).
   float2 o[NT][C::kM][2];
-  // ref: minus the reference of a column's exponents, 0 at first; over: what a score may pass it by before it is followed
-  // (-inf before the first score).
-  float2 ref[NT], over[NT], sum[NT], base_sum[NT];
+  // ref: minus the reference of a column's exponents, -0 before its first score (and never -0 after); over: what a score may
+  // pass it by before it is followed (-inf while a column of the lane has had none).
+  float2 ref[NT], sum[NT], base_sum[NT];
+  float over;
+  constexpr float kNone = -0.f;
+  auto none = [](float x) { return __float_as_uint(x) == 0x80000000u; };
   // Sum of the operands p s, by the tensor cores: 8 times it is taken from o every few tiles, which makes the codes -8 to 7.
   // (Else o grows with the number of tokens while its sum with base_sum does not, and the rounding of the accumulators shows.)
-  float2 csum[NT][2];
+  // NT = 4: of the lane's own tokens, before they are rounded, by additions (the registers of [1], which nothing needs, are
+  // short there; the difference is of the size of the rounding).
+  constexpr bool kSumTc = NT <= 2;
+  float2 csum[NT][kSumTc ? 2 : 1];
   int consumed = 0, stage = 0, k = warp;
   uint32_t phase = 0;
-  bool dead = false;  // a wait ran out
-  // [w]: parts that warp w has left, as far as this warp has come
-  volatile uint32_t* parts = reinterpret_cast<volatile uint32_t*>(smem + C::kFlag + 56 + 2 * 4 * kWarps) + kWarps * warp;
-  bool owed = false;        // a stage holds this warp's part, or will, and could not be filled
-  uint32_t own_parts = 0;   // parts that this warp has left
-  bool part_out = false;    // this warp has left a part and not heard that it was taken
-  auto fill_owed = [&]() {  // (the part was written and read by threads, the tile comes by the async proxy)
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    owed = part_out = false;
-    fill_next();
-  };
+  uint32_t own_parts = 0;  // parts that this warp has left
+  // a warp that fills its own ring: stages read and not filled again; the next unit's q has been sent for, units whose q has been
+  int free_stages = 0;
+  bool q_sent = false;
+  uint32_t q_count = 1;
   // ldmatrix rows of V: matrices (tokens 0-7, 8-15) x two 16-byte chunks of the rows
   uint32_t v_row[D / 64];
 #pragma unroll
   for (int q = 0; q < D / 64; ++q) {
     const int tok = (lane & 7) + (lane & 8), chunk = 2 * q + (lane >> 4);
-    v_row[q] = ring + tok * C::kCode + ((chunk ^ (D == 128 ? (lane & 7) >> 1 : (lane & 7) >> 2)) << 4);
+    v_row[q] = base + stage_at(warp, 0) + tok * C::kCode + ((chunk ^ (D == 128 ? (lane & 7) >> 1 : (lane & 7) >> 2)) << 4);
   }
+  // Tells the other blocks of the first unit's part that this warp has written, and finds whether it was the unit's last
+  // (flag[0]: 0 nothing written, 1 + warp written, 5 told, -1 all parts are there) -- some tiles after it has been written:
+  // a fence right behind it waits for memory that is busy with tiles (7 us here).
+  int tell_at = -1;  // when so many tiles have been read
+  auto tell = [&]() {
+    if (flag[0] != 1 + warp) return;
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) {
+      const bool all = atomicAdd(p.arrived + flag[3], 1) == flag[4] - flag[3];
+      __threadfence();
+      flag[0] = all ? -1 : 5;
+    }
+    __syncwarp();
+  };
   const float2 zero2 = make_float2(0.f, 0.f);
   auto centre = [&]() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float2 even = mul2(csum[n][0], make_float2(-8.f * 0x1p-24f, -8.f * 0x1p-24f));
-      const float2 both = mul2(csum[n][0], make_float2(-136.f * 0x1p-24f, -136.f * 0x1p-24f));
+      float2 total = csum[n][0];
+      if constexpr (!kSumTc) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          total.x += __shfl_xor_sync(kFull, total.x, off);
+          total.y += __shfl_xor_sync(kFull, total.y, off);
+        }
+      }
+      const float2 even = mul2(total, make_float2(-8.f * 0x1p-24f, -8.f * 0x1p-24f));
+      const float2 both = mul2(total, make_float2(-136.f * 0x1p-24f, -136.f * 0x1p-24f));
 #pragma unroll
       for (int i = 0; i < C::kM; ++i) {
         o[n][i][0] = add2(o[n][i][0], even);
         o[n][i][1] = add2(o[n][i][1], both);
       }
-      csum[n][0] = csum[n][1] = zero2;
+      csum[n][0] = zero2;
+      if constexpr (kSumTc) csum[n][1] = zero2;
     }
   };
 
+  float2 top[NT];
+  int j, row0;  // kv head and first row of the unit
   for (uint32_t seg = 0;; ++seg) {
     const int k1 = min(run, at.end());
-    const int j = at.u / p.row_blocks, row0 = (at.u - j * p.row_blocks) * C::kRows;
+    j = at.u / p.row_blocks, row0 = (at.u - j * p.row_blocks) * C::kRows;
     const int len = at.s.len;
-    // ---- q as operands: lane (r, c) forms those of row r, quarter c of the dims, of an n tile. Even dims meet single
-    // codes, odd dims code pairs (even + 16 odd): x = q_odd / 16 and q_even - x, each rounded.
     uint32_t qf[C::kQreg ? NT : 1][C::kM][2];
-    float2 qs[NT];  // sum(q), and
-    float f[NT];    // the factor of the scores, times which qs is
-    auto operands = [&](const float (&q)[D / 4], uint32_t (&h)[C::kM][2], float& total, float& factor) {
-      uint32_t most = 0;  // bits of the largest finite magnitude
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) {
-        const uint32_t m = __float_as_uint(q[i]) & 0x7fffffffu;
-        most = max(most, m < 0x7f800000u ? m : 0u);
-      }
-      most = __reduce_max_sync(kFull, most);  // (one factor for the 8 rows)
-      const int e = min(max(static_cast<int>(most >> 23) - 127, -80), 127);  // 2^e <= largest < 2^(e + 1)
-      // (two factors: their product may leave the range)
-      const float up0 = pow2((13 - e) / 2), up1 = pow2((13 - e) - (13 - e) / 2);
-      const float sign = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
-      total = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < C::kM; ++ks) {
-        const int d = ks / 2 * 8 + (ks & 1) * 2;  // dims d, d + 1 and d + 4, d + 5
-        __half2 x, y;
-        x.x = __float2half_rn(q[d + 1] * sign * up0 * up1 * 0.0625f);
-        x.y = __float2half_rn(q[d + 5] * sign * up0 * up1 * 0.0625f);
-        const float2 xf = __half22float2(x);
-        y.x = __float2half_rn(q[d] * sign * up0 * up1 - xf.x);
-        y.y = __float2half_rn(q[d + 4] * sign * up0 * up1 - xf.y);
-        const float2 yf = __half22float2(y);
-        total += yf.x + yf.y + 17.f * (xf.x + xf.y);
-        h[ks][0] = *reinterpret_cast<const uint32_t*>(&y);
-        h[ks][1] = *reinterpret_cast<const uint32_t*>(&x);
-      }
-      total += __shfl_xor_sync(kFull, total, 1);
-      total += __shfl_xor_sync(kFull, total, 2);
-      factor = fabsf(p.scale) * 1.4426950408889634f * 0x1p24f / up0 / up1;
-      total *= 0x1p-24f * factor;
-    };
+    float2 qs[C::kQreg ? NT : 1];  // sum(q), and
+    float f[C::kQreg ? NT : 1];    // the factor of the scores, times which qs is (NT = 4: read where they are used)
     if constexpr (C::kQreg) {
+      if (!dead) dead = !__all_sync(kFull, mbar_wait(q_come, seg & 1, p.wait_ns));
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        float4 q4[D / 16];
+        const bool live = q_row(at, n) != nullptr;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          q4[i] = live ? reinterpret_cast<const float4*>(smem + C::kQ + (n * 32 + lane) * C::kSlot)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
         float total, factor;
-        operands(q[n], qf[n], total, factor);
+        operands(q4, qf[n], total, factor);
         qs[n] = make_float2(__shfl_sync(kFull, total, 8 * c), __shfl_sync(kFull, total, 8 * c + 4));
         f[n] = factor;
       }
-    } else {
-      static_assert(C::kQreg || NT == kWarps, "each warp forms the operands of one n tile");
-      float total, factor;
-      operands(q[0], qf[0], total, factor);
-      __syncthreads();  // the unit before has been read
-      float2* rows = reinterpret_cast<float2*>(smem + C::kQsum);
-#pragma unroll
-      for (int ks = 0; ks < C::kM; ++ks)
-        *reinterpret_cast<uint2*>(smem + C::kQ + ((ks * (NT / 2) + warp / 2) * 32 + lane) * 16 + (warp & 1) * 8) = make_uint2(qf[0][ks][0], qf[0][ks][1]);
-      if (c == 0) rows[8 * warp + r] = make_float2(total, factor);
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float2 a = rows[8 * n + 2 * c], b = rows[8 * n + 2 * c + 1];
-        qs[n] = make_float2(a.x, b.x);
-        f[n] = a.y;
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_read);
+      q_sent = k1 >= run;  // (nothing to send)
     }
+    auto send_next_q = [&]() {  // warp 0, when every warp has read this unit's
+      Place u = at;
+      u.next(p, units);
+      if (seg == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the first unit's was written by threads)
+      send_q(u);
+      q_sent = true;
+      ++q_count;
+    };
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      ref[n] = zero2;
-      over[n] = make_float2(-INFINITY, -INFINITY);
-      sum[n] = base_sum[n] = csum[n][0] = csum[n][1] = zero2;
+      ref[n] = make_float2(kNone, kNone);
+      sum[n] = base_sum[n] = csum[n][0] = zero2;
+      if constexpr (kSumTc) csum[n][1] = zero2;
 #pragma unroll
       for (int i = 0; i < C::kM; ++i) o[n][i][0] = o[n][i][1] = zero2;
     }
+    over = -INFINITY;
     int vexp = -100;  // every V scale so far is below 2^vexp = vlim; vf = 2^(kBoost - vexp)
     float vlim = pow2(-100), vf = pow2(kBoost + 100);
+    if (!C::kQreg && k1 < run) {  // the next unit's rows of q into the L2 cache
+      Place u = at;
+      u.next(p, units);
+      const float* row = q_row(u, warp);
+      if (row != nullptr) prefetch_l2(row);
+    }
     // rows of this block: tokens first_tok .. last_tok of the new ones
     const int first_tok = row0 / p.group, last_tok = (min(row0 + C::kRows, p.rows) - 1) / p.group;
     const int full_to = len - p.n_new + first_tok + 1;  // every row sees the tokens before, from full_from
     const int full_from = p.window > 0 ? max(0, len - p.n_new + last_tok + 1 - p.window) : 0;
 
-    if constexpr (C::kQreg) {
-      if (owed && !dead && __all_sync(kFull, reached(taken_count + 4 * warp, own_parts))) fill_owed();
-    }
     // NT <= 2: the warp with the unit's last tile of this run takes the others' parts
     const int k0 = max(at.base, 0);
     const int merger = C::kQreg ? (k1 - 1) % kWarps : 0;
     for (; k < k1; k += kWarps) {
-      if (!dead && !__all_sync(kFull, mbar_test(bars + 8 * stage, phase)))
-        dead = !__all_sync(kFull, mbar_wait(bars + 8 * stage, phase, p.wait_ns));
+      {
+        if (C::kQreg && warp == 0 && !q_sent && __all_sync(kFull, mbar_test(q_read, seg & 1))) send_next_q();
+        // a stage that holds this warp's part is empty when the part has been taken; with no tile left to go on with, that
+        // is waited for
+        while (free_stages > 0 && fill_k < run && !dead) {
+          const int st = issued % STAGES;
+          const uint32_t parity = (issued / STAGES - 1) & 1;
+          if (!__all_sync(kFull, mbar_test(empty(warp, st), parity))) {
+            if (consumed < issued) break;
+            dead = !__all_sync(kFull, mbar_wait(empty(warp, st), parity, p.wait_ns));
+            if (dead) break;
+          }
+          fill_next(warp, st);
+          --free_stages;
+        }
+      }
+      if (!dead && !__all_sync(kFull, mbar_test(full(warp, stage), phase)))
+        dead = !__all_sync(kFull, mbar_wait(full(warp, stage), phase, p.wait_ns));
       if (dead) continue;
-      const unsigned char* keys = smem + (warp * STAGES + stage) * C::kStage + C::kTileCodes;
-      const unsigned char* pairs = smem + C::kPairRing + (warp * STAGES + stage) * C::kPairs;
+      const unsigned char* keys = smem + stage_at(warp, stage) + C::kTileCodes;
+      const unsigned char* pairs = smem + pairs_at(warp, stage);
       const int t0 = (at.s.first + k - at.base) * kU4Tile;
       const bool edge = t0 < full_from || t0 + kU4Tile > full_to;
-#pragma unroll 1
+#pragma unroll(NT == 4 ? 1 : 4)
       for (int sub = 0; sub < 4 / C::kMt; ++sub) {
         const int tok0 = 16 * C::kMt * sub + r;  // a lane's tokens: tok0 + 16 mt + 8 h
         // ---- S^T: [tile of 16 tokens][n tile], rows r, r + 8
         float2 s[C::kMt][NT][2];
+        // (a step of every tile after the other: the products of a tile wait for each other)
+        uint32_t kw[C::kMt][2][D / 32];
 #pragma unroll
-        for (int mt = 0; mt < C::kMt; ++mt) {
-          uint32_t kw[2][D / 32];
+        for (int mt = 0; mt < C::kMt; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const unsigned char* src = keys + (tok0 + 16 * mt + 8 * h) * C::kCode + c * (D / 8);
             if constexpr (D == 128) {
               const uint4 v = *reinterpret_cast<const uint4*>(src);
-              kw[h][0] = v.x, kw[h][1] = v.y, kw[h][2] = v.z, kw[h][3] = v.w;
+              kw[mt][h][0] = v.x, kw[mt][h][1] = v.y, kw[mt][h][2] = v.z, kw[mt][h][3] = v.w;
             } else {
               const uint2 v = *reinterpret_cast<const uint2*>(src);
-              kw[h][0] = v.x, kw[h][1] = v.y;
+              kw[mt][h][0] = v.x, kw[mt][h][1] = v.y;
             }
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) s[mt][n][0] = s[mt][n][1] = zero2;
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t a[C::kMt][2][2], b[C::kMt][2][2];  // [k16 step][row]
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            uint32_t a[2][2], b[2][2];  // [k16 step][row]
-            split_codes(kw[0][w], a[0][0], b[0][0], a[1][0], b[1][0]);
-            split_codes(kw[1][w], a[0][1], b[0][1], a[1][1], b[1][1]);
+          for (int mt = 0; mt < C::kMt; ++mt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int ks = 2 * w + i;
+            for (int h = 0; h < 2; ++h) split_codes(kw[mt][h][w], a[mt][0][h], b[mt][0][h], a[mt][1][h], b[mt][1][h]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int ks = 2 * w + i;
+            uint32_t qv[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
               if constexpr (C::kQreg) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(s[mt][n], a[i][0], a[i][1], b[i][0], b[i][1], qf[n][ks][0], qf[n][ks][1]);
-              } else {
-#pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                  const uint4 v = *reinterpret_cast<const uint4*>(smem + C::kQ + ((ks * (NT / 2) + n / 2) * 32 + lane) * 16);
-                  mma_f16(s[mt][n], a[i][0], a[i][1], b[i][0], b[i][1], v.x, v.y);
-                  mma_f16(s[mt][n + 1], a[i][0], a[i][1], b[i][0], b[i][1], v.z, v.w);
-                }
+                qv[n][0] = qf[n][ks][0], qv[n][1] = qf[n][ks][1];
+              } else if (n % 2 == 0) {
+                const uint4 v = *reinterpret_cast<const uint4*>(smem + C::kQ + ((ks * (NT / 2) + n / 2) * 32 + lane) * 16);
+                qv[n][0] = v.x, qv[n][1] = v.y, qv[n + 1][0] = v.z, qv[n + 1][1] = v.w;
               }
             }
+#pragma unroll
+            for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                if (ks == 0)
+                  mma_f16_first(s[mt][n], a[mt][i][0], a[mt][i][1], b[mt][i][0], b[mt][i][1], qv[n][0], qv[n][1]);
+                else
+                  mma_f16(s[mt][n], a[mt][i][0], a[mt][i][1], b[mt][i][0], b[mt][i][1], qv[n][0], qv[n][1]);
+              }
           }
         }
         // ---- arguments of 2^x, the V pairs, and whether a maximum moves
@@ -629,10 +715,18 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
             const float ks = u4_scale(kp), km = u4_min(kp);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              const float k_f = ks * f[n];
+              float2 qn;
+              float fn;
+              if constexpr (C::kQreg) {
+                qn = qs[n], fn = f[n];
+              } else {
+                const float4 v = reinterpret_cast<const float4*>(smem + C::kQsum)[4 * n + c];
+                qn = make_float2(v.x, v.z), fn = v.y;
+              }
+              const float k_f = ks * fn;
               float2& x = s[mt][n][h];
-              x.x = fmaf(x.x, k_f, fmaf(km, qs[n].x, ref[n].x));
-              x.y = fmaf(x.y, k_f, fmaf(km, qs[n].y, ref[n].y));
+              x.x = fmaf(x.x, k_f, fmaf(km, qn.x, ref[n].x));
+              x.y = fmaf(x.y, k_f, fmaf(km, qn.y, ref[n].y));
             }
           }
         if (edge) {
@@ -674,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
             most[n].x = max3(most[n].x, s[mt][n][0].x, s[mt][n][1].x);
             most[n].y = max3(most[n].y, s[mt][n][0].y, s[mt][n][1].y);
           }
-          moves |= most[n].x > over[n].x || most[n].y > over[n].y;
+          moves |= fmaxf(most[n].x, most[n].y) > over;
         }
         if (__any_sync(kFull, moves)) {
           const uint32_t big = __reduce_max_sync(kFull, vmost < INFINITY ? __float_as_uint(vmost) : 0u);
@@ -683,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
           vexp = e2;
           vlim = __uint_as_float(static_cast<uint32_t>(min(e2 + 127, 255)) << 23);
           vf = pow2(kBoost - vexp);
+          bool all = true;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float2 m = most[n];
@@ -692,13 +787,15 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
               m.y = fmaxf(m.y, __shfl_xor_sync(kFull, m.y, off));
             }
             // the reference goes up by m where that is above 0, or there was none (and m is a score)
-            const float2 up = make_float2(over[n].x == -INFINITY ? (m.x == -INFINITY ? 0.f : m.x) : fmaxf(m.x, 0.f),
-                                          over[n].y == -INFINITY ? (m.y == -INFINITY ? 0.f : m.y) : fmaxf(m.y, 0.f));
-            const float2 by = make_float2(over[n].x == -INFINITY ? 0.f : fast_exp2(-up.x), over[n].y == -INFINITY ? 0.f : fast_exp2(-up.y));
+            const bool none_x = none(ref[n].x), none_y = none(ref[n].y);
+            const float2 up = make_float2(none_x ? (m.x == -INFINITY ? 0.f : m.x) : fmaxf(m.x, 0.f),
+                                          none_y ? (m.y == -INFINITY ? 0.f : m.y) : fmaxf(m.y, 0.f));
+            const float2 by = make_float2(none_x ? 0.f : fast_exp2(-up.x), none_y ? 0.f : fast_exp2(-up.y));
             const float2 scale = make_float2(by.x * down, by.y * down);
-            if (m.x != -INFINITY) over[n].x = kSlack;
-            if (m.y != -INFINITY) over[n].y = kSlack;
-            ref[n] = make_float2(ref[n].x - up.x, ref[n].y - up.y);
+            // (0 - up: +0 for up = 0)
+            if (!none_x || m.x != -INFINITY) ref[n].x = (none_x ? 0.f : ref[n].x) - up.x;
+            if (!none_y || m.y != -INFINITY) ref[n].y = (none_y ? 0.f : ref[n].y) - up.y;
+            all = all && !none(ref[n].x) && !none(ref[n].y);
             sum[n] = mul2(sum[n], by);
             base_sum[n] = mul2(base_sum[n], by);
             csum[n][0] = mul2(csum[n][0], scale);
@@ -712,6 +809,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
 #pragma unroll
               for (int h = 0; h < 2; ++h) s[mt][n][h] = make_float2(s[mt][n][h].x - up.x, s[mt][n][h].y - up.y);
           }
+          over = all ? kSlack : -INFINITY;
         }
         // ---- p, and p s as the operand of O
         uint32_t pb[C::kMt][NT][2];
@@ -727,7 +825,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
               sum[n] = add2(sum[n], pr);
               base_sum[n].x = fmaf(pr.x, vm, base_sum[n].x);
               base_sum[n].y = fmaf(pr.y, vm, base_sum[n].y);
-              pb[mt][n][h] = transpose8(pack_half2(pr.x * v, pr.y * v));
+              const float2 w = make_float2(pr.x * v, pr.y * v);
+              if constexpr (!kSumTc) csum[n][0] = add2(csum[n][0], w);
+              pb[mt][n][h] = transpose8(pack_half2(w.x, w.y));
             }
           }
         // ---- O^T += V^T P^T: a transposed 8 x 8 matrix of 16-bit pieces holds four codes of a token in each half, tokens
@@ -736,7 +836,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
 #pragma unroll
         for (int mt = 0; mt < C::kMt; ++mt) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(csum[n], ones, ones, ones, ones, pb[mt][n][0], pb[mt][n][1]);
+          for (int n = 0; n < NT; ++n)
+            if constexpr (kSumTc) mma_f16(csum[n], ones, ones, ones, ones, pb[mt][n][0], pb[mt][n][1]);
 #pragma unroll
           for (int q = 0; q < D / 64; ++q) {
             uint32_t v[4];  // chunk 2 q: tokens 0-7, 8-15; chunk 2 q + 1
@@ -755,28 +856,24 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
           }
         }
       }
-      __syncwarp();  // the stage has been read
-      if (C::kQreg && owed && !dead) {
-        dead = !__all_sync(kFull, wait_count(taken_count + 4 * warp, own_parts, p.wait_ns));
-        if (!dead) fill_owed();
-      }
-      if (fill_k < run && !dead) {
-        if (C::kQreg && k + kWarps >= k1 && warp != merger)
-          owed = true;  // the part goes into this stage first
-        else
-          fill_next();
-      }
+      __syncwarp();  // the stage has been read; the last of a unit takes this warp's part first
+      if (lane == 0 && !(C::kQreg && warp != merger && k + kWarps >= k1 && k1 < run)) mbar_arrive(empty(warp, stage));
+      ++free_stages;
       if ((++consumed & 1) == 0) centre();
+      if (consumed == tell_at) tell();
       if (++stage == STAGES) stage = 0, phase ^= 1;
+    }
+    if (C::kQreg && warp == 0 && !q_sent) {
+      if (!dead) dead = !__all_sync(kFull, mbar_wait(q_read, seg & 1, p.wait_ns));
+      if (!dead) send_next_q();
     }
 
     // ---------------------------------------------- the end of the unit
     // o in units of V, base_sum in it
     centre();
-    float2 top[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      top[n] = make_float2(over[n].x == -INFINITY ? -INFINITY : -ref[n].x, over[n].y == -INFINITY ? -INFINITY : -ref[n].y);
+      top[n] = make_float2(none(ref[n].x) ? -INFINITY : -ref[n].x, none(ref[n].y) ? -INFINITY : -ref[n].y);
     const float out0 = pow2(min(max(vexp - kBoost, -126), 127)), out1 = 0x1p24f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -795,6 +892,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
                                  fmaf((both.y - even.y) * out0, out1 * 0.0625f, base_sum[n].y));
       }
     }
+    if (k1 >= run) break;
+
+    // ------------------------------------ a unit that ends inside the run
     auto merge = [&](const float2 (&m2)[NT], const float2 (&s2)[NT], auto&& load) {  // another part into this one
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -829,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
       }
     };
     if constexpr (C::kQreg) {
-      // A warp leaves its part in the stage that it has read last and goes on with the next unit; the stage is filled when
+      // A warp leaves its part in the stage that it has read last and goes on with the next unit; the stage is empty when
       // the part has been taken. Warps without a tile of the unit have no part.
       const int later = (merger + 1) % kWarps;  // the others in the order of their tiles
       uint32_t leaving = 0;
@@ -838,23 +938,26 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
         if (w != merger && k1 - 1 - (merger - w + kWarps) % kWarps >= k0) leaving |= 1u << w;
       if (lane < kWarps) parts[lane] += leaving >> lane & 1;
       __syncwarp();
+      auto ml_of = [&](int w, int st) {
+        return smem + (NT == 1 ? stage_at(w, st) + C::kPart : C::kMl + (w * STAGES + st) * C::kPartMl);
+      };
       if (warp == merger) {
         for (int i = 0; i < kWarps - 1; ++i) {
           const int w = (later + i) % kWarps;
           if (!(leaving >> w & 1)) continue;
           const uint32_t n = parts[w];
           if (!dead) dead = !__all_sync(kFull, wait_count(left_count + 4 * w, n, p.wait_ns));
-          if (!dead) take(smem + (w * STAGES + where[w]) * C::kStage, smem + C::kMl + w * C::kPartMl);
+          if (dead) continue;
+          const int st = where[2 * w + (n & 1)];
+          take(smem + stage_at(w, st), ml_of(w, st));
           __syncwarp();
-          if (lane == 0) publish(taken_count + 4 * w, n);
+          if (lane == 0) mbar_arrive(empty(w, st));
         }
-      } else if (leaving >> warp & 1) {
-        const int last_stage = stage == 0 ? STAGES - 1 : stage - 1;
-        if (part_out && !dead) dead = !__all_sync(kFull, wait_count(taken_count + 4 * warp, own_parts, p.wait_ns));
-        part_out = true;
+      } else if ((leaving >> warp & 1) && !dead) {
+        const int st = stage == 0 ? STAGES - 1 : stage - 1;  // the one read last
         ++own_parts;
-        if (!dead) leave(smem + (warp * STAGES + last_stage) * C::kStage, smem + C::kMl + warp * C::kPartMl);
-        if (lane == 0) where[warp] = last_stage;
+        leave(smem + stage_at(warp, st), ml_of(warp, st));
+        if (lane == 0) where[2 * warp + (own_parts & 1)] = st;
         __syncwarp();
         if (lane == 0) publish(left_count + 4 * warp, own_parts);
       }
@@ -862,19 +965,19 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
       // The four warps' parts meet in a chain, warp 3's into warp 2's registers and so on, through one place. A warp that
       // has left its part goes on with the next unit.
       if (warp == kWarps - 1) {
-        if (seg > 0 && !dead) dead = !__all_sync(kFull, mbar_wait(taken, (seg - 1) & 1, p.wait_ns));
+        if (seg > 0 && !dead) dead = !__all_sync(kFull, mbar_wait(chain_free, (seg - 1) & 1, p.wait_ns));
       } else {
-        if (!dead) dead = !__all_sync(kFull, mbar_wait(left + 8 * (warp + 1), seg & 1, p.wait_ns));
+        if (!dead) dead = !__all_sync(kFull, mbar_wait(chain + 8 * (warp + 1), seg & 1, p.wait_ns));
         take(smem + C::kMerge, smem + C::kMl);
       }
       if (warp != 0) leave(smem + C::kMerge, smem + C::kMl);
       __syncwarp();
-      if (lane == 0) mbar_arrive(warp == 0 ? taken : left + 8 * warp);
+      if (lane == 0) mbar_arrive(warp == 0 ? chain_free : chain + 8 * warp);
     }
     if (warp == merger) {
-      if (!p.whole && (at.base < 0 || at.end() > run)) {  // other blocks have parts of this unit
-        const long long first = (start + at.base) / run_len, last = (start + at.end() - 1) / run_len;
-        float* mine = p.part + (2 * blockIdx.x + (at.base < 0 ? 0 : 1)) * static_cast<long long>(C::kRows * (D + 2));
+      if (at.base < 0) {  // other blocks have parts of it
+        const long long first = (start + at.base) / run_len, last = blockIdx.x;
+        float* mine = p.part + 2 * blockIdx.x * static_cast<long long>(C::kRows * (D + 2));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -886,88 +989,141 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
             *reinterpret_cast<float2*>(mine + C::kRows * (D + 1) + 8 * n + 2 * c) = sum[n];
           }
         }
-        // told to the other blocks at the end of the run: a fence waits for memory that is busy with tiles (7 us here)
-        if (lane == 0) {
-          volatile int* todo = flag + (at.base < 0 ? 0 : 5);
-          todo[0] = 1 + warp, todo[1] = at.b, todo[2] = at.u, todo[3] = static_cast<int>(first), todo[4] = static_cast<int>(last);
-        }
+        if (lane == 0) flag[0] = 1 + warp, flag[1] = at.b, flag[2] = at.u, flag[3] = static_cast<int>(first), flag[4] = static_cast<int>(last);
+        __syncwarp();
+        tell_at = consumed + 2;
       } else {
         write_rows(p, at.b, j, row0, top, sum, o, 0);
       }
     }
-    if (k1 >= run) break;
     at.next(p, units);
+    if constexpr (!C::kQreg) {
+      float4 q4[D / 16];
+      const float4* src = reinterpret_cast<const float4*>(q_row(at, warp));
 #pragma unroll
-    for (int n = 0; n < (C::kQreg ? NT : 1); ++n) load_q(at, C::kQreg ? n : warp, q[n]);
-    prefetch_q(at);
+      for (int i = 0; i < D / 16; ++i) q4[i] = src != nullptr ? src[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+      share_q(q4);
+    }
   }
 
-  // The last block to have left its part of a unit merges the unit's parts, in the order of the blocks; every warp takes
-  // a quarter of the dims.
-  if (!p.whole) {
-    for (int which = 0; which < 2; ++which) {
-      volatile int* todo = flag + 5 * which;
-      if (todo[0] != 1 + warp) continue;  // (this warp has written the part)
-      __threadfence();
-      __syncwarp();
-      if (lane != 0) continue;
-      const bool all = atomicAdd(p.arrived + todo[3], 1) == todo[4] - todo[3];
-      __threadfence();
-      todo[0] = all ? -1 : 0;
+  // ------------------------------------------------ the end of the run
+  // Every warp leaves its part of the last unit in its ring; then each has a quarter of the dims, of all four.
+  constexpr int kQuarter = C::kM / kWarps;
+  float2 acc[NT][kQuarter][2];
+  auto clear = [&]() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      top[n] = make_float2(-INFINITY, -INFINITY);
+      sum[n] = zero2;
+#pragma unroll
+      for (int i = 0; i < kQuarter; ++i) acc[n][i][0] = acc[n][i][1] = zero2;
     }
+  };
+  auto add_part = [&](int n, float2 m2, float2 s2, const float4 (&v)[kQuarter]) {
+    float2 wa, wb;
+    weights(top[n], m2, wa, wb);
+    sum[n] = fma2(sum[n], wa, mul2(s2, wb));
+#pragma unroll
+    for (int i = 0; i < kQuarter; ++i) {
+      acc[n][i][0] = fma2(acc[n][i][0], wa, mul2(make_float2(v[i].x, v[i].y), wb));
+      acc[n][i][1] = fma2(acc[n][i][1], wa, mul2(make_float2(v[i].z, v[i].w), wb));
+    }
+  };
+  const int own_stage = C::kQreg ? (stage == 0 ? STAGES - 1 : stage - 1) : 0;  // (NT = 4: the whole ring)
+  const int reads = (consumed + STAGES - 1 - own_stage) / STAGES;                // of that stage
+  if (C::kQreg && reads > 0 && !dead)  // (it may hold the part of a unit before)
+    dead = !__all_sync(kFull, mbar_wait(empty(warp, own_stage), (reads - 1) & 1, p.wait_ns));
+  float4* own = reinterpret_cast<float4*>(smem + stage_at(warp, own_stage));
+  float2* own_ml = reinterpret_cast<float2*>(smem + C::kEnd + warp * C::kEndStep);
+  volatile int* end_stage = flag + 10 + kWarps * (3 + kWarps);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    own_ml[n * 32 + lane] = top[n];
+    own_ml[(NT + n) * 32 + lane] = sum[n];
+#pragma unroll
+    for (int i = 0; i < C::kM; ++i) own[(n * C::kM + i) * 32 + lane] = make_float4(o[n][i][0].x, o[n][i][0].y, o[n][i][1].x, o[n][i][1].y);
+  }
+  if (lane == 0) end_stage[warp] = own_stage;
+  __syncthreads();
+  clear();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float4* src = reinterpret_cast<const float4*>(smem + stage_at(w, end_stage[w]));
+    const float2* ml = reinterpret_cast<const float2*>(smem + C::kEnd + w * C::kEndStep);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float4 v[kQuarter];
+#pragma unroll
+      for (int i = 0; i < kQuarter; ++i) v[i] = src[(n * C::kM + warp * kQuarter + i) * 32 + lane];
+      add_part(n, ml[n * 32 + lane], ml[(NT + n) * 32 + lane], v);
+    }
+  }
+  if (p.whole || (at.base >= 0 && at.end() == run)) {
+    write_rows(p, at.b, j, row0, top, sum, acc, warp * kQuarter);
+  } else {
+    // Other blocks have parts of the unit: this one's is written, and the last block to say so merges them, in the order
+    // of the blocks. The place of a unit that the block did not begin is the first of its two.
+    const int first = static_cast<int>((start + at.base) / run_len), last = static_cast<int>((start + at.end() - 1) / run_len);
+    float* mine = p.part + (2 * blockIdx.x + (at.base < 0 ? 0 : 1)) * static_cast<long long>(C::kRows * (D + 2));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < kQuarter; ++i)
+        reinterpret_cast<float4*>(mine)[(n * C::kM + warp * kQuarter + i) * 32 + lane] =
+            make_float4(acc[n][i][0].x, acc[n][i][0].y, acc[n][i][1].x, acc[n][i][1].y);
+      if (warp == 0 && r == 0) {
+        *reinterpret_cast<float2*>(mine + C::kRows * D + 8 * n + 2 * c) = top[n];
+        *reinterpret_cast<float2*>(mine + C::kRows * (D + 1) + 8 * n + 2 * c) = sum[n];
+      }
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      flag[5] = atomicAdd(p.arrived + first, 1) == last - first ? -1 : 0;
+      flag[6] = at.b, flag[7] = at.u, flag[8] = first, flag[9] = last;
+      __threadfence();
+    }
+  }
+  if (!p.whole) {
+    tell();
     __syncthreads();
     for (int which = 0; which < 2; ++which) {
       volatile int* todo = flag + 5 * which;
-      if (todo[0] == 0) continue;
-      const int b_of = todo[1], u = todo[2], first = todo[3], last = todo[4], j = u / p.row_blocks, row0 = (u - j * p.row_blocks) * C::kRows;
-      constexpr int kPart = C::kM / kWarps;
-      float2 acc[NT][kPart][2], top[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        top[n] = make_float2(-INFINITY, -INFINITY);
-        sum[n] = zero2;
-#pragma unroll
-        for (int i = 0; i < kPart; ++i) acc[n][i][0] = acc[n][i][1] = zero2;
-      }
+      if (todo[0] >= 0) continue;
+      const int u = todo[2], from_block = todo[3], to_block = todo[4], ju = u / p.row_blocks;
       constexpr int kAhead = NT == 1 ? 4 : 2;  // parts whose loads are issued together
-      for (int b0 = first; b0 <= last; b0 += kAhead) {
+      clear();
+      for (int b0 = from_block; b0 <= to_block; b0 += kAhead) {
         float2 m2[kAhead][NT], s2[kAhead][NT];
-        float4 v[kAhead][NT][kPart];
+        float4 v[kAhead][NT][kQuarter];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
-          const int b = min(b0 + a, last);
-          const float* src = p.part + (2 * b + (b == first ? 1 : 0)) * static_cast<long long>(C::kRows * (D + 2));
+          const int b = min(b0 + a, to_block);
+          const float* src = p.part + (2 * b + (b == from_block ? 1 : 0)) * static_cast<long long>(C::kRows * (D + 2));
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             m2[a][n] = __ldcg(reinterpret_cast<const float2*>(src + C::kRows * D + 8 * n + 2 * c));
             s2[a][n] = __ldcg(reinterpret_cast<const float2*>(src + C::kRows * (D + 1) + 8 * n + 2 * c));
 #pragma unroll
-            for (int i = 0; i < kPart; ++i) v[a][n][i] = __ldcg(reinterpret_cast<const float4*>(src) + (n * C::kM + warp * kPart + i) * 32 + lane);
+            for (int i = 0; i < kQuarter; ++i)
+              v[a][n][i] = __ldcg(reinterpret_cast<const float4*>(src) + (n * C::kM + warp * kQuarter + i) * 32 + lane);
           }
         }
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
-          if (b0 + a > last) break;
+          if (b0 + a > to_block) break;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float2 wa, wb;
-            weights(top[n], m2[a][n], wa, wb);
-            sum[n] = fma2(sum[n], wa, mul2(s2[a][n], wb));
-#pragma unroll
-            for (int i = 0; i < kPart; ++i) {
-              acc[n][i][0] = fma2(acc[n][i][0], wa, mul2(make_float2(v[a][n][i].x, v[a][n][i].y), wb));
-              acc[n][i][1] = fma2(acc[n][i][1], wa, mul2(make_float2(v[a][n][i].z, v[a][n][i].w), wb));
-            }
-          }
+          for (int n = 0; n < NT; ++n) add_part(n, m2[a][n], s2[a][n], v[a][n]);
         }
       }
-      write_rows(p, b_of, j, row0, top, sum, acc, warp * kPart);
+      write_rows(p, todo[1], ju, (u - ju * p.row_blocks) * C::kRows, top, sum, acc, warp * kQuarter);
     }
   }
-  if (dead) {
+  if (dead) {  // the copies under way land before the block ends
     if (lane == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_TIMEOUT));
+    if (C::kQreg && warp == 0) mbar_wait(q_come, (q_count - 1) & 1, kWaitLimitNs);
     for (; consumed < issued; ++consumed) {
-      mbar_wait(bars + 8 * stage, phase, kWaitLimitNs);
+      mbar_wait(full(warp, stage), phase, kWaitLimitNs);
       if (++stage == STAGES) stage = 0, phase ^= 1;
     }
   }

@@ -443,3 +443,27 @@ def test_timeout_then_normal_call(m, splits):
     lay.wait_limit_ns = 0
     err, after = call()
     assert err == 0 and torch.equal(before, after)
+
+
+@pytest.mark.parametrize("group", [4, 12, 32])
+def test_units_shorter_than_a_block_has_warps(m, group):
+    """Thousands of units of one to three tiles, so that the warps of a block are several units apart: the same bits on
+    every call, and no wait that runs out."""
+    g = torch.Generator(DEV).manual_seed(81)
+    B, hkv, L = 400, 8, 190
+    codes = [torch.randint(0, 256, (B, hkv, 192, 64), generator=g, dtype=torch.uint8, device=DEV) for _ in "kv"]
+    pairs = [torch.rand(B, hkv, 192, 2, generator=g, device=DEV).to(torch.bfloat16) for _ in "kv"]
+    lay = m.layout_contiguous(codes[0], codes[1], hkv * group, 0, pairs[0], pairs[1], cache_dtype=m.MQA_U4)
+    q, lens = torch.randn(B, hkv * group, 128, generator=g, device=DEV), torch.randint(1, L + 1, (B,), generator=g, dtype=torch.int32, device=DEV)
+    bufs, whole = m.DecodeBuffers.allocate(lay, L), m.DecodeBuffers.allocate(lay, L, num_splits=1)
+    m.gqa_decode_attention(lay, q, lens, L, 0.09, 1, whole.out, whole.lse, err=whole.err)
+    first = None
+    for _ in range(40):
+        m.gqa_decode_attention(lay, q, lens, L, 0.09, 0, bufs.out, bufs.lse, bufs.workspace, err=bufs.err)
+        torch.cuda.synchronize()
+        assert int(bufs.err) == 0 and int(whole.err) == 0
+        first = bufs.out.clone() if first is None else first
+        assert torch.equal(first, bufs.out)
+    # split otherwise the same sums are formed in another order, and the probabilities relative to other maxima: each
+    # result is within 2^-10 of the values (2.5 at most here) and a rounding to bf16
+    assert torch.all((first.float() - whole.out.float()).abs() <= 2 * (16 * 2.0 ** -10 + 2.0 ** -8 * first.float().abs()))

@@ -1244,14 +1244,12 @@ mqa_status step_impl(const mqa_kv_layout* layout, int n_new, const void* q_new, 
   if (out_dtype != MQA_BF16 && out_dtype != MQA_F32) return MQA_ERR_UNSUPPORTED;
   const int v = resolve_variant(layout, variant);
   if (!variant_supports(v, layout->cache_dtype) || !multi_supported(layout, v, n_new)) return MQA_ERR_UNSUPPORTED;
-  {
-    const int req = num_splits == 0 ? choose_splits(layout, max_seq_len, v, n_new) : num_splits;
-    int splits, chunk;
-    split_plan(layout, req, read_span(layout, max_seq_len, n_new), &splits, &chunk);
-    const size_t need = partial_bytes(layout, splits, n_new);
-    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MQA_ERR_WORKSPACE;
-    if (need > 0 && !aligned(workspace, 256)) return MQA_ERR_INVALID_ARG;
-  }
+  const int req = num_splits == 0 ? choose_splits(layout, max_seq_len, v, n_new) : num_splits;
+  int splits, chunk;
+  split_plan(layout, req, read_span(layout, max_seq_len, n_new), &splits, &chunk);
+  const size_t need = partial_bytes(layout, splits, n_new);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MQA_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 256)) return MQA_ERR_INVALID_ARG;
   const mqa_status ca = check_append_args(layout, q_new, k_new, v_new, pos, rope_base, q_rot, err_word);
   if (ca != MQA_OK) return ca;
   if ((n_new == 1 && fusable(layout, v)) || fusable_multi(layout, v, n_new)) {
@@ -1260,8 +1258,8 @@ mqa_status step_impl(const mqa_kv_layout* layout, int n_new, const void* q_new, 
     return attention_impl(layout, q_rot, seq_lens, max_seq_len, scale, num_splits, out, out_dtype, lse_out,
                           workspace, workspace_bytes, variant, err_word, stream, /*early=*/0, &rope, n_new);
   }
-  // (a 4-bit cache: the append clears the attention's counters)
-  const bool runs = layout->cache_dtype == MQA_U4 && num_splits != 1;
+  // (a 4-bit cache in equal runs: the append clears the attention's counters)
+  const bool runs = layout->cache_dtype == MQA_U4 && need > 0;
   const mqa_status a = append_impl(layout, q_new, k_new, v_new, pos, rope_base, q_rot, err_word, stream, n_new, nullptr,
                                    runs ? static_cast<int32_t*>(workspace) : nullptr,
                                    runs ? u4_plan(layout, n_new).ctas : 0);

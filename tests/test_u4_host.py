@@ -59,6 +59,9 @@ def _read(lib, lay, **kw):
     return lib.kv_read_rows(ctypes.byref(lay), a["n"], a["start"], a["rows"], a["k"], a["v"], a["dt"], a["err"], None)
 
 
+PAGED = _layout(paged=1, capacity=0, page_size=16, num_pages=32, max_pages_per_seq=16, block_table=FAKE)
+
+
 @pytest.mark.parametrize("call", [_attend, _step, _norm, _read])
 def test_layout_refusals(lib, call):
     assert call(lib, _layout(head_dim=96)) == NOT
@@ -76,12 +79,13 @@ def test_layout_refusals(lib, call):
 def test_attention_refusals(lib, call):
     for bad in (dict(n=0), dict(n=33), dict(lens=None), dict(most=0), dict(most=257), dict(n=4, most=3), dict(scale=float("nan")),
                 dict(splits=-1), dict(out=None), dict(out=FAKE + 8), dict(lse=FAKE + 2), dict(variant=9), dict(err=None),
-                dict(ws=FAKE + 64)):
+                dict(splits=2, ws=FAKE + 64)):
         assert call(lib, _layout(), **bad) == BAD, bad
     assert call(lib, _layout(), dt=_abi.MQA_U8) == NOT
     assert call(lib, _layout(), variant=_abi.MQA_VARIANT_CUDA_CORE) == NOT
-    assert call(lib, _layout(), ws=None) == WS
-    assert call(lib, _layout(), size=100) == WS
+    for lay, splits in ((_layout(), 2), (PAGED, 0)):  # equal runs, on any device
+        assert call(lib, lay, splits=splits, ws=None) == WS
+        assert call(lib, lay, splits=splits, size=100) == WS
 
 
 def test_other_calls_refuse_four_bits(lib):
@@ -96,14 +100,18 @@ def test_other_calls_refuse_four_bits(lib):
 
 
 def test_queries(lib):
-    p = ctypes.byref(_layout())
-    assert lib.mqa_workspace_size_multi(p, 1, 100, 1, 0) == 0
-    assert lib.mqa_workspace_size_multi(p, 1, 100, 0, 0) == lib.mqa_workspace_size_multi(p, 1, 100, 5, 0) > 0
-    assert lib.mqa_choose_splits_multi(p, 1, 100, 0) == 2
-    assert lib.mqa_choose_splits_multi(p, 1, 300, 0) == -1
-    fused = ctypes.c_int32(7)
-    assert lib.mqa_step_launches(p, 1, 100, 0, 0, ctypes.byref(fused)) == 2 and fused.value == 0
-    assert lib.mqa_step_launches(p, 1, 100, 0, _abi.MQA_VARIANT_CUDA_CORE, None) == -1
+    """One split needs no workspace, equal runs one size whatever their number; the library's choice is one of the two."""
+    for lay in (_layout(), PAGED):
+        p = ctypes.byref(lay)
+        size = [lib.mqa_workspace_size_multi(p, 1, 100, n, 0) for n in (1, 2, 5)]
+        assert size[0] == 0 < size[1] == size[2]
+        choice = lib.mqa_choose_splits_multi(p, 1, 100, 0)
+        assert choice in (1, 2) and lib.mqa_workspace_size_multi(p, 1, 100, 0, 0) == size[choice - 1]
+        assert choice == 2 or not lay.paged
+        assert lib.mqa_choose_splits_multi(p, 1, 300, 0) == -1
+        fused = ctypes.c_int32(7)
+        assert lib.mqa_step_launches(p, 1, 100, 0, 0, ctypes.byref(fused)) == 2 and fused.value == 0
+        assert lib.mqa_step_launches(p, 1, 100, 0, _abi.MQA_VARIANT_CUDA_CORE, None) == -1
 
 
 def _opts(**kw):

@@ -7,18 +7,21 @@
 //
 // A stored key is the 64-bit result rounded once to the type of k_new; a
 // one-byte or 4-bit cache holds that bf16 row encoded. A rounding that falls the
-// other way changes a whole code there, so the key is formed in pairs of floats
-// (a value and what its rounding left, 2^-37 of the pair's length and better)
-// instead of fp64, whose rate on this part is 1/64 of fp32's: sine and cosine
-// from their Taylor series about the nearest multiple of pi / 2 (only the
-// reduction of the angle is fp64: 7 operations for each pair of a token), the
-// sum of squares and its root likewise. A query, which fp32 holds, takes the
-// fp32 part alone.
+// other way changes a whole code there. So the key is formed in fp32 first, with
+// a bound on its error; where a value lies so near a rounding border that this
+// does not settle it (a normal row of 128: 3 in 100 with a norm, 1 without) the
+// row is formed again in pairs of floats (a value and what its rounding left, 2^-37 of the
+// pair's length and better), not in fp64, whose rate on this part is 1/64 of
+// fp32's. The sines and cosines are such pairs, from their Taylor series about
+// the nearest multiple of pi / 2; only the reduction of the angle is fp64. A
+// query, which fp32 holds, takes the fp32 part alone.
 //
-// One warp forms a row, a lane 4 (d = 128) or 2 (d = 64) neighbouring values.
-// A block serves one token: its d / 2 sines and cosines are formed once, then
-// its warps take the heads. What bounds it is the memory: a prompt writes 4
-// bytes for each value of q it reads.
+// A lane holds 8 neighbouring values of a row, so a warp two rows (d = 128) or
+// four (d = 64) at a time: what a row costs once -- its scale, its addresses,
+// the steps of its sums -- is paid by half or a quarter of a warp. Of the query
+// several such groups are requested together. A block serves one token, or four
+// (eight) of a long prompt: their d / 2 sines and cosines are formed once, by
+// all threads, then its warps take the heads, the keys and values first.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -74,16 +77,16 @@ __device__ __forceinline__ Dd horner(double c, Dd z, Dd v) {
 }
 
 // cos and sin of pos * theta. The angle is formed and reduced by the nearest
-// multiple k of pi / 2 in fp64 (three parts of pi / 2, as reduce_two_pi), then
+// multiple k of pi / 2 in fp64 (pi / 2 in two parts, 106 bits), then
 // both series in z = r^2, |r| <= pi / 4: the terms that are below 2^-14 of the
 // result are summed in fp32, the others as pairs (error 2^-37).
 __device__ __forceinline__ void cos_sin(int pos, double theta, Dd* c, Dd* s) {
   const double x = static_cast<double>(pos) * theta;
-  const double k = rint(x * (4.0 * kInvTwoPi));
+  // k = the nearest whole number to 2 x / pi: by adding 1.5 2^52, whose low bits then hold it
+  const double big = fma(x, 4.0 * kInvTwoPi, 0x1.8p52), k = big - 0x1.8p52;
   double r = fma(-k, 0.25 * kTwoPi1, x);
   r = fma(-k, 0.25 * kTwoPi2, r);
-  r = fma(-k, 0.25 * kTwoPi3, r);
-  const int quad = static_cast<int>(static_cast<long long>(k) & 3);
+  const int quad = __double2loint(big) & 3;
   Dd a;
   a.h = static_cast<float>(r);
   a.l = static_cast<float>(r - static_cast<double>(a.h));
@@ -108,32 +111,36 @@ __device__ __forceinline__ void cos_sin(int pos, double theta, Dd* c, Dd* s) {
   *s = {fs * ss.h, fs * ss.l};
 }
 
-__device__ __forceinline__ Dd warp_sum(Dd v) {
+// sum over the L lanes that hold a row
+template <int L>
+__device__ __forceinline__ Dd row_sum(Dd v) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
+  for (int off = L / 2; off > 0; off >>= 1)
     v = add(v, {__shfl_xor_sync(0xffffffffu, v.h, off), __shfl_xor_sync(0xffffffffu, v.l, off)});
   return v;
 }
 
-// 1 / sqrt(mean + eps) of the row whose values the lanes hold, by one Newton
+// 1 / sqrt(mean + eps) of the row of d values that L lanes hold, by one Newton
 // step on the fp32 root: with r0 = (1 + e) / sqrt(h), r0 (1 + (1 - h r0^2) / 2)
 // is within 1.5 e^2. Squares that leave the fp32 range are formed of values
-// scaled by 2^-70.
-template <int N>
-__device__ __forceinline__ Dd inv_rms(const float (&x)[N], int d, float eps) {
-  Dd sum = {0.f, 0.f};
+// scaled by 2^-70. (All lanes of the warp take part.)
+template <int L>
+__device__ __noinline__ Dd inv_rms(const float (&x)[8], float eps) {
+  Dd sum = {0.f, 0.f}, low = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < N; ++i) sum = add(sum, two_prod(x[i], x[i]));
-  sum = warp_sum(sum);
+  for (int i = 0; i < 8; ++i) sum = add(sum, two_prod(x[i], x[i]));
+  sum = row_sum<L>(sum);
   float down = 1.f;
-  if (!(sum.h < 0x1p120f)) {  // the same for all lanes
-    down = 0x1p-70f;
-    sum = {0.f, 0.f};
+  if (__any_sync(0xffffffffu, !(sum.h < 0x1p120f))) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum = add(sum, two_prod(x[i] * down, x[i] * down));
-    sum = warp_sum(sum);
+    for (int i = 0; i < 8; ++i) low = add(low, two_prod(x[i] * 0x1p-70f, x[i] * 0x1p-70f));
+    low = row_sum<L>(low);
+    if (!(sum.h < 0x1p120f)) {
+      down = 0x1p-70f;
+      sum = low;
+    }
   }
-  const float inv_d = 1.f / static_cast<float>(d);  // a power of two
+  constexpr float inv_d = 1.f / (8 * L);  // a power of two
   const Dd v = add({sum.h * inv_d, sum.l * inv_d}, {eps * (down * down), 0.f});
   const float r = rsqrtf(v.h);
   const Dd q = two_prod(r, r);
@@ -141,6 +148,21 @@ __device__ __forceinline__ Dd inv_rms(const float (&x)[N], int d, float eps) {
   e = fmaf(-v.h, q.l, e);
   e = fmaf(-v.l, q.h, e);
   return {r * down, 0.5f * r * e * down};
+}
+
+// The same in fp32, within 8.5 2^-24 for bf16 values: their squares are exact,
+// four sums in a lane, four between lanes and the one with eps 2^-24 each, half
+// of them in the root; rsqrtf adds two units of 2^-23. inf, 0 or NaN where the
+// sum leaves the range.
+template <int L>
+__device__ __forceinline__ float fast_inv_rms(const float (&x)[8], float eps) {
+  float a = x[0] * x[0], b = x[4] * x[4];
+#pragma unroll
+  for (int i = 1; i < 4; ++i) a = fmaf(x[i], x[i], a), b = fmaf(x[4 + i], x[4 + i], b);
+  float s = a + b;
+#pragma unroll
+  for (int off = L / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  return rsqrtf(fmaf(s, 1.f / (8 * L), eps));
 }
 
 // hi + lo rounded once to bf16: hi with its last bit made sticky (odd where
@@ -152,232 +174,367 @@ __device__ __forceinline__ float round_bf16_once(Dd v) {
   return __bfloat162float(__float2bfloat16_rn(__uint_as_float(b)));
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void load_row(const void* src, long long at, float (&x)[N]) {
-  if constexpr (std::is_same<T, float>::value) {
-    const float* p = static_cast<const float*>(src) + at;
-    if constexpr (N == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p);
-      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(p);
-      x[0] = v.x, x[1] = v.y;
-    }
-  } else {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(src) + at;
-    if constexpr (N == 4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      x[0] = bf16lo_to_f32(v.x), x[1] = bf16hi_to_f32(v.x), x[2] = bf16lo_to_f32(v.y), x[3] = bf16hi_to_f32(v.y);
-    } else {
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-      x[0] = bf16lo_to_f32(v), x[1] = bf16hi_to_f32(v);
-    }
-  }
+__device__ __forceinline__ float approx_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <bool NAN_STAYS>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (NAN_STAYS)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool NAN_STAYS>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (NAN_STAYS)
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
-// A row of bf16 values (fp32 for an fp32 cache) as the cache holds it, row =
-// its index; lane's values N lane ..
-template <int CACHE, int N>
-__device__ __forceinline__ void store_row(void* cache, void* sz, long long row, int lane, const float (&x)[N]) {
-  constexpr int D = 32 * N;
+// 8 values of a row of T
+template <typename T>
+struct Piece;
+template <>
+struct Piece<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const void* src, long long at) {
+    w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src) + at);
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    x[0] = bf16lo_to_f32(w.x), x[1] = bf16hi_to_f32(w.x), x[2] = bf16lo_to_f32(w.y), x[3] = bf16hi_to_f32(w.y);
+    x[4] = bf16lo_to_f32(w.z), x[5] = bf16hi_to_f32(w.z), x[6] = bf16lo_to_f32(w.w), x[7] = bf16hi_to_f32(w.w);
+  }
+};
+template <>
+struct Piece<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* src, long long at) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
+    a = p[0], b = p[1];
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+
+__device__ __forceinline__ uint32_t e5m2_pair(uint32_t w) {  // (a NaN keeps its sign)
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(bf16hi_to_f32(w)), "f"(bf16lo_to_f32(w)));
+  return r | (w >> 8 & 0x80u) | (w >> 16 & 0x8000u);
+}
+
+// A row of bf16 values (fp32 for an fp32 cache) as the cache holds it: x this
+// lane's 8 from place 8 at on, row its index. L lanes hold it; `live`: it is
+// stored (all lanes of the warp come here).
+template <int CACHE, int L, typename T>
+__device__ __forceinline__ void store_row(void* cache, void* sz, long long row, int at, bool live, const Piece<T>& x) {
+  constexpr int D = 8 * L;
   if constexpr (CACHE == kDtypeF32) {
-    float* dst = static_cast<float*>(cache) + row * D + N * lane;
-    if constexpr (N == 4)
-      *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-    else
-      *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[1]);
+    if (!live) return;
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(cache) + row * D + 8 * at);
+    dst[0] = x.a, dst[1] = x.b;
   } else if constexpr (CACHE == kDtypeBf16) {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(cache) + row * D + N * lane);
-    if constexpr (N == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-    else
-      *dst = pack_bf16x2(x[0], x[1]);
+    if (live) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + row * D + 8 * at) = x.w;
+  } else if constexpr (CACHE == kDtypeF8) {
+    if (live)
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D + 8 * at) =
+          make_uint2(e5m2_pair(x.w.x) | e5m2_pair(x.w.y) << 16, e5m2_pair(x.w.z) | e5m2_pair(x.w.w) << 16);
   } else {
-    uint32_t code[N] = {};
-    if constexpr (CACHE == kDtypeF8) {
+    // (maximum, -minimum) of the row
+    constexpr bool kNan = CACHE == kDtypeU4;
+    const uint32_t mx = max2<kNan>(max2<kNan>(x.w.x, x.w.y), max2<kNan>(x.w.z, x.w.w));
+    const uint32_t mn = min2<kNan>(min2<kNan>(x.w.x, x.w.y), min2<kNan>(x.w.z, x.w.w)) ^ 0x80008000u;
+    uint32_t r = max2<kNan>(__byte_perm(mx, mn, 0x5410), __byte_perm(mx, mn, 0x7632));
 #pragma unroll
-      for (int i = 0; i < N; ++i) code[i] = e5m2_code_f(x[i]);
+    for (int off = L / 2; off > 0; off >>= 1) r = max2<kNan>(r, __shfl_xor_sync(0xffffffffu, r, off));
+    if (!live) return;
+    const float hi = bf16lo_to_f32(r), lo = -bf16hi_to_f32(r);
+    float v[8];
+    x.values(v);
+    if constexpr (CACHE == kDtypeU8) {
+      const float2 p = u8_params(lo, hi);
+      uint32_t w[2] = {};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i / 4] |= u8_code(v[i], p) << (8 * (i % 4));
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D + 8 * at) = make_uint2(w[0], w[1]);
+      if (at == 0) static_cast<float2*>(sz)[row] = p;
     } else {
-      float lo = x[0], hi = x[0];
-      bool bad = false;
+      const bool finite = hi < INFINITY && lo > -INFINITY;
+      const uint32_t pair = finite ? u4_pair(u4_clamp(lo), u4_clamp(hi)) : kU4NanPair;
+      float s = u4_scale(pair), m = u4_min(pair);
+      uint32_t w = 0;
+      if (u4_plain(lo, hi, s)) {
+        w = u4_codes(v, s, m, approx_rcp(s));
+      } else if (s > 0.f) {  // (not 0, not NaN: codes 0)
+        const float up = s < 0x1p-100f ? 0x1p64f : 1.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        bad |= !isfinite(x[i]);
+        for (int i = 0; i < 8; ++i) v[i] = u4_clamp(v[i]) * up;
+        w = u4_codes(v, s * up, m * up, approx_rcp(s * up));
       }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-      }
-      if constexpr (CACHE == kDtypeU8) {
-        const float2 p = u8_params(lo, hi);
-#pragma unroll
-        for (int i = 0; i < N; ++i) code[i] = u8_code(x[i], p);
-        if (lane == 0) static_cast<float2*>(sz)[row] = p;
-      } else {
-        lo = u4_clamp(lo), hi = u4_clamp(hi);
-        const uint32_t pair = __any_sync(0xffffffffu, bad) ? kU4NanPair : u4_pair(lo, hi);
-        const float s0 = u4_scale(pair);
-        const float up = s0 < 0x1p-100f ? 0x1p64f : 1.f;  // (a NaN scale gives codes 0 below)
-        const float s = s0 * up, m = u4_min(pair) * up, inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
-        uint32_t w = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) w |= (s > 0.f ? u4_code(u4_clamp(x[i]) * up, s, m, inv) : 0u) << (4 * i);
-        uint8_t* dst = static_cast<uint8_t*>(cache) + row * (D / 2) + N / 2 * lane;
-        if constexpr (N == 4)
-          *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(w);
-        else
-          *dst = static_cast<uint8_t>(w);
-        if (lane == 0) static_cast<uint32_t*>(sz)[row] = pair;
-        return;
-      }
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(cache) + row * (D / 2) + 4 * at) = w;
+      if (at == 0) static_cast<uint32_t*>(sz)[row] = pair;
     }
-    uint8_t* dst = static_cast<uint8_t*>(cache) + row * D + N * lane;
-    if constexpr (N == 4)
-      *reinterpret_cast<uint32_t*>(dst) = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
-    else
-      *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(code[0] | code[1] << 8);
   }
 }
 
-template <int CACHE, int D>
-__global__ void __launch_bounds__(kNormThreads) append_norm_kernel(const NormAppendParams p) {
+// A key row in pairs of floats: x the row, w its weights (norm), cs and low the
+// lane's (cos, sin) and what their rounding left; y rounded once to T.
+template <int L, typename T>
+__device__ __noinline__ void exact_key(const Piece<T>& k, const float (&w)[8], bool norm, float eps, const float2* cs,
+                                       const float2* low, Piece<T>& out) {
+  float x[8], y[8];
+  k.values(x);
+  Dd r = {1.f, 0.f};
+  if (norm) r = inv_rms<L>(x, eps);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const Dd c = {cs[j / 2].x, low[j / 2].x}, s = {cs[j / 2].y, low[j / 2].y};
+    Dd a = {x[j], 0.f}, e = {x[j + 1], 0.f};
+    if (norm) {
+      a = two_prod(x[j], w[j]);
+      e = two_prod(x[j + 1], w[j + 1]);
+    }
+    const Dd es = mul(e, s), ec = mul(e, c);
+    Dd u = add(mul(a, c), {-es.h, -es.l}), v = add(mul(a, s), ec);
+    if (norm) {
+      u = mul(u, r);
+      v = mul(v, r);
+    }
+    if constexpr (std::is_same<T, float>::value) {
+      y[j] = __fadd_rn(u.h, u.l);
+      y[j + 1] = __fadd_rn(v.h, v.l);
+    } else {
+      y[j] = round_bf16_once(u);
+      y[j + 1] = round_bf16_once(v);
+    }
+  }
+  if constexpr (std::is_same<T, float>::value) {
+    out.a = make_float4(y[0], y[1], y[2], y[3]);
+    out.b = make_float4(y[4], y[5], y[6], y[7]);
+  } else {
+    out.w = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+  }
+}
+
+// 8 floats; `wide`: their place is a multiple of 32 bytes
+__device__ __forceinline__ void store8(float* dst, const float (&y)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(dst), "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]) : "memory");
+  } else {
+    reinterpret_cast<float4*>(dst)[0] = make_float4(y[0], y[1], y[2], y[3]);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(y[4], y[5], y[6], y[7]);
+  }
+}
+
+// TOK tokens a block; blockIdx.y: a share of the heads (TOK = 1). Q groups of
+// query rows at a time.
+template <int CACHE, int D, int TOK, int Q>
+__global__ void __launch_bounds__(kNormThreads, 4) append_norm_kernel(const NormAppendParams p) {
   using T = typename std::conditional<CACHE == kDtypeF32, float, __nv_bfloat16>::type;
-  constexpr int N = D / 32, kHalf = D / 2;
-  __shared__ Dd s_cos[kHalf], s_sin[kHalf];
+  constexpr int L = D / 8, kRows = 32 / L, kHalf = D / 2;
+  __shared__ __align__(16) float2 s_cs[TOK][kHalf], s_low[TOK][kHalf];  // (cos, sin), and what their rounding left
+  __shared__ long long s_row[TOK];                                     // kv head 0's row of the token, or -1
   grid_dependents_launch();  // the attention launch of the same step may start its prologue
-  const int bt = blockIdx.x;  // (sequence, new token)
-  const int b = bt / p.n_new, i = bt - b * p.n_new;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pos = p.pos[b] + i;
-  if (threadIdx.x < kHalf) {
+  const int tokens = p.batch * p.n_new, bt0 = blockIdx.x * TOK;  // (sequence, new token)
+  for (int i = threadIdx.x; i < TOK * kHalf; i += kNormThreads) {
+    const int tok = i / kHalf, t = i % kHalf, bt = bt0 + tok;
+    if (bt >= tokens) break;
+    const int b = bt / p.n_new, pos = p.pos[b] + (bt - b * p.n_new);
     int at = pos;
     if (p.axis_pos != nullptr) {
       int axis = 0;
-      while (axis < kMaxAxes - 1 && static_cast<int>(threadIdx.x) >= p.section_end[axis]) ++axis;
-      at = p.axis_pos[static_cast<long long>(axis) * p.batch * p.n_new + bt];
+      while (axis < kMaxAxes - 1 && t >= p.section_end[axis]) ++axis;
+      at = p.axis_pos[static_cast<long long>(axis) * tokens + bt];
     }
-    cos_sin(at, p.theta[threadIdx.x], &s_cos[threadIdx.x], &s_sin[threadIdx.x]);
+    Dd c, s;
+    cos_sin(at, p.theta[t], &c, &s);
+    s_cs[tok][t] = make_float2(c.h, s.h);
+    s_low[tok][t] = make_float2(c.l, s.l);
+    if (t != 0) continue;
+    long long row = -1;
+    int bad = 0;
+    if (p.paged) {
+      const int lp = pos >= 0 ? pos / p.page_size : p.max_pages;
+      if (lp >= p.max_pages) {
+        bad = MQA_DEVERR_POS_RANGE;
+      } else {
+        const int page = p.block_table[static_cast<long long>(b) * p.max_pages + lp];
+        if (page < 0 || page >= p.num_pages)
+          bad = MQA_DEVERR_PAGE_RANGE;
+        else
+          row = static_cast<long long>(page) * p.h_kv * p.page_size + pos % p.page_size;
+      }
+    } else if (pos < 0 || pos >= p.capacity) {
+      bad = MQA_DEVERR_POS_RANGE;
+    } else {
+      row = static_cast<long long>(b) * p.h_kv * p.capacity + pos;
+    }
+    if (bad && blockIdx.y == 0) atomicOr(p.err, bad);
+    s_row[tok] = row;
   }
   if (p.zero != nullptr && blockIdx.x == 0 && blockIdx.y == 0)
     for (int k = threadIdx.x; k < p.zero_count; k += kNormThreads) p.zero[k] = 0;
   __syncthreads();
 
-  // the place of the token's rows, of kv head 0, and from one head to the next
-  long long row0 = -1, stride = 0;
-  int bad = 0;
-  if (p.paged) {
-    const int lp = pos >= 0 ? pos / p.page_size : p.max_pages;
-    if (lp >= p.max_pages) {
-      bad = MQA_DEVERR_POS_RANGE;
-    } else {
-      const int page = p.block_table[static_cast<long long>(b) * p.max_pages + lp];
-      if (page < 0 || page >= p.num_pages)
-        bad = MQA_DEVERR_PAGE_RANGE;
-      else
-        row0 = static_cast<long long>(page) * p.h_kv * p.page_size + pos % p.page_size;
-      stride = p.page_size;
-    }
-  } else if (pos < 0 || pos >= p.capacity) {
-    bad = MQA_DEVERR_POS_RANGE;
-  } else {
-    row0 = static_cast<long long>(b) * p.h_kv * p.capacity + pos;
-    stride = p.capacity;
-  }
-  if (bad && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, bad);
-
   const bool norm_q = p.q_weight != nullptr, norm_k = p.k_weight != nullptr;
-  float wq[N], wk[N];
-  if (norm_q) load_row<T>(p.q_weight, N * lane, wq);
-  if (norm_k) load_row<T>(p.k_weight, N * lane, wk);
-  // the kv heads first: theirs is the longer work
-  const int rows = p.h_kv + p.h_q;
-  for (int h = blockIdx.y * kNormWarps + warp; h < rows; h += gridDim.y * kNormWarps) {
-    float x[N];
-    if (h >= p.h_kv) {
-      const long long at = (static_cast<long long>(bt) * p.h_q + (h - p.h_kv)) * D + N * lane;
-      load_row<T>(p.q_new, at, x);
-      float r = 1.f;
-      if (norm_q) r = inv_rms(x, D, p.eps).h;
-      float y[N];
+  const bool wide = (reinterpret_cast<uintptr_t>(p.q_rot) & 31u) == 0;
+  const int at = lane % L, sub = lane / L;  // place in the row, row of the group
+  const int here = tokens - bt0 < TOK ? tokens - bt0 : TOK;
+  const int kv_items = (p.h_kv + kRows - 1) / kRows, q_items = (p.h_q + kRows * Q - 1) / (kRows * Q);
+  for (int it = blockIdx.y * kNormWarps + warp; it < here * (kv_items + q_items); it += gridDim.y * kNormWarps) {
+    if (it < here * kv_items) {
+      const int tok = TOK == 1 ? 0 : it / kv_items;
+      if (s_row[tok] < 0) continue;
+      const int h = (it - tok * kv_items) * kRows + sub;
+      const bool live = h < p.h_kv;
+      const int head = live ? h : p.h_kv - 1;
+      const long long src = (static_cast<long long>(bt0 + tok) * p.h_kv + head) * D + 8 * at;
+      const long long row = s_row[tok] + head * (p.paged ? static_cast<long long>(p.page_size) : p.capacity);
+      Piece<T> k, v, key;
+      k.load(p.k_new, src);
+      v.load(p.v_new, src);
+      float w[8];
+      if (norm_k) {
+        Piece<T> t;
+        t.load(p.k_weight, 8 * at);
+        t.values(w);
+      } else {
 #pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        const int t = (N * lane + j) / 2;
-        const float c = s_cos[t].h, s = s_sin[t].h;
-        const float a = norm_q ? x[j] * wq[j] * r : x[j], e = norm_q ? x[j + 1] * wq[j + 1] * r : x[j + 1];
-        y[j] = fmaf(a, c, -(e * s));
-        y[j + 1] = fmaf(a, s, e * c);
+        for (int i = 0; i < 8; ++i) w[i] = 1.f;
       }
-      if constexpr (N == 4)
-        *reinterpret_cast<float4*>(p.q_rot + at) = make_float4(y[0], y[1], y[2], y[3]);
-      else
-        *reinterpret_cast<float2*>(p.q_rot + at) = make_float2(y[0], y[1]);
+      const float2* cs = &s_cs[tok][4 * at];
+      bool settled = false;
+      if constexpr (CACHE != kDtypeF32) {
+        // u = a c - e s with a = x w exact: the product e s, its rounding and the low parts of c and s are added up apart, so
+        // that what is left is 2^-24 |u| of each of two sums (and 2^-45 (|a| + |e|)). With a norm r is within 8.5 2^-24 and
+        // its product 2^-24; a border's own sum adds 2^-24. A row with squares that leave the range is not settled.
+        float x[8], r = 1.f, bound = 3.5f * 0x1p-24f;
+        k.values(x);
+        if (norm_k) {
+          r = fast_inv_rms<L>(x, p.eps);
+          bound = 13.f * 0x1p-24f;
+        }
+        settled = r > 0x1p-58f && r < 0x1p30f;
+        const float2* low = &s_low[tok][4 * at];
+        uint32_t out[4];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float2 t = cs[j / 2], tl = low[j / 2];
+          const float a = x[j] * w[j], e = x[j + 1] * w[j + 1], size = (fabsf(a) + fabsf(e)) * r;
+          const float es = e * t.y, ec = e * t.x;
+          const float u = __fadd_rn(fmaf(a, t.x, -es), fmaf(a, tl.x, -fmaf(e, tl.y, fmaf(e, t.y, -es)))) * r;
+          const float z = __fadd_rn(fmaf(a, t.y, ec), fmaf(a, tl.y, fmaf(e, tl.x, fmaf(e, t.x, -ec)))) * r;
+          const float ou = fmaf(fabsf(u), bound, size * 0x1p-36f), oz = fmaf(fabsf(z), bound, size * 0x1p-36f);
+          out[j / 2] = pack_bf16x2(__fsub_rn(u, ou), __fsub_rn(z, oz));
+          settled = settled && out[j / 2] == pack_bf16x2(__fadd_rn(u, ou), __fadd_rn(z, oz)) &&
+                    ((size >= 0x1p-60f && size <= 0x1p120f) || size == 0.f);
+        }
+        key.w = make_uint4(out[0], out[1], out[2], out[3]);
+      }
+      if (!__all_sync(0xffffffffu, settled)) exact_key<L>(k, w, norm_k, p.eps, cs, &s_low[tok][4 * at], key);
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i)  // (one copy of the code: what holds this kernel up first is its size)
+        store_row<CACHE, L>(i ? p.v_cache : p.k_cache, i ? p.v_sz : p.k_sz, row, at, live, i ? v : key);
       continue;
     }
-    if (row0 < 0) continue;
-    const long long at = (static_cast<long long>(bt) * p.h_kv + h) * D + N * lane, row = row0 + h * stride;
-    float v[N];
-    load_row<T>(p.k_new, at, x);
-    load_row<T>(p.v_new, at, v);
-    Dd r = {1.f, 0.f};
-    if (norm_k) r = inv_rms(x, D, p.eps);
-    float y[N];
+    const int qi = it - here * kv_items, tok = TOK == 1 ? 0 : qi / q_items;
+    const int h0 = (qi - tok * q_items) * (kRows * Q) + sub;
+    const long long src = (static_cast<long long>(bt0 + tok) * p.h_q + h0) * D + 8 * at;
+    Piece<T> q[Q];
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
-      const int t = (N * lane + j) / 2;
-      const Dd c = s_cos[t], s = s_sin[t];
-      Dd a = {x[j], 0.f}, e = {x[j + 1], 0.f};
-      if (norm_k) {
-        a = two_prod(x[j], wk[j]);
-        e = two_prod(x[j + 1], wk[j + 1]);
+    for (int g = 0; g < Q; ++g)  // (a row behind the last head: the first again)
+      q[g].load(p.q_new, h0 + g * kRows < p.h_q ? src + g * (kRows * D) : 8 * at);
+    float w[8];
+    if (norm_q) {
+      Piece<T> t;
+      t.load(p.q_weight, 8 * at);
+      t.values(w);
+    }
+    float2 cs[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cs[j] = s_cs[tok][4 * at + j];
+    float r[Q];
+    if (norm_q) {
+      bool out_of_range = false;
+#pragma unroll
+      for (int g = 0; g < Q; ++g) {
+        float x[8];
+        q[g].values(x);
+        r[g] = fast_inv_rms<L>(x, p.eps);
+        out_of_range = out_of_range || !(r[g] > 0x1p-58f);
       }
-      const Dd es = mul(e, s), ec = mul(e, c);
-      Dd u = add(mul(a, c), {-es.h, -es.l}), w = add(mul(a, s), ec);
-      if (norm_k) {
-        u = mul(u, r);
-        w = mul(w, r);
-      }
-      if constexpr (CACHE == kDtypeF32) {
-        y[j] = __fadd_rn(u.h, u.l);
-        y[j + 1] = __fadd_rn(w.h, w.l);
-      } else {
-        y[j] = round_bf16_once(u);
-        y[j + 1] = round_bf16_once(w);
+      if (__any_sync(0xffffffffu, out_of_range)) {
+#pragma unroll
+        for (int g = 0; g < Q; ++g) {
+          float x[8];
+          q[g].values(x);
+          r[g] = inv_rms<L>(x, p.eps).h;
+        }
       }
     }
-    store_row<CACHE>(p.k_cache, p.k_sz, row, lane, y);
-    store_row<CACHE>(p.v_cache, p.v_sz, row, lane, v);
+#pragma unroll
+    for (int g = 0; g < Q; ++g) {
+      float x[8], y[8];
+      q[g].values(x);
+      if (norm_q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= w[i] * r[g];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        y[j] = fmaf(x[j], cs[j / 2].x, -(x[j + 1] * cs[j / 2].y));
+        y[j + 1] = fmaf(x[j], cs[j / 2].y, x[j + 1] * cs[j / 2].x);
+      }
+      if (h0 + g * kRows < p.h_q) store8(p.q_rot + src + g * (kRows * D), y, wide);
+    }
   }
 }
 
-template <int CACHE>
-cudaError_t launch_norm_c(const NormAppendParams& p, dim3 grid, cudaStream_t stream) {
+// A block a token with its heads spread over several blocks, while that fills
+// the GPU; with four blocks an SM and more, several tokens a block, which fill
+// its threads with sines and cosines, and more query rows at a time.
+template <int CACHE, int D>
+cudaError_t launch_norm_d(const NormAppendParams& p, int sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
   cfg.blockDim = dim3(kNormThreads);
   cfg.stream = stream;
-  return p.head_dim == 128 ? cudaLaunchKernelEx(&cfg, append_norm_kernel<CACHE, 128>, p)
-                           : cudaLaunchKernelEx(&cfg, append_norm_kernel<CACHE, 64>, p);
+  const int tokens = p.batch * p.n_new;
+  constexpr int kTok = 512 / D, kRows = 256 / D;
+  if (tokens / kTok >= 4 * sms) {
+    cfg.gridDim = dim3(static_cast<unsigned>((tokens - 1) / kTok + 1));
+    return cudaLaunchKernelEx(&cfg, append_norm_kernel<CACHE, D, kTok, CACHE == kDtypeF32 ? 2 : 4>, p);
+  }
+  const int items = (p.h_kv + kRows - 1) / kRows + (p.h_q + kRows - 1) / kRows;
+  const int most = (items + kNormWarps - 1) / kNormWarps;
+  int y = 4 * sms / tokens;
+  y = y < 1 ? 1 : y > most ? most : y;
+  cfg.gridDim = dim3(static_cast<unsigned>(tokens), static_cast<unsigned>(y));
+  return cudaLaunchKernelEx(&cfg, append_norm_kernel<CACHE, D, 1, 1>, p);
+}
+
+template <int CACHE>
+cudaError_t launch_norm_c(const NormAppendParams& p, int sms, cudaStream_t stream) {
+  return p.head_dim == 128 ? launch_norm_d<CACHE, 128>(p, sms, stream) : launch_norm_d<CACHE, 64>(p, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_append_norm(const NormAppendParams& p, int sms, cudaStream_t stream) {
-  // few tokens: their heads over several blocks, while that fills the GPU
-  const long long tokens = static_cast<long long>(p.batch) * p.n_new;
-  const int most = (p.h_q + p.h_kv + kNormWarps - 1) / kNormWarps;
-  long long y = 4ll * sms / tokens;
-  y = y < 1 ? 1 : y > most ? most : y;
-  if (y > 65535) y = 65535;
-  const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(y));
   switch (p.cache_dtype) {
-    case kDtypeBf16: return launch_norm_c<kDtypeBf16>(p, grid, stream);
-    case kDtypeF32: return launch_norm_c<kDtypeF32>(p, grid, stream);
-    case kDtypeU8: return launch_norm_c<kDtypeU8>(p, grid, stream);
-    case kDtypeF8: return launch_norm_c<kDtypeF8>(p, grid, stream);
-    default: return launch_norm_c<kDtypeU4>(p, grid, stream);
+    case kDtypeBf16: return launch_norm_c<kDtypeBf16>(p, sms, stream);
+    case kDtypeF32: return launch_norm_c<kDtypeF32>(p, sms, stream);
+    case kDtypeU8: return launch_norm_c<kDtypeU8>(p, sms, stream);
+    case kDtypeF8: return launch_norm_c<kDtypeF8>(p, sms, stream);
+    default: return launch_norm_c<kDtypeU4>(p, sms, stream);
   }
 }
 

@@ -32,8 +32,9 @@ struct Piece<kDtypeU4> {
   }
   __device__ __forceinline__ void values(float (&x)[8]) const {
     const float s = u4_scale(pair), m = u4_min(pair);
+    // (a code in the low bits of 2^23: conversions run at a quarter of the rate)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf(static_cast<float>(w >> (4 * i) & 15u), s, m);
+    for (int i = 0; i < 8; ++i) x[i] = fmaf(__uint_as_float((w >> (4 * i) & 15u) | 0x4b000000u) - 0x1p23f, s, m);
   }
 };
 template <>
@@ -47,7 +48,7 @@ struct Piece<kDtypeU8> {
   __device__ __forceinline__ void values(float (&x)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      x[i] = __fmul_rn(__fsub_rn(static_cast<float>((i < 4 ? w.x : w.y) >> (8 * (i & 3)) & 255u), sz.y), sz.x);
+      x[i] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(i < 4 ? w.x : w.y, 0x4b000000u, 0x7540 + (i & 3))) - 0x1p23f, sz.y), sz.x);
   }
 };
 template <>

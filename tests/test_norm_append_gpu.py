@@ -177,6 +177,7 @@ SHAPES = {
     "only_q": (4, 1, 128, [31], 2, 0, "q", None),
     "only_k": (4, 1, 128, [31], 2, 16, "k", [0, 64]),
     "prompt": (5, 1, 128, [0, 3], 150, 64, "both", [16, 24, 24]),
+    "long_prompt": (5, 1, 64, [0, 3, 40, 9, 600], 487, 16, "both", [16, 10, 6]),
     "one_head": (1, 1, 64, [0], 1, 0, "both", None),
     "many_heads": (64, 64, 64, [2], 1, 0, "both", None),
 }

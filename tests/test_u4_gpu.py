@@ -344,6 +344,21 @@ def test_step(m, name, splits):
     assert err == 0 and torch.equal(again.view_as(out), out) and torch.equal(lse.view_as(bufs.lse), bufs.lse)
 
 
+def test_step_leaves_a_workspace_it_does_not_need(m):
+    """A step that the library gives one block per unit needs no workspace, and writes none that is passed."""
+    c = U4Case(8, 8, 128, [5] * 60, seed=47, garbage=False)
+    lay = c.layout(m)
+    if m.workspace_size(lay, 5, 0) != 0:
+        pytest.skip("more than 960 blocks on this GPU")
+    q_new, k_new, v_new = _new_rows(c, 8)
+    bufs = m.DecodeBuffers.allocate(lay, 5)
+    memory = torch.full((8192,), 0xAB, dtype=torch.uint8, device=DEV)
+    bufs.workspace = memory[:256]
+    m.decode_step(lay, q_new.to(DEV), k_new.to(DEV), v_new.to(DEV), _i32([4] * 60), _i32(c.lens), 5, bufs)
+    torch.cuda.synchronize()
+    assert int(bufs.err) == 0 and bool((memory == 0xAB).all())
+
+
 def test_noalloc(m):
     c = U4Case(8, 2, 128, [500, 40], 1, seed=50)
     lay, err = c.layout(m), _i32([0])

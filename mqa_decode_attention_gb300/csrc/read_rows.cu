@@ -1,12 +1,17 @@
 // kv_read_rows kernel: rows of a cache of any type as bf16 or fp32 values, in
 // the layout of a contiguous cache [batch, h_kv, n_rows, head_dim].
 //
-// A thread turns 8 neighbouring values (4 bytes of a 4-bit cache, up to 32 of
-// an fp32 one) into 16 or 32 bytes; kUnroll such pieces of rows further on are
-// requested together, so that enough loads are in flight to keep the memory
-// busy, which is all that bounds this kernel. uint8: (code - zero) * scale, one
-// subtraction and one product in fp32; 4 bit: m + s * code in one fused
-// multiply-add. Then one rounding to bf16.
+// A thread turns 16 neighbouring values (8 bytes of a 4-bit cache, up to 64 of
+// an fp32 one) into one or two stores of 32 bytes; kUnroll such pieces of rows
+// further on are requested together, so that enough loads are in flight to keep
+// the memory busy. uint8: (code - zero) * scale, one subtraction and one
+// product in fp32; 4 bit: m + s * code in one fused multiply-add. Then one
+// rounding to bf16.
+//
+// What bounds it is the memory, once a value costs few instructions: with 8
+// values a thread, sizes that only the launch knew and conversions of codes
+// (a quarter of the rate; here a code is put into the low bits of 2^23) half of
+// the time was the issue of instructions.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -21,78 +26,113 @@ namespace {
 constexpr int kReadThreads = 256;
 constexpr int kUnroll = 4;
 
+// code of 8 bits, byte b of w, as a float
+template <int B>
+__device__ __forceinline__ float byte_value(uint32_t w) {
+  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + B)) - 0x1p23f;
+}
+
 template <int CACHE>
-struct Piece;  // 8 values as they are stored, and what their row adds
+struct Piece;  // 16 values as they are stored, and what their row adds
 template <>
 struct Piece<kDtypeU4> {
-  uint32_t w, pair;
-  __device__ __forceinline__ void load(const void* c, const void* sz, long long row, int at, int d) {
-    w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(c) + row * (d / 2) + at / 2);
+  uint2 w;
+  uint32_t pair;
+  __device__ __forceinline__ void load(const void* c, const void* sz, long long row, long long at) {
+    w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c) + at / 2);
     pair = static_cast<const uint32_t*>(sz)[row];
   }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
+  __device__ __forceinline__ void values(float (&x)[16]) const {
     const float s = u4_scale(pair), m = u4_min(pair);
-    // (a code in the low bits of 2^23: conversions run at a quarter of the rate)
+    const uint32_t half[4] = {w.x, w.x >> 16, w.y, w.y >> 16};
+    // (a code of bits 4 j .. 4 j + 3 is c in the mantissa of 2^(23 - 4 j))
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf(__uint_as_float((w >> (4 * i) & 15u) | 0x4b000000u) - 0x1p23f, s, m);
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t one = 0x4b000000u - i % 4 * 0x02000000u;
+      x[i] = fmaf(__uint_as_float((half[i / 4] & (15u << (4 * (i % 4)))) | one) - __uint_as_float(one), s, m);
+    }
   }
 };
 template <>
 struct Piece<kDtypeU8> {
-  uint2 w;
+  uint4 w;
   float2 sz;
-  __device__ __forceinline__ void load(const void* c, const void* s, long long row, int at, int d) {
-    w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c) + row * d + at);
+  __device__ __forceinline__ void load(const void* c, const void* s, long long row, long long at) {
+    w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c) + at);
     sz = static_cast<const float2*>(s)[row];
   }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
+  __device__ __forceinline__ void values(float (&x)[16]) const {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(i < 4 ? w.x : w.y, 0x4b000000u, 0x7540 + (i & 3))) - 0x1p23f, sz.y), sz.x);
+    for (int i = 0; i < 4; ++i) {
+      x[4 * i] = byte_value<0>(v[i]), x[4 * i + 1] = byte_value<1>(v[i]);
+      x[4 * i + 2] = byte_value<2>(v[i]), x[4 * i + 3] = byte_value<3>(v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__fsub_rn(x[i], sz.y), sz.x);
   }
 };
 template <>
 struct Piece<kDtypeF8> {
-  uint2 w;
-  __device__ __forceinline__ void load(const void* c, const void*, long long row, int at, int d) {
-    w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c) + row * d + at);
+  uint4 w;
+  __device__ __forceinline__ void load(const void* c, const void*, long long, long long at) {
+    w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c) + at);
   }
-  __device__ __forceinline__ void values(float (&x)[8]) const {  // an e5m2 code is the high byte of a half
+  __device__ __forceinline__ void values(float (&x)[16]) const {  // an e5m2 code is the high byte of a half
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(((i < 4 ? w.x : w.y) >> (8 * (i & 3)) & 255u) << 8)));
+    for (int i = 0; i < 16; ++i)
+      x[i] = __half2float(__ushort_as_half(static_cast<unsigned short>((v[i / 4] >> (8 * (i % 4)) & 255u) << 8)));
   }
 };
 template <>
 struct Piece<kDtypeBf16> {
-  uint4 w;
-  __device__ __forceinline__ void load(const void* c, const void*, long long row, int at, int d) {
-    w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c) + row * d + at);
+  uint4 w[2];
+  __device__ __forceinline__ void load(const void* c, const void*, long long, long long at) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c) + at);
+    w[0] = p[0], w[1] = p[1];
   }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
-    x[0] = bf16lo_to_f32(w.x), x[1] = bf16hi_to_f32(w.x), x[2] = bf16lo_to_f32(w.y), x[3] = bf16hi_to_f32(w.y);
-    x[4] = bf16lo_to_f32(w.z), x[5] = bf16hi_to_f32(w.z), x[6] = bf16lo_to_f32(w.w), x[7] = bf16hi_to_f32(w.w);
+  __device__ __forceinline__ void values(float (&x)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[8 * i] = bf16lo_to_f32(w[i].x), x[8 * i + 1] = bf16hi_to_f32(w[i].x);
+      x[8 * i + 2] = bf16lo_to_f32(w[i].y), x[8 * i + 3] = bf16hi_to_f32(w[i].y);
+      x[8 * i + 4] = bf16lo_to_f32(w[i].z), x[8 * i + 5] = bf16hi_to_f32(w[i].z);
+      x[8 * i + 6] = bf16lo_to_f32(w[i].w), x[8 * i + 7] = bf16hi_to_f32(w[i].w);
+    }
   }
 };
 template <>
 struct Piece<kDtypeF32> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* c, const void*, long long row, int at, int d) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(c) + row * d + at);
-    a = p[0], b = p[1];
+  float4 v[4];
+  __device__ __forceinline__ void load(const void* c, const void*, long long, long long at) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(c) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = p[i];
   }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  __device__ __forceinline__ void values(float (&x)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[4 * i] = v[i].x, x[4 * i + 1] = v[i].y, x[4 * i + 2] = v[i].z, x[4 * i + 3] = v[i].w;
   }
 };
 
+// 32 bytes; `wide`: their place is a multiple of 32
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+  } else {
+    static_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // blockIdx.x: chunk of rows of one (sequence, kv head), all of them in order;
 // blockIdx.y: K or V
-template <int CACHE, bool BF16>
-__global__ void __launch_bounds__(kReadThreads) read_rows_kernel(const ReadParams p, int chunks) {
-  const int per_row = p.head_dim / 8, per_pass = kReadThreads / per_row;
-  const int chunk = blockIdx.x % chunks;
-  const int unit = blockIdx.x / chunks;  // sequence * h_kv + head
+template <int CACHE, int D, bool PAGED, bool BF16>
+__global__ void __launch_bounds__(kReadThreads) read_rows_kernel(const ReadParams p, int chunks, int page_shift) {
+  constexpr int kPerRow = D / 16, kPass = kReadThreads / kPerRow;
+  const int unit = blockIdx.x / chunks, chunk = blockIdx.x - unit * chunks;  // unit: sequence * h_kv + head
   const int b = unit / p.h_kv;
   const int start = p.start != nullptr ? p.start[b] : 0, rows = p.num_rows != nullptr ? p.num_rows[b] : p.n_rows;
   int bad = 0;
@@ -104,61 +144,75 @@ __global__ void __launch_bounds__(kReadThreads) read_rows_kernel(const ReadParam
     if (chunk == 0 && unit == b * p.h_kv && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.err, bad);
     return;
   }
-  const int at = threadIdx.x % per_row * 8;
-  const int first = chunk * per_pass * kUnroll + threadIdx.x / per_row;
-  if (first >= rows) return;
+  const int at = threadIdx.x % kPerRow * 16;
+  const unsigned row0 = static_cast<unsigned>(chunk) * (kPass * kUnroll) + threadIdx.x / kPerRow;  // (past 2^31 behind the last row)
+  if (row0 >= static_cast<unsigned>(rows)) return;
+  const int first = static_cast<int>(row0);
   const void* cache = blockIdx.y ? p.v_cache : p.k_cache;
   const void* sz = blockIdx.y ? p.v_sz : p.k_sz;
   Piece<CACHE> piece[kUnroll];
   bool live[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int i = first + u * per_pass;
-    live[u] = i < rows;
+    live[u] = u * kPass < rows - first;
     if (!live[u]) continue;
-    const int t = start + i;
+    const int t = start + first + u * kPass;
     long long row;
-    if (p.paged) {
-      const int page = p.block_table[static_cast<long long>(b) * p.max_pages + t / p.page_size];
+    if constexpr (PAGED) {
+      const int page = p.block_table[static_cast<long long>(b) * p.max_pages + (t >> page_shift)];
       if (page < 0 || page >= p.num_pages) {
         live[u] = false;
         atomicOr(p.err, static_cast<int>(MQA_DEVERR_PAGE_RANGE));
         continue;
       }
-      row = (static_cast<long long>(page) * p.h_kv + (unit - b * p.h_kv)) * p.page_size + t % p.page_size;
+      row = ((static_cast<long long>(page) * p.h_kv + (unit - b * p.h_kv)) << page_shift) + (t & (p.page_size - 1));
     } else {
       row = unit * p.capacity + t;
     }
-    piece[u].load(cache, sz, row, at, p.head_dim);
+    piece[u].load(cache, sz, row, row * D + at);
   }
   void* out = blockIdx.y ? p.v_out : p.k_out;
+  const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     if (!live[u]) continue;
-    const long long dst = (static_cast<long long>(unit) * p.n_rows + first + u * per_pass) * p.head_dim + at;
-    float x[8];
+    const long long dst = (static_cast<long long>(unit) * p.n_rows + first + u * kPass) * D + at;
+    float x[16];
     piece[u].values(x);
+    uint32_t w[8];
     if constexpr (BF16) {
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + dst) =
-          make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+      store32(static_cast<__nv_bfloat16*>(out) + dst, w, wide);
     } else {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + dst);
-      o[0] = make_float4(x[0], x[1], x[2], x[3]);
-      o[1] = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[8 * h + i]);
+        store32(static_cast<float*>(out) + dst + 8 * h, w, wide);
+      }
     }
   }
 }
 
-template <int CACHE>
-cudaError_t launch_read_c(const ReadParams& p, cudaStream_t stream) {
-  const int per_block = kReadThreads / (p.head_dim / 8) * kUnroll;
-  const int chunks = (p.n_rows + per_block - 1) / per_block;
+template <int CACHE, int D, bool PAGED>
+cudaError_t launch_read_d(const ReadParams& p, cudaStream_t stream) {
+  constexpr int kPerBlock = kReadThreads / (D / 16) * kUnroll;
+  const int chunks = (p.n_rows - 1) / kPerBlock + 1;
+  int shift = 0;
+  while (PAGED && (1 << shift) < p.page_size) ++shift;
   const dim3 grid(static_cast<unsigned>(static_cast<long long>(chunks) * p.batch * p.h_kv), 2);
   if (p.out_dtype == kDtypeBf16)
-    read_rows_kernel<CACHE, true><<<grid, kReadThreads, 0, stream>>>(p, chunks);
+    read_rows_kernel<CACHE, D, PAGED, true><<<grid, kReadThreads, 0, stream>>>(p, chunks, shift);
   else
-    read_rows_kernel<CACHE, false><<<grid, kReadThreads, 0, stream>>>(p, chunks);
+    read_rows_kernel<CACHE, D, PAGED, false><<<grid, kReadThreads, 0, stream>>>(p, chunks, shift);
   return cudaGetLastError();
+}
+
+template <int CACHE>
+cudaError_t launch_read_c(const ReadParams& p, cudaStream_t stream) {
+  if (p.head_dim == 128) return p.paged ? launch_read_d<CACHE, 128, true>(p, stream) : launch_read_d<CACHE, 128, false>(p, stream);
+  return p.paged ? launch_read_d<CACHE, 64, true>(p, stream) : launch_read_d<CACHE, 64, false>(p, stream);
 }
 
 }  // namespace

@@ -157,9 +157,10 @@ typedef enum mqa_variant {
  * tree calls and kv_keep_path return MQA_ERR_UNSUPPORTED (a prompt runs over
  * a bf16 layout and is appended to the 4-bit one as well; kv_read_rows gives the
  * bf16 rows of a prefix for it). num_splits: 1 = one block per (sequence, kv
- * head), no workspace; > 1 = equal runs of the cached tokens over all SMs,
- * whatever the number and the lengths; 0 = the library's choice of the two (runs
- * for a paged pool, and while such blocks would fill half the GPU or less). Calls that may
+ * head, block of up to 32 query rows), no workspace; > 1 = the cached tokens
+ * shared by as many blocks as are resident, whatever the number; 0 = the
+ * library's choice of the two, by the bound on the lengths (mqa_choose_splits:
+ * 1 or 2). Calls that may
  * overlap on the GPU need a workspace each. The query is rounded to fp16 (11
  * bits), the probabilities times s to 11 bits; the values of a window's or a
  * sequence's tokens that a query does not see are multiplied by a zero

@@ -162,9 +162,9 @@ bool multi_supported(const mqa_kv_layout* L, int variant, int n_new) {
                                                                byte_cache(L->cache_dtype)));
 }
 
-// A 4-bit cache: blocks take equal runs of all tiles (attn_u4.cu), whatever the
-// lengths, unless one split is asked for. The workspace holds a counter and two
-// partial results for each block.
+// A 4-bit cache: one block takes a unit (sequence, kv head, block of query rows),
+// or all resident blocks share all tiles (attn_u4.cu); then the workspace holds
+// a counter and two partial results for each block.
 struct U4Plan {
   U4Shape shape;
   int row_blocks;
@@ -202,10 +202,15 @@ int read_span(const mqa_kv_layout* L, int max_len, int n_new = 1) {
 // paged batch of lengths spread over [128, 16384].
 int choose_splits(const mqa_kv_layout* L, int max_len_in, int variant, int n_new = 1) {
   if (L->cache_dtype == MQA_U4) {
-    // equal runs, but for contiguous caches with units for more than half of the blocks: a block for each then loses less
-    // by its unequal load than the runs by their merging (256 units of 4096 tokens 34 us, in runs 41; the lengths of a paged
-    // batch are taken as unequal)
+    // One block for each unit, where the others' merging would cost more than its unequal load: for units of few tiles
+    // (a tile's time goes with its dims and rows; head_dim 128 and 8 rows: 8 units of 16 tiles 10.0 us, shared 10.4, of 32
+    // tiles 15.6 and 11.6; 160 units of 16 tiles 12.4 and 14.5), and for contiguous caches with units for more than half of
+    // the blocks (256 units of 64 tiles 34 us, shared 41; the lengths of a paged batch are taken as unequal).
     const U4Plan c = u4_plan(L, n_new);
+    long long span = max_len_in;
+    if (L->window > 0) span = std::min(span, static_cast<long long>(L->window) + n_new - 1 + kU4Tile - 1);
+    const long long tiles = (span + kU4Tile - 1) / kU4Tile;
+    if (tiles * L->head_dim * c.shape.rows <= 16 * 128 * 8) return 1;
     return !L->paged && 2ll * L->batch * L->h_kv * c.row_blocks > c.ctas ? 1 : 2;
   }
   const int max_len = read_span(L, max_len_in);
@@ -231,7 +236,7 @@ int choose_splits(const mqa_kv_layout* L, int max_len_in, int variant, int n_new
 }
 
 // Effective split count and chunk for a requested count (a 4-bit cache: one, or
-// more than one, which stands for equal runs).
+// more than one, which stands for shared tiles).
 void split_plan(const mqa_kv_layout* L, int requested, int max_len, int* splits, int* chunk) {
   if (L->cache_dtype == MQA_U4) {
     *splits = requested > 1 ? 2 : 1;
@@ -715,6 +720,8 @@ mqa_status u4_attention(const mqa_kv_layout* L, int n_new, const float* q_rot, c
   p.lse_out = lse_out;
   p.whole = whole;
   p.min_tiles = 4;
+  p.parts = static_cast<int>(c.ctas / (static_cast<long long>(L->batch) * L->h_kv * c.row_blocks));
+  p.min_part = 4;
   p.arrived = static_cast<int32_t*>(workspace);
   p.part = whole ? nullptr : reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.counters);
   p.err = err_word;
@@ -1258,7 +1265,7 @@ mqa_status step_impl(const mqa_kv_layout* layout, int n_new, const void* q_new, 
     return attention_impl(layout, q_rot, seq_lens, max_seq_len, scale, num_splits, out, out_dtype, lse_out,
                           workspace, workspace_bytes, variant, err_word, stream, /*early=*/0, &rope, n_new);
   }
-  // (a 4-bit cache in equal runs: the append clears the attention's counters)
+  // (a 4-bit cache whose tiles are shared: the append clears the attention's counters)
   const bool runs = layout->cache_dtype == MQA_U4 && need > 0;
   const mqa_status a = append_impl(layout, q_new, k_new, v_new, pos, rope_base, q_rot, err_word, stream, n_new, nullptr,
                                    runs ? static_cast<int32_t*>(workspace) : nullptr,

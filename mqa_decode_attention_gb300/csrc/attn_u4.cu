@@ -283,12 +283,22 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
   Place at;
   int run;             // tiles of the run
   long long start = 0, run_len = 1;  // place of the run among all tiles, length of the runs
+  int me = blockIdx.x;  // place of this block's work in the order of the tiles
+  // one of `parts` equal parts of a unit; the first parts of all units go to the first blocks, which are spread over the SMs
+  auto part_of_unit = [&](int parts, int least) {
+    const int all = p.batch * units, part = blockIdx.x / all, unit = blockIdx.x - part * all;
+    me = unit * parts + part;
+    at.b = unit / units;
+    at.u = unit - at.b * units;
+    at.s = part < parts ? span_of(p, p.seq_lens[at.b]) : Span{0, 0, 0, 0};
+    const int per = max(least, (at.s.tiles + parts - 1) / parts);
+    at.base = -part * per;
+    run = max(0, min(per, at.s.tiles - part * per));
+    run_len = per;
+    start = run_len * me;
+  };
   if (p.whole) {
-    at.b = blockIdx.x / units;
-    at.u = blockIdx.x - at.b * units;
-    at.base = 0;
-    at.s = span_of(p, p.seq_lens[at.b]);
-    run = at.s.tiles;
+    part_of_unit(1, 1);
     if (run == 0 && at.u == 0 && threadIdx.x == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_SEQ_LEN));
   } else {
     // (every warp finds it for itself; 32 sequences at a time, the first 32 kept)
@@ -296,22 +306,32 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
     const int mine = lane < p.batch ? span_of(p, first_len).tiles : 0;
     bool bad = lane < p.batch && mine == 0;
     unsigned long long total = __reduce_add_sync(kFull, static_cast<unsigned>(mine));
+    int most = __reduce_max_sync(kFull, mine);
     for (int b0 = 32; b0 < p.batch; b0 += 32) {
       const int t = tiles_of(b0 + lane);
       bad |= b0 + lane < p.batch && t == 0;
       total += __reduce_add_sync(kFull, static_cast<unsigned>(t));
+      most = max(most, __reduce_max_sync(kFull, t));
     }
     if (blockIdx.x == 0 && warp == 0 && __any_sync(kFull, bad) && lane == 0)
       atomicOr(p.err, static_cast<int>(MQA_DEVERR_SEQ_LEN));
     total *= units;
+    bool placed = false;
     run_len = total < 1ull << 31 ? static_cast<unsigned>(total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
     run_len = max(run_len, static_cast<long long>(p.min_tiles));
-    start = run_len * blockIdx.x;
-    run = static_cast<int>(max(0ll, min(run_len, static_cast<long long>(total) - start)));
+    // Parts of units where each has two and more and the longest is not much longer than a run: a block has one unit then (8 x 8
+    // units of 32 tiles 14 us, in runs 19; 64 units of 128 tiles for 32 query rows 51, in runs 59).
+    if (p.parts > 1 && (most + p.parts - 1) / p.parts <= run_len + run_len / 2 + 4) {
+      part_of_unit(p.parts, p.min_part);
+      placed = true;
+    } else {
+      at.b = at.u = at.base = 0;
+      at.s = {0, 0, 0, 1};
+      start = run_len * blockIdx.x;
+      run = static_cast<int>(max(0ll, min(run_len, static_cast<long long>(total) - start)));
+    }
     long long seen = 0;  // tiles of the sequences before (of one unit each)
-    at.b = at.u = at.base = 0;
-    at.s = {0, 0, 0, 1};
-    for (int b0 = 0; run > 0 && b0 < p.batch; b0 += 32) {
+    for (int b0 = 0; !placed && run > 0 && b0 < p.batch; b0 += 32) {
       const int t = b0 == 0 ? mine : tiles_of(b0 + lane);
       unsigned upto = t;
 #pragma unroll
@@ -351,13 +371,15 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
     const int t = fill_t + at_row;
     return at_row < kU4Tile && t < fill.s.len && t + piece > fill.s.lo;
   };
-  auto look = [&]() {  // tile fill_k's place, and its pages (looked up one fill ahead)
-    if (fill_k >= run) return;
+  const int page_shift = PAGED ? __ffs(p.page_size) - 1 : 0;
+  auto enter = [&]() {  // tile fill_k is the first of its unit, or of the run, that is filled here
     while (fill_k >= fill.end()) fill.next(p, units);
     head = fill.u / p.row_blocks;
     if (!PAGED) head += fill.b * p.h_kv;
     fill_t = (fill.s.first + fill_k - fill.base) * kU4Tile;
-    if (PAGED) page = wanted() ? p.block_table[static_cast<long long>(fill.b) * p.max_pages + (fill_t + at_row) / p.page_size] : -1;
+  };
+  auto look = [&]() {  // this lane's page of tile fill_k (looked up one fill ahead)
+    if (PAGED && fill_k < run && wanted()) page = p.block_table[static_cast<long long>(fill.b) * p.max_pages + ((fill_t + at_row) >> page_shift)];
   };
   auto fill_next = [&](int w, int st) {  // tile fill_k < run; the stage is empty
     const uint32_t bar = full(w, st);
@@ -366,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
     // (a part of a unit may have been written and read there by threads, the tile comes by the async proxy)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (PAGED) {
-      const bool copy = page >= 0 && page < p.num_pages;
-      if (!copy && kind == 0 && wanted()) atomicOr(p.err, static_cast<int>(MQA_DEVERR_PAGE_RANGE));
+      const bool seen = wanted(), copy = seen && page >= 0 && page < p.num_pages;
+      if (seen && !copy && kind == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_PAGE_RANGE));
       const int copies = __popc(__ballot_sync(kFull, copy)) / 4;
       if (lane == 0) mbar_arrive_expect_tx(bar, copies * piece * (2 * C::kCode + 8));
       __syncwarp();
@@ -376,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
         if (kind == 0)
           tma_load_4d(dst, &tmap_v, 0, in_page, head, page, bar);
         else
-          bulk_g2s(dst, from + ((static_cast<long long>(page) * p.h_kv + head) * p.page_size + in_page) * size, piece * size, bar);
+          bulk_g2s(dst, from + (((static_cast<long long>(page) * p.h_kv + head) << page_shift) + in_page) * size, piece * size, bar);
       }
     } else {
       // (the capacity is a multiple of 4 rows: copies of 16 bytes; the tensor map's are whole tiles)
@@ -390,10 +412,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
     }
     ++issued;
     fill_k += kWarps;
-    if (!PAGED && fill_k < min(run, fill.end()))
-      fill_t += kWarps * kU4Tile;
-    else
-      look();
+    fill_t += kWarps * kU4Tile;
+    if (fill_k >= fill.end() && fill_k < run) enter();
+    look();
   };
   // A unit's query rows: lane (r, c) has row r of an n tile, quarter c of its dims.
   auto q_row = [&](const Place& u, int n) -> const float* {  // null past the last row
@@ -419,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
   };
   bool dead = false;  // a wait ran out
   // before the append has ended only a tile without new rows
+  if (fill_k < run) enter();
   look();
   if (p.early && fill_k < run && fill_t + kU4Tile <= fill.s.len - p.n_new) fill_next(warp, 0);
   grid_dependency_wait();
@@ -976,8 +998,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
     }
     if (warp == merger) {
       if (at.base < 0) {  // other blocks have parts of it
-        const long long first = (start + at.base) / run_len, last = blockIdx.x;
-        float* mine = p.part + 2 * blockIdx.x * static_cast<long long>(C::kRows * (D + 2));
+        const long long first = (start + at.base) / run_len, last = me;
+        float* mine = p.part + 2 * me * static_cast<long long>(C::kRows * (D + 2));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -1064,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
     // Other blocks have parts of the unit: this one's is written, and the last block to say so merges them, in the order
     // of the blocks. The place of a unit that the block did not begin is the first of its two.
     const int first = static_cast<int>((start + at.base) / run_len), last = static_cast<int>((start + at.end() - 1) / run_len);
-    float* mine = p.part + (2 * blockIdx.x + (at.base < 0 ? 0 : 1)) * static_cast<long long>(C::kRows * (D + 2));
+    float* mine = p.part + (2 * me + (at.base < 0 ? 0 : 1)) * static_cast<long long>(C::kRows * (D + 2));
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll

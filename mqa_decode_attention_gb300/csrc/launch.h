@@ -127,8 +127,9 @@ struct U4Params {
   void* out;
   int out_dtype;
   float* lse_out;
-  int whole;         // 1: one block for each unit, no workspace; 0: equal runs
+  int whole;         // 1: one block for each unit, no workspace; 0: parts of units or equal runs
   int min_tiles;     // a run is at least this long
+  int parts, min_part;  // parts of a unit, a block each, and their least tiles, where that is no longer than the runs are
   int32_t* arrived;  // [blocks] zero: blocks that have left a partial of the unit that starts in block c
   float* part;       // [2 blocks] partial results
   int32_t* err;

@@ -59,7 +59,7 @@ def _read(lib, lay, **kw):
     return lib.kv_read_rows(ctypes.byref(lay), a["n"], a["start"], a["rows"], a["k"], a["v"], a["dt"], a["err"], None)
 
 
-PAGED = _layout(paged=1, capacity=0, page_size=16, num_pages=32, max_pages_per_seq=16, block_table=FAKE)
+PAGED = _layout(paged=1, capacity=0, page_size=16, num_pages=32, max_pages_per_seq=256, block_table=FAKE)
 
 
 @pytest.mark.parametrize("call", [_attend, _step, _norm, _read])
@@ -83,7 +83,7 @@ def test_attention_refusals(lib, call):
         assert call(lib, _layout(), **bad) == BAD, bad
     assert call(lib, _layout(), dt=_abi.MQA_U8) == NOT
     assert call(lib, _layout(), variant=_abi.MQA_VARIANT_CUDA_CORE) == NOT
-    for lay, splits in ((_layout(), 2), (PAGED, 0)):  # equal runs, on any device
+    for lay, splits in ((_layout(), 2), (PAGED, 3)):
         assert call(lib, lay, splits=splits, ws=None) == WS
         assert call(lib, lay, splits=splits, size=100) == WS
 
@@ -100,18 +100,26 @@ def test_other_calls_refuse_four_bits(lib):
 
 
 def test_queries(lib):
-    """One split needs no workspace, equal runs one size whatever their number; the library's choice is one of the two."""
+    """One split needs no workspace, more than one a size whatever their number; the library's choice is one of the two."""
     for lay in (_layout(), PAGED):
         p = ctypes.byref(lay)
         size = [lib.mqa_workspace_size_multi(p, 1, 100, n, 0) for n in (1, 2, 5)]
         assert size[0] == 0 < size[1] == size[2]
         choice = lib.mqa_choose_splits_multi(p, 1, 100, 0)
         assert choice in (1, 2) and lib.mqa_workspace_size_multi(p, 1, 100, 0, 0) == size[choice - 1]
-        assert choice == 2 or not lay.paged
-        assert lib.mqa_choose_splits_multi(p, 1, 300, 0) == -1
+        assert lib.mqa_choose_splits_multi(p, 1, 16 * 256 + 1, 0) == -1
         fused = ctypes.c_int32(7)
         assert lib.mqa_step_launches(p, 1, 100, 0, 0, ctypes.byref(fused)) == 2 and fused.value == 0
         assert lib.mqa_step_launches(p, 1, 100, 0, _abi.MQA_VARIANT_CUDA_CORE, None) == -1
+
+
+def test_choice_by_length(lib):
+    """Short contexts, or windows, need no workspace; long ones of a paged pool are shared."""
+    for kw, n, most, choice in ((dict(), 1, 1024, 1), (dict(), 1, 1025, 2), (dict(head_dim=64), 1, 2048, 1), (dict(head_dim=64), 1, 2049, 2),
+                                (dict(), 4, 512, 1), (dict(), 4, 513, 2), (dict(), 8, 256, 1), (dict(), 8, 257, 2),
+                                (dict(window=960), 1, 4096, 1), (dict(window=962), 1, 4096, 2)):
+        lay = _layout(paged=1, capacity=0, page_size=16, num_pages=32, max_pages_per_seq=256, block_table=FAKE, **kw)
+        assert lib.mqa_choose_splits_multi(ctypes.byref(lay), n, most, 0) == choice, (kw, n, most)
 
 
 def _opts(**kw):

@@ -4,32 +4,48 @@
 // With K = m + s c and V alike, the scaling stays outside the products:
 //   q . K_t = s_t (q . c_t) + m_t sum(q)
 //   O       = sum_t (p_t s_t) c_t + sum_t p_t m_t,
-// so the tensor cores multiply codes as they are. A code in bits 0-3 of a half
-// is the fp16 number c 2^-24, in bits 4-7 16 c 2^-24 (subnormal and small
-// normal numbers, exact): one AND for two codes makes an operand, a shift for
-// every second one. The 16 is taken out of q (K) and of the output (V), the
-// 2^-24 out of the scores' factor and of the output.
+// so the tensor cores multiply codes as they are. A code in the low bits of a
+// half is the fp16 number c 2^-24, and the byte of two codes (c_even + 16 c_odd)
+// 2^-24, both exact: an AND each makes an operand, without a shift or a
+// conversion. So K's even places meet q_even - q_odd / 16, its odd ones q_odd / 16,
+// and V's odd dims are (both - even) / 16 of what comes out. The 2^-24 goes into
+// the scores' factor and the output.
 //
-// q enters as fp16 (11 bits), each row scaled by a power of two to a largest
+// q enters as fp16 (11 bits), 8 rows scaled by one power of two to a largest
 // value in [2^13, 2^14); sum(q) is that of the rounded values, since s c and m
 // cancel in part. p s enters as fp16 too: with E the power of two above the
 // largest s a warp has met (a running exponent, as the softmax's running maximum)
-// p s 2^(11 - E) has its 11 bits down to 2^-25 of the largest. Scores, maxima, sums and O are
-// fp32. A maximum is only followed when a score passes it by more than 4 (in
-// log2), so p <= 16.
+// p s 2^(11 - E) has its 11 bits down to 2^-25 of the largest. Scores, maxima,
+// sums and O are fp32. A maximum is only followed when a score passes it by more
+// than 4 (in log2), so p <= 16. Every two tiles 8 sum(p s) is taken from O, which
+// makes the codes -8 to 7: else O and sum p m grow with the number of tokens
+// while what they leave does not (131072 tokens: error 1.7e-3, without 2.5e-3).
 //
-// A warp takes 8 NT query rows of one kv head and tiles of 32 tokens: S^T = K Q^T
+// A warp takes 8 NT query rows of one kv head and tiles of 64 tokens: S^T = K Q^T
 // (m16n8k16, tokens on the rows), softmax over the lanes that hold a column,
 // P^T transposed in registers (movmatrix), O^T += V^T P^T (dims on the rows, so
-// O's columns are S's). Codes stream through a ring of stages of its own, filled
-// with bulk copies by the warp itself: four warps of a block share a run of
-// tiles and meet at the end of a unit only (unit: sequence, kv head, block of
-// query rows).
+// O's columns are S's): nothing but K, V and q passes through shared memory.
+// Codes stream through a ring of two stages of its own, filled with bulk copies
+// by the warp itself: four warps of a block meet at the end of a unit only (unit:
+// sequence, kv head, block of query rows).
 //
-// The tiles of all units in order are cut into equal runs, one for each block
-// (as many as are resident at once), so lengths of any spread load all SMs
-// alike. A unit that several blocks share is merged by the last of them to
-// arrive, in the order of the blocks, so that equal calls give equal bits.
+// Who does what: a block takes a whole unit; or all resident blocks share the
+// tiles, a unit in equal parts, or all units in order cut into equal runs, so
+// that lengths of any spread load all SMs alike. A unit that several blocks share
+// is merged by the last of them to arrive, in the order of the blocks, so that
+// equal calls give equal bits. (Both sides of these choices are measured where
+// they are made.)
+//
+// What bounds it. Up to 8 rows with 3 blocks on every SM: HBM (1024 units of 8192
+// tokens 187 us, 6.1 TB/s; pages of 64 tokens 202, of 16, whose tile is 16 copies,
+// 232). With fewer units the chain products - softmax - products of a warp, 1.3 us
+// a tile (256 units of 4096 tokens 32 us, 4.4 TB/s), at the least 5.5 us for the
+// launch, the first tile and the last merge. 9 to 32 rows: the tensor pipes, 256
+// multiply-adds a cycle and scheduler with mma.sync, half busy, since the registers
+// leave two warps to a scheduler (64 MQA units of 8192 tokens 51 us, floor by
+// products 15). For runs four warps and three blocks on an SM were the best of
+// 6 x 2, 8 x 1 and 12 x 1; a fifth warp that fills the rings cost its registers
+// more than it gave.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -41,14 +57,13 @@
 namespace mqa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kBoost = 11;      // p s 2^(kBoost - E), p <= 2^kSlack
 constexpr float kSlack = 4.f;
 constexpr uint32_t kFull = 0xffffffffu;
 
-template <int D, int NT, int STAGES>
+template <int D, int NT, int STAGES, int WARPS>
 struct Cfg {
+  static constexpr int kWarps = WARPS;
   static constexpr int kMt = NT == 1 ? 4 : NT == 2 ? 2 : 1;      // tiles of 16 tokens whose scores are held at a time
   static constexpr int kCode = D / 2;              // bytes of a row's codes
   static constexpr int kTileCodes = kU4Tile * kCode;
@@ -242,9 +257,10 @@ __device__ __forceinline__ void write_rows(const U4Params& p, int b, int j, int 
     }
 }
 
-template <int D, int NT, bool PAGED, int STAGES, int CTAS>
-__global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_constant__ CUtensorMap tmap_v, const U4Params p) {
-  using C = Cfg<D, NT, STAGES>;
+template <int D, int NT, bool PAGED, int STAGES, int CTAS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_constant__ CUtensorMap tmap_v, const U4Params p) {
+  using C = Cfg<D, NT, STAGES, WARPS>;
+  constexpr int kWarps = WARPS, kThreads = 32 * WARPS;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
@@ -284,21 +300,23 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
   int run;             // tiles of the run
   long long start = 0, run_len = 1;  // place of the run among all tiles, length of the runs
   int me = blockIdx.x;  // place of this block's work in the order of the tiles
-  // one of `parts` equal parts of a unit; the first parts of all units go to the first blocks, which are spread over the SMs
-  auto part_of_unit = [&](int parts, int least) {
+  // one of the equal parts of a unit, of which the first `more` units have one more than the others; the first parts of all
+  // units go to the first blocks, which are spread over the SMs
+  auto part_of_unit = [&](int parts, int more, int least) {
     const int all = p.batch * units, part = blockIdx.x / all, unit = blockIdx.x - part * all;
-    me = unit * parts + part;
+    const int of = parts + (unit < more ? 1 : 0);
+    me = unit * parts + min(unit, more) + part;
     at.b = unit / units;
     at.u = unit - at.b * units;
-    at.s = part < parts ? span_of(p, p.seq_lens[at.b]) : Span{0, 0, 0, 0};
-    const int per = max(least, (at.s.tiles + parts - 1) / parts);
+    at.s = part < of ? span_of(p, p.seq_lens[at.b]) : Span{0, 0, 0, 0};
+    const int per = max(least, (at.s.tiles + of - 1) / of);
     at.base = -part * per;
     run = max(0, min(per, at.s.tiles - part * per));
     run_len = per;
     start = run_len * me;
   };
   if (p.whole) {
-    part_of_unit(1, 1);
+    part_of_unit(1, 0, 1);
     if (run == 0 && at.u == 0 && threadIdx.x == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_SEQ_LEN));
   } else {
     // (every warp finds it for itself; 32 sequences at a time, the first 32 kept)
@@ -319,10 +337,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
     bool placed = false;
     run_len = total < 1ull << 31 ? static_cast<unsigned>(total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
     run_len = max(run_len, static_cast<long long>(p.min_tiles));
-    // Parts of units where each has two and more and the longest is not much longer than a run: a block has one unit then (8 x 8
-    // units of 32 tiles 14 us, in runs 19; 64 units of 128 tiles for 32 query rows 51, in runs 59).
-    if (p.parts > 1 && (most + p.parts - 1) / p.parts <= run_len + run_len / 2 + 4) {
-      part_of_unit(p.parts, p.min_part);
+    // Parts of units where the longest is not much longer than a run, in which a change of unit costs as much as some 16
+    // tiles (8 x 8 units of 32 tiles 14 us, in runs 19; 160 units of 64 tiles 28 and 31; 256 units of 128 tiles 67 and 62; 64
+    // units of 128 tiles for 32 query rows 51 and 59).
+    if (p.parts > 0 && (most + p.parts - 1) / p.parts <= run_len + run_len / 2 + 16) {
+      part_of_unit(p.parts, gridDim.x - p.parts * p.batch * units, p.min_part);
       placed = true;
     } else {
       at.b = at.u = at.base = 0;
@@ -355,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
   if (run <= 0) return;  // the whole block
 
   // -------------------------------------------------- filling the rings
-  // Tile k of the run goes to warp k % 4, into stage k / 4 % STAGES of its ring. Four lanes, each a copy: V codes (through a tensor map, so that they land swizzled), K codes, K
-  // pairs, V pairs; of a paged pool four lanes for each page.
+  // Tile k of the run goes to warp k % 4, into stage k / 4 % STAGES of its ring. Four lanes, each a copy: V codes (through a
+  // tensor map, so that they land swizzled), K codes, K pairs, V pairs; of a paged pool four lanes for each page.
   Place fill = at;
   int fill_k = warp, issued = 0;
   int fill_t = 0, head = 0, page = 0;  // the next tile's first token, its kv head, this lane's page of it
@@ -1029,8 +1048,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
   }
 
   // ------------------------------------------------ the end of the run
-  // Every warp leaves its part of the last unit in its ring; then each has a quarter of the dims, of all four.
-  constexpr int kQuarter = C::kM / kWarps;
+  // Every warp leaves its part of the last unit in its ring; then each of four has a quarter of the dims, of all parts.
+  constexpr int kQuarter = C::kM / 4;
+  const bool joins = warp < 4;
   float2 acc[NT][kQuarter][2];
   auto clear = [&]() {
 #pragma unroll
@@ -1070,6 +1090,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
   clear();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
+    if (!joins) break;
     const float4* src = reinterpret_cast<const float4*>(smem + stage_at(w, end_stage[w]));
     const float2* ml = reinterpret_cast<const float2*>(smem + C::kEnd + w * C::kEndStep);
 #pragma unroll
@@ -1081,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
     }
   }
   if (p.whole || (at.base >= 0 && at.end() == run)) {
-    write_rows(p, at.b, j, row0, top, sum, acc, warp * kQuarter);
+    if (joins) write_rows(p, at.b, j, row0, top, sum, acc, warp * kQuarter);
   } else {
     // Other blocks have parts of the unit: this one's is written, and the last block to say so merges them, in the order
     // of the blocks. The place of a unit that the block did not begin is the first of its two.
@@ -1089,6 +1110,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
     float* mine = p.part + (2 * me + (at.base < 0 ? 0 : 1)) * static_cast<long long>(C::kRows * (D + 2));
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      if (!joins) break;
 #pragma unroll
       for (int i = 0; i < kQuarter; ++i)
         reinterpret_cast<float4*>(mine)[(n * C::kM + warp * kQuarter + i) * 32 + lane] =
@@ -1111,7 +1133,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) attn_u4_kernel(const __grid_co
     __syncthreads();
     for (int which = 0; which < 2; ++which) {
       volatile int* todo = flag + 5 * which;
-      if (todo[0] >= 0) continue;
+      if (todo[0] >= 0 || !joins) continue;
       const int u = todo[2], from_block = todo[3], to_block = todo[4], ju = u / p.row_blocks;
       constexpr int kAhead = NT == 1 ? 4 : 2;  // parts whose loads are issued together
       clear();
@@ -1156,10 +1178,10 @@ __global__ void u4_clear_kernel(int32_t* arrived, int count) {
   for (int i = threadIdx.x; i < count; i += blockDim.x) arrived[i] = 0;
 }
 
-template <int D, int NT, bool PAGED, int STAGES, int CTAS>
+template <int D, int NT, bool PAGED, int STAGES, int CTAS, int WARPS>
 cudaError_t launch_u4_t(const U4Params& p, const CUtensorMap& tmap_v, int ctas, bool clear, cudaStream_t stream) {
-  using C = Cfg<D, NT, STAGES>;
-  const auto kernel = attn_u4_kernel<D, NT, PAGED, STAGES, CTAS>;
+  using C = Cfg<D, NT, STAGES, WARPS>;
+  const auto kernel = attn_u4_kernel<D, NT, PAGED, STAGES, CTAS, WARPS>;
   // (an attribute of the function on the current device: set on each call, as it costs nothing beside the launch)
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
@@ -1170,7 +1192,7 @@ cudaError_t launch_u4_t(const U4Params& p, const CUtensorMap& tmap_v, int ctas, 
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.whole ? static_cast<long long>(p.batch) * p.h_kv * p.row_blocks : ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * WARPS);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1186,9 +1208,15 @@ constexpr int kCtas1 = 3, kCtas2 = 2, kCtas4 = 2;
 
 template <int D, bool PAGED>
 cudaError_t launch_u4_d(const U4Params& p, const CUtensorMap& tv, int ctas, bool clear, cudaStream_t stream) {
-  if (p.rows <= 8) return launch_u4_t<D, 1, PAGED, kStages, kCtas1>(p, tv, ctas, clear, stream);
-  if (p.rows <= 16) return launch_u4_t<D, 2, PAGED, kStages, kCtas2>(p, tv, ctas, clear, stream);
-  return launch_u4_t<D, 4, PAGED, kStages, kCtas4>(p, tv, ctas, clear, stream);
+  if (p.rows <= 8) {
+    // A unit a block, two blocks an SM at most: six warps a block (256 units of 64 tiles 34.5 us with four, 32.4 with six, of
+    // 256 tiles 119 and 106; 456 units, which four warps take three blocks an SM of, 45 and 55).
+    if (p.whole && static_cast<long long>(p.batch) * p.h_kv <= ctas / kCtas1 * 2)
+      return launch_u4_t<D, 1, PAGED, kStages, 2, 6>(p, tv, ctas, clear, stream);
+    return launch_u4_t<D, 1, PAGED, kStages, kCtas1, 4>(p, tv, ctas, clear, stream);
+  }
+  if (p.rows <= 16) return launch_u4_t<D, 2, PAGED, kStages, kCtas2, 4>(p, tv, ctas, clear, stream);
+  return launch_u4_t<D, 4, PAGED, kStages, kCtas4, 4>(p, tv, ctas, clear, stream);
 }
 
 }  // namespace

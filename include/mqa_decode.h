@@ -147,7 +147,7 @@ typedef enum mqa_variant {
  * k_scale_zero / v_scale_zero (bf16 [batch, h_kv, capacity, 2], or [num_pages,
  * h_kv, page_size, 2]); the value is m + s * code. k_cache / v_cache have
  * head_dim / 2 bytes in the place of head_dim elements; a contiguous capacity
- * is a multiple of 4. The append rounds the turned key once to bf16, as for a
+ * is a multiple of 4, the tokens of a sequence at most 2^31 - 1024. The append rounds the turned key once to bf16, as for a
  * bf16 cache, and stores the bf16 rows of k and v so: m = the row's minimum, s
  * = the smallest bf16 with 15 s >= maximum - m, code = (x - m) / s rounded to
  * nearest, ties to even, every decision exact. Magnitudes above 2^126 are taken
@@ -160,8 +160,8 @@ typedef enum mqa_variant {
  * head, block of up to 32 query rows), no workspace; > 1 = the cached tokens
  * shared by as many blocks as are resident, whatever the number; 0 = the
  * library's choice of the two, by the bound on the lengths (mqa_choose_splits:
- * 1 or 2). Calls that may
- * overlap on the GPU need a workspace each. The query is rounded to fp16 (11
+ * 1 or 2). Calls that may overlap on the GPU need a workspace each. The query is
+ * rounded to fp16 (8 of a kv head's rows by one power of two; 11
  * bits), the probabilities times s to 11 bits; the values of a window's or a
  * sequence's tokens that a query does not see are multiplied by a zero
  * probability, so they have to be finite; rows outside [0, L), and before the

@@ -38,6 +38,9 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 bool is_pow2(long long x) { return x > 0 && (x & (x - 1)) == 0; }
 
+long long token_limit(const mqa_kv_layout* L) {
+  return L->paged ? static_cast<long long>(L->max_pages_per_seq) * L->page_size : L->capacity;
+}
 
 mqa_status check_layout(const mqa_kv_layout* L) {
   if (L == nullptr) return MQA_ERR_INVALID_ARG;
@@ -64,11 +67,9 @@ mqa_status check_layout(const mqa_kv_layout* L) {
     if (!aligned(L->block_table, 4)) return MQA_ERR_INVALID_ARG;
     if (static_cast<long long>(L->max_pages_per_seq) * L->page_size > (1ll << 31) - 1) return MQA_ERR_INVALID_ARG;
   }
+  // (token indexes of a few tiles past the last one are formed in 32 bits)
+  if (L->cache_dtype == MQA_U4 && token_limit(L) > (1ll << 31) - 1024) return MQA_ERR_UNSUPPORTED;
   return MQA_OK;
-}
-
-long long token_limit(const mqa_kv_layout* L) {
-  return L->paged ? static_cast<long long>(L->max_pages_per_seq) * L->page_size : L->capacity;
 }
 
 int resolve_variant(const mqa_kv_layout* L, int variant) {
@@ -523,6 +524,8 @@ struct TreeAppend {
 mqa_status norm_append(const mqa_kv_layout* layout, int n_new, const void* q_new, const void* k_new, const void* v_new,
                        const int32_t* pos, const mqa_norm_rope* options, double rope_base, float* q_rot, int32_t* zero,
                        int zero_count, int32_t* err_word, cudaStream_t stream) {
+  // (a block's tokens are counted past the last one)
+  if (static_cast<long long>(layout->batch) * n_new > (1ll << 31) - 64) return MQA_ERR_INVALID_ARG;
   NormAppendParams p;
   std::memset(&p, 0, sizeof(p));
   p.batch = layout->batch;

@@ -262,6 +262,30 @@ def test_out_of_range(m):
         _check(c, before, x, pos, q_rot, only=[0] if page else [0, 3])
 
 
+@pytest.mark.parametrize("kind", CACHES)
+def test_places_of_16_bytes(m, kind):
+    """Outputs whose addresses are multiples of 16 bytes, not of 32: the append's query, rows read back."""
+    for d, page in ((128, 0), (64, 16)):
+        c = Cache(m, kind, 3, 3, d, 70, 9, page, seed=9)
+        x = _inputs(kind, 3, 2, 9, 3, d, 19)
+        before = c.snapshot()
+        memory = torch.full((3 * 2 * 9 * d + 8,), 9.0, device=DEV)
+        q_rot, err = _run(m, c, 2, x, [0, 31, 68], q_rot=memory[4:-4].view(3, 2, 9, d))
+        assert err == 0 and torch.all(memory[:4] == 9.0) and torch.all(memory[-4:] == 9.0)
+        _check(c, before, x, [0, 31, 68], q_rot)
+        for dt, step in ((torch.bfloat16, 8), (torch.float32, 4)):
+            aligned = [torch.empty(3, 3, 70, d, dtype=dt, device=DEV) for _ in "kv"]
+            shifted = [torch.full((3 * 3 * 70 * d + 2 * step,), 9.0, dtype=dt, device=DEV) for _ in "kv"]
+            err = _i32([0])
+            m.kv_read_rows(c.layout, None, None, *aligned, err)
+            m.kv_read_rows(c.layout, None, None, *(t[step:-step].view(3, 3, 70, d) for t in shifted), err)
+            torch.cuda.synchronize()
+            assert int(err) == 0
+            for a, t in zip(aligned, shifted):
+                assert torch.equal(t[step:-step].view_as(a).nan_to_num(7.0), a.nan_to_num(7.0))
+                assert torch.all(t[:step] == 9.0) and torch.all(t[-step:] == 9.0)
+
+
 def test_not_finite(m):
     """A key with a value that is not finite: NaN in its row only."""
     c = Cache(m, "bf16", 2, 2, 64, 4, 2)

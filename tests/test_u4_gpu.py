@@ -98,6 +98,38 @@ def test_attention(m, name, splits):
     _check(c, out, lse, scale)
 
 
+RUNS = {
+    # name: (hq, hkv, d, n_new, page, window)
+    "rows4": (32, 8, 128, 1, 0, 0),
+    "rows8_paged": (64, 8, 128, 1, 16, 0),
+    "rows16": (32, 8, 128, 4, 0, 0),
+    "rows32_paged_d64": (32, 8, 64, 8, 64, 0),
+    "window_d64": (24, 8, 64, 1, 0, 100),
+    "rows9_window_paged": (24, 8, 128, 3, 32, 200),
+}
+
+
+@pytest.mark.parametrize("name", list(RUNS))
+def test_more_units_than_blocks(m, name):
+    """480 units of 1 to 40 tiles: every block takes a run of tiles through several of them."""
+    hq, hkv, d, n, page, window = RUNS[name]
+    lens = [int(x) for x in np.random.default_rng(50).integers(n, 400, 60)]
+    lens[17], lens[18], lens[19], lens[59] = 2500, n, 64, 65
+    c = U4Case(hq, hkv, d, lens, n, page, window, seed=51)
+    out, lse, err = _attend(m, c, splits=2)
+    assert err == 0
+    _check(c, out, lse, 1 / math.sqrt(d), skip=set(range(60)) - {0, 1, 16, 17, 18, 19, 20, 37, 58, 59})
+    again, lse2, err = _attend(m, c, splits=2)
+    assert err == 0 and torch.equal(again, out) and torch.equal(lse2, lse)
+    one, lse1, err = _attend(m, c, splits=1)
+    assert err == 0
+    _check(c, one, lse1, 1 / math.sqrt(d), skip=set(range(60)) - {17, 18, 37})
+    # Both round q alike. p s to 11 bits moves either by 2^-11 of the values' range (8 at most here), fp32 sums by 2^-16 of
+    # it, and each is rounded to bf16; scores are below 60, their fp32 parts 2^-18 of them.
+    assert torch.all((one.float() - out.float()).abs() <= 16 * (2.0 ** -11 + 2.0 ** -16) + 1.01 * 2.0 ** -7 * out.float().abs())
+    assert torch.all((lse1 - lse).abs() <= 2 * 61 * 2.0 ** -18)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.1, 0.5])
 def test_scales(m, scale):
     c = U4Case(8, 2, 128, [50, 3, 200], 2, seed=5)
@@ -433,12 +465,11 @@ def test_two_streams(m):
         _check(c, b.out.view(2, 1, 16, 128), b.lse.view(2, 1, 16), 1 / math.sqrt(128))
 
 
-@pytest.mark.parametrize("splits", [0, 1])
-def test_timeout_then_normal_call(m, splits):
+@pytest.mark.parametrize("splits,B,hkv,L", [(2, 8, 2, 40000), (1, 64, 8, 4096), (1, 32, 8, 4096)])
+def test_timeout_then_normal_call(m, splits, B, hkv, L):
     """With a limit of 1 ns the waits for tiles run out (runs of many tiles, faster used than loaded): the call comes back,
     says so, and the next one gives what the call before gave."""
     g = torch.Generator(DEV).manual_seed(80)
-    B, hkv, L = (8, 2, 40000) if splits == 0 else (64, 8, 4096)
     codes = [torch.randint(0, 256, (B, hkv, L, 64), generator=g, dtype=torch.uint8, device=DEV) for _ in "kv"]
     pairs = [torch.rand(B, hkv, L, 2, generator=g, device=DEV).to(torch.bfloat16) for _ in "kv"]
     lay = m.layout_contiguous(codes[0], codes[1], 8, 0, pairs[0], pairs[1], cache_dtype=m.MQA_U4)
@@ -470,11 +501,11 @@ def test_units_shorter_than_a_block_has_warps(m, group):
     pairs = [torch.rand(B, hkv, 192, 2, generator=g, device=DEV).to(torch.bfloat16) for _ in "kv"]
     lay = m.layout_contiguous(codes[0], codes[1], hkv * group, 0, pairs[0], pairs[1], cache_dtype=m.MQA_U4)
     q, lens = torch.randn(B, hkv * group, 128, generator=g, device=DEV), torch.randint(1, L + 1, (B,), generator=g, dtype=torch.int32, device=DEV)
-    bufs, whole = m.DecodeBuffers.allocate(lay, L), m.DecodeBuffers.allocate(lay, L, num_splits=1)
+    bufs, whole = m.DecodeBuffers.allocate(lay, L, num_splits=2), m.DecodeBuffers.allocate(lay, L, num_splits=1)
     m.gqa_decode_attention(lay, q, lens, L, 0.09, 1, whole.out, whole.lse, err=whole.err)
     first = None
     for _ in range(40):
-        m.gqa_decode_attention(lay, q, lens, L, 0.09, 0, bufs.out, bufs.lse, bufs.workspace, err=bufs.err)
+        m.gqa_decode_attention(lay, q, lens, L, 0.09, 2, bufs.out, bufs.lse, bufs.workspace, err=bufs.err)
         torch.cuda.synchronize()
         assert int(bufs.err) == 0 and int(whole.err) == 0
         first = bufs.out.clone() if first is None else first

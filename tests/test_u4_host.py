@@ -70,6 +70,8 @@ def test_layout_refusals(lib, call):
     assert call(lib, _layout(v_scale_zero=FAKE + 8)) == BAD
     assert call(lib, _layout(capacity=254)) == NOT  # pairs are copied in units of 16 bytes
     assert call(lib, _layout(capacity=0)) == BAD
+    assert call(lib, _layout(capacity=2 ** 31 - 4)) == NOT
+    assert call(lib, _layout(paged=1, capacity=0, page_size=16, num_pages=4, max_pages_per_seq=(1 << 27) - 1, block_table=FAKE)) == NOT
     assert call(lib, _layout(k_cache=None)) == BAD
     assert call(lib, _layout(paged=1, page_size=8, num_pages=4, max_pages_per_seq=9, block_table=FAKE)) == NOT
     assert call(lib, _layout(cache_dtype=6)) == NOT

@@ -10,8 +10,10 @@
 //
 // What bounds it is the memory, once a value costs few instructions: with 8
 // values a thread, sizes that only the launch knew and conversions of codes
-// (a quarter of the rate; here a code is put into the low bits of 2^23) half of
-// the time was the issue of instructions.
+// (a quarter of the rate; here a code is put into a mantissa) half of the time
+// was the issue of instructions. 32 x 8 x 4096 rows of 4 bits as bf16 29 us, 5.8
+// TB/s, 86% of the copy rate (34 so); 24 ragged prefixes of uint8 pages as fp32
+// 42 us, 5.5 TB/s (48).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -37,12 +37,13 @@
 // they are made.)
 //
 // What bounds it. Up to 8 rows with 3 blocks on every SM: HBM (1024 units of 8192
-// tokens 187 us, 6.1 TB/s; pages of 64 tokens 202, of 16, whose tile is 16 copies,
-// 232). With fewer units the chain products - softmax - products of a warp, 1.3 us
-// a tile (256 units of 4096 tokens 32 us, 4.4 TB/s), at the least 5.5 us for the
-// launch, the first tile and the last merge. 9 to 32 rows: the tensor pipes, 256
-// multiply-adds a cycle and scheduler with mma.sync, half busy, since the registers
-// leave two warps to a scheduler (64 MQA units of 8192 tokens 51 us, floor by
+// tokens 187 us, 6.1 TB/s; pages of 64 tokens 203; of 16, whose tile is 8 bulk
+// copies, 218, and 232 with the pairs by bulk copies too). With fewer units the
+// chain products - softmax - products of a warp, 1.3 us a tile (256 units of 4096
+// tokens 32 us, 4.5 TB/s), at the least 5.5 us for the launch, the first tile and
+// the last merge. 9 to 32 rows: the tensor pipes, 256 multiply-adds a cycle and
+// scheduler with mma.sync, half busy, since the registers leave two warps to a
+// scheduler (64 MQA units of 8192 tokens 51 us, floor by
 // products 15). For runs four warps and three blocks on an SM were the best of
 // 6 x 2, 8 x 1 and 12 x 1; a fifth warp that fills the rings cost its registers
 // more than it gave.
@@ -171,6 +172,14 @@ __device__ __forceinline__ void split_codes(uint32_t x, uint32_t& c0, uint32_t& 
   c2 = b2 & 0x000f000fu;
 }
 
+// 16 bytes to shared memory, and an arrival when this thread's such copies have landed
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // normal e
 
 // the tiles that a sequence's units have: those with a token some row sees
@@ -287,7 +296,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
   for (int i = threadIdx.x; i < C::kWords; i += kThreads) flag[i] = 0;
   if (threadIdx.x == 0) {
     prefetch_tensormap(&tmap_v);
-    for (int i = 0; i < 2 * kWarps * STAGES; ++i) mbar_init(base + C::kBar + 8 * i, 1);
+    for (int i = 0; i < 2 * kWarps * STAGES; ++i) mbar_init(base + C::kBar + 8 * i, i < kWarps * STAGES ? 1 + 32 : 1);  // (see fill_next)
     mbar_init(q_come, 1);
     mbar_init(q_read, kWarps);
     for (int w = 0; w <= kWarps; ++w) mbar_init(chain + 8 * w, 1);
@@ -374,18 +383,17 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
   if (run <= 0) return;  // the whole block
 
   // -------------------------------------------------- filling the rings
-  // Tile k of the run goes to warp k % 4, into stage k / 4 % STAGES of its ring. Four lanes, each a copy: V codes (through a
-  // tensor map, so that they land swizzled), K codes, K pairs, V pairs; of a paged pool four lanes for each page.
+  // Tile k of the run goes to warp k % kWarps, into stage k / kWarps % STAGES of its ring. Two lanes, each a bulk copy: V
+  // codes (through a tensor map, so that they land swizzled) and K codes; of a paged pool two lanes for each page. The pairs
+  // of K and V, 16 bytes a lane: copies that lanes issue one after the other are what the warp waits for.
   Place fill = at;
   int fill_k = warp, issued = 0;
   int fill_t = 0, head = 0, page = 0;  // the next tile's first token, its kv head, this lane's page of it
-  const int kind = lane & 3;
-  const int size = kind < 2 ? C::kCode : 4;  // bytes of a row
-  const unsigned char* from = kind == 1   ? p.k_cache
-                              : kind == 2 ? reinterpret_cast<const unsigned char*>(p.k_sm)
-                                          : reinterpret_cast<const unsigned char*>(p.v_sm);
-  const int piece = PAGED ? min(p.page_size, kU4Tile) : kU4Tile;  // tokens of a copy
-  const int at_row = (lane >> 2) * piece;                         // a lane's first token in the tile
+  const int kind = lane & 1;
+  const int piece_shift = PAGED ? min(__ffs(p.page_size), __ffs(kU4Tile)) - 1 : 0, piece = PAGED ? 1 << piece_shift : kU4Tile;  // tokens of a copy
+  const int at_row = (lane >> 1) * piece;  // a lane's first token in the tile
+  const unsigned char* pairs_from = reinterpret_cast<const unsigned char*>(lane < 16 ? p.k_sm : p.v_sm);
+  const int pair_row = 4 * (lane & 15);
   auto wanted = [&]() {  // this lane's page has a token that is seen
     const int t = fill_t + at_row;
     return at_row < kU4Tile && t < fill.s.len && t + piece > fill.s.lo;
@@ -402,33 +410,40 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
   };
   auto fill_next = [&](int w, int st) {  // tile fill_k < run; the stage is empty
     const uint32_t bar = full(w, st);
-    const uint32_t dst = base + at_row * size +
-                         (kind < 2 ? stage_at(w, st) + (kind == 1 ? C::kTileCodes : 0) : pairs_at(w, st) + (kind == 3 ? 4 * kU4Tile : 0));
+    const uint32_t dst = base + at_row * C::kCode + stage_at(w, st) + (kind == 1 ? C::kTileCodes : 0);
+    const uint32_t pair_dst = base + pairs_at(w, st) + 16 * lane;
     // (a part of a unit may have been written and read there by threads, the tile comes by the async proxy)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (PAGED) {
       const bool seen = wanted(), copy = seen && page >= 0 && page < p.num_pages;
       if (seen && !copy && kind == 0) atomicOr(p.err, static_cast<int>(MQA_DEVERR_PAGE_RANGE));
-      const int copies = __popc(__ballot_sync(kFull, copy)) / 4;
-      if (lane == 0) mbar_arrive_expect_tx(bar, copies * piece * (2 * C::kCode + 8));
+      const int copies = __popc(__ballot_sync(kFull, copy)) / 2;
+      if (lane == 0) mbar_arrive_expect_tx(bar, copies * piece * (2 * C::kCode));
       __syncwarp();
+      const int pair_page = __shfl_sync(kFull, copy ? page : -1, 2 * (pair_row >> piece_shift));
+      if (pair_page >= 0)
+        copy16(pair_dst, pairs_from + 4 * (((static_cast<long long>(pair_page) * p.h_kv + head) << page_shift) +
+                                           ((fill_t + pair_row) & (p.page_size - 1))));
       if (copy) {
         const int in_page = (fill_t + at_row) & (p.page_size - 1);
         if (kind == 0)
           tma_load_4d(dst, &tmap_v, 0, in_page, head, page, bar);
         else
-          bulk_g2s(dst, from + (((static_cast<long long>(page) * p.h_kv + head) << page_shift) + in_page) * size, piece * size, bar);
+          bulk_g2s(dst, p.k_cache + (((static_cast<long long>(page) * p.h_kv + head) << page_shift) + in_page) * C::kCode, piece * C::kCode, bar);
       }
     } else {
       // (the capacity is a multiple of 4 rows: copies of 16 bytes; the tensor map's are whole tiles)
       const int n = min(kU4Tile, (fill.s.len - fill_t + 3) & ~3);
+      const long long row = head * p.capacity + fill_t;
+      if (pair_row < n) copy16(pair_dst, pairs_from + 4 * (row + pair_row));
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar, kU4Tile * C::kCode + n * (C::kCode + 8));
+        mbar_arrive_expect_tx(bar, (kU4Tile + n) * C::kCode);
         tma_load_3d(dst, &tmap_v, 0, fill_t, head, bar);
+        bulk_g2s(dst + C::kTileCodes, p.k_cache + row * C::kCode, n * C::kCode, bar);
       }
       __syncwarp();
-      if (lane - 1u < 3u) bulk_g2s(dst, from + (head * p.capacity + fill_t) * size, n * size, bar);
     }
+    arrive_copies(bar);
     ++issued;
     fill_k += kWarps;
     fill_t += kWarps * kU4Tile;

@@ -37,8 +37,8 @@
 // they are made.)
 //
 // What bounds it. Up to 8 rows with 3 blocks on every SM: HBM (1024 units of 8192
-// tokens 187 us, 6.1 TB/s; pages of 64 tokens 203; of 16, whose tile is 8 bulk
-// copies, 218, and 232 with the pairs by bulk copies too). With fewer units the
+// tokens 187 us, 6.1 TB/s; pages of 64 tokens 204; of 16, whose tile is 8 bulk
+// copies, 219, and 232 with the pairs by bulk copies too). With fewer units the
 // chain products - softmax - products of a warp, 1.3 us a tile (256 units of 4096
 // tokens 32 us, 4.5 TB/s), at the least 5.5 us for the launch, the first tile and
 // the last merge. 9 to 32 rows: the tensor pipes, 256 multiply-adds a cycle and

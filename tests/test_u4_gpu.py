@@ -349,7 +349,7 @@ STEP = {
 }
 
 
-@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("splits", [0, 1, 2])
 @pytest.mark.parametrize("name", list(STEP))
 def test_step(m, name, splits):
     """The step is the append and the attention over what it wrote, bit for bit, in two launches."""
@@ -391,7 +391,8 @@ def test_step_leaves_a_workspace_it_does_not_need(m):
     assert int(bufs.err) == 0 and bool((memory == 0xAB).all())
 
 
-def test_noalloc(m):
+@pytest.mark.parametrize("splits", [0, 1, 2])
+def test_noalloc(m, splits):
     c = U4Case(8, 2, 128, [500, 40], 1, seed=50)
     lay, err = c.layout(m), _i32([0])
     out = torch.empty(2, 8, 128, dtype=torch.bfloat16, device=DEV)
@@ -400,14 +401,15 @@ def test_noalloc(m):
     fn, vp = m.library().gqa_decode_attention_noalloc, ctypes.c_void_p
     fn.restype, q, lens = ctypes.c_int32, c.q.to(DEV), _i32(c.lens)
     st = fn(ctypes.byref(lay), vp(q.data_ptr()), vp(lens.data_ptr()), ctypes.c_int32(500), ctypes.c_float(1 / math.sqrt(128)),
-            ctypes.c_int32(0), vp(out.data_ptr()), ctypes.c_int32(0), None, ctypes.c_int32(0), vp(err.data_ptr()),
+            ctypes.c_int32(splits), vp(out.data_ptr()), ctypes.c_int32(0), None, ctypes.c_int32(0), vp(err.data_ptr()),
             vp(torch.cuda.current_stream().cuda_stream))
     torch.cuda.synchronize()
     assert st == 0 and int(err) == 0
     _check(c, out.view(2, 1, 8, 128), None, 1 / math.sqrt(128))
 
 
-def test_generation(m):
+@pytest.mark.parametrize("splits", [0, 2])
+def test_generation(m, splits):
     """Tokens decoded one after the other into an empty cache, through a captured graph that is replayed: each step's
     result is the attention over the quantised rows so far."""
     B, hq, hkv, d, steps = 2, 8, 2, 128, 40
@@ -417,17 +419,17 @@ def test_generation(m):
     c.k, c.ksm = torch.zeros(6, hkv, 16, d // 2, dtype=torch.uint8), torch.zeros(6, hkv, 16, 2, dtype=torch.bfloat16)
     c.v, c.vsm = c.k.clone(), c.ksm.clone()
     lay = c.layout(m)
-    bufs = m.DecodeBuffers.allocate(lay, steps)
+    bufs = m.DecodeBuffers.allocate(lay, steps, num_splits=splits)
     new = [torch.zeros(B, h, d, dtype=torch.bfloat16, device=DEV) for h in (hq, hkv, hkv)]
     pos, lens = _i32([0] * B), _i32([1] * B)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
-        m.decode_step(lay, *new, pos, lens, steps, bufs)
+        m.decode_step(lay, *new, pos, lens, steps, bufs, num_splits=splits)
     torch.cuda.current_stream().wait_stream(side)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        m.decode_step(lay, *new, pos, lens, steps, bufs)
+        m.decode_step(lay, *new, pos, lens, steps, bufs, num_splits=splits)
     K, V = np.zeros((B, hkv, steps, d)), np.zeros((B, hkv, steps, d))
     for t in range(steps):
         rows = [torch.randn(x.shape, generator=g).to(torch.bfloat16) for x in new]
@@ -445,6 +447,40 @@ def test_generation(m):
         c.values = lambda b, upto=None: (K[b, :, : t + 1], V[b, :, : t + 1])
         c.q = bufs.q_rot.cpu().view(B, 1, hq, d)
         _check(c, bufs.out.view(B, 1, hq, d), bufs.lse.view(B, 1, hq), 1 / math.sqrt(d))
+
+
+def test_two_graphs_share_a_workspace(m):
+    """Graphs of calls of different forms over one workspace, replayed one after the other on a stream."""
+    cases = [U4Case(16, 2, 128, [3000 + 1, 700], 1, seed=72, garbage=False), U4Case(32, 1, 128, [1300, 90, 2000], 2, 16, seed=73, garbage=False),
+             U4Case(8, 8, 64, [int(x) for x in range(1, 600, 10)], 1, seed=74, garbage=False)]
+    lays, calls, outs, graphs = [c.layout(m) for c in cases], [], [], []
+    ws = torch.empty(max(m.workspace_size(lay, max(c.lens), 2, n_new=c.n) for lay, c in zip(lays, cases)), dtype=torch.uint8, device=DEV)
+    err = _i32([0])
+    for c, lay in zip(cases, lays):
+        out, lse = torch.zeros(c.B, c.n, c.hq, c.d, device=DEV), torch.zeros(c.B, c.n, c.hq, device=DEV)
+        q, lens = c.q.to(DEV), _i32(c.lens)
+        calls.append(lambda c=c, lay=lay, q=q, lens=lens, out=out, lse=lse: m.gqa_decode_attention_multi(
+            lay, c.n, q, lens, max(c.lens), 1 / math.sqrt(c.d), 2, out, lse, ws, err=err))
+        outs.append((out, lse))
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    first = [(o.clone(), l.clone()) for o, l in outs]
+    for call in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    for _ in range(10):
+        for o, l in outs:
+            o.zero_(), l.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        for (o, l), (o1, l1) in zip(outs, first):
+            assert torch.equal(o, o1) and torch.equal(l, l1)
+    for c, (o, l) in list(zip(cases, outs))[:2]:
+        _check(c, o, l, 1 / math.sqrt(c.d))
 
 
 def test_two_streams(m):

@@ -206,7 +206,7 @@ int choose_splits(const mqa_kv_layout* L, int max_len_in, int variant, int n_new
     // One block for each unit, where the others' merging would cost more than its unequal load: for units of few tiles
     // (a tile's time goes with its dims and rows; head_dim 128 and 8 rows: 8 units of 16 tiles 10.0 us, shared 10.4, of 32
     // tiles 15.6 and 11.6; 160 units of 16 tiles 12.4 and 14.5), and for contiguous caches with units for more than half of
-    // the blocks (256 units of 64 tiles 34 us, shared 41; the lengths of a paged batch are taken as unequal).
+    // the blocks (256 units of 64 tiles 32 us, shared 38; the lengths of a paged batch are taken as unequal).
     const U4Plan c = u4_plan(L, n_new);
     long long span = max_len_in;
     if (L->window > 0) span = std::min(span, static_cast<long long>(L->window) + n_new - 1 + kU4Tile - 1);

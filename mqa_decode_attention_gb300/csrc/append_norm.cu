@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kNormThreads, 4) append_norm_kernel(const Norm
       }
       if (!__all_sync(0xffffffffu, settled)) exact_key<L>(k, w, norm_k, p.eps, cs, &s_low[tok][4 * at], key);
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i)  // (one copy of the code: what holds this kernel up first is its size)
+      for (int i = 0; i < 2; ++i)  // (one copy of the code: with more the warps wait for instructions)
         store_row<CACHE, L>(i ? p.v_cache : p.k_cache, i ? p.v_sz : p.k_sz, row, at, live, i ? v : key);
       continue;
     }

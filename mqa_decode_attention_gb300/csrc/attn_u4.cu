@@ -13,11 +13,17 @@
 //
 // q enters as fp16 (11 bits), 8 rows scaled by one power of two to a largest
 // value in [2^13, 2^14); sum(q) is that of the rounded values, since s c and m
-// cancel in part. p s enters as fp16 too: with E the power of two above the
-// largest s a warp has met (a running exponent, as the softmax's running maximum)
-// p s 2^(11 - E) has its 11 bits down to 2^-25 of the largest. Scores, maxima,
-// sums and O are fp32. A maximum is only followed when a score passes it by more
-// than 4 (in log2), so p <= 16. Every two tiles 8 sum(p s) is taken from O, which
+// cancel in part. p s enters as fp16 too. What has to keep its bits there is a
+// column's largest p s, whatever other rows hold: so the reference that a
+// column's p are relative to follows the maximum of score + log2 of the row's
+// size, not of the score alone. A row's size 2^l is the power of two above s and
+// |m| / 16, over 2^E and taken as 2^-60 at the least (E = 0, but where the rows of
+// the unit's first tile are far from 1); p s 2^(11 - E) has its 11 bits down to
+// 2^-25 of the column's largest, and p, which may be 2^64, and its sums are fp32.
+// (With p relative to the largest score, and 2^E above the largest s met, one row
+// of 2^36 times the others' scale and no weight took all their codes.) Scores,
+// maxima, sums and O are fp32. The reference is only followed when it is passed
+// by more than 4 (in log2). Every two tiles 8 sum(p s) is taken from O, which
 // makes the codes -8 to 7: else O and sum p m grow with the number of tokens
 // while what they leave does not (131072 tokens: error 1.7e-3, without 2.5e-3).
 //
@@ -58,8 +64,11 @@
 namespace mqa {
 namespace {
 
-constexpr int kBoost = 11;      // p s 2^(kBoost - E), p <= 2^kSlack
+constexpr int kBoost = 11;      // p s 2^(kBoost - E), p s <= 2^(E + kSlack)
 constexpr float kSlack = 4.f;
+// log2 of a row's size over 2^E: a smaller row counts as 2^kLeast (bounds p), one above 2^kMost moves E. (Parts of a unit
+// are merged by weights of down to 2^(kLeast - kMost), which fp32 holds.)
+constexpr float kLeast = -60.f, kMost = 66.f;
 constexpr uint32_t kFull = 0xffffffffu;
 
 template <int D, int NT, int STAGES, int WARPS>
@@ -559,11 +568,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
   // Columns 2 c, 2 c + 1 of each n tile as pairs. o: rows r (the even dims) and
   // r + 8 (even + 16 odd, until the unit ends). base_sum: sum p (m + 8 s).
   float2 o[NT][C::kM][2];
-  // ref: minus the reference of a column's exponents, -0 before its first score (and never -0 after); over: what a score may
-  // pass it by before it is followed (-inf while a column of the lane has had none).
+  // ref: minus the reference of a column's exponents, -0 before its first score (and never -0 after); over: what a score and
+  // its row's size may pass it by before it is followed (-inf while a column of the lane has had none).
   float2 ref[NT], sum[NT], base_sum[NT];
   float over;
-  constexpr float kNone = -0.f;
+  constexpr float kNone = -0.f, kNothing = -200.f;  // kNothing: log2 of the size of a row of zeros
   auto none = [](float x) { return __float_as_uint(x) == 0x80000000u; };
   // Sum of the operands p s, by the tensor cores: 8 times it is taken from o every few tiles, which makes the codes -8 to 7.
   // (Else o grows with the number of tokens while its sum with base_sum does not, and the rounding of the accumulators shows.)
@@ -668,8 +677,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
       for (int i = 0; i < C::kM; ++i) o[n][i][0] = o[n][i][1] = zero2;
     }
     over = -INFINITY;
-    int vexp = -100;  // every V scale so far is below 2^vexp = vlim; vf = 2^(kBoost - vexp)
-    float vlim = pow2(-100), vf = pow2(kBoost + 100);
+    // sizes of V rows are relative to 2^E: vf = 2^(kBoost - E), size_from = kSizeFrom + E; both 0 before a row that is not 0 has
+    // been met (0 operands of O then)
+    constexpr float kSizeFrom = 0x1p23f + 126.f;  // (a float's exponent bits e in the low bits of 2^23: 2^(e - 126) is above it)
+    float size_from = 0.f, vf = 0.f;
     if (!C::kQreg && k1 < run) {  // the next unit's rows of q into the L2 cache
       Place u = at;
       u.next(p, units);
@@ -808,14 +819,18 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
                 }
             }
         }
-        float vs[C::kMt][2], vmost = 0.f;
+        float vs[C::kMt][2], smost = 0.f, mmost = 0.f;
 #pragma unroll
         for (int mt = 0; mt < C::kMt; ++mt) {
           vs[mt][0] = u4_scale(vp[mt][0]), vs[mt][1] = u4_scale(vp[mt][1]);
-          vmost = max3(vmost, fabsf(vs[mt][0]), fabsf(vs[mt][1]));
+          smost = max3(smost, fabsf(vs[mt][0]), fabsf(vs[mt][1]));
+          mmost = max3(mmost, fabsf(u4_min(vp[mt][0])), fabsf(u4_min(vp[mt][1])));
         }
+        // log2 of the size of the lane's largest row: with its largest score a bound on what the reference follows
+        const float size = __uint_as_float(0x4b000000u | __float_as_uint(fmaxf(smost, 0.0625f * mmost)) >> 23) - size_from;
+        const float limit = over - fmaxf(size, kLeast);
         float2 most[NT];
-        bool moves = vmost >= vlim;
+        bool moves = size > kMost;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           most[n] = make_float2(fmaxf(s[0][n][0].x, s[0][n][1].x), fmaxf(s[0][n][0].y, s[0][n][1].y));
@@ -824,19 +839,45 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
             most[n].x = max3(most[n].x, s[mt][n][0].x, s[mt][n][1].x);
             most[n].y = max3(most[n].y, s[mt][n][0].y, s[mt][n][1].y);
           }
-          moves |= fmaxf(most[n].x, most[n].y) > over;
+          moves |= fmaxf(most[n].x, most[n].y) > limit;
         }
         if (__any_sync(kFull, moves)) {
-          const uint32_t big = __reduce_max_sync(kFull, vmost < INFINITY ? __float_as_uint(vmost) : 0u);
-          const int e2 = max(vexp, static_cast<int>(big >> 23) - 126);
-          const float down = pow2(max(vexp - e2, -126));
-          vexp = e2;
-          vlim = __uint_as_float(static_cast<uint32_t>(min(e2 + 127, 255)) << 23);
-          vf = pow2(kBoost - vexp);
+          float rel[C::kMt][2], big = kNothing;  // log2 of the rows' sizes
+#pragma unroll
+          for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t e = __float_as_uint(fmaxf(fabsf(vs[mt][h]), 0.0625f * fabsf(u4_min(vp[mt][h])))) >> 23;
+              rel[mt][h] = e == 0 || e == 255 ? kNothing : static_cast<float>(static_cast<int>(e) - 126);
+              big = fmaxf(big, rel[mt][h]);
+            }
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, off));
+          float e1 = 0.f, down = 1.f;
+          if (size_from != 0.f || big != kNothing) {
+            if (size_from == 0.f) {  // the first rows that are not 0
+              e1 = big < kLeast + 10.f || big > kMost - 6.f ? fmaxf(big, -110.f) : 0.f;
+            } else {
+              const float e0 = size_from - kSizeFrom;
+              e1 = fmaxf(e0, big - kMost);
+              down = pow2(max(static_cast<int>(e0 - e1), -126));
+            }
+            size_from = kSizeFrom + e1;
+            vf = pow2(kBoost - static_cast<int>(e1));
+          }
+#pragma unroll
+          for (int mt = 0; mt < C::kMt; ++mt) rel[mt][0] = fmaxf(rel[mt][0] - e1, kLeast), rel[mt][1] = fmaxf(rel[mt][1] - e1, kLeast);
           bool all = true;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float2 m = most[n];
+            float2 m = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+            for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                m.x = fmaxf(m.x, s[mt][n][h].x + rel[mt][h]);
+                m.y = fmaxf(m.y, s[mt][n][h].y + rel[mt][h]);
+              }
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
               m.x = fmaxf(m.x, __shfl_xor_sync(kFull, m.x, off));
@@ -930,7 +971,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       top[n] = make_float2(none(ref[n].x) ? -INFINITY : -ref[n].x, none(ref[n].y) ? -INFINITY : -ref[n].y);
-    const float out0 = pow2(min(max(vexp - kBoost, -126), 127)), out1 = 0x1p24f;
+    const float out0 = size_from == 0.f ? 0.f : pow2(static_cast<int>(size_from - kSizeFrom) - kBoost), out1 = 0x1p24f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll

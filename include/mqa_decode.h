@@ -161,7 +161,7 @@ typedef enum mqa_variant {
  * shared by as many blocks as are resident, whatever the number; 0 = the
  * library's choice of the two, by the bound on the lengths (mqa_choose_splits:
  * 1 or 2). Calls that may overlap on the GPU need a workspace each. The query is
- * rounded to fp16 (8 of a kv head's rows by one power of two; 11
+ * rounded to fp16 (each head's by a power of two of its own; 11
  * bits), the probabilities times s to 11 bits, down to 2^-25 of a query's largest
  * such product (of scales up to 2^60 apart); the values of a window's or a
  * sequence's tokens that a query does not see are multiplied by a zero

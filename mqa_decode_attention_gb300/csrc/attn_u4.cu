@@ -11,7 +11,7 @@
 // and V's odd dims are (both - even) / 16 of what comes out. The 2^-24 goes into
 // the scores' factor and the output.
 //
-// q enters as fp16 (11 bits), 8 rows scaled by one power of two to a largest
+// q enters as fp16 (11 bits), each row scaled by a power of two to a largest
 // value in [2^13, 2^14); sum(q) is that of the rounded values, since s c and m
 // cancel in part. p s enters as fp16 too. What has to keep its bits there is a
 // column's largest p s, whatever other rows hold: so the reference that a
@@ -512,7 +512,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
       const uint32_t m = __float_as_uint(q[i]) & 0x7fffffffu;
       most = max(most, m < 0x7f800000u ? m : 0u);
     }
-    most = __reduce_max_sync(kFull, most);  // (one factor for the 8 rows)
+    most = max(most, __shfl_xor_sync(kFull, most, 1));  // (a factor for each row)
+    most = max(most, __shfl_xor_sync(kFull, most, 2));
     const int e = min(max(static_cast<int>(most >> 23) - 127, -80), 127);  // 2^e <= largest < 2^(e + 1)
     // (two factors: their product may leave the range)
     const float up0 = pow2((13 - e) / 2), up1 = pow2((13 - e) - (13 - e) / 2);
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
     const int len = at.s.len;
     uint32_t qf[C::kQreg ? NT : 1][C::kM][2];
     float2 qs[C::kQreg ? NT : 1];  // sum(q), and
-    float f[C::kQreg ? NT : 1];    // the factor of the scores, times which qs is (NT = 4: read where they are used)
+    float2 f[C::kQreg ? NT : 1];   // the factor of the scores, times which qs is (NT = 4: read where they are used)
     if constexpr (C::kQreg) {
       if (!dead) dead = !__all_sync(kFull, mbar_wait(q_come, seg & 1, p.wait_ns));
 #pragma unroll
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
         float total, factor;
         operands(q4, qf[n], total, factor);
         qs[n] = make_float2(__shfl_sync(kFull, total, 8 * c), __shfl_sync(kFull, total, 8 * c + 4));
-        f[n] = factor;
+        f[n] = make_float2(__shfl_sync(kFull, factor, 8 * c), __shfl_sync(kFull, factor, 8 * c + 4));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(q_read);
@@ -782,18 +783,16 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
             const float ks = u4_scale(kp), km = u4_min(kp);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              float2 qn;
-              float fn;
+              float2 qn, fn;
               if constexpr (C::kQreg) {
                 qn = qs[n], fn = f[n];
               } else {
                 const float4 v = reinterpret_cast<const float4*>(smem + C::kQsum)[4 * n + c];
-                qn = make_float2(v.x, v.z), fn = v.y;
+                qn = make_float2(v.x, v.z), fn = make_float2(v.y, v.w);
               }
-              const float k_f = ks * fn;
               float2& x = s[mt][n][h];
-              x.x = fmaf(x.x, k_f, fmaf(km, qn.x, ref[n].x));
-              x.y = fmaf(x.y, k_f, fmaf(km, qn.y, ref[n].y));
+              x.x = fmaf(x.x, ks * fn.x, fmaf(km, qn.x, ref[n].x));
+              x.y = fmaf(x.y, ks * fn.y, fmaf(km, qn.y, ref[n].y));
             }
           }
         if (edge) {

@@ -34,6 +34,10 @@ def _attend(m, c, splits, out_dtype=torch.float32):
     return out.double().cpu().numpy(), lse.double().cpu().numpy()
 
 
+def _lse(s):
+    return s.max() + np.log(np.exp(s - s.max()).sum())
+
+
 def _check(c, out, lse):
     """Against 64 bits, with an error that goes by what a query's weights make of each row, not by the largest row.
 
@@ -72,9 +76,11 @@ def _check(c, out, lse):
                 worst = np.max(np.abs(got - want) / (tol + rounding(want, torch.float32)))
                 assert worst <= 1, f"sequence {b}, token {i}, head {h}: {worst} of the tolerance"
                 at = top + np.log(total)
-                # the sum of weights is off by a factor within exp(+-D) of each, its logarithm by the largest that counts
-                dl = np.log((p * np.exp(D)).sum()) + 2.0 ** -18 + 2.0 ** -20 * abs(at)
-                assert abs(lse[b, i, h] - at) <= max(dl, -np.log((p * np.exp(-D)).sum()) + 2.0 ** -18 + 2.0 ** -20 * abs(at)), (b, i, h)
+                # ln sum exp(s) is off by no more than it moves when every score does, up or down, by its D_t (which is not cut
+                # off here: the exponentials are taken in the logarithm)
+                D = terms * 2.0 ** -11 + (1 + terms) * 2.0 ** -18
+                up, down = (_lse(s + x) - at for x in (D, -D))
+                assert abs(lse[b, i, h] - at) <= max(up, -down) + 2.0 ** -18 + 2.0 ** -20 * abs(at), (b, i, h)
 
 
 FORMS = {
@@ -153,4 +159,14 @@ def test_constant_rows_alone(m, name):
         for t in range(c.lens[b]):
             c.vsm[c.slot(b, t)][..., 1] = 0.0 if t < 100 else 2.0 ** ((37 * t) % 80 - 40)
     c.ksm[..., 0], c.ksm[..., 1] = 1.0, -7.5
+    _check(c, *_attend(m, c, splits))
+
+
+@pytest.mark.parametrize("name", ["rows4", "rows16", "rows32"])
+def test_queries_of_very_different_sizes(m, name):
+    """Heads of one kv head whose queries are 2^36 apart: each keeps its bits."""
+    c, splits = _case(name, 8)
+    c.q = torch.randn(c.q.shape, generator=torch.Generator().manual_seed(9))
+    c.q *= torch.where(torch.arange(c.hq) % 4 == 2, 2.0 ** 36, 1.0)[None, None, :, None]
+    c.ksm[..., 0], c.ksm[..., 1] = 0.35, -2.6
     _check(c, *_attend(m, c, splits))

@@ -132,32 +132,31 @@ __device__ __forceinline__ Dd row_sum(Dd v) {
 
 // 1 / sqrt(mean + eps) of the row of d values that L lanes hold, by one Newton
 // step on the fp32 root: with r0 = (1 + e) / sqrt(h), r0 (1 + (1 - h r0^2) / 2)
-// is within 1.5 e^2. Squares that leave the fp32 range are formed of values
-// scaled by 2^-70. (All lanes of the warp take part.)
+// is within 1.5 e^2. Squares at the ends of the fp32 range, or beyond, are formed
+// of values scaled by 2^-70 or 2^60 (*scale): the root then is that of the scaled
+// row, which goes with x *scale. (All lanes of the warp take part.)
 template <int L>
-__device__ __noinline__ Dd inv_rms(const float (&x)[8], float eps) {
-  Dd sum = {0.f, 0.f}, low = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) sum = add(sum, two_prod(x[i], x[i]));
-  sum = row_sum<L>(sum);
-  float down = 1.f;
-  if (__any_sync(0xffffffffu, !(sum.h < 0x1p120f))) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) low = add(low, two_prod(x[i] * 0x1p-70f, x[i] * 0x1p-70f));
-    low = row_sum<L>(low);
-    if (!(sum.h < 0x1p120f)) {
-      down = 0x1p-70f;
-      sum = low;
-    }
-  }
+__device__ __noinline__ Dd inv_rms(const float (&x)[8], float eps, float* scale) {
   constexpr float inv_d = 1.f / (8 * L);  // a power of two
-  const Dd v = add({sum.h * inv_d, sum.l * inv_d}, {eps * (down * down), 0.f});
+  float sc = 1.f;
+  Dd v = {0.f, 0.f};
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    Dd sum = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = add(sum, two_prod(x[i] * sc, x[i] * sc));
+    sum = row_sum<L>(sum);
+    v = add({sum.h * inv_d, sum.l * inv_d}, {eps * sc * sc, 0.f});
+    if (round == 0) sc = !(v.h < 0x1p113f) ? 0x1p-70f : v.h < 0x1p-100f ? 0x1p60f : 1.f;
+    if (!__any_sync(0xffffffffu, sc != 1.f)) break;
+  }
+  *scale = sc;
   const float r = rsqrtf(v.h);
   const Dd q = two_prod(r, r);
   float e = fmaf(-v.h, q.h, 1.f);
   e = fmaf(-v.h, q.l, e);
   e = fmaf(-v.l, q.h, e);
-  return {r * down, 0.5f * r * e * down};
+  return {r, 0.5f * r * e};
 }
 
 // The same in fp32, within 8.5 2^-24 for bf16 values: their squares are exact,
@@ -299,23 +298,27 @@ __device__ __forceinline__ void store_row(void* cache, void* sz, long long row, 
 template <int L, typename T>
 __device__ __noinline__ void exact_key(const Piece<T>& k, const float (&w)[8], bool norm, float eps, const float2* cs,
                                        const float2* low, Piece<T>& out) {
-  float x[8], y[8];
+  float x[8], y[8], scale = 1.f;
   k.values(x);
   Dd r = {1.f, 0.f};
-  if (norm) r = inv_rms<L>(x, eps);
+  if (norm) r = inv_rms<L>(x, eps, &scale);
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const Dd c = {cs[j / 2].x, low[j / 2].x}, s = {cs[j / 2].y, low[j / 2].y};
-    Dd a = {x[j], 0.f}, e = {x[j + 1], 0.f};
+    Dd a = {x[j], 0.f}, e = {x[j + 1], 0.f}, root = r;
     if (norm) {
-      a = two_prod(x[j], w[j]);
-      e = two_prod(x[j + 1], w[j + 1]);
+      // (a row above 2^56 has small values as they are: scaled, they would leave the normal numbers)
+      const bool as_is = scale < 1.f && fmaxf(fabsf(x[j]), fabsf(x[j + 1])) <= 1.f;
+      const float f = as_is ? 1.f : scale;
+      a = two_prod(x[j] * f, w[j]);
+      e = two_prod(x[j + 1] * f, w[j + 1]);
+      if (as_is) root = {r.h * scale, r.l * scale};
     }
     const Dd es = mul(e, s), ec = mul(e, c);
     Dd u = add(mul(a, c), {-es.h, -es.l}), v = add(mul(a, s), ec);
     if (norm) {
-      u = mul(u, r);
-      v = mul(v, r);
+      u = mul(u, root);
+      v = mul(v, root);
     }
     if constexpr (std::is_same<T, float>::value) {
       y[j] = __fadd_rn(u.h, u.l);
@@ -480,14 +483,15 @@ __global__ void __launch_bounds__(kNormThreads, 4) append_norm_kernel(const Norm
         float x[8];
         q[g].values(x);
         r[g] = fast_inv_rms<L>(x, p.eps);
-        out_of_range = out_of_range || !(r[g] > 0x1p-58f);
+        out_of_range = out_of_range || !(r[g] > 0x1p-58f && r[g] < 0x1p50f);
       }
       if (__any_sync(0xffffffffu, out_of_range)) {
 #pragma unroll
         for (int g = 0; g < Q; ++g) {
-          float x[8];
+          float x[8], scale;
           q[g].values(x);
-          r[g] = inv_rms<L>(x, p.eps).h;
+          const float h = inv_rms<L>(x, p.eps, &scale).h;
+          r[g] = h * scale;
         }
       }
     }

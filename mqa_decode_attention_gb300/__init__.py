@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import warnings
 from dataclasses import dataclass
 
 import torch
@@ -125,16 +126,30 @@ def _four_bit(what: str, codes: torch.Tensor, pairs) -> None:
                              f"got {None if x is None else (x.dtype, tuple(x.shape))}")
 
 
-def _cache_kind(k: torch.Tensor, v: torch.Tensor, k_sz, v_sz, cache_dtype: int | None) -> tuple[int, int]:
-    """(cache dtype code, head_dim) of a cache pair; cache_dtype only says that uint8 tensors hold 4-bit codes."""
+def _u8_pairs(what: str, codes: torch.Tensor, pairs):
+    """The (scale, zero point) pairs of uint8 codes. Pairs that the kernels would read or write past their end, as the bf16
+    pairs of a 4-bit cache, are left out: every call refuses a uint8 layout without pairs."""
+    if pairs is None or (pairs.dtype is torch.float32 and pairs.is_contiguous() and pairs.numel() >= codes.numel() // codes.shape[3] * 2):
+        return pairs
+    warnings.warn(f"{what} pairs of a uint8 cache: contiguous float32 (scale, zero point) for each of its rows is wanted, got "
+                  f"{pairs.dtype} {tuple(pairs.shape)}; the calls will refuse this layout (a 4-bit cache is said by cache_dtype=MQA_U4)",
+                  stacklevel=4)
+    return None
+
+
+def _cache_kind(k: torch.Tensor, v: torch.Tensor, k_sz, v_sz, cache_dtype: int | None) -> tuple:
+    """(cache dtype code, head_dim, K pairs, V pairs) of a cache pair; cache_dtype only says that uint8 tensors hold 4-bit
+    codes."""
     if cache_dtype == MQA_U4:
         _four_bit("K", k, k_sz)
         _four_bit("V", v, v_sz)
-        return MQA_U4, 2 * k.shape[3]
+        return MQA_U4, 2 * k.shape[3], k_sz, v_sz
     kind = _dtype_code(k.dtype)
     if cache_dtype not in (None, kind):
         raise ValueError(f"cache_dtype {cache_dtype} with tensors of {k.dtype}")
-    return kind, k.shape[3]
+    if kind == MQA_U8:
+        k_sz, v_sz = _u8_pairs("K", k, k_sz), _u8_pairs("V", v, v_sz)
+    return kind, k.shape[3], k_sz, v_sz
 
 
 def layout_contiguous(k_cache: torch.Tensor, v_cache: torch.Tensor, h_q: int, window: int = 0,
@@ -145,11 +160,13 @@ def layout_contiguous(k_cache: torch.Tensor, v_cache: torch.Tensor, h_q: int, wi
     2] scale / zero-point pairs; with cache_dtype=MQA_U4 uint8 [batch, h_kv,
     capacity, head_dim / 2] of two 4-bit codes to a byte, with bf16 [batch, h_kv,
     capacity, 2] scale / minimum pairs); window > 0 restricts the attention to
-    the last `window` tokens."""
+    the last `window` tokens. Without cache_dtype uint8 codes are those of a uint8
+    cache; pairs that are not its own are left out with a warning, and the calls
+    refuse the layout."""
     assert k_cache.shape == v_cache.shape and k_cache.dim() == 4
     assert k_cache.is_contiguous() and v_cache.is_contiguous()
     B, h_kv, cap, _ = k_cache.shape
-    kind, d = _cache_kind(k_cache, v_cache, k_scale_zero, v_scale_zero, cache_dtype)
+    kind, d, k_scale_zero, v_scale_zero = _cache_kind(k_cache, v_cache, k_scale_zero, v_scale_zero, cache_dtype)
     lay = KVLayout(kind, B, h_q, h_kv, d, 0, k_cache.data_ptr(), v_cache.data_ptr(), cap,
                    0, 0, 0, window, None, _ptr(k_scale_zero), _ptr(v_scale_zero))
     lay._tensors = (k_cache, v_cache, k_scale_zero, v_scale_zero)  # the struct holds raw pointers: keep them alive
@@ -167,7 +184,7 @@ def layout_paged(k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.
     assert k_pool.shape == v_pool.shape and k_pool.dim() == 4
     assert block_table.dtype == torch.int32 and block_table.is_contiguous()
     n, h_kv, ps, _ = k_pool.shape
-    kind, d = _cache_kind(k_pool, v_pool, k_scale_zero, v_scale_zero, cache_dtype)
+    kind, d, k_scale_zero, v_scale_zero = _cache_kind(k_pool, v_pool, k_scale_zero, v_scale_zero, cache_dtype)
     B, mp = block_table.shape
     lay = KVLayout(kind, B, h_q, h_kv, d, 1, k_pool.data_ptr(), v_pool.data_ptr(), 0, ps, n,
                    mp, window, block_table.data_ptr(), _ptr(k_scale_zero), _ptr(v_scale_zero))

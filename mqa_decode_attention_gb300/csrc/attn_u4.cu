@@ -389,7 +389,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
       seen += __shfl_sync(kFull, upto, 31);
     }
   }
-  if (run <= 0) return;  // the whole block
+  if (run <= 0) {  // the whole block; after the append, so that a launch without any work does not end before it
+    grid_dependency_wait();
+    return;
+  }
 
   // -------------------------------------------------- filling the rings
   // Tile k of the run goes to warp k % kWarps, into stage k / kWarps % STAGES of its ring. Two lanes, each a bulk copy: V

@@ -1,0 +1,58 @@
+"""GPU: steps over a 4-bit cache whose attention has nothing to do."""
+
+import math
+
+import pytest
+import torch
+
+from u4_cases import U4Case
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def m(built_lib):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import mqa_decode_attention_gb300 as mod
+
+    mod.library()
+    return mod
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("page", [0, 16])
+def test_step_of_lengths_out_of_range(m, page, splits):
+    """Every length is out of range, so that all blocks of the attention leave at once: what follows on the stream still
+    finds the rows that the step appended."""
+    B, hq, hkv, d, n = 48, 8, 8, 128, 32
+    c = U4Case(hq, hkv, d, [256] * B, n, page, seed=3, garbage=False)
+    g = torch.Generator().manual_seed(5)
+    new = [torch.randn(B, n, h, d, generator=g).to(torch.bfloat16).to(DEV) for h in (hq, hkv, hkv)]
+    lay = c.layout(m)
+    bufs = m.DecodeBuffers.allocate(lay, 256, num_splits=splits, n_new=n)
+    want = {}
+    pos, rot, err = _i32([11] * B), torch.empty(B, n, hq, d, device=DEV), _i32([0])
+    m.kv_append_rope_multi(lay, n, *new, pos, 10000.0, rot, err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    want = {x: c.dev[x].clone() for x in ("k", "v", "ksm", "vsm")}
+    lens = _i32([0, 257, -3, 31] * (B // 4))
+    for _ in range(5):
+        for x in want:
+            c.dev[x].zero_()
+        bufs.err.zero_()
+        m.decode_step_multi(lay, n, *new, pos, lens, 256, bufs, scale=1 / math.sqrt(d), num_splits=splits)
+        found = {x: c.dev[x].clone() for x in want}  # on the same stream, right behind the step
+        torch.cuda.synchronize()
+        assert int(bufs.err) == m.MQA_DEVERR_SEQ_LEN
+        for x in want:
+            for b in range(0, B, 7):
+                for t in range(11, 11 + n):
+                    at = c.slot(b, t)
+                    assert torch.equal(found[x][at].view(torch.uint8), want[x][at].view(torch.uint8)), (x, b, t)

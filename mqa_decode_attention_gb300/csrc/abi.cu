@@ -174,6 +174,8 @@ struct U4Plan {
   size_t workspace;
 };
 
+constexpr int kWholeTiles = 128;  // (see choose_splits)
+
 U4Plan u4_plan(const mqa_kv_layout* L, int n_new) {
   int dev = 0;
   cudaGetDevice(&dev);
@@ -206,13 +208,19 @@ int choose_splits(const mqa_kv_layout* L, int max_len_in, int variant, int n_new
     // One block for each unit, where the others' merging would cost more than its unequal load: for units of few tiles
     // (a tile's time goes with its dims and rows; head_dim 128 and 8 rows: 8 units of 16 tiles 10.0 us, shared 10.4, of 32
     // tiles 15.6 and 11.6; 160 units of 16 tiles 12.4 and 14.5), and for contiguous caches with units for more than half of
-    // the blocks (256 units of 64 tiles 32 us, shared 38; the lengths of a paged batch are taken as unequal).
+    // the blocks and a bound of up to kWholeTiles tiles (the lengths of a paged batch are taken as unequal). The lengths are
+    // not known here. 32 x 8 units, equal / spread evenly up to the bound / one of the bound and the others of 1000 tokens, us:
+    //   64 tiles    32 and 37 shared    29 and 42    27 and 25     .. of 32 rows    87 and 88    73 and 109     71 and 40 (others of 300)
+    //   128 tiles   56 and 62           48 and 58    46 and 29                     161 and 163  152 and 204    132 and 53
+    //   256 tiles  105 and 103          98 and 82    84 and 34                     304 and 305  296 and 218    245 and 60
+    //   2048 tiles, one of the bound: 616 and 58. (16 rows are between; units past a whole number of waves, 464 of 64 tiles:
+    //   65 and 58, 456 of them 46 and 48.)
     const U4Plan c = u4_plan(L, n_new);
     long long span = max_len_in;
     if (L->window > 0) span = std::min(span, static_cast<long long>(L->window) + n_new - 1 + kU4Tile - 1);
     const long long tiles = (span + kU4Tile - 1) / kU4Tile;
     if (tiles * L->head_dim * c.shape.rows <= 16 * 128 * 8) return 1;
-    return !L->paged && 2ll * L->batch * L->h_kv * c.row_blocks > c.ctas ? 1 : 2;
+    return !L->paged && tiles <= kWholeTiles && 2ll * L->batch * L->h_kv * c.row_blocks > c.ctas ? 1 : 2;
   }
   const int max_len = read_span(L, max_len_in);
   int dev = 0;

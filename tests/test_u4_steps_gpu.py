@@ -1,4 +1,4 @@
-"""GPU: steps over a 4-bit cache whose attention has nothing to do."""
+"""GPU: steps over a 4-bit cache whose attention has nothing to do, and waits of its wider kernels that run out."""
 
 import math
 
@@ -56,3 +56,39 @@ def test_step_of_lengths_out_of_range(m, page, splits):
                 for t in range(11, 11 + n):
                     at = c.slot(b, t)
                     assert torch.equal(found[x][at].view(torch.uint8), want[x][at].view(torch.uint8)), (x, b, t)
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("group,splits", [(12, 1), (12, 2), (32, 1), (32, 2)])
+def test_timeout_of_wider_kernels(m, group, splits, page):
+    """The waits of the 16-row and 32-row kernels and of paged tiles with a limit of 1 ns: the call comes back, says so, and
+    the next one gives what the call before gave."""
+    B, hkv, d, L = 24, 4, 128, 6000
+    g = torch.Generator(DEV).manual_seed(7)
+    shape = (B * -(-L // 16), hkv, 16) if page else (B, hkv, L)
+    codes = [torch.randint(0, 256, (*shape, d // 2), generator=g, dtype=torch.uint8, device=DEV) for _ in "kv"]
+    pairs = [torch.rand(*shape, 2, generator=g, device=DEV).to(torch.bfloat16) for _ in "kv"]
+    if page:
+        table = torch.randperm(shape[0], generator=g, device=DEV).int().view(B, -1)
+        lay = m.layout_paged(codes[0], codes[1], table, hkv * group, 0, pairs[0], pairs[1], cache_dtype=m.MQA_U4)
+    else:
+        lay = m.layout_contiguous(codes[0], codes[1], hkv * group, 0, pairs[0], pairs[1], cache_dtype=m.MQA_U4)
+    q, lens = torch.randn(B, hkv * group, d, generator=g, device=DEV), _i32([L] * (B - 2) + [L - 77, 130])
+    bufs = m.DecodeBuffers.allocate(lay, L, num_splits=splits)
+
+    def call():
+        bufs.err.zero_()
+        m.gqa_decode_attention(lay, q, lens, L, 0.09, splits, bufs.out, bufs.lse, bufs.workspace, err=bufs.err)
+        torch.cuda.synchronize()
+        return int(bufs.err), bufs.out.clone()
+
+    err, before = call()
+    assert err == 0 and torch.isfinite(before).all()
+    lay.wait_limit_ns = 1
+    for _ in range(5):
+        err, out = call()
+        # (a wait that finds its tile at the first look does not run out: 32 rows take longer over a tile than its load)
+        assert err == m.MQA_DEVERR_TIMEOUT or (err == 0 and torch.equal(before, out))
+    lay.wait_limit_ns = 0
+    err, after = call()
+    assert err == 0 and torch.equal(before, after)

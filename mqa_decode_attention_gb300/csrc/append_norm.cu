@@ -514,8 +514,11 @@ __global__ void __launch_bounds__(kNormThreads, 4) append_norm_kernel(const Norm
 }
 
 // A block a token with its heads spread over several blocks, while that fills
-// the GPU; with four blocks an SM and more, several tokens a block, which fill
-// its threads with sines and cosines, and more query rows at a time.
+// the GPU; with two such blocks an SM and more, several tokens a block, which fill
+// its threads with sines and cosines, and more query rows at a time. (One token a
+// block and several, 32 and 8 heads of 128 into a 4-bit cache: 640 tokens, one
+// block an SM of several, 11.4 and 12.3 us; 1216 tokens, two, 16.0 and 14.6; 2368,
+// three, 28.1 and 21.6; 3648, six, 39.9 and 32.0. A bf16 cache alike.)
 template <int CACHE, int D>
 cudaError_t launch_norm_d(const NormAppendParams& p, int sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -523,7 +526,7 @@ cudaError_t launch_norm_d(const NormAppendParams& p, int sms, cudaStream_t strea
   cfg.stream = stream;
   const int tokens = p.batch * p.n_new;
   constexpr int kTok = 512 / D, kRows = 256 / D;
-  if (tokens / kTok >= 4 * sms) {
+  if (tokens / kTok >= 2 * sms) {
     cfg.gridDim = dim3(static_cast<unsigned>((tokens - 1) / kTok + 1));
     return cudaLaunchKernelEx(&cfg, append_norm_kernel<CACHE, D, kTok, CACHE == kDtypeF32 ? 2 : 4>, p);
   }

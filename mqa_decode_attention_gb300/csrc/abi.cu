@@ -181,7 +181,7 @@ U4Plan u4_plan(const mqa_kv_layout* L, int n_new) {
   cudaGetDevice(&dev);
   U4Plan c;
   const int rows = (L->h_q / L->h_kv) * n_new;
-  c.shape = u4_shape(L->head_dim, rows);
+  c.shape = u4_shape(rows);
   c.row_blocks = (rows + c.shape.rows - 1) / c.shape.rows;
   c.ctas = device_info(dev).sms * c.shape.ctas_per_sm;
   c.counters = (static_cast<size_t>(c.ctas) * 4 + 255) / 256 * 256;
@@ -730,9 +730,7 @@ mqa_status u4_attention(const mqa_kv_layout* L, int n_new, const float* q_rot, c
   p.out_dtype = out_dtype == MQA_BF16 ? kDtypeBf16 : kDtypeF32;
   p.lse_out = lse_out;
   p.whole = whole;
-  p.min_tiles = 4;
   p.parts = static_cast<int>(c.ctas / (static_cast<long long>(L->batch) * L->h_kv * c.row_blocks));
-  p.min_part = 4;
   p.arrived = static_cast<int32_t*>(workspace);
   p.part = whole ? nullptr : reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.counters);
   p.err = err_word;

@@ -37,6 +37,24 @@
 namespace mqa {
 namespace {
 
+// e5m2_code of a float, in float arithmetic: every step is exact for a float
+// input (scalings by powers of two, one rint), so the code equals
+// e5m2_code(double(x)) without fp64 work.
+__device__ __forceinline__ uint32_t e5m2_code_f(float x) {
+  uint32_t code = 0x7Fu;
+  if (!isnan(x)) {
+    const float ax = fabsf(x);
+    float r = 57344.0f;
+    if (ax < 57344.0f) {
+      const int e = ax > 0.0f ? ilogbf(ax) : -14;
+      const int qe = (e < -14 ? -14 : e) - 2;
+      r = fminf(ldexpf(rintf(ldexpf(ax, -qe)), qe), 57344.0f);
+    }
+    code = static_cast<uint32_t>(__half_as_ushort(__float2half_rn(r))) >> 8;
+  }
+  return code | (signbit(x) ? 0x80u : 0u);
+}
+
 // The key pair (x, y) turned by the reduced angle and rounded once to e5m2,
 // decided in fp32 as rope_k_bf16_fast decides a bf16 rounding: the rotation
 // from the fp32 cosine / sine cf, sf of the angle is within 8e-7 (|x| + |y|)

@@ -32,8 +32,9 @@
 // P^T transposed in registers (movmatrix), O^T += V^T P^T (dims on the rows, so
 // O's columns are S's): nothing but K, V and q passes through shared memory.
 // Codes stream through a ring of two stages of its own, filled with bulk copies
-// by the warp itself: four warps of a block meet at the end of a unit only (unit:
-// sequence, kv head, block of query rows).
+// by the warp itself: the warps of a block, four, or six where units are whole and
+// few, meet at the end of a unit only (unit: sequence, kv head, block of query
+// rows).
 //
 // Who does what: a block takes a whole unit; or all resident blocks share the
 // tiles, a unit in equal parts, or all units in order cut into equal runs, so
@@ -70,6 +71,11 @@ constexpr float kSlack = 4.f;
 // are merged by weights of down to 2^(kLeast - kMost), which fp32 holds.)
 constexpr float kLeast = -60.f, kMost = 66.f;
 constexpr uint32_t kFull = 0xffffffffu;
+// The least tiles of a run (one of 1, 2, 4, 8: a batch of 8 x 32 units, one sequence of 2048 tokens and 31 of 100 in pages,
+// 15.0, 14.8, 13.8, 20.4 us; 4 x 64 units, one of 4096 tokens and 63 of 64, 20.0, 20.1, 19.0, 31.9) and of a part of a unit
+// (8 units of 2048 tokens 20.0, 14.8, 12.8, 12.5 us, of 1200 tokens 15.4, 12.1, 11.6, 12.1; MQA, 8 x 2048, 29.6, 24.1, 19.3,
+// 20.3).
+constexpr int kMinRun = 4, kMinPart = 4;
 
 template <int D, int NT, int STAGES, int WARPS>
 struct Cfg {
@@ -354,12 +360,12 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attn_u4_kernel(const __grid_
     total *= units;
     bool placed = false;
     run_len = total < 1ull << 31 ? static_cast<unsigned>(total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
-    run_len = max(run_len, static_cast<long long>(p.min_tiles));
+    run_len = max(run_len, static_cast<long long>(kMinRun));
     // Parts of units where the longest is not much longer than a run, in which a change of unit costs as much as some 16
     // tiles (8 x 8 units of 32 tiles 14 us, in runs 19; 160 units of 64 tiles 28 and 31; 256 units of 128 tiles 67 and 62; 64
     // units of 128 tiles for 32 query rows 51 and 59).
     if (p.parts > 0 && (most + p.parts - 1) / p.parts <= run_len + run_len / 2 + 16) {
-      part_of_unit(p.parts, gridDim.x - p.parts * p.batch * units, p.min_part);
+      part_of_unit(p.parts, gridDim.x - p.parts * p.batch * units, kMinPart);
       placed = true;
     } else {
       at.b = at.u = at.base = 0;
@@ -1279,8 +1285,7 @@ cudaError_t launch_u4_d(const U4Params& p, const CUtensorMap& tv, int ctas, bool
 
 }  // namespace
 
-U4Shape u4_shape(int head_dim, int rows) {
-  (void)head_dim;
+U4Shape u4_shape(int rows) {
   if (rows <= 8) return {8, kCtas1};
   if (rows <= 16) return {16, kCtas2};
   return {32, kCtas4};

@@ -58,7 +58,8 @@ struct AppendParams {
 };
 
 // kv_append_norm_rope, and kv_append_rope over a 4-bit cache (append_norm.cu):
-// one warp for a (token, head) row, normalised when the weight is given.
+// 8 lanes (head_dim 64) or 16 for a (token, head) row, normalised when the weight
+// is given.
 constexpr int kMaxAxes = 4;
 struct NormAppendParams {
   int batch, h_q, h_kv, head_dim, cache_dtype, paged;
@@ -128,8 +129,7 @@ struct U4Params {
   int out_dtype;
   float* lse_out;
   int whole;         // 1: one block for each unit, no workspace; 0: parts of units or equal runs
-  int min_tiles;     // a run is at least this long
-  int parts, min_part;  // parts of a unit, a block each, and their least tiles, where that is no longer than the runs are
+  int parts;         // parts of a unit, a block each, where that is no longer than the runs are
   int32_t* arrived;  // [blocks] zero: blocks that have left a partial of the unit that starts in block c
   float* part;       // [2 blocks] partial results
   int32_t* err;
@@ -280,7 +280,7 @@ struct U4Shape {
   int rows;
   int ctas_per_sm;
 };
-U4Shape u4_shape(int head_dim, int rows);
+U4Shape u4_shape(int rows);
 // floats of one partial result: each row's sums, maximum (log2 domain) and sum
 inline size_t u4_part_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
 // ctas: blocks of a launch with p.whole == 0. clear: the counters are cleared by

@@ -45,24 +45,6 @@ __device__ __forceinline__ uint32_t e5m2_code(double x) {
   return code | (signbit(x) ? 0x80u : 0u);
 }
 
-// e5m2_code of a float, in float arithmetic: every step is exact for a float
-// input (scalings by powers of two, one rint), so the code equals
-// e5m2_code(double(x)) without fp64 work.
-__device__ __forceinline__ uint32_t e5m2_code_f(float x) {
-  uint32_t code = 0x7Fu;
-  if (!isnan(x)) {
-    const float ax = fabsf(x);
-    float r = 57344.0f;
-    if (ax < 57344.0f) {
-      const int e = ax > 0.0f ? ilogbf(ax) : -14;
-      const int qe = (e < -14 ? -14 : e) - 2;
-      r = fminf(ldexpf(rintf(ldexpf(ax, -qe)), qe), 57344.0f);
-    }
-    code = static_cast<uint32_t>(__half_as_ushort(__float2half_rn(r))) >> 8;
-  }
-  return code | (signbit(x) ? 0x80u : 0u);
-}
-
 // The fused append of a one-byte cache: sequence b's new token at `pos`, kv
 // head j, element offset `row` of its cache row (negative: nothing is
 // written), by one whole warp (lane i owns rotation pairs i, i + 32, ...),

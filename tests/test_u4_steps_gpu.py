@@ -1,4 +1,4 @@
-"""GPU: steps over a 4-bit cache whose attention has nothing to do, and waits of its wider kernels that run out."""
+"""GPU: steps over a 4-bit cache whose attention has nothing to do, waits of its wider kernels that run out, large caches."""
 
 import math
 
@@ -92,3 +92,52 @@ def test_timeout_of_wider_kernels(m, group, splits, page):
     lay.wait_limit_ns = 0
     err, after = call()
     assert err == 0 and torch.equal(before, after)
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_offsets_past_32_bits(m, page):
+    """The last of 68 sequences of 2^20 rows: its codes lie past 2^32 bytes. Appended, attended to and read back as in a
+    small cache, bit for bit."""
+    B, hq, hkv, d, rows, n = 68, 4, 1, 128, 1 << 20, 3
+    small = U4Case(hq, hkv, d, [300], n, seed=9, garbage=False)
+    g = torch.Generator().manual_seed(2)
+    new = [torch.randn(1, n, h, d, generator=g).to(torch.bfloat16).to(DEV) for h in (hq, hkv, hkv)]
+    shape = (B * rows // 16, hkv, 16) if page else (B, hkv, rows)
+    codes = [torch.zeros(*shape, d // 2, dtype=torch.uint8, device=DEV) for _ in "kv"]
+    pairs = [torch.zeros(*shape, 2, dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+    if page:  # 19 pages of the sequence, the last of the pool, from the last one down
+        pages = shape[0] - 1 - torch.arange(19)
+        table = pages.int().view(1, 19).to(DEV)
+        for t in range(300):
+            for x, y in zip(codes + pairs, (small.k, small.v, small.ksm, small.vsm)):
+                x[int(pages[t // 16]), :, t % 16] = y[0, :, t].to(DEV)
+        lay = m.layout_paged(codes[0], codes[1], table, hq, 0, pairs[0], pairs[1], cache_dtype=m.MQA_U4)
+        first, batch = 0, 1
+    else:
+        for x, y in zip(codes + pairs, (small.k, small.v, small.ksm, small.vsm)):
+            x[-1, :, : y.shape[2]] = y[0].to(DEV)
+        lay = m.layout_contiguous(codes[0], codes[1], hq, 0, pairs[0], pairs[1], cache_dtype=m.MQA_U4)
+        first, batch = B - 1, B
+    ref = small.layout(m)
+    outs = []
+    for layout, at, size in ((ref, 0, 1), (lay, first, batch)):
+        x = [torch.zeros(size, *t.shape[1:], dtype=t.dtype, device=DEV) for t in new]
+        for a, b in zip(x, new):
+            a[at] = b[0]
+        pos = torch.zeros(size, dtype=torch.int32, device=DEV)
+        pos[at] = 297
+        bufs = m.DecodeBuffers.allocate(layout, 300, num_splits=2, n_new=n)
+        m.decode_step_multi(layout, n, *x, pos, pos + n, 300, bufs, num_splits=2)
+        w = torch.full((d,), 1.25, dtype=torch.bfloat16, device=DEV)
+        rows_out = [torch.zeros(size, hkv, 300, d, device=DEV) for _ in "kv"]
+        m.kv_read_rows(layout, None, pos + n, *rows_out, bufs.err)
+        step = [bufs.out[at].clone()] + [r[at].clone() for r in rows_out]
+        m.kv_append_norm_rope(layout, n, *x, pos, 1e4, bufs.q_rot, bufs.err, q_weight=w, k_weight=w)
+        m.kv_read_rows(layout, None, pos + n, *rows_out, bufs.err)
+        torch.cuda.synchronize()
+        assert int(bufs.err) == 0
+        outs.append(step + [r[at].clone() for r in rows_out])
+    # (the runs of tiles differ with the number of units: the output within its bf16 rounding and the sums' order)
+    assert torch.all((outs[0][0].float() - outs[1][0].float()).abs() <= 16 * (2.0 ** -11 + 2.0 ** -16) + 1.01 * 2.0 ** -7 * outs[0][0].float().abs())
+    for a, b in zip(outs[0][1:], outs[1][1:]):
+        assert torch.equal(a, b)

@@ -160,7 +160,9 @@ typedef enum mqa_variant {
  * head, block of up to 32 query rows), no workspace; > 1 = the cached tokens
  * shared by as many blocks as are resident, whatever the number; 0 = the
  * library's choice of the two, by the bound on the lengths (mqa_choose_splits:
- * 1 or 2). Calls that may overlap on the GPU need a workspace each. The query is
+ * 1 or 2). A kv head with more than 32 query rows has its cache read and
+ * multiplied once for each block of 32, which takes longer than a bf16 cache of
+ * the same tokens. Calls that may overlap on the GPU need a workspace each. The query is
  * rounded to fp16 (each head's by a power of two of its own; 11
  * bits), the probabilities times s to 11 bits, down to 2^-25 of a query's largest
  * such product (of scales up to 2^60 apart); the values of a window's or a

@@ -44,13 +44,13 @@
 // they are made.)
 //
 // What bounds it. Up to 8 rows with 3 blocks on every SM: HBM (1024 units of 8192
-// tokens 187 us, 6.1 TB/s; pages of 64 tokens 204; of 16, whose tile is 8 bulk
-// copies, 219, and 232 with the pairs by bulk copies too). With fewer units the
+// tokens 191 us, 6.0 TB/s; pages of 64 tokens 211; of 16, whose tile is 8 bulk
+// copies, 225, and some 13 more with the pairs by bulk copies too). With fewer units the
 // chain products - softmax - products of a warp, 1.3 us a tile (256 units of 4096
 // tokens 32 us, 4.5 TB/s), at the least 5.5 us for the launch, the first tile and
 // the last merge. 9 to 32 rows: the tensor pipes, 256 multiply-adds a cycle and
 // scheduler with mma.sync, half busy, since the registers leave two warps to a
-// scheduler (64 MQA units of 8192 tokens 51 us, floor by
+// scheduler (64 MQA units of 8192 tokens 50 us, floor by
 // products 15). For runs four warps and three blocks on an SM were the best of
 // 6 x 2, 8 x 1 and 12 x 1; a fifth warp that fills the rings cost its registers
 // more than it gave.
